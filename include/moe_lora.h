@@ -68,6 +68,7 @@ extern "C" {
 #define MOE_LORA_WS_FWD_SCRATCH 2 /* forward temporaries */
 #define MOE_LORA_WS_BWD_SCRATCH 3 /* backward temporaries */
 #define MOE_LORA_WS_ROUTER_SCRATCH 4 /* router error word and backward temporaries */
+#define MOE_LORA_WS_BALANCE_SCRATCH 5 /* balance loss error word and partial sums */
 
 /* Problem sizes.  H and I must be multiples of 64 (the 64-element K step of every
  * contraction; the 128- and 256-wide output tiles need not divide them: loads past
@@ -304,6 +305,120 @@ MOE_LORA_API int moe_lora_router_backward(const moe_lora_dims* dims, const uint1
 /* Reads (and keeps) the device error word of a router scratch buffer
  * (MOE_LORA_DEV_* bits); synchronises `stream`. */
 MOE_LORA_API int moe_lora_router_get_error(const void* scratch, void* stream);
+
+/* ---- the training step around the expert layer ----
+ * Layer norm ahead of the router and the experts, the router's balance loss, and the
+ * AdamW step over the trained tensors.  The pages give none of them; each is the usual
+ * definition, stated below.  Element types are passed as MOE_LORA_F32 / _BF16 / _F16;
+ * all sums, statistics and states are held in fp32 unless stated. */
+#define MOE_LORA_F32 0
+#define MOE_LORA_BF16 1
+#define MOE_LORA_F16 2
+
+/* Layer norm over the last axis of [rows, n].  Rows may be farther apart than n: the
+ * ld fields are row strides in elements (0 = n, else >= n); elements of a row are
+ * contiguous.  rows >= 0 and 1 <= n <= 2^24; rows = 0 is a no-op (a backward's weight
+ * gradients are then zero). */
+typedef struct moe_lora_norm {
+  int64_t rows;
+  int64_t ldx;     /* x */
+  int64_t ldy;     /* y (forward), dy (backward) */
+  int64_t lddx;    /* dx */
+  int64_t lddres;  /* dres */
+  int32_t n;
+  int32_t dtype;   /* x, y, dy, dres, dx */
+  int32_t wdtype;  /* gamma, beta */
+  float eps;       /* > 0; forward only (the backward takes rstd) */
+} moe_lora_norm;
+
+/* y = (x - mean) * rstd * gamma + beta with mean = avg x, rstd = 1/sqrt(avg (x - mean)^2 + eps),
+ * one rounding to y's type.  gamma / beta [n] may be NULL (1 / 0).  mean, rstd [rows] fp32 are
+ * written when non-NULL (both or neither); the backward needs them.  y may be x. */
+MOE_LORA_API int moe_lora_layernorm_forward(const moe_lora_norm* nm, const void* x, const void* gamma,
+                                            const void* beta, void* y, float* mean, float* rstd, void* stream);
+
+/* With h = (x - mean) * rstd and u = dy * gamma (gamma NULL = 1):
+ *   dx = rstd * (u - avg u - h * avg(u h)) + dres      (dres NULL = 0: the gradient that
+ *        reaches x on another path, e.g. the residual stream; one rounding to dx's type)
+ *   dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy      [n] fp32; each may be NULL
+ * dx may be dy or dres (same stride); sums over rows run in a fixed order, so equal calls give
+ * equal bits.  scratch: device buffer of moe_lora_layernorm_scratch_bytes(nm) bytes (0 for bad
+ * sizes); may be NULL when both weight gradients are. */
+MOE_LORA_API size_t moe_lora_layernorm_scratch_bytes(const moe_lora_norm* nm);
+MOE_LORA_API int moe_lora_layernorm_backward(const moe_lora_norm* nm, const void* x, const void* gamma,
+                                             const float* mean, const float* rstd, const void* dy, const void* dres,
+                                             void* dx, float* dgamma, float* dbeta, void* scratch,
+                                             size_t scratch_bytes, void* stream);
+
+/* Balance loss of the routing step, with the per-expert counts.  For adapter a (its tokens as in
+ * moe_lora_plan; NULL offsets when A == 1): a token is live when at least one of its k ids is in
+ * [0, E) (-1 = masked route; other ids are dropped and flagged MOE_LORA_DEV_BAD_ID); N = live
+ * tokens, c_e = routes to expert e, R = sum_e c_e, p_t = softmax(l_t) over all E,
+ *     prob_e = (1/N) sum over live t of p_te,   f_e = c_e / R,   loss = coef * E * sum_e f_e prob_e,
+ *     dlogits_te = dloss * coef * E / N * p_te * (f_e - sum_e' p_te' f_e')
+ * for live tokens and 0 for the others, whose logits are not used (they may hold anything).  The
+ * counts are steps in the logits and have no gradient.  A logit of -inf has probability 0; a row of
+ * -inf alone contributes nothing; NaN and +inf give NaN.  Without live tokens loss, prob and
+ * dlogits are 0.
+ *   logits  [T, E] of `dtype` (MOE_LORA_F32 / _BF16 / _F16), rows ld elements apart (0 = E)
+ *   dloss   [A] fp32, the gradient that reaches each loss (NULL = 1); used by dlogits alone
+ *   loss [A] fp32, counts [A,E] int32, prob [A,E] fp32
+ *   dlogits [T,E] fp32, or NULL for the forward alone
+ * dims gives T, E <= 1024 (else MOE_LORA_ERR_UNSUPPORTED), k and A.  `scratch` is a device buffer
+ * of moe_lora_workspace_bytes(.., MOE_LORA_WS_BALANCE_SCRATCH); its first word is the device error
+ * word, cleared here and read by moe_lora_router_get_error().  Sums run in a fixed order that
+ * depends on the adapter's own tokens alone: each adapter's results equal its standalone run bit
+ * for bit. */
+MOE_LORA_API int moe_lora_balance_loss(const moe_lora_dims* dims, const void* logits, int32_t dtype, int64_t ld,
+                                       const int32_t* topk_ids, const int64_t* adapter_offsets, float coef,
+                                       const float* dloss, float* loss, int32_t* counts, float* prob, float* dlogits,
+                                       void* scratch, size_t scratch_bytes, void* stream);
+
+/* moe_lora_router_backward with a gradient dlogits_aux [T,E] fp32 (e.g. the balance loss's; NULL =
+ * none) added to the routes' own before dW_r, grad-x and the dlogits output are formed.  Unlike the
+ * routes' part it is not limited to the selected experts. */
+MOE_LORA_API int moe_lora_router_backward_aux(const moe_lora_dims* dims, const uint16_t* x, const uint16_t* Wr,
+                                              const int64_t* adapter_offsets, const int32_t* topk_ids,
+                                              const float* topk_w, const float* dw, const float* dlogits_aux,
+                                              float* dlogits, float* dWr, uint16_t* dx, void* scratch,
+                                              size_t scratch_bytes, void* stream);
+
+/* AdamW over n tensors at once.  With g the gradient times *grad_scale, t = step, in fp32:
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g g,
+ *     w = w (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps),
+ * each operation rounded on its own (no fused multiply-add), p = w rounded to its type.  w is
+ * `master` where that is given, else p.  state 0: m and v are fp32.  state 1: they are held in 8
+ * bits, in blocks of 256 consecutive elements (the last may be short): m and r = sqrt(v) as E4M3
+ * codes times one fp32 scale per block, max|.| * fp32(1/448), of x * ((1 / max|.|) * 448) (a block
+ * whose maximum is below 2^-100 is stored as zeros, scale 0).  r, not v: E4M3 spans a ratio of 2^18, which on r is gradients that
+ * differ by 2^18 inside a block, on v only by 2^9.  The step uses the new m and v before they are
+ * rounded.  A non-finite gradient spoils its own element only: scales are taken over finite
+ * values, a non-finite m or r becomes the NaN code. */
+typedef struct moe_lora_adamw_tensor {
+  void* p;             /* [numel] parameter, read (unless master is given) and written */
+  float* master;       /* [numel] fp32 parameter of a bf16 / fp16 p, read and written; or NULL */
+  const void* g;       /* [numel] gradient */
+  void* m;             /* [numel] fp32, or E4M3 codes */
+  void* v;             /* [numel] fp32, or E4M3 codes of r */
+  float* m_scale;      /* state 1: [ceil(numel / 256)] */
+  float* v_scale;      /* state 1: [ceil(numel / 256)] */
+  int64_t numel;       /* 0 = skipped */
+  int32_t p_dtype, g_dtype; /* MOE_LORA_F32 / _BF16 / _F16 */
+  int32_t state;       /* 0 = 32 bits, 1 = 8 bits */
+  double lr, weight_decay;
+} moe_lora_adamw_tensor;
+
+typedef struct moe_lora_adamw {
+  double beta1, beta2; /* in [0, 1) */
+  double eps;          /* > 0 */
+  int64_t step;        /* 1 for the first step */
+  const float* grad_scale; /* DEVICE scalar (e.g. a clipping factor; 4-byte aligned), or NULL for 1 */
+} moe_lora_adamw;
+
+/* tensors [n]: HOST array, read before the call returns.  The tensors do not overlap.  One launch
+ * per 352 tensors of a state. */
+MOE_LORA_API int moe_lora_adamw_step(const moe_lora_adamw* opt, const moe_lora_adamw_tensor* tensors, int32_t n,
+                                     void* stream);
 
 /* Static description of a return code. */
 MOE_LORA_API const char* moe_lora_strerror(int code);

@@ -27,6 +27,7 @@ LIB_PATH = _build.LIB
 
 MOE_LORA_WS_PLAN, MOE_LORA_WS_SAVED, MOE_LORA_WS_FWD_SCRATCH, MOE_LORA_WS_BWD_SCRATCH = 0, 1, 2, 3
 MOE_LORA_WS_ROUTER_SCRATCH = 4
+MOE_LORA_WS_BALANCE_SCRATCH = 5
 MOE_LORA_DEV_BAD_ID, MOE_LORA_DEV_TIMEOUT = 1, 2
 
 
@@ -46,6 +47,23 @@ class Dims(ctypes.Structure):
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("W1", "W3", "W2", "A1", "A3", "B1", "B3", "A2", "B2",
                                                  "S1", "S3", "S2")]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("lddx", ctypes.c_int64),
+                ("lddres", ctypes.c_int64), ("n", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] + [
+        ("numel", ctypes.c_int64), ("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+        ("lr", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class AdamW(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("grad_scale", ctypes.c_void_p)]
 
 
 class Grads(ctypes.Structure):
@@ -115,6 +133,21 @@ def lib() -> ctypes.CDLL:
                                                P]
         L.moe_lora_router_get_error.restype = ctypes.c_int
         L.moe_lora_router_get_error.argtypes = [P, P]
+        L.moe_lora_layernorm_forward.restype = ctypes.c_int
+        L.moe_lora_layernorm_forward.argtypes = [ctypes.POINTER(Norm), P, P, P, P, P, P, P]
+        L.moe_lora_layernorm_scratch_bytes.restype = ctypes.c_size_t
+        L.moe_lora_layernorm_scratch_bytes.argtypes = [ctypes.POINTER(Norm)]
+        L.moe_lora_layernorm_backward.restype = ctypes.c_int
+        L.moe_lora_layernorm_backward.argtypes = [ctypes.POINTER(Norm), P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t,
+                                                  P]
+        L.moe_lora_balance_loss.restype = ctypes.c_int
+        L.moe_lora_balance_loss.argtypes = [ctypes.POINTER(Dims), P, ctypes.c_int32, ctypes.c_int64, P, P,
+                                            ctypes.c_float, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_lora_router_backward_aux.restype = ctypes.c_int
+        L.moe_lora_router_backward_aux.argtypes = [ctypes.POINTER(Dims), P, P, P, P, P, P, P, P, P, P, P,
+                                                   ctypes.c_size_t, P]
+        L.moe_lora_adamw_step.restype = ctypes.c_int
+        L.moe_lora_adamw_step.argtypes = [ctypes.POINTER(AdamW), P, ctypes.c_int32, P]
         _lib = L
     return _lib
 
@@ -393,6 +426,181 @@ def moe_lora_profile_read() -> Dict[str, tuple]:
 
 def moe_lora_launch_count(reset: bool = False) -> int:
     return int(lib().moe_lora_launch_count(1 if reset else 0))
+
+
+# ------------------------------------------------------------------ training step
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
+    """Pointer and row stride of a [rows, n] tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [rows, n] with n >= 1")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name} must be {tuple(like.shape)} {like.dtype}, got {tuple(t.shape)} {t.dtype}")
+    rows, n = t.shape
+    ld, step = t.stride()
+    if (n > 1 and step != 1) or (rows > 1 and ld < n):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), ld if rows > 1 else n
+
+
+def _vec(t: Optional[torch.Tensor], n: int, name: str, dtype=None) -> Optional[int]:
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return _ptr(t, dtype, name)
+
+
+def moe_lora_layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                               y: torch.Tensor, mean: Optional[torch.Tensor] = None,
+                               rstd: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None) -> None:
+    """Layer norm of the rows of x [rows, n] (fp32, bf16 or fp16; rows may be strided) into y;
+    gamma / beta [n] of one type or None; mean, rstd [rows] fp32 kept for the backward if given."""
+    px, ldx = _rows(x, "x")
+    py, ldy = _rows(y, "y", x)
+    rows, n = x.shape
+    w = gamma if gamma is not None else beta
+    if beta is not None and beta.dtype != w.dtype:
+        raise ValueError("gamma and beta must have one type")
+    nm = Norm(rows, ldx, ldy, 0, 0, n, _dtype(x, "x"), 0 if w is None else _dtype(w, "gamma"), eps)
+    rc = lib().moe_lora_layernorm_forward(nm, px, _vec(gamma, n, "gamma"), _vec(beta, n, "beta"), py,
+                                          _vec(mean, rows, "mean", torch.float32),
+                                          _vec(rstd, rows, "rstd", torch.float32), _stream(stream))
+    _check(rc, "moe_lora_layernorm_forward")
+
+
+def layernorm_scratch(rows: int, n: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_lora_layernorm_backward's weight gradients."""
+    b = int(lib().moe_lora_layernorm_scratch_bytes(Norm(rows, 0, 0, 0, 0, n, 0, 0, 1.0)))
+    if b == 0:
+        raise MoeLoraError(-2, "moe_lora_layernorm_scratch_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def moe_lora_layernorm_backward(x: torch.Tensor, gamma: Optional[torch.Tensor], mean: torch.Tensor,
+                                rstd: torch.Tensor, dy: torch.Tensor, dres: Optional[torch.Tensor], dx: torch.Tensor,
+                                dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                                scratch: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx of the layer norm (plus dres, a gradient that reaches x on another path, if given) and,
+    where given, its weights' gradients dgamma, dbeta [n] fp32 (these need `scratch`)."""
+    px, ldx = _rows(x, "x")
+    pdy, ldy = _rows(dy, "dy", x)
+    pdx, lddx = _rows(dx, "dx", x)
+    pdr, lddr = (None, 0) if dres is None else _rows(dres, "dres", x)
+    rows, n = x.shape
+    nm = Norm(rows, ldx, ldy, lddx, lddr, n, _dtype(x, "x"), 0 if gamma is None else _dtype(gamma, "gamma"), 1.0)
+    rc = lib().moe_lora_layernorm_backward(nm, px, _vec(gamma, n, "gamma"), _vec(mean, rows, "mean", torch.float32),
+                                           _vec(rstd, rows, "rstd", torch.float32), pdy, pdr, pdx,
+                                           _vec(dgamma, n, "dgamma", torch.float32),
+                                           _vec(dbeta, n, "dbeta", torch.float32), _ptr(scratch, None, "scratch"),
+                                           0 if scratch is None else scratch.numel() * scratch.element_size(),
+                                           _stream(stream))
+    _check(rc, "moe_lora_layernorm_backward")
+
+
+def balance_scratch(dims: Dims, device="cuda") -> torch.Tensor:
+    n = moe_lora_workspace_bytes(dims, MOE_LORA_WS_BALANCE_SCRATCH)
+    if n == 0:
+        raise MoeLoraError(-5, "moe_lora_workspace_bytes(BALANCE_SCRATCH)")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_lora_balance_loss(dims: Dims, logits: torch.Tensor, topk_ids: torch.Tensor,
+                          adapter_offsets: Optional[Sequence[int]], coef: float, loss: torch.Tensor,
+                          counts: torch.Tensor, prob: torch.Tensor, scratch: torch.Tensor,
+                          dlogits: Optional[torch.Tensor] = None, dloss: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
+    """Balance loss [A] of the routes topk_ids [T,k] int32 (-1 = masked) under the router's logits
+    [T,E], with counts [A,E] int32 and mean probabilities prob [A,E]; dlogits [T,E] fp32 receives
+    its gradient (for the upstream gradient dloss [A], None = 1) in the same pass if given.
+    moe_lora_router_get_error(scratch) reads the device error word."""
+    pl, ld = _rows(logits, "logits")
+    T, E, A = dims.T, dims.E, dims.A
+    if logits.shape[0] != T or logits.shape[1] != E:
+        raise ValueError(f"logits must be [{T}, {E}], got {tuple(logits.shape)}")
+    offs = _offsets(adapter_offsets)
+    if offs is not None and len(offs) != A + 1:
+        raise ValueError(f"adapter_offsets must have {A + 1} entries")
+    rc = lib().moe_lora_balance_loss(dims, pl, _dtype(logits, "logits"), ld,
+                                     _vec(topk_ids, T * dims.k, "topk_ids", torch.int32),
+                                     offs, coef, _vec(dloss, A, "dloss", torch.float32),
+                                     _vec(loss, A, "loss", torch.float32), _vec(counts, A * E, "counts", torch.int32),
+                                     _vec(prob, A * E, "prob", torch.float32),
+                                     _vec(dlogits, T * E, "dlogits", torch.float32),
+                                     _ptr(scratch, None, "scratch"), scratch.numel() * scratch.element_size(),
+                                     _stream(stream))
+    _check(rc, "moe_lora_balance_loss")
+
+
+def moe_lora_router_backward_aux(dims: Dims, x: torch.Tensor, Wr: torch.Tensor, topk_ids: torch.Tensor,
+                                 topk_w: torch.Tensor, dw: torch.Tensor, dlogits_aux: Optional[torch.Tensor],
+                                 dlogits: Optional[torch.Tensor], dWr: torch.Tensor, dx: torch.Tensor,
+                                 scratch: torch.Tensor, stream=None,
+                                 adapter_offsets: Optional[Sequence[int]] = None) -> None:
+    """moe_lora_router_backward with dlogits_aux [T,E] fp32 (e.g. moe_lora_balance_loss's dlogits)
+    added to the routes' logit gradient."""
+    rc = lib().moe_lora_router_backward_aux(dims, _ptr(x, torch.bfloat16, "x"), _ptr(Wr, torch.bfloat16, "Wr"),
+                                            _offsets(adapter_offsets), _ptr(topk_ids, torch.int32, "topk_ids"),
+                                            _ptr(topk_w, torch.float32, "topk_w"), _ptr(dw, torch.float32, "dw"),
+                                            _vec(dlogits_aux, dims.T * dims.E, "dlogits_aux", torch.float32),
+                                            _ptr(dlogits, torch.float32, "dlogits"), _ptr(dWr, torch.float32, "dWr"),
+                                            _ptr(dx, torch.bfloat16, "dx"), _ptr(scratch),
+                                            scratch.numel() * scratch.element_size(), _stream(stream))
+    _check(rc, "moe_lora_router_backward_aux")
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)  # 8-bit moments
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, listed once and kept between steps.  Each entry is a dict:
+    p (fp32, bf16 or fp16), g, m, v, and optionally master (fp32, for a 16-bit p), m_scale and
+    v_scale (fp32, one per 256 elements, started at zero; with them m and v are 8-bit codes,
+    uint8 or float8_e4m3fn, v holding sqrt(v)), lr (1e-3) and weight_decay (0).  All contiguous;
+    no two overlap.  The entries hold the tensors alive."""
+
+    def __init__(self, entries: Sequence[Dict]):
+        self.entries = [dict(e) for e in entries]
+        self.table = (AdamWTensor * max(1, len(self.entries)))()
+        for d, e in zip(self.table, self.entries):
+            p, n = e["p"], e["p"].numel()
+            eight = e.get("m_scale") is not None
+            if eight != (e.get("v_scale") is not None):
+                raise ValueError("m_scale and v_scale come together")
+            blocks = (n + 255) // 256
+            for name in ("m", "v"):
+                if eight and e[name].dtype not in _CODES:
+                    raise ValueError(f"{name} must be uint8 or float8_e4m3fn codes, got {e[name].dtype}")
+            state = None if eight else torch.float32
+            d.p, d.g = _vec(p, n, "p"), _vec(e["g"], n, "g")
+            d.master = _vec(e.get("master"), n, "master", torch.float32)
+            d.m, d.v = _vec(e["m"], n, "m", state), _vec(e["v"], n, "v", state)
+            d.m_scale = _vec(e.get("m_scale"), blocks, "m_scale", torch.float32)
+            d.v_scale = _vec(e.get("v_scale"), blocks, "v_scale", torch.float32)
+            d.numel, d.p_dtype, d.g_dtype, d.state = n, _dtype(p, "p"), _dtype(e["g"], "g"), int(eight)
+            d.lr, d.weight_decay = e.get("lr", 1e-3), e.get("weight_decay", 0.0)
+
+    def set_lr(self, lr: float) -> None:
+        for d in self.table:
+            d.lr = lr
+
+
+def moe_lora_adamw_step(tensors: AdamWTensors, step: int, beta1: float = 0.9, beta2: float = 0.999,
+                        eps: float = 1e-8, grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step (number `step`, from 1) over all tensors; grad_scale: a device fp32 scalar that
+    multiplies every gradient (e.g. a clipping factor)."""
+    opt = AdamW(beta1, beta2, eps, step, _vec(grad_scale, 1, "grad_scale", torch.float32))
+    rc = lib().moe_lora_adamw_step(opt, tensors.table, len(tensors.entries), _stream(stream))
+    _check(rc, "moe_lora_adamw_step")
 
 
 # ------------------------------------------------------------------ convenience

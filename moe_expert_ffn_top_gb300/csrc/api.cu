@@ -99,7 +99,7 @@ int tmap_fp4_unpacked(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1
 // ------------------------------------------------------------------ device
 // Requires the current device to be an sm_103 GPU; returns its SM count (or the
 // MOELORA_NUM_SMS override, for running beside other work).
-static int device_sms(int* sms) {
+int device_sms(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_LORA_ERR_DEVICE;
   int major = 0, minor = 0, n = 0;
@@ -116,13 +116,7 @@ static int device_sms(int* sms) {
   return MOE_LORA_OK;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static int check_ptr(const void* p) {
-  if (!p) return MOE_LORA_ERR_NULL;
-  if (!aligned16(p)) return MOE_LORA_ERR_ALIGN;
-  return MOE_LORA_OK;
-}
+static bool aligned16(const void* p) { return check_opt(p) == MOE_LORA_OK; }
 
 static int check_weights(const moe_lora_dims* d, const moe_lora_weights* w) {
   if (!w) return MOE_LORA_ERR_NULL;
@@ -159,6 +153,7 @@ size_t moe_lora_workspace_bytes(const moe_lora_dims* d, int which) {
     case MOE_LORA_WS_FWD_SCRATCH: return fwd_layout(d).total;
     case MOE_LORA_WS_BWD_SCRATCH: return bwd_layout(d).total;
     case MOE_LORA_WS_ROUTER_SCRATCH: return check_router_dims(d) == MOE_LORA_OK ? router_layout(d).total : 0;
+    case MOE_LORA_WS_BALANCE_SCRATCH: return balance_scratch_bytes(d);
     default: return 0;
   }
 }
@@ -247,10 +242,10 @@ int moe_lora_router_forward(const moe_lora_dims* d, const uint16_t* x, const uin
   return run_router_forward(d, at, x, Wr, topk_ids, topk_w, logits, scratch, sms, static_cast<cudaStream_t>(stream));
 }
 
-int moe_lora_router_backward(const moe_lora_dims* d, const uint16_t* x, const uint16_t* Wr,
-                             const int64_t* adapter_offsets, const int32_t* topk_ids, const float* topk_w,
-                             const float* dw, float* dlogits, float* dWr, uint16_t* dx, void* scratch,
-                             size_t scratch_bytes, void* stream) {
+int moe_lora_router_backward_aux(const moe_lora_dims* d, const uint16_t* x, const uint16_t* Wr,
+                                 const int64_t* adapter_offsets, const int32_t* topk_ids, const float* topk_w,
+                                 const float* dw, const float* dlogits_aux, float* dlogits, float* dWr, uint16_t* dx,
+                                 void* scratch, size_t scratch_bytes, void* stream) {
   int rc = check_router_dims(d);
   if (rc) return rc;
   AdapterTable at;
@@ -259,6 +254,7 @@ int moe_lora_router_backward(const moe_lora_dims* d, const uint16_t* x, const ui
   if (scratch_bytes < router_layout(d).total) return MOE_LORA_ERR_WORKSPACE;
   if ((rc = check_ptr(Wr)) || (rc = check_ptr(dWr))) return rc;
   if (dlogits && !aligned16(dlogits)) return MOE_LORA_ERR_ALIGN;
+  if ((rc = check_opt(dlogits_aux))) return rc;
   if (d->T > 0) {
     const void* ps[] = {x, topk_ids, topk_w, dw, dx};
     for (const void* p : ps)
@@ -266,8 +262,16 @@ int moe_lora_router_backward(const moe_lora_dims* d, const uint16_t* x, const ui
   }
   int sms;
   if ((rc = device_sms(&sms))) return rc;
-  return run_router_backward(d, at, x, Wr, topk_ids, topk_w, dw, dlogits, dWr, dx, scratch, sms,
+  return run_router_backward(d, at, x, Wr, topk_ids, topk_w, dw, dlogits_aux, dlogits, dWr, dx, scratch, sms,
                              static_cast<cudaStream_t>(stream));
+}
+
+int moe_lora_router_backward(const moe_lora_dims* d, const uint16_t* x, const uint16_t* Wr,
+                             const int64_t* adapter_offsets, const int32_t* topk_ids, const float* topk_w,
+                             const float* dw, float* dlogits, float* dWr, uint16_t* dx, void* scratch,
+                             size_t scratch_bytes, void* stream) {
+  return moe_lora_router_backward_aux(d, x, Wr, adapter_offsets, topk_ids, topk_w, dw, nullptr, dlogits, dWr, dx,
+                                      scratch, scratch_bytes, stream);
 }
 
 int moe_lora_router_get_error(const void* scratch, void* stream) {

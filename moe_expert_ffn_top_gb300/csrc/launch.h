@@ -34,6 +34,18 @@ inline int make_adapter_table(const moe_lora_dims* d, const int64_t* adapter_off
   return MOE_LORA_OK;
 }
 
+// Host checks shared by the entry points (api.cu).  device_sms: the current device must
+// be an sm_103 GPU; its SM count (or the MOELORA_NUM_SMS override).  check_ptr: non-NULL
+// and 16-byte aligned; check_opt: 16-byte aligned or NULL.
+int device_sms(int* sms);
+inline int check_opt(const void* p) {
+  return reinterpret_cast<uintptr_t>(p) & 15u ? MOE_LORA_ERR_ALIGN : MOE_LORA_OK;
+}
+inline int check_ptr(const void* p) { return p ? check_opt(p) : MOE_LORA_ERR_NULL; }
+
+// Bytes of the balance loss's scratch (balance.cu); 0 for sizes it does not take.
+size_t balance_scratch_bytes(const moe_lora_dims* d);
+
 // The plan kernels' launch sequence.  chunk_base: the per-chunk group histograms,
 // A*E*max(1, ceil(T*k/1024)) ints of device memory whose contents on entry do not
 // matter (moe_lora_plan passes the end of its workspace, moe_lora_plan_noalloc a

@@ -21,8 +21,8 @@ int run_backward(const moe_lora_dims* d, const void* plan_ws, const void* saved,
 int run_router_forward(const moe_lora_dims* d, const AdapterTable& at, const uint16_t* x, const uint16_t* Wr,
                        int32_t* ids, float* w, float* logits, void* scratch, int num_sms, cudaStream_t stream);
 int run_router_backward(const moe_lora_dims* d, const AdapterTable& at, const uint16_t* x, const uint16_t* Wr,
-                        const int32_t* ids, const float* w, const float* dw, float* dlogits, float* dWr, uint16_t* dx,
-                        void* scratch, int num_sms, cudaStream_t stream);
+                        const int32_t* ids, const float* w, const float* dw, const float* dl_aux, float* dlogits,
+                        float* dWr, uint16_t* dx, void* scratch, int num_sms, cudaStream_t stream);
 
 // pair != 0: on the two-SM (cta_group::2) engine; starve != 0: no operand copy is
 // issued, so the pipeline's bounded waits expire (error-path self-test).

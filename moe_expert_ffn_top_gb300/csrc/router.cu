@@ -273,9 +273,11 @@ struct ProbRouterDW {
   }
 };
 
-// dl [T,E] bf16 (and fp32 if asked for): one warp per token, lane j holds slot j.
+// dl [T,E] bf16 (and fp32 if asked for), aux [T,E] added where given: one warp per token,
+// lane j holds slot j.
 __global__ void __launch_bounds__(256) router_dl_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w,
-                                                        const float* __restrict__ dw, int64_t T, int k, int E,
+                                                        const float* __restrict__ dw,
+                                                        const float* __restrict__ aux, int64_t T, int k, int E,
                                                         uint16_t* __restrict__ dl, float* __restrict__ dl32) {
   const int lane = threadIdx.x & 31;
   const int64_t nw = (int64_t)gridDim.x * (blockDim.x >> 5);
@@ -297,7 +299,10 @@ __global__ void __launch_bounds__(256) router_dl_kernel(const int32_t* __restric
     const float g = wj * (dwj - s);
     float acc[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
+    for (int q = 0; q < 8; ++q) {
+      const int e = lane + 32 * q;
+      acc[q] = aux && e < E ? aux[t * E + e] : 0.0f;
+    }
     for (int j = 0; j < k; ++j) {
       const int idj = __shfl_sync(0xffffffffu, id, j);
       const float gj = __shfl_sync(0xffffffffu, g, j);
@@ -355,8 +360,8 @@ static int router_split(int64_t tokens) {
 }
 
 int run_router_backward(const moe_lora_dims* d, const AdapterTable& at, const uint16_t* x, const uint16_t* Wr,
-                        const int32_t* ids, const float* w, const float* dw, float* dlogits, float* dWr, uint16_t* dx,
-                        void* scratch, int num_sms, cudaStream_t stream) {
+                        const int32_t* ids, const float* w, const float* dw, const float* dl_aux, float* dlogits,
+                        float* dWr, uint16_t* dx, void* scratch, int num_sms, cudaStream_t stream) {
   const RouterLayout L = router_layout(d);
   char* sc = static_cast<char*>(scratch);
   int* err = (int*)(sc + L.err);
@@ -373,7 +378,7 @@ int run_router_backward(const moe_lora_dims* d, const AdapterTable& at, const ui
     const int64_t blocks = (T + 7) / 8;
     const int grid = (int)(blocks < 8LL * num_sms ? blocks : 8LL * num_sms);
     prof_begin(K_ROUTER_DL, stream);
-    router_dl_kernel<<<grid, 256, 0, stream>>>(ids, w, dw, T, d->k, E, dl, dlogits);
+    router_dl_kernel<<<grid, 256, 0, stream>>>(ids, w, dw, dl_aux, T, d->k, E, dl, dlogits);
     prof_end(K_ROUTER_DL, stream);
     LAUNCH(cudaGetLastError());
   }
