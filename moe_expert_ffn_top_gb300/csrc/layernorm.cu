@@ -1,5 +1,7 @@
 // Layer norm over rows of [rows, n], forward and backward (definitions in
 // include/moe_lora.h).
+#include <algorithm>
+
 #include "element.cuh"
 #include "launch.h"
 #include "prof.h"
@@ -8,10 +10,560 @@ namespace moelora {
 
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormParts = 64;  // row slices of the weight gradients' sums
+// A row is handled by a group of `tpr` threads (8, 16, or whole warps); a block holds
+// `groups` groups, each with rows of its own.  Thread i of a group holds slots i,
+// i + tpr, ... of the row, NV of them, in registers as loaded: a slot is 16 bytes, or
+// (VL = 1) two single elements tpr columns apart.
+constexpr int kFwdThreads = 512;
+constexpr int kBwdThreads = 768;  // 80 registers a thread
+constexpr int kNormParts = 152;   // most partial rows of the weight gradients: one per block
 
-// Sum over the block, the same value in every thread.
+struct RowShape {
+  int tpr, groups, threads;
+  int64_t steps;  // rows / groups
+};
+// Row `st * groups + group`; a group past the last row repeats it (and stores nothing).
+struct RowAt {
+  int64_t r;
+  bool on;
+  __device__ __forceinline__ RowAt(const RowShape& rs, int64_t rows, int64_t st, int group) {
+    r = st * rs.groups + group;
+    on = r < rows;
+    if (!on) r = rows - 1;
+  }
+};
+// Column and second-element distance of a thread's slot i.
+template <int VL>
+struct SlotAt {
+  int c, hop;
+  bool in;
+  __device__ __forceinline__ SlotAt(int lane, int i, int tpr, int n) {
+    c = VL == 1 ? lane + 2 * i * tpr : (lane + i * tpr) * VL;
+    in = c < n;
+    hop = VL == 1 && c + tpr < n ? tpr : 0;
+  }
+  // v for both elements of a pair, 0 for the second where that is past the end
+  __device__ __forceinline__ float2 pair(float v) const { return make_float2(v, VL == 1 && !hop ? 0.f : v); }
+};
+
+// Sums over a row's threads, the same in all of them: lanes of a warp, or whole warps
+// that meet at barrier `bar`.  Alternating buffers make one barrier per sum enough.
+struct RowSum {
+  int tpr, bar;
+  float2* red;  // this group's part of a buffer of 32; the second buffer 32 further
+  int buf = 0;
+  __device__ __forceinline__ float2 operator()(float2 v) {
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    return tpr <= 32 ? v : across(v);
+  }
+  __device__ __forceinline__ float operator()(float v) {
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return tpr <= 32 ? v : across(make_float2(v, 0.f)).x;
+  }
+  __device__ __forceinline__ float2 across(float2 v) {
+    float2* r = red + buf * 32;
+    buf ^= 1;
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x % tpr >> 5] = v;
+    if (bar < 0)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+    v = r[0];
+    for (int w = 1; w < tpr >> 5; ++w) v = add2(v, r[w]);
+    return v;
+  }
+};
+
+// gamma or beta: NULL, or n elements of a type that is known at run time only (a uniform
+// branch at each load, against three times the kernels).
+struct Weight {
+  const void* p;
+  int dtype;
+  // elements of a slot, `none` where there are no weights
+  template <int VL, int kP>
+  __device__ __forceinline__ void slot(const SlotAt<VL>& at, float none, float2 (&f)[kP]) const {
+    if (!p) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) f[j] = both(none);
+    } else if (dtype == MOE_LORA_F32) {
+      ld_pairs<float, VL>(static_cast<const float*>(p) + at.c, at.hop, f);
+    } else if (dtype == MOE_LORA_BF16) {
+      ld_pairs<__nv_bfloat16, VL>(static_cast<const __nv_bfloat16*>(p) + at.c, at.hop, f);
+    } else {
+      ld_pairs<__half, VL>(static_cast<const __half*>(p) + at.c, at.hop, f);
+    }
+  }
+  template <int VL, int kP>
+  __device__ __forceinline__ void vec(int c, float none, float2 (&f)[kP]) const {
+    SlotAt<VL> at(0, 0, 0, 1);
+    at.c = c;
+    slot(at, none, f);
+  }
+  __device__ __forceinline__ float at(int64_t c, float none) const {
+    return !p                        ? none
+           : dtype == MOE_LORA_F32  ? static_cast<const float*>(p)[c]
+           : dtype == MOE_LORA_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[c])
+                                    : to_f32(static_cast<const __half*>(p)[c]);
+  }
+  // the whole vector, widened, into shared memory
+  __device__ __forceinline__ void stage(float* sm, int n, float none) const {
+    for (int c = threadIdx.x; c < n; c += blockDim.x) sm[c] = at(c, none);
+  }
+};
+
+// Few rows, or rows that 16-byte vectors do not fit.  The weights are asked for together
+// with the row, so that their latency passes with its.  Groups of more than one warp
+// have the block for themselves (groups = 1).
+template <class T, int VL, int NV>
+__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm, RowShape rs, const T* x,
+                                                               Weight gamma, Weight beta, T* y, float* mean,
+                                                               float* rstd) {
+  __shared__ float2 red[2 * 32];
+  constexpr int kP = Vec<T, VL>::kPairs;
+  const int n = nm.n;
+  const int lane = threadIdx.x % rs.tpr, group = threadIdx.x / rs.tpr;
+  RowSum sum{rs.tpr, -1, red};
+  const float rn = 1.0f / n;
+  constexpr int kAhead = VL == 1 ? 8 : 2;  // slots whose weights fit in registers beside the row
+  for (int64_t st = blockIdx.x; st < rs.steps; st += gridDim.x) {
+    const RowAt row(rs, nm.rows, st, group);
+    const T* xr = x + row.r * nm.ldx;
+    Vec<T, VL> v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (at.in)
+        v[i].load(xr + at.c, at.hop);
+      else
+        v[i].clear();
+    }
+    float2 g[NV > kAhead ? 1 : NV][kP], b[NV > kAhead ? 1 : NV][kP];
+    if (NV <= kAhead)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const SlotAt<VL> at(lane, i, rs.tpr, n);
+        if (at.in) {
+          gamma.slot(at, 1.f, g[i]);
+          beta.slot(at, 0.f, b[i]);
+        }
+      }
+    float2 s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < kP; ++j) s = add2(s, v[i].get(j));
+    const float mu = sum(s.x + s.y) * rn;
+    float2 q = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (at.in)
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          const float2 d = add2(v[i].get(j), at.pair(-mu));
+          q = fma2(d, d, q);
+        }
+    }
+    const float rt = 1.0f / sqrtf(sum(q.x + q.y) * rn + nm.eps);
+    T* yr = y + row.r * nm.ldy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (at.in && row.on) {
+        if (NV > kAhead) {
+          gamma.slot(at, 1.f, g[0]);
+          beta.slot(at, 0.f, b[0]);
+        }
+        const auto &gi = g[NV > kAhead ? 0 : i], &bi = b[NV > kAhead ? 0 : i];
+        Vec<T, VL> o;
+#pragma unroll
+        for (int j = 0; j < kP; ++j) o.put(j, fma2(mul2(add2(v[i].get(j), both(-mu)), both(rt)), gi[j], bi[j]));
+        o.store(yr + at.c, at.hop);
+      }
+    }
+    if (mean && row.on && lane == 0) {
+      mean[row.r] = mu;
+      rstd[row.r] = rt;
+    }
+  }
+}
+
+// Rows of whole 16-byte vectors stream through shared memory: one resident block per SM,
+// its teams (the threads of a row: 8, 16 or 32 lanes, or several warps) take rows in
+// turn.  Every thread copies its own slots kStages - 1 rows ahead with asynchronous
+// copies and reads only those, so rows in flight cost neither registers nor barriers; a
+// thread has the same columns in every row, so its weights stay in its registers.
+constexpr int kStreamThreads = 512;  // 128 registers a thread
+struct StreamShape {
+  int tpr, teams;
+};
+
+// A thread's ring: kStages rows of kTensors x NV slots, those of a warp side by side.
+template <int kStages, int kSlots>
+struct Ring {
+  uint4* base;
+  __device__ __forceinline__ explicit Ring(void* sm)
+      : base(static_cast<uint4*>(sm) + (threadIdx.x >> 5) * (kStages * kSlots * 32) + (threadIdx.x & 31)) {}
+  __device__ __forceinline__ uint4* slot(int stage, int i) const { return base + (stage * kSlots + i) * 32; }
+};
+template <int kStages, int kSlots>
+constexpr size_t ring_bytes(int threads) {
+  return (size_t)threads * kStages * kSlots * 16;
+}
+
+// What a thread knows of its columns: slot i starts at column c0 + i * dc, `nv` slots lie
+// inside the row.
+struct Columns {
+  int c0, dc, nv;
+  __device__ __forceinline__ Columns(int lane, int tpr, int n, int vl) {
+    c0 = lane * vl;
+    dc = tpr * vl;
+    nv = c0 < n ? (n - c0 + dc - 1) / dc : 0;
+  }
+  __device__ __forceinline__ bool in(int i) const { return i < nv; }
+  __device__ __forceinline__ int col(int i) const { return c0 + i * dc; }
+};
+
+template <class T, int NV, int kStages>
+__global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
+                                                                            Weight gamma, Weight beta, T* y,
+                                                                            float* mean, float* rstd) {
+  constexpr int VL = 16 / sizeof(T), kP = VL / 2;
+  extern __shared__ __align__(16) uint8_t ring_sm[];
+  __shared__ float2 red[2 * 32];
+  const int n = nm.n;
+  const Ring<kStages, NV> ring(ring_sm);
+  const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
+  const Columns cl(lane, ss.tpr, n, VL);
+  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * (ss.tpr >> 5) : 0)};
+  const float rn = 1.0f / n;
+  const int64_t step = (int64_t)gridDim.x * ss.teams;
+  const auto copy_row = [&](int64_t r, int s) {
+    if (r < nm.rows) {
+      const T* xr = x + r * nm.ldx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cl.in(i)) async_copy16(ring.slot(s, i), xr + cl.col(i));
+    }
+    async_commit();
+  };
+  const int64_t first = blockIdx.x * (int64_t)ss.teams + team;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
+  float2 g[NV][kP], b[NV][kP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (cl.in(i)) {
+      gamma.vec<VL>(cl.col(i), 1.f, g[i]);
+      beta.vec<VL>(cl.col(i), 0.f, b[i]);
+    }
+  int s = 0;
+  // all teams of the block leave together: one without a row works on what its slots hold
+  for (int64_t r = first; r - team < nm.rows; r += step) {
+    copy_row(r + (kStages - 1) * step, s == 0 ? kStages - 1 : s - 1);
+    async_wait<kStages - 1>();
+    float2 v[NV][kP];
+    float2 t[2] = {both(0.f), both(0.f)};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cl.in(i)) {
+        Vec<T, VL> w;
+        w.from_smem(ring.slot(s, i));
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          v[i][j] = w.get(j);
+          t[j & 1] = add2(t[j & 1], v[i][j]);
+        }
+      }
+    t[0] = add2(t[0], t[1]);
+    const float mu = sum(t[0].x + t[0].y) * rn;
+    t[0] = t[1] = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cl.in(i))
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          v[i][j] = add2(v[i][j], both(-mu));
+          t[j & 1] = fma2(v[i][j], v[i][j], t[j & 1]);
+        }
+    t[0] = add2(t[0], t[1]);
+    const float rt = 1.0f / sqrtf(sum(t[0].x + t[0].y) * rn + nm.eps);
+    if (r < nm.rows) {
+      T* yr = y + r * nm.ldy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cl.in(i)) {
+          Vec<T, VL> o;
+#pragma unroll
+          for (int j = 0; j < kP; ++j) o.put(j, fma2(mul2(v[i][j], both(rt)), g[i][j], b[i][j]));
+          o.store(yr + cl.col(i), 0);
+        }
+      if (mean && lane == 0) {
+        mean[r] = mu;
+        rstd[r] = rt;
+      }
+    }
+    s = s == kStages - 1 ? 0 : s + 1;
+  }
+}
+
+// dx, and per block the sums of the weight gradients over its rows: dgamma / dbeta at
+// block * part_ld (the partial rows, or the outputs themselves when one block has all
+// rows).  Same streaming; dx needs one sum (of two values) per row, the weight gradients
+// stay in registers until the block's rows are done.
+template <class T, int NV, int kStages>
+__global__ void __launch_bounds__(kStreamThreads, 1) norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
+                                                                            Weight gamma, const float* mean,
+                                                                            const float* rstd, const T* dy,
+                                                                            const T* dres, T* dx, float* dgamma,
+                                                                            float* dbeta, int64_t part_ld) {
+  constexpr int VL = 16 / sizeof(T), kP = VL / 2;
+  extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [2][n]
+  __shared__ float2 red[2 * 32];
+  const int n = nm.n;
+  const Ring<kStages, 3 * NV> ring(ring_sm);
+  const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
+  const Columns cl(lane, ss.tpr, n, VL);
+  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * (ss.tpr >> 5) : 0)};
+  const float rn = 1.0f / n;
+  const int64_t step = (int64_t)gridDim.x * ss.teams;
+  const auto copy_row = [&](int64_t r, int s) {
+    if (r < nm.rows) {
+      const T *xr = x + r * nm.ldx, *gr = dy + r * nm.ldy, *er = dres + r * nm.lddres;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cl.in(i)) {
+          async_copy16(ring.slot(s, i), xr + cl.col(i));
+          async_copy16(ring.slot(s, NV + i), gr + cl.col(i));
+          if (dres) async_copy16(ring.slot(s, 2 * NV + i), er + cl.col(i));
+        }
+    }
+    async_commit();
+  };
+  const int64_t first = blockIdx.x * (int64_t)ss.teams + team;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
+  float2 g[NV][kP], dg[NV][kP], db[NV][kP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (cl.in(i)) gamma.vec<VL>(cl.col(i), 1.f, g[i]);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) dg[i][j] = db[i][j] = both(0.f);
+  }
+  const auto stat = [&](const float* p, int64_t r) { return r < nm.rows ? p[r] : 0.f; };
+  float mu = stat(mean, first), rt = stat(rstd, first);
+  int s = 0;
+  for (int64_t r = first; r - team < nm.rows; r += step) {
+    copy_row(r + (kStages - 1) * step, s == 0 ? kStages - 1 : s - 1);
+    const float mu1 = stat(mean, r + step), rt1 = stat(rstd, r + step);
+    async_wait<kStages - 1>();
+    const bool on = r < nm.rows;
+    float2 h[NV][kP], u[NV][kP];
+    float2 su = both(0.f), sh = both(0.f);
+    if (on)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cl.in(i)) {
+          Vec<T, VL> xv, gv;
+          xv.from_smem(ring.slot(s, i));
+          gv.from_smem(ring.slot(s, NV + i));
+#pragma unroll
+          for (int j = 0; j < kP; ++j) {
+            const float2 d = gv.get(j);
+            h[i][j] = mul2(add2(xv.get(j), both(-mu)), both(rt));
+            u[i][j] = mul2(d, g[i][j]);
+            su = add2(su, u[i][j]);
+            sh = fma2(u[i][j], h[i][j], sh);
+            dg[i][j] = fma2(d, h[i][j], dg[i][j]);
+            db[i][j] = add2(db[i][j], d);
+          }
+        }
+    const float2 t = sum(make_float2(su.x + su.y, sh.x + sh.y));
+    const float2 na = both(-t.x * rn), nb = both(-t.y * rn);
+    if (on) {
+      T* dr = dx + r * nm.lddx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cl.in(i)) {
+          Vec<T, VL> o, ev;
+          if (dres) ev.from_smem(ring.slot(s, 2 * NV + i));
+#pragma unroll
+          for (int j = 0; j < kP; ++j) {
+            const float2 w = fma2(h[i][j], nb, add2(u[i][j], na));
+            o.put(j, dres ? fma2(w, both(rt), ev.get(j)) : mul2(w, both(rt)));
+          }
+          o.store(dr + cl.col(i), 0);
+        }
+    }
+    mu = mu1;
+    rt = rt1;
+    s = s == kStages - 1 ? 0 : s + 1;
+  }
+  if (!dgamma && !dbeta) return;
+  async_wait<0>();
+  __syncthreads();
+  float* acc = reinterpret_cast<float*>(ring_sm);
+  // the teams are added in order, the last one stores
+  for (int k = 0; k < ss.teams; ++k) {
+    if (team == k) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cl.in(i))
+#pragma unroll
+          for (int j = 0; j < kP; ++j) {
+            const int e = cl.col(i) + 2 * j;
+            float2 *ag = reinterpret_cast<float2*>(acc + e), *ab = reinterpret_cast<float2*>(acc + n + e);
+            if (k > 0) {
+              dg[i][j] = add2(dg[i][j], *ag);
+              db[i][j] = add2(db[i][j], *ab);
+            }
+            if (k < ss.teams - 1) {
+              *ag = dg[i][j];
+              *ab = db[i][j];
+            } else {
+              if (dgamma) *reinterpret_cast<float2*>(dgamma + blockIdx.x * part_ld + e) = dg[i][j];
+              if (dbeta) *reinterpret_cast<float2*>(dbeta + blockIdx.x * part_ld + e) = db[i][j];
+            }
+          }
+    }
+    __syncthreads();
+  }
+}
+
+// The same for rows that 16-byte vectors do not fit (VL = 1), rows in registers.
+template <class T, int VL, int NV, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(moe_lora_norm nm, RowShape rs, const T* x, Weight gamma,
+                                                               const float* mean, const float* rstd, const T* dy,
+                                                               const T* dres, T* dx, float* dgamma, float* dbeta,
+                                                               int64_t part_ld) {
+  extern __shared__ __align__(16) float wsm[];  // gamma; then, where a block has several groups, their sums [2][n]
+  __shared__ float2 red[2 * 32];
+  constexpr int kP = Vec<T, VL>::kPairs;
+  const int n = nm.n;
+  const int lane = threadIdx.x % rs.tpr, group = threadIdx.x / rs.tpr;
+  RowSum sum{rs.tpr, group + 1, red + (rs.tpr > 32 ? group * (rs.tpr >> 5) : 0)};
+  const float rn = 1.0f / n;
+  gamma.stage(wsm, n, 1.f);
+  __syncthreads();
+  float2 dg[NV][kP], db[NV][kP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) dg[i][j] = db[i][j] = both(0.f);
+  for (int64_t st = blockIdx.x; st < rs.steps; st += gridDim.x) {
+    const RowAt row(rs, nm.rows, st, group);
+    const T *xr = x + row.r * nm.ldx, *gr = dy + row.r * nm.ldy, *er = dres + row.r * nm.lddres;
+    Vec<T, VL> xv[NV], gv[NV], ev[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (at.in) {
+        xv[i].load(xr + at.c, at.hop);
+        gv[i].load(gr + at.c, at.hop);
+        if (dres) ev[i].load(er + at.c, at.hop);
+      }
+    }
+    const float mu = mean[row.r], rt = rstd[row.r];
+    float2 su = both(0.f), sh = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (at.in) {
+        float2 g[kP];
+        ld_pairs<float, VL>(wsm + at.c, at.hop, g);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          const float2 d = gv[i].get(j), h = mul2(add2(xv[i].get(j), at.pair(-mu)), both(rt)), u = mul2(d, g[j]);
+          su = add2(su, u);
+          sh = fma2(u, h, sh);
+          if (row.on) {
+            dg[i][j] = fma2(d, h, dg[i][j]);
+            db[i][j] = add2(db[i][j], d);
+          }
+        }
+      }
+    }
+    const float2 s = sum(make_float2(su.x + su.y, sh.x + sh.y));
+    const float2 na = both(-s.x * rn), nb = both(-s.y * rn);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (at.in && row.on) {
+        float2 g[kP];
+        ld_pairs<float, VL>(wsm + at.c, at.hop, g);
+        Vec<T, VL> o;
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          const float2 h = mul2(add2(xv[i].get(j), at.pair(-mu)), both(rt));
+          float2 t = fma2(h, nb, fma2(gv[i].get(j), g[j], na));
+          t = dres ? fma2(t, both(rt), ev[i].get(j)) : mul2(t, both(rt));
+          o.put(j, t);
+        }
+        o.store(dx + row.r * nm.lddx + at.c, at.hop);
+      }
+    }
+  }
+  if (!dgamma && !dbeta) return;
+  float* acc_sm = wsm + n;
+  // the block's groups are added in order, the last one stores
+  for (int k = 0; k < rs.groups; ++k) {
+    if (group == k) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const SlotAt<VL> at(lane, i, rs.tpr, n);
+        if (at.in)
+#pragma unroll
+          for (int j = 0; j < kP; ++j)
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+              if (VL == 1 && l == 1 && !at.hop) continue;
+              const int e = VL == 1 ? at.c + l * at.hop : at.c + 2 * j + l;
+              float a = l ? dg[i][j].y : dg[i][j].x, b = l ? db[i][j].y : db[i][j].x;
+              if (k > 0) {
+                a += acc_sm[e];
+                b += acc_sm[n + e];
+              }
+              if (k < rs.groups - 1) {
+                acc_sm[e] = a;
+                acc_sm[n + e] = b;
+              } else {
+                if (dgamma) dgamma[blockIdx.x * part_ld + e] = a;
+                if (dbeta) dbeta[blockIdx.x * part_ld + e] = b;
+              }
+            }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// dgamma and dbeta (blockIdx.y) from the blocks' partial rows: 32 columns per block,
+// warp w adds every 8th partial, then the warps' sums are added in order.
+__global__ void __launch_bounds__(256) norm_wgrad_kernel(int n, int parts, const float* part, float* dgamma,
+                                                         float* dbeta) {
+  __shared__ float sm[8][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float* out = blockIdx.y ? dbeta : dgamma;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!out) return;
+  float s = 0.f;
+  if (c < n)
+#pragma unroll 4
+    for (int p = w; p < parts; p += 8) s += part[((int64_t)p * 2 + blockIdx.y) * n + c];
+  sm[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < n) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sm[i][lane];
+    out[c] = s;
+  }
+}
+
+// Rows longer than a block's registers hold: the row is read again for every pass.
+constexpr int kLongThreads = 512;
 __device__ __forceinline__ float block_sum(float v, float* sm) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -19,13 +571,12 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = 0.f;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += sm[w];
+  for (int w = 0; w < kLongThreads / 32; ++w) s += sm[w];
   return s;
 }
-
-template <class T, class W>
-__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(moe_lora_norm nm, const T* x, const W* gamma,
-                                                                const W* beta, T* y, float* mean, float* rstd) {
+template <class T>
+__global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(moe_lora_norm nm, const T* x, Weight gamma,
+                                                                     Weight beta, T* y, float* mean, float* rstd) {
   __shared__ float sm[32];
   const int n = nm.n;
   for (int64_t r = blockIdx.x; r < nm.rows; r += gridDim.x) {
@@ -42,7 +593,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(moe_lora_norm nm
     T* yr = y + r * nm.ldy;
     for (int c = threadIdx.x; c < n; c += blockDim.x) {
       const float h = (to_f32(xr[c]) - mu) * rs;
-      yr[c] = from_f32<T>(h * (gamma ? to_f32(gamma[c]) : 1.f) + (beta ? to_f32(beta[c]) : 0.f));
+      yr[c] = from_f32<T>(h * gamma.at(c, 1.f) + beta.at(c, 0.f));
     }
     if (mean && threadIdx.x == 0) {
       mean[r] = mu;
@@ -50,11 +601,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(moe_lora_norm nm
     }
   }
 }
-
-template <class T, class W>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(moe_lora_norm nm, const T* x, const W* gamma,
-                                                                const float* mean, const float* rstd, const T* dy,
-                                                                const T* dres, T* dx) {
+template <class T>
+__global__ void __launch_bounds__(kLongThreads) norm_bwd_long_kernel(moe_lora_norm nm, const T* x, Weight gamma,
+                                                                     const float* mean, const float* rstd,
+                                                                     const T* dy, const T* dres, T* dx) {
   __shared__ float sm[32];
   const int n = nm.n;
   for (int64_t r = blockIdx.x; r < nm.rows; r += gridDim.x) {
@@ -62,24 +612,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(moe_lora_norm nm
     const float mu = mean[r], rs = rstd[r];
     float a = 0.f, b = 0.f;
     for (int c = threadIdx.x; c < n; c += blockDim.x) {
-      const float u = to_f32(gr[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
+      const float u = to_f32(gr[c]) * gamma.at(c, 1.f);
       a += u;
       b += u * ((to_f32(xr[c]) - mu) * rs);
     }
     a = block_sum(a, sm) / n;
     b = block_sum(b, sm) / n;
     for (int c = threadIdx.x; c < n; c += blockDim.x) {
-      const float u = to_f32(gr[c]) * (gamma ? to_f32(gamma[c]) : 1.f), h = (to_f32(xr[c]) - mu) * rs;
+      const float u = to_f32(gr[c]) * gamma.at(c, 1.f), h = (to_f32(xr[c]) - mu) * rs;
       const float d = rs * (u - a - h * b) + (dres ? to_f32(dres[r * nm.lddres + c]) : 0.f);
       dx[r * nm.lddx + c] = from_f32<T>(d);
     }
   }
 }
-
-// Partial sums of the weight gradients over one slice of the rows: part[slice][2][n].
 template <class T>
-__global__ void __launch_bounds__(kNormThreads) norm_part_kernel(moe_lora_norm nm, const T* x, const float* mean,
-                                                                 const float* rstd, const T* dy, float* part) {
+__global__ void __launch_bounds__(256) norm_part_long_kernel(moe_lora_norm nm, const T* x, const float* mean,
+                                                             const float* rstd, const T* dy, float* part) {
   const int n = nm.n, c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= n) return;
   const int64_t per = (nm.rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * per;
@@ -92,19 +640,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(moe_lora_norm n
   }
   part[(int64_t)blockIdx.y * 2 * n + c] = dg;
   part[(int64_t)blockIdx.y * 2 * n + n + c] = db;
-}
-
-__global__ void __launch_bounds__(kNormThreads) norm_wgrad_kernel(int n, int parts, const float* part, float* dgamma,
-                                                                  float* dbeta) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= n) return;
-  float dg = 0.f, db = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    dg += part[(int64_t)p * 2 * n + c];
-    db += part[(int64_t)p * 2 * n + n + c];
-  }
-  if (dgamma) dgamma[c] = dg;
-  if (dbeta) dbeta[c] = db;
 }
 
 int check_ld(int64_t* ld, int n) {
@@ -125,48 +660,244 @@ int check_norm(const moe_lora_norm* in, moe_lora_norm* out) {
   return MOE_LORA_OK;
 }
 
-template <class T, class W>
-int run_fwd(const moe_lora_norm& nm, const void* x, const void* gamma, const void* beta, void* y, float* mean,
-            float* rstd, int sms, cudaStream_t s) {
-  const int grid = (int)(nm.rows < 8LL * sms ? nm.rows : 8LL * sms);
-  prof_begin(K_NORM_FWD, s);
-  norm_fwd_kernel<T, W><<<grid, kNormThreads, 0, s>>>(nm, (const T*)x, (const W*)gamma, (const W*)beta, (T*)y, mean,
-                                                     rstd);
-  prof_end(K_NORM_FWD, s);
+// 16-byte vectors need every row of every tensor to start on a 16-byte boundary (the
+// bases do) and to end on one.
+bool rows_aligned(const moe_lora_norm& nm, bool bwd, bool dres) {
+  int64_t a = nm.n | nm.ldx | nm.ldy;
+  if (bwd) a |= nm.lddx;
+  if (dres) a |= nm.lddres;
+  return a % (16 / dtype_bytes(nm.dtype)) == 0;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Threads for rows of `slots` slots, nv at most per thread: the fewest that hold a row
+// (8, 16 or whole warps).
+int row_threads(int slots, int nv) {
+  const int need = (int)ceil_div(slots, nv);
+  return need <= 8 ? 8 : need <= 16 ? 16 : (int)ceil_div(need, 32) * 32;
+}
+RowShape row_shape(int64_t rows, int tpr, int groups) {
+  return RowShape{tpr, groups, tpr * groups, ceil_div(rows, groups)};
+}
+
+struct FwdArgs {
+  const moe_lora_norm& nm;
+  const void* x;
+  Weight gamma, beta;
+  void* y;
+  float *mean, *rstd;
+  int sms;
+  cudaStream_t s;
+};
+
+template <class T, int VL, int NV>
+int launch_fwd(const FwdArgs& a, const RowShape& rs) {
+  const int64_t grid = std::min<int64_t>(rs.steps, 0x7fffffff);
+  prof_begin(K_NORM_FWD, a.s);
+  norm_fwd_kernel<T, VL, NV>
+      <<<(unsigned)grid, rs.threads, 0, a.s>>>(a.nm, rs, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd);
+  prof_end(K_NORM_FWD, a.s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-template <class T, class W>
-int run_bwd(const moe_lora_norm& nm, const void* x, const void* gamma, const float* mean, const float* rstd,
-            const void* dy, const void* dres, void* dx, float* dgamma, float* dbeta, float* part, int sms,
-            cudaStream_t s) {
-  const int cols = (nm.n + kNormThreads - 1) / kNormThreads;
-  if (dgamma || dbeta) {  // before dx, which may overwrite dy
-    prof_begin(K_NORM_WGRAD, s);
-    norm_part_kernel<T><<<dim3(cols, kNormParts), kNormThreads, 0, s>>>(nm, (const T*)x, mean, rstd, (const T*)dy,
-                                                                        part);
-    prof_end(K_NORM_WGRAD, s);
-    prof_begin(K_NORM_WGRAD, s);
-    norm_wgrad_kernel<<<cols, kNormThreads, 0, s>>>(nm.n, kNormParts, part, dgamma, dbeta);
-    prof_end(K_NORM_WGRAD, s);
+// Rows in flight per thread: 96 KB (forward) and 144 KB (backward, 16-bit) of copies
+// under way per SM; an SM needs about 45 KB to hide the memory's latency.
+template <class T>
+constexpr int fwd_stages() { return sizeof(T) == 2 ? 4 : 3; }
+template <class T>
+constexpr int bwd_stages() { return sizeof(T) == 2 ? 4 : 2; }
+
+// Teams of the fewest threads that hold a row with nv slots each, as many as a block has room for.
+StreamShape stream_shape(int slots, int nv) {
+  StreamShape ss;
+  ss.tpr = row_threads(slots, nv);
+  ss.teams = kStreamThreads / ss.tpr;
+  if (ss.tpr > 32) ss.teams = std::min(ss.teams, 15);  // one named barrier each
+  return ss;
+}
+
+template <class T, int NV>
+int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss) {
+  const auto kernel = norm_fwd_stream_kernel<T, NV, fwd_stages<T>()>;
+  const int threads = ss.tpr * ss.teams;
+  const size_t smem = ring_bytes<fwd_stages<T>(), NV>(threads);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_LORA_ERR_CUDA;
+  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), a.sms);
+  prof_begin(K_NORM_FWD, a.s);
+  kernel<<<grid, threads, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd);
+  prof_end(K_NORM_FWD, a.s);
+  return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+}
+
+template <class T, int VL>
+int pick_fwd(const FwdArgs& a) {
+  const int slots = (int)ceil_div(a.nm.n, VL == 1 ? 2 : VL);
+  if (slots > kFwdThreads * 16) {
+    const int grid = (int)std::min<int64_t>(a.nm.rows, 4LL * a.sms);
+    prof_begin(K_NORM_FWD, a.s);
+    norm_fwd_long_kernel<T><<<grid, kLongThreads, 0, a.s>>>(a.nm, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean,
+                                                           a.rstd);
+    prof_end(K_NORM_FWD, a.s);
+    return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
   }
-  const int grid = (int)(nm.rows < 8LL * sms ? nm.rows : 8LL * sms);
-  prof_begin(K_NORM_BWD, s);
-  norm_bwd_kernel<T, W><<<grid, kNormThreads, 0, s>>>(nm, (const T*)x, (const W*)gamma, mean, rstd, (const T*)dy,
-                                                     (const T*)dres, (T*)dx);
-  prof_end(K_NORM_BWD, s);
+  if constexpr (VL > 1) {
+    constexpr int kNV = 32 / VL;  // 32 columns a thread
+    const int nv = slots <= 8 ? 1 : slots <= 16 ? 2 : kNV;
+    const StreamShape ss = stream_shape(slots, nv);
+    if (ss.teams > 0 && a.nm.rows >= 4LL * ss.teams * a.sms)
+      return nv == 1   ? launch_fwd_stream<T, 1>(a, ss)
+             : nv == 2 ? launch_fwd_stream<T, 2>(a, ss)
+                       : launch_fwd_stream<T, kNV>(a, ss);
+  }
+  // few rows want many threads
+  int nv = 16;
+  while (nv > 1 && (slots <= 8 * (nv / 2) || (a.nm.rows * ceil_div(slots, nv) < 512LL * a.sms &&
+                                               ceil_div(slots, nv / 2) <= kFwdThreads)))
+    nv /= 2;
+  const int tpr = row_threads(slots, nv);
+  const RowShape rs = row_shape(a.nm.rows, tpr, tpr > 32 ? 1 : a.nm.rows > 32LL * a.sms ? 128 / tpr : 32 / tpr);
+  switch (nv) {
+    case 1: return launch_fwd<T, VL, 1>(a, rs);
+    case 2: return launch_fwd<T, VL, 2>(a, rs);
+    case 4: return launch_fwd<T, VL, 4>(a, rs);
+    case 8: return launch_fwd<T, VL, 8>(a, rs);
+    default: return launch_fwd<T, VL, 16>(a, rs);
+  }
+}
+
+template <class T>
+int run_fwd(const FwdArgs& a) {
+  return rows_aligned(a.nm, false, false) ? pick_fwd<T, 16 / sizeof(T)>(a) : pick_fwd<T, 1>(a);
+}
+
+// The partial rows' sum, launched while the kernel before it still runs.
+int launch_wgrad(int n, int parts, const float* part, float* dgamma, float* dbeta, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)ceil_div(n, 32), 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  prof_begin(K_NORM_WGRAD, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_wgrad_kernel, n, parts, part, dgamma, dbeta);
+  prof_end(K_NORM_WGRAD, s);
+  return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+}
+
+struct BwdArgs {
+  const moe_lora_norm& nm;
+  const void* x;
+  Weight gamma;
+  const float *mean, *rstd;
+  const void *dy, *dres;
+  void* dx;
+  float *dgamma, *dbeta, *part;
+  int sms;
+  cudaStream_t s;
+};
+
+// Where a backward kernel of `grid` blocks leaves its sums: in the outputs, or as partial
+// rows for the kernel that adds them.
+struct WgradTo {
+  float *dgamma, *dbeta;
+  bool parts;
+  WgradTo(const BwdArgs& a, int grid) {
+    parts = (a.dgamma || a.dbeta) && grid > 1;
+    dgamma = parts ? a.part : a.dgamma;
+    dbeta = parts ? a.part + a.nm.n : a.dbeta;
+  }
+};
+int finish_bwd(const BwdArgs& a, const WgradTo& to, int grid) {
+  if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
+  return to.parts ? launch_wgrad(a.nm.n, grid, a.part, a.dgamma, a.dbeta, a.s) : MOE_LORA_OK;
+}
+
+template <class T, int NV>
+int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss) {
+  const auto kernel = norm_bwd_stream_kernel<T, NV, bwd_stages<T>()>;
+  const int threads = ss.tpr * ss.teams;
+  const size_t ring = ring_bytes<bwd_stages<T>(), 3 * NV>(threads), sums = 2 * sizeof(float) * (size_t)a.nm.n;
+  const size_t smem = std::max(ring, sums);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_LORA_ERR_CUDA;
+  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), std::min(a.sms, kNormParts));
+  const WgradTo to(a, grid);
+  prof_begin(K_NORM_BWD, a.s);
+  kernel<<<grid, threads, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.mean, a.rstd, (const T*)a.dy,
+                                       (const T*)a.dres, (T*)a.dx, to.dgamma, to.dbeta, 2LL * a.nm.n);
+  prof_end(K_NORM_BWD, a.s);
+  return finish_bwd(a, to, grid);
+}
+
+template <class T, int NV, int kThreads>
+int launch_bwd_odd(const BwdArgs& a, const RowShape& rs) {
+  const auto kernel = norm_bwd_kernel<T, 1, NV, kThreads>;
+  const int64_t n = a.nm.n;
+  const int grid = (int)std::min<int64_t>(rs.steps, std::min(a.sms, kNormParts));
+  const WgradTo to(a, grid);
+  const size_t smem = sizeof(float) * n * (to.dgamma || to.dbeta ? 3 : 1);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_LORA_ERR_CUDA;
+  prof_begin(K_NORM_BWD, a.s);
+  kernel<<<grid, rs.threads, smem, a.s>>>(a.nm, rs, (const T*)a.x, a.gamma, a.mean, a.rstd, (const T*)a.dy,
+                                          (const T*)a.dres, (T*)a.dx, to.dgamma, to.dbeta, 2 * n);
+  prof_end(K_NORM_BWD, a.s);
+  return finish_bwd(a, to, grid);
+}
+
+template <class T>
+int launch_bwd_long(const BwdArgs& a) {
+  if (a.dgamma || a.dbeta) {  // before dx, which may overwrite dy
+    prof_begin(K_NORM_WGRAD, a.s);
+    norm_part_long_kernel<T><<<dim3((unsigned)ceil_div(a.nm.n, 256), kNormParts), 256, 0, a.s>>>(
+        a.nm, (const T*)a.x, a.mean, a.rstd, (const T*)a.dy, a.part);
+    prof_end(K_NORM_WGRAD, a.s);
+    if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
+    const int rc = launch_wgrad(a.nm.n, kNormParts, a.part, a.dgamma, a.dbeta, a.s);
+    if (rc) return rc;
+  }
+  const int grid = (int)std::min<int64_t>(a.nm.rows, 4LL * a.sms);
+  prof_begin(K_NORM_BWD, a.s);
+  norm_bwd_long_kernel<T><<<grid, kLongThreads, 0, a.s>>>(a.nm, (const T*)a.x, a.gamma, a.mean, a.rstd,
+                                                            (const T*)a.dy, (const T*)a.dres, (T*)a.dx);
+  prof_end(K_NORM_BWD, a.s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-// CALL<T, W>(args) for the element types of nm.
-#define NORM_DISPATCH(CALL, ...)                                                                          \
-  (nm.dtype == MOE_LORA_F32    ? NORM_DISPATCH_W(CALL, float, __VA_ARGS__)                                \
-   : nm.dtype == MOE_LORA_BF16 ? NORM_DISPATCH_W(CALL, __nv_bfloat16, __VA_ARGS__)                        \
-                               : NORM_DISPATCH_W(CALL, __half, __VA_ARGS__))
-#define NORM_DISPATCH_W(CALL, T, ...)                                        \
-  (nm.wdtype == MOE_LORA_F32    ? CALL<T, float>(__VA_ARGS__)                \
-   : nm.wdtype == MOE_LORA_BF16 ? CALL<T, __nv_bfloat16>(__VA_ARGS__)        \
-                                : CALL<T, __half>(__VA_ARGS__))
+template <class T>
+int run_bwd(const BwdArgs& a) {
+  const int n = a.nm.n;
+  if (rows_aligned(a.nm, true, a.dres != nullptr)) {
+    constexpr int VL = 16 / sizeof(T), kNV = 16 / VL;  // 16 columns a thread
+    const int slots = n / VL;
+    if (slots <= 8) return launch_bwd_stream<T, 1>(a, stream_shape(slots, 1));
+    if (slots <= kStreamThreads * kNV) return launch_bwd_stream<T, kNV>(a, stream_shape(slots, kNV));
+    return launch_bwd_long<T>(a);
+  }
+  constexpr int kNV = 8;  // two columns each
+  const int slots = (n + 1) / 2;
+  if (slots > 1024 * kNV) return launch_bwd_long<T>(a);
+  const int tpr = row_threads(slots, kNV);
+  // groups that share a block share its partial row; but every SM gets rows first
+  int groups = std::max(1, kBwdThreads / tpr);
+  while (groups > std::max(1, 32 / tpr) && ceil_div(a.nm.rows, groups) < a.sms) groups = (groups + 1) / 2;
+  if (tpr < 32) groups = (int)ceil_div(groups, 32 / tpr) * (32 / tpr);
+  if (tpr > 32) groups = std::min(groups, 15);  // one named barrier each
+  const RowShape rs = row_shape(a.nm.rows, tpr, groups);
+  return tpr > kBwdThreads ? launch_bwd_odd<T, kNV, 1024>(a, rs) : launch_bwd_odd<T, kNV, kBwdThreads>(a, rs);
+}
+
+// CALL<T>(args) for the element type of nm.
+#define NORM_DISPATCH(CALL, ...)                                  \
+  (nm.dtype == MOE_LORA_F32    ? CALL<float>(__VA_ARGS__)         \
+   : nm.dtype == MOE_LORA_BF16 ? CALL<__nv_bfloat16>(__VA_ARGS__) \
+                               : CALL<__half>(__VA_ARGS__))
 
 }  // namespace
 
@@ -189,7 +920,8 @@ int moe_lora_layernorm_forward(const moe_lora_norm* in, const void* x, const voi
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return NORM_DISPATCH(run_fwd, nm, x, gamma, beta, y, mean, rstd, sms, s);
+  const FwdArgs a{nm, x, {gamma, nm.wdtype}, {beta, nm.wdtype}, y, mean, rstd, sms, s};
+  return NORM_DISPATCH(run_fwd, a);
 }
 
 size_t moe_lora_layernorm_scratch_bytes(const moe_lora_norm* in) {
@@ -223,8 +955,9 @@ int moe_lora_layernorm_backward(const moe_lora_norm* in, const void* x, const vo
       (rc = check_ptr(dx)))
     return rc;
   if ((rc = device_sms(&sms))) return rc;
-  return NORM_DISPATCH(run_bwd, nm, x, gamma, mean, rstd, dy, dres, dx, dgamma, dbeta, static_cast<float*>(scratch),
-                       sms, static_cast<cudaStream_t>(stream));
+  const BwdArgs a{nm, x, {gamma, nm.wdtype}, mean, rstd, dy, dres, dx, dgamma, dbeta, static_cast<float*>(scratch), sms,
+                  static_cast<cudaStream_t>(stream)};
+  return NORM_DISPATCH(run_bwd, a);
 }
 
 }  // extern "C"
