@@ -46,36 +46,68 @@ struct SlotAt {
   __device__ __forceinline__ float2 pair(float v) const { return make_float2(v, VL == 1 && !hop ? 0.f : v); }
 };
 
-// Sums over a row's threads, the same in all of them: lanes of a warp, or whole warps
-// that meet at barrier `bar`.  Alternating buffers make one barrier per sum enough.
+// Sums over a row's threads, the same in all of them: lanes of a warp, or up to 16 whole
+// warps (32 in a block of one row) that meet at barrier `bar`.  Alternating buffers make
+// one barrier per sum enough.
 struct RowSum {
   int tpr, bar;
-  float2* red;  // this group's part of a buffer of 32; the second buffer 32 further
+  float* red;  // this group's 2 x kRedWords floats
   int buf = 0;
-  __device__ __forceinline__ float2 operator()(float2 v) {
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  static constexpr int kRedWords = 64;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    if (tpr >= 32) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      if (tpr > 32) across(v);
+    } else {
+      for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
-    return tpr <= 32 ? v : across(v);
   }
-  __device__ __forceinline__ float operator()(float v) {
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return tpr <= 32 ? v : across(make_float2(v, 0.f)).x;
-  }
-  __device__ __forceinline__ float2 across(float2 v) {
-    float2* r = red + buf * 32;
+  template <int N>
+  __device__ __forceinline__ void across(float (&v)[N]) {
+    float* r = red + buf * kRedWords;
     buf ^= 1;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x % tpr >> 5] = v;
+    const int gw = tpr >> 5;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) r[(threadIdx.x % tpr >> 5) * N + k] = v[k];
     if (bar < 0)
       __syncthreads();
     else
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
-    v = r[0];
-    for (int w = 1; w < tpr >> 5; ++w) v = add2(v, r[w]);
-    return v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.f;
+    int w = 0;
+    for (; w + 4 / N <= gw; w += 4 / N) {  // 16 bytes at a time
+      const float4 u = *reinterpret_cast<const float4*>(r + w * N);
+      if (N == 1) {
+        v[0] += (u.x + u.y) + (u.z + u.w);
+      } else {
+        v[0] += u.x + u.z;
+        v[N - 1] += u.y + u.w;
+      }
+    }
+    for (; w < gw; ++w)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += r[w * N + k];
+  }
+  __device__ __forceinline__ float operator()(float x) {
+    float v[1] = {x};
+    (*this)(v);
+    return v[0];
+  }
+  __device__ __forceinline__ float2 operator()(float2 x) {
+    float v[2] = {x.x, x.y};
+    (*this)(v);
+    return make_float2(v[0], v[1]);
   }
 };
+constexpr int kMaxTeams = 15;  // of several warps: one named barrier each
 
 // gamma or beta: NULL, or n elements of a type that is known at run time only (a uniform
 // branch at each load, against three times the kernels).
@@ -121,7 +153,7 @@ template <class T, int VL, int NV>
 __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm, RowShape rs, const T* x,
                                                                Weight gamma, Weight beta, T* y, float* mean,
                                                                float* rstd) {
-  __shared__ float2 red[2 * 32];
+  __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
   constexpr int kP = Vec<T, VL>::kPairs;
   const int n = nm.n;
   const int lane = threadIdx.x % rs.tpr, group = threadIdx.x / rs.tpr;
@@ -167,7 +199,7 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
           q = fma2(d, d, q);
         }
     }
-    const float rt = 1.0f / sqrtf(sum(q.x + q.y) * rn + nm.eps);
+    const float rt = rsqrtf(sum(q.x + q.y) * rn + nm.eps);
     T* yr = y + row.r * nm.ldy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -196,7 +228,11 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
 // turn.  Every thread copies its own slots kStages - 1 rows ahead with asynchronous
 // copies and reads only those, so rows in flight cost neither registers nor barriers; a
 // thread has the same columns in every row, so its weights stay in its registers.
-constexpr int kStreamThreads = 512;  // 128 registers a thread
+// Forward: 64 columns a thread, 255 registers: what a warp does once per row (sums,
+// addresses, waits) is half of the instructions at 32 columns (65,536 x 4,096 bf16: 163
+// us against 179 us, and 253 us at 16).  Backward: 16 columns and their two sums.
+constexpr int kFwdStreamThreads = 256, kFwdColumns = 64;
+constexpr int kBwdStreamThreads = 512, kBwdColumns = 16;
 struct StreamShape {
   int tpr, teams;
 };
@@ -215,7 +251,7 @@ constexpr size_t ring_bytes(int threads) {
 }
 
 // What a thread knows of its columns: slot i starts at column c0 + i * dc, `nv` slots lie
-// inside the row.
+// inside the row (kFull kernels: all of them do, for every thread).
 struct Columns {
   int c0, dc, nv;
   __device__ __forceinline__ Columns(int lane, int tpr, int n, int vl) {
@@ -227,18 +263,18 @@ struct Columns {
   __device__ __forceinline__ int col(int i) const { return c0 + i * dc; }
 };
 
-template <class T, int NV, int kStages>
-__global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
+template <class T, int NV, int kStages, bool kFull>
+__global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
                                                                             Weight gamma, Weight beta, T* y,
                                                                             float* mean, float* rstd) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   extern __shared__ __align__(16) uint8_t ring_sm[];
-  __shared__ float2 red[2 * 32];
+  __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
   const int n = nm.n;
   const Ring<kStages, NV> ring(ring_sm);
   const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
   const Columns cl(lane, ss.tpr, n, VL);
-  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * (ss.tpr >> 5) : 0)};
+  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / n;
   const int64_t step = (int64_t)gridDim.x * ss.teams;
   const auto copy_row = [&](int64_t r, int s) {
@@ -246,7 +282,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_
       const T* xr = x + r * nm.ldx;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (cl.in(i)) async_copy16(ring.slot(s, i), xr + cl.col(i));
+        if (kFull || cl.in(i)) async_copy16(ring.slot(s, i), xr + cl.col(i));
     }
     async_commit();
   };
@@ -256,7 +292,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_
   float2 g[NV][kP], b[NV][kP];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (cl.in(i)) {
+    if (kFull || cl.in(i)) {
       gamma.vec<VL>(cl.col(i), 1.f, g[i]);
       beta.vec<VL>(cl.col(i), 0.f, b[i]);
     }
@@ -269,7 +305,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_
     float2 t[2] = {both(0.f), both(0.f)};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (cl.in(i)) {
+      if (kFull || cl.in(i)) {
         Vec<T, VL> w;
         w.from_smem(ring.slot(s, i));
 #pragma unroll
@@ -283,19 +319,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_
     t[0] = t[1] = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (cl.in(i))
+      if (kFull || cl.in(i))
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
           v[i][j] = add2(v[i][j], both(-mu));
           t[j & 1] = fma2(v[i][j], v[i][j], t[j & 1]);
         }
     t[0] = add2(t[0], t[1]);
-    const float rt = 1.0f / sqrtf(sum(t[0].x + t[0].y) * rn + nm.eps);
+    const float rt = rsqrtf(sum(t[0].x + t[0].y) * rn + nm.eps);
     if (r < nm.rows) {
       T* yr = y + r * nm.ldy;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (cl.in(i)) {
+        if (kFull || cl.in(i)) {
           Vec<T, VL> o;
 #pragma unroll
           for (int j = 0; j < kP; ++j) o.put(j, fma2(mul2(v[i][j], both(rt)), g[i][j], b[i][j]));
@@ -315,19 +351,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_fwd_stream_kernel(moe_
 // rows).  Same streaming; dx needs one sum (of two values) per row, the weight gradients
 // stay in registers until the block's rows are done.
 template <class T, int NV, int kStages>
-__global__ void __launch_bounds__(kStreamThreads, 1) norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
+__global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
                                                                             Weight gamma, const float* mean,
                                                                             const float* rstd, const T* dy,
                                                                             const T* dres, T* dx, float* dgamma,
                                                                             float* dbeta, int64_t part_ld) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [2][n]
-  __shared__ float2 red[2 * 32];
+  __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
   const int n = nm.n;
   const Ring<kStages, 3 * NV> ring(ring_sm);
   const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
   const Columns cl(lane, ss.tpr, n, VL);
-  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * (ss.tpr >> 5) : 0)};
+  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / n;
   const int64_t step = (int64_t)gridDim.x * ss.teams;
   const auto copy_row = [&](int64_t r, int s) {
@@ -440,11 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(moe_lora_norm nm,
                                                                const T* dres, T* dx, float* dgamma, float* dbeta,
                                                                int64_t part_ld) {
   extern __shared__ __align__(16) float wsm[];  // gamma; then, where a block has several groups, their sums [2][n]
-  __shared__ float2 red[2 * 32];
+  __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
   constexpr int kP = Vec<T, VL>::kPairs;
   const int n = nm.n;
   const int lane = threadIdx.x % rs.tpr, group = threadIdx.x / rs.tpr;
-  RowSum sum{rs.tpr, group + 1, red + (rs.tpr > 32 ? group * (rs.tpr >> 5) : 0)};
+  RowSum sum{rs.tpr, group + 1, red + (rs.tpr > 32 ? group * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / n;
   gamma.stage(wsm, n, 1.f);
   __syncthreads();
@@ -701,25 +737,36 @@ int launch_fwd(const FwdArgs& a, const RowShape& rs) {
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-// Rows in flight per thread: 96 KB (forward) and 144 KB (backward, 16-bit) of copies
-// under way per SM; an SM needs about 45 KB to hide the memory's latency.
+// Stages of the rings: three rows of copies under way per team (two in fp32), 96 KB per SM
+// at full width; an SM needs about 45 KB to hide the memory's latency.
 template <class T>
 constexpr int fwd_stages() { return sizeof(T) == 2 ? 4 : 3; }
 template <class T>
 constexpr int bwd_stages() { return sizeof(T) == 2 ? 4 : 2; }
 
-// Teams of the fewest threads that hold a row with nv slots each, as many as a block has room for.
-StreamShape stream_shape(int slots, int nv) {
+// Slots per thread (one of `nvs`, descending) and threads of a row: the most slots that
+// every thread fills completely (no bounds checks), else the fewest threads.
+template <int N>
+StreamShape stream_shape(int slots, const int (&nvs)[N], int threads, int* nv) {
+  *nv = 0;
+  for (int v : nvs) {
+    const int t = slots / v;
+    if (!*nv && slots % v == 0 && (t == 8 || t == 16 || t % 32 == 0) && t <= threads) *nv = v;
+  }
+  if (!*nv)
+    for (int v : nvs)
+      if (!*nv || slots <= 8 * v) *nv = v;
   StreamShape ss;
-  ss.tpr = row_threads(slots, nv);
-  ss.teams = kStreamThreads / ss.tpr;
-  if (ss.tpr > 32) ss.teams = std::min(ss.teams, 15);  // one named barrier each
+  ss.tpr = row_threads(slots, *nv);
+  ss.teams = threads / ss.tpr;
   return ss;
 }
 
 template <class T, int NV>
 int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss) {
-  const auto kernel = norm_fwd_stream_kernel<T, NV, fwd_stages<T>()>;
+  const bool full = a.nm.n == ss.tpr * NV * 16 / (int)sizeof(T);
+  const auto kernel = full ? norm_fwd_stream_kernel<T, NV, fwd_stages<T>(), true>
+                           : norm_fwd_stream_kernel<T, NV, fwd_stages<T>(), false>;
   const int threads = ss.tpr * ss.teams;
   const size_t smem = ring_bytes<fwd_stages<T>(), NV>(threads);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -743,13 +790,16 @@ int pick_fwd(const FwdArgs& a) {
     return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
   }
   if constexpr (VL > 1) {
-    constexpr int kNV = 32 / VL;  // 32 columns a thread
-    const int nv = slots <= 8 ? 1 : slots <= 16 ? 2 : kNV;
-    const StreamShape ss = stream_shape(slots, nv);
+    constexpr int nvs[] = {kFwdColumns / VL, sizeof(T) == 2 ? 6 : 12, kFwdColumns / VL / 2, kFwdColumns / VL / 4, 2, 1};
+    int nv;
+    const StreamShape ss = stream_shape(slots, nvs, kFwdStreamThreads, &nv);
     if (ss.teams > 0 && a.nm.rows >= 4LL * ss.teams * a.sms)
-      return nv == 1   ? launch_fwd_stream<T, 1>(a, ss)
-             : nv == 2 ? launch_fwd_stream<T, 2>(a, ss)
-                       : launch_fwd_stream<T, kNV>(a, ss);
+      return nv == nvs[0]   ? launch_fwd_stream<T, nvs[0]>(a, ss)
+             : nv == nvs[1] ? launch_fwd_stream<T, nvs[1]>(a, ss)
+             : nv == nvs[2] ? launch_fwd_stream<T, nvs[2]>(a, ss)
+             : nv == nvs[3] ? launch_fwd_stream<T, nvs[3]>(a, ss)
+             : nv == 2      ? launch_fwd_stream<T, 2>(a, ss)
+                            : launch_fwd_stream<T, 1>(a, ss);
   }
   // few rows want many threads
   int nv = 16;
@@ -874,11 +924,15 @@ template <class T>
 int run_bwd(const BwdArgs& a) {
   const int n = a.nm.n;
   if (rows_aligned(a.nm, true, a.dres != nullptr)) {
-    constexpr int VL = 16 / sizeof(T), kNV = 16 / VL;  // 16 columns a thread
+    constexpr int VL = 16 / sizeof(T), kNV = kBwdColumns / VL;
     const int slots = n / VL;
-    if (slots <= 8) return launch_bwd_stream<T, 1>(a, stream_shape(slots, 1));
-    if (slots <= kStreamThreads * kNV) return launch_bwd_stream<T, kNV>(a, stream_shape(slots, kNV));
-    return launch_bwd_long<T>(a);
+    if (slots > kBwdStreamThreads * kNV) return launch_bwd_long<T>(a);
+    const int nvs[] = {kNV, kNV / 2, 1};
+    int nv;
+    const StreamShape ss = stream_shape(slots, nvs, kBwdStreamThreads, &nv);
+    return nv == kNV       ? launch_bwd_stream<T, kNV>(a, ss)
+           : nv == kNV / 2 ? launch_bwd_stream<T, kNV / 2>(a, ss)
+                           : launch_bwd_stream<T, 1>(a, ss);
   }
   constexpr int kNV = 8;  // two columns each
   const int slots = (n + 1) / 2;
@@ -888,7 +942,7 @@ int run_bwd(const BwdArgs& a) {
   int groups = std::max(1, kBwdThreads / tpr);
   while (groups > std::max(1, 32 / tpr) && ceil_div(a.nm.rows, groups) < a.sms) groups = (groups + 1) / 2;
   if (tpr < 32) groups = (int)ceil_div(groups, 32 / tpr) * (32 / tpr);
-  if (tpr > 32) groups = std::min(groups, 15);  // one named barrier each
+  if (tpr > 32) groups = std::min(groups, kMaxTeams);
   const RowShape rs = row_shape(a.nm.rows, tpr, groups);
   return tpr > kBwdThreads ? launch_bwd_odd<T, kNV, 1024>(a, rs) : launch_bwd_odd<T, kNV, kBwdThreads>(a, rs);
 }
