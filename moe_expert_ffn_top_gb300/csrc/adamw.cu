@@ -12,8 +12,10 @@ namespace moelora {
 namespace {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamBlock = 256;        // elements per warp step = per scale of an 8-bit state
-constexpr int kAdamTensors = 352;      // per launch: the table travels in the kernel's parameters (32 KB at most)
+constexpr int kAdamBlock = 256;  // elements of a warp's step = of one scale of an 8-bit state
+// Tensors per launch.  The table travels in the kernel's parameters (32 KB at most), so
+// nothing is copied to the device ahead of the launch and a graph captures it.
+constexpr int kAdamFew = 40, kAdamMany = 352;
 
 struct AdamTensor {
   void* p;
@@ -31,14 +33,57 @@ struct AdamHyper {
   float b1, c1, b2, c2, rbc2, eps;  // c = 1 - b; rbc2 = 1 / sqrt(1 - beta2^t)
   const float* gs;
 };
+template <int kCap>
 struct AdamTable {
   int n;
   AdamHyper h;
-  int64_t base[kAdamTensors + 1];  // first 256-element block of each tensor
-  AdamTensor t[kAdamTensors];
+  int64_t base[kCap + 1];  // first 256-element block of each tensor
+  AdamTensor t[kCap];
 };
-static_assert(sizeof(AdamTable) <= 32764, "kernel parameter limit");
+static_assert(sizeof(AdamTable<kAdamMany>) <= 32764, "kernel parameter limit");
 
+// Eight consecutive elements of a 16- or 32-bit type as loaded, and widened.  Loading and
+// widening are apart so that all of a step's loads are under way before the first is used.
+struct Raw8 {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* p, int dtype, int64_t i) {
+    const char* q = static_cast<const char*>(p) + (dtype == MOE_LORA_F32 ? 4 : 2) * i;
+    a = *reinterpret_cast<const uint4*>(q);
+    if (dtype == MOE_LORA_F32) b = *reinterpret_cast<const uint4*>(q + 16);
+  }
+  __device__ __forceinline__ void widen(int dtype, float (&f)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (dtype == MOE_LORA_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = dtype == MOE_LORA_BF16 ? Two<__nv_bfloat16>::get(w + i) : Two<__half>::get(w + i);
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+      }
+    }
+  }
+};
+__device__ __forceinline__ void store8(void* p, int dtype, int64_t i, const float (&f)[8]) {
+  uint32_t w[8];
+  if (dtype == MOE_LORA_F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 t = make_float2(f[2 * j], f[2 * j + 1]);
+    if (dtype == MOE_LORA_BF16)
+      Two<__nv_bfloat16>::put(w + j, t);
+    else
+      Two<__half>::put(w + j, t);
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 __device__ __forceinline__ float ld_any(const void* p, int dtype, int64_t i) {
   return dtype == MOE_LORA_F32    ? static_cast<const float*>(p)[i]
          : dtype == MOE_LORA_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[i])
@@ -52,13 +97,14 @@ __device__ __forceinline__ void st_any(void* p, int dtype, int64_t i, float v) {
   else
     static_cast<__half*>(p)[i] = from_f32<__half>(v);
 }
-__device__ __forceinline__ float from_e4m3(uint8_t c) {
+// Two E4M3 codes (the low byte first) to fp32, exactly.
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return __half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu)));
+  return __half22float2(reinterpret_cast<const __half2&>(h));
 }
 
-// Scale of a block from its largest finite magnitude `top`: codes are x * inv, values
+// Scale of a block from its largest finite magnitude `top`: codes are of x * inv, values
 // code * scale.
 __device__ __forceinline__ void block_scale(float top, float& inv, float& scale) {
   const bool some = top >= 7.888609052210118e-31f;  // 2^-100
@@ -72,74 +118,145 @@ __device__ __forceinline__ float finite_abs(float x) {
 __device__ __forceinline__ float warp_top(float v) {  // v >= 0: ordered as its bits
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
-// the NaN code where x is not finite (x - x is then NaN; the conversion alone would saturate an infinity)
-__device__ __forceinline__ uint8_t to_e4m3(float x, float inv) {
-  return (uint8_t)e4m3x2(__fadd_rn(__fmul_rn(x, inv), __fsub_rn(x, x)), 0.f);
+// Codes of a warp's block (this lane's eight values) and its scale.  x - x makes the NaN
+// code of what is not finite; the conversion alone would saturate an infinity.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float& scale) {
+  float top = 0.f, inv, q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(x[i]));
+  block_scale(warp_top(top), inv, scale);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = __fadd_rn(__fmul_rn(x[i], inv), __fsub_rn(x[i], x[i]));
+  return make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
 }
 
-template <bool kEight>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable tab) {
+// One element: new moments (v as its root r too) and weight.  Every operation is rounded
+// on its own, so that the result does not depend on what a compiler fuses.
+__device__ __forceinline__ void adam_element(const AdamHyper& h, float decay, float lr, float g, float& m, float& v,
+                                             float& r, float& w) {
+  m = __fadd_rn(__fmul_rn(h.b1, m), __fmul_rn(h.c1, g));
+  v = __fadd_rn(__fmul_rn(h.b2, v), __fmul_rn(__fmul_rn(h.c2, g), g));
+  r = __fsqrt_rn(v);
+  const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, h.rbc2), h.eps));
+  w = __fsub_rn(__fmul_rn(w, decay), __fmul_rn(lr, u));
+}
+
+// A warp takes blocks of 256 elements in turn, a lane eight consecutive ones.
+template <bool kEight, int kCap>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<kCap> tab) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kAdamThreads / 32);
   const AdamHyper& h = tab.h;
   const float gs = h.gs ? *h.gs : 1.0f;
   int ti = 0;
   for (int64_t b = (int64_t)blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5); b < tab.base[tab.n]; b += warps) {
-    while (b >= tab.base[ti + 1]) ++ti;
+    if (b >= tab.base[ti + 1]) {  // the tensor of block b, further on in the table
+      int lo = ti + 1, hi = tab.n - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b >= tab.base[mid])
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      ti = lo;
+    }
     const AdamTensor& t = tab.t[ti];
-    const int64_t blk = b - tab.base[ti], i0 = blk * kAdamBlock + lane;
-    float m[8], r[8];
-    float tm = 0.f, tr = 0.f, sm = 0.f, sr = 0.f;
+    const int64_t blk = b - tab.base[ti], i = blk * kAdamBlock + lane * 8;
+    const bool whole = i + 8 <= t.numel;
+    float g[8], m[8], v[8], w[8], sm = 0.f, sv = 0.f;
     if (kEight) {
       sm = t.ms[blk];
-      sr = t.vs[blk];
+      sv = t.vs[blk];
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t i = i0 + 32 * j;
-      m[j] = r[j] = 0.f;
-      if (i >= t.numel) continue;
-      const float g = __fmul_rn(ld_any(t.g, t.g_dtype, i), gs);
-      float m0, v0;
+    if (whole) {
+      Raw8 rg, rw, rm, rv;
+      rg.load(t.g, t.g_dtype, i);
+      if (t.master)
+        rw.load(t.master, MOE_LORA_F32, i);
+      else
+        rw.load(t.p, t.p_dtype, i);
+      uint2 cm, cv;
       if (kEight) {
-        m0 = __fmul_rn(from_e4m3(static_cast<const uint8_t*>(t.m)[i]), sm);
-        const float q = __fmul_rn(from_e4m3(static_cast<const uint8_t*>(t.v)[i]), sr);
-        v0 = __fmul_rn(q, q);
+        cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
+        cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
       } else {
-        m0 = static_cast<const float*>(t.m)[i];
-        v0 = static_cast<const float*>(t.v)[i];
+        rm.load(t.m, MOE_LORA_F32, i);
+        rv.load(t.v, MOE_LORA_F32, i);
       }
-      m0 = __fadd_rn(__fmul_rn(h.b1, m0), __fmul_rn(h.c1, g));
-      v0 = __fadd_rn(__fmul_rn(h.b2, v0), __fmul_rn(__fmul_rn(h.c2, g), g));
-      const float rt = __fsqrt_rn(v0);
-      float w = t.master ? t.master[i] : ld_any(t.p, t.p_dtype, i);
-      const float u = __fdiv_rn(m0, __fadd_rn(__fmul_rn(rt, h.rbc2), h.eps));
-      w = __fsub_rn(__fmul_rn(w, t.decay), __fmul_rn(t.lr, u));
-      if (t.master) t.master[i] = w;
-      st_any(t.p, t.p_dtype, i, w);
-      if (!kEight) {
-        static_cast<float*>(t.m)[i] = m0;
-        static_cast<float*>(t.v)[i] = v0;
+      rg.widen(t.g_dtype, g);
+      rw.widen(t.master ? MOE_LORA_F32 : t.p_dtype, w);
+      if (kEight) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 a = from_e4m3x2((j < 2 ? cm.x : cm.y) >> (16 * (j & 1)));
+          const float2 c = from_e4m3x2((j < 2 ? cv.x : cv.y) >> (16 * (j & 1)));
+          m[2 * j] = a.x;
+          m[2 * j + 1] = a.y;
+          v[2 * j] = c.x;
+          v[2 * j + 1] = c.y;
+        }
+      } else {
+        rm.widen(MOE_LORA_F32, m);
+        rv.widen(MOE_LORA_F32, v);
       }
-      m[j] = m0;
-      r[j] = rt;
-      tm = fmaxf(tm, finite_abs(m0));
-      tr = fmaxf(tr, finite_abs(rt));
-    }
-    if (kEight) {
-      float im, ir;
-      block_scale(warp_top(tm), im, sm);
-      block_scale(warp_top(tr), ir, sr);
+    } else {  // the end of a tensor, element by element
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t i = i0 + 32 * j;
-        if (i >= t.numel) continue;
-        static_cast<uint8_t*>(t.m)[i] = to_e4m3(m[j], im);
-        static_cast<uint8_t*>(t.v)[i] = to_e4m3(r[j], ir);
+        const bool in = i + j < t.numel;
+        g[j] = in ? ld_any(t.g, t.g_dtype, i + j) : 0.f;
+        w[j] = !in ? 0.f : t.master ? t.master[i + j] : ld_any(t.p, t.p_dtype, i + j);
+        if (kEight) {
+          m[j] = in ? from_e4m3x2(static_cast<const uint8_t*>(t.m)[i + j]).x : 0.f;
+          v[j] = in ? from_e4m3x2(static_cast<const uint8_t*>(t.v)[i + j]).x : 0.f;
+        } else {
+          m[j] = in ? static_cast<const float*>(t.m)[i + j] : 0.f;
+          v[j] = in ? static_cast<const float*>(t.v)[i + j] : 0.f;
+        }
       }
+    }
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (kEight) {
+        m[j] = __fmul_rn(m[j], sm);
+        v[j] = __fmul_rn(v[j], sv);
+        v[j] = __fmul_rn(v[j], v[j]);
+      }
+      adam_element(h, t.decay, t.lr, __fmul_rn(g[j], gs), m[j], v[j], r[j], w[j]);
+    }
+    uint2 cm, cv;
+    if (kEight) {
+      cm = encode8(m, sm);
+      cv = encode8(r, sv);
       if (lane == 0) {
         t.ms[blk] = sm;
-        t.vs[blk] = sr;
+        t.vs[blk] = sv;
+      }
+    }
+    if (whole) {
+      if (t.master) store8(t.master, MOE_LORA_F32, i, w);
+      store8(t.p, t.p_dtype, i, w);
+      if (kEight) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = cm;
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = cv;
+      } else {
+        store8(t.m, MOE_LORA_F32, i, m);
+        store8(t.v, MOE_LORA_F32, i, v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (i + j >= t.numel) break;
+        if (t.master) t.master[i + j] = w[j];
+        st_any(t.p, t.p_dtype, i + j, w[j]);
+        if (kEight) {
+          static_cast<uint8_t*>(t.m)[i + j] = (uint8_t)((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
+          static_cast<uint8_t*>(t.v)[i + j] = (uint8_t)((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
+        } else {
+          static_cast<float*>(t.m)[i + j] = m[j];
+          static_cast<float*>(t.v)[i + j] = v[j];
+        }
       }
     }
   }
@@ -159,18 +276,39 @@ int check_tensor(const moe_lora_adamw_tensor& t) {
   return MOE_LORA_OK;
 }
 
-// One launch over tab's tensors.
-int launch_adamw(AdamTable& tab, int state, int sms, cudaStream_t s) {
-  const int64_t blocks = tab.base[tab.n], per = kAdamThreads / 32;
-  const int64_t want = (blocks + per - 1) / per;
-  const int grid = (int)(want < 8LL * sms ? want : 8LL * sms);
+template <bool kEight, int kCap>
+int launch_adamw(const AdamTable<kCap>& tab, int sms, cudaStream_t s) {
+  const auto kernel = adamw_kernel<kEight, kCap>;
+  int per = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kAdamThreads, 0) != cudaSuccess || per < 1)
+    return MOE_LORA_ERR_CUDA;
+  const int64_t want = (tab.base[tab.n] + kAdamThreads / 32 - 1) / (kAdamThreads / 32), most = (int64_t)per * sms;
   prof_begin(K_ADAMW, s);
-  if (state)
-    adamw_kernel<true><<<grid, kAdamThreads, 0, s>>>(tab);
-  else
-    adamw_kernel<false><<<grid, kAdamThreads, 0, s>>>(tab);
+  kernel<<<(int)(want < most ? want : most), kAdamThreads, 0, s>>>(tab);
   prof_end(K_ADAMW, s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+}
+
+// Launches over the tensors of one state kind, kCap at a time.
+template <bool kEight, int kCap>
+int run_adamw(const AdamHyper& h, double bc1, const moe_lora_adamw_tensor* tensors, int n, int sms, cudaStream_t s) {
+  AdamTable<kCap> tab;
+  tab.h = h;
+  tab.n = 0;
+  tab.base[0] = 0;
+  for (int i = 0; i < n; ++i) {
+    const moe_lora_adamw_tensor& t = tensors[i];
+    if ((t.state == 1) != kEight || t.numel == 0) continue;
+    tab.t[tab.n] = AdamTensor{t.p, t.master, t.g, t.m, t.v, t.m_scale, t.v_scale, t.numel,
+                              (float)(1 - t.lr * t.weight_decay), (float)(t.lr / bc1), t.p_dtype, t.g_dtype};
+    tab.base[tab.n + 1] = tab.base[tab.n] + (t.numel + kAdamBlock - 1) / kAdamBlock;
+    if (++tab.n == kCap) {
+      const int rc = launch_adamw<kEight>(tab, sms, s);
+      if (rc) return rc;
+      tab.n = 0;
+    }
+  }
+  return tab.n ? launch_adamw<kEight>(tab, sms, s) : MOE_LORA_OK;
 }
 
 }  // namespace
@@ -192,25 +330,12 @@ extern "C" int moe_lora_adamw_step(const moe_lora_adamw* o, const moe_lora_adamw
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   const double bc1 = 1 - pow(o->beta1, (double)o->step), bc2 = 1 - pow(o->beta2, (double)o->step);
-  AdamTable tab;
-  tab.h = AdamHyper{(float)o->beta1, (float)(1 - o->beta1), (float)o->beta2, (float)(1 - o->beta2),
+  const AdamHyper h{(float)o->beta1, (float)(1 - o->beta1), (float)o->beta2, (float)(1 - o->beta2),
                     (float)(1 / sqrt(bc2)), (float)o->eps, o->grad_scale};
-  for (int state = 0; state < 2; ++state) {
-    tab.n = 0;
-    tab.base[0] = 0;
-    for (int i = 0; i < n; ++i) {
-      const moe_lora_adamw_tensor& t = tensors[i];
-      if (t.state != state || t.numel == 0) continue;
-      AdamTensor& d = tab.t[tab.n];
-      d = AdamTensor{t.p, t.master, t.g, t.m, t.v, t.m_scale, t.v_scale, t.numel, (float)(1 - t.lr * t.weight_decay),
-                     (float)(t.lr / bc1), t.p_dtype, t.g_dtype};
-      tab.base[tab.n + 1] = tab.base[tab.n] + (t.numel + kAdamBlock - 1) / kAdamBlock;
-      if (++tab.n == kAdamTensors) {
-        if ((rc = launch_adamw(tab, state, sms, static_cast<cudaStream_t>(stream)))) return rc;
-        tab.n = 0;
-      }
-    }
-    if (tab.n && (rc = launch_adamw(tab, state, sms, static_cast<cudaStream_t>(stream)))) return rc;
-  }
-  return MOE_LORA_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = n <= kAdamFew ? run_adamw<false, kAdamFew>(h, bc1, tensors, n, sms, s)
+                          : run_adamw<false, kAdamMany>(h, bc1, tensors, n, sms, s)))
+    return rc;
+  return n <= kAdamFew ? run_adamw<true, kAdamFew>(h, bc1, tensors, n, sms, s)
+                       : run_adamw<true, kAdamMany>(h, bc1, tensors, n, sms, s);
 }
