@@ -386,11 +386,12 @@ MOE_LORA_API int moe_lora_router_backward_aux(const moe_lora_dims* dims, const u
 /* AdamW over n tensors at once.  With g the gradient times *grad_scale, t = step, in fp32:
  *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g g,
  *     w = w (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps),
- * each operation rounded on its own (no fused multiply-add), p = w rounded to its type.  w is
- * `master` where that is given, else p.  state 0: m and v are fp32.  state 1: they are held in 8
- * bits, in blocks of 256 consecutive elements (the last may be short): m and r = sqrt(v) as E4M3
- * codes times one fp32 scale per block, max|.| * fp32(1/448), of x * ((1 / max|.|) * 448) (a block
- * whose maximum is below 2^-100 is stored as zeros, scale 0).  r, not v: E4M3 spans a ratio of 2^18, which on r is gradients that
+ * each operation rounded on its own (no fused multiply-add; the quotient to 2 units in the last
+ * place), p = w rounded to its type.  w is `master` where that is given, else p.
+ * state 0: m and v are fp32.  state 1: they are held in 8 bits, in blocks of 256 consecutive
+ * elements (the last may be short): m and r = sqrt(v) as E4M3 codes of x * ((1 / max|.|) * 448),
+ * times one fp32 scale per block, max|.| * fp32(1/448) (a block whose maximum is below 2^-100 is
+ * stored as zeros, scale 0).  r, not v: E4M3 spans a ratio of 2^18, which on r is gradients that
  * differ by 2^18 inside a block, on v only by 2^9.  The step uses the new m and v before they are
  * rounded.  A non-finite gradient spoils its own element only: scales are taken over finite
  * values, a non-finite m or r becomes the NaN code. */

@@ -25,7 +25,7 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
 // ------------------------------------------------------------------ pairs of fp32
-// Two fp32 operations in one instruction (each rounded as on its own).
+// Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
