@@ -365,14 +365,18 @@ MOE_LORA_API int moe_lora_layernorm_backward(const moe_lora_norm* nm, const void
  *   loss [A] fp32, counts [A,E] int32, prob [A,E] fp32
  *   dlogits [T,E] fp32, or NULL for the forward alone
  * dims gives T, E <= 1024 (else MOE_LORA_ERR_UNSUPPORTED), k and A.  `scratch` is a device buffer
- * of moe_lora_workspace_bytes(.., MOE_LORA_WS_BALANCE_SCRATCH); its first word is the device error
- * word, cleared here and read by moe_lora_router_get_error().  Sums run in a fixed order that
+ * of moe_lora_workspace_bytes(.., MOE_LORA_WS_BALANCE_SCRATCH).  Sums run in a fixed order that
  * depends on the adapter's own tokens alone: each adapter's results equal its standalone run bit
- * for bit. */
+ * for bit.  One launch where every adapter has at most 2^18 logits (T_a * E) and 32,768 tokens, two
+ * otherwise. */
 MOE_LORA_API int moe_lora_balance_loss(const moe_lora_dims* dims, const void* logits, int32_t dtype, int64_t ld,
                                        const int32_t* topk_ids, const int64_t* adapter_offsets, float coef,
                                        const float* dloss, float* loss, int32_t* counts, float* prob, float* dlogits,
                                        void* scratch, size_t scratch_bytes, void* stream);
+
+/* Reads the device error bits (MOE_LORA_DEV_*, of all adapters) that the last
+ * moe_lora_balance_loss of these sizes left in its scratch; synchronises `stream`. */
+MOE_LORA_API int moe_lora_balance_get_error(const moe_lora_dims* dims, const void* scratch, void* stream);
 
 /* moe_lora_router_backward with a gradient dlogits_aux [T,E] fp32 (e.g. the balance loss's; NULL =
  * none) added to the routes' own before dW_r, grad-x and the dlogits output are formed.  Unlike the

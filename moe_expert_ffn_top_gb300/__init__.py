@@ -143,6 +143,8 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_balance_loss.restype = ctypes.c_int
         L.moe_lora_balance_loss.argtypes = [ctypes.POINTER(Dims), P, ctypes.c_int32, ctypes.c_int64, P, P,
                                             ctypes.c_float, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_lora_balance_get_error.restype = ctypes.c_int
+        L.moe_lora_balance_get_error.argtypes = [ctypes.POINTER(Dims), P, P]
         L.moe_lora_router_backward_aux.restype = ctypes.c_int
         L.moe_lora_router_backward_aux.argtypes = [ctypes.POINTER(Dims), P, P, P, P, P, P, P, P, P, P, P,
                                                    ctypes.c_size_t, P]
@@ -522,7 +524,7 @@ def moe_lora_balance_loss(dims: Dims, logits: torch.Tensor, topk_ids: torch.Tens
     """Balance loss [A] of the routes topk_ids [T,k] int32 (-1 = masked) under the router's logits
     [T,E], with counts [A,E] int32 and mean probabilities prob [A,E]; dlogits [T,E] fp32 receives
     its gradient (for the upstream gradient dloss [A], None = 1) in the same pass if given.
-    moe_lora_router_get_error(scratch) reads the device error word."""
+    moe_lora_balance_get_error(dims, scratch) reads the device error bits."""
     pl, ld = _rows(logits, "logits")
     T, E, A = dims.T, dims.E, dims.A
     if logits.shape[0] != T or logits.shape[1] != E:
@@ -539,6 +541,13 @@ def moe_lora_balance_loss(dims: Dims, logits: torch.Tensor, topk_ids: torch.Tens
                                      _ptr(scratch, None, "scratch"), scratch.numel() * scratch.element_size(),
                                      _stream(stream))
     _check(rc, "moe_lora_balance_loss")
+
+
+def moe_lora_balance_get_error(dims: Dims, scratch: torch.Tensor, stream=None) -> int:
+    rc = lib().moe_lora_balance_get_error(dims, _ptr(scratch), _stream(stream))
+    if rc < 0:
+        raise MoeLoraError(rc, "moe_lora_balance_get_error")
+    return rc
 
 
 def moe_lora_router_backward_aux(dims: Dims, x: torch.Tensor, Wr: torch.Tensor, topk_ids: torch.Tensor,

@@ -149,7 +149,34 @@ __device__ __forceinline__ void async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The same elements of a weight vector, widened.
+// Column and second-element distance of a thread's slot i in a row of n, shared by tpr threads.
+template <int VL>
+struct SlotAt {
+  int c, hop;
+  bool in;
+  __device__ __forceinline__ SlotAt(int lane, int i, int tpr, int n) {
+    c = VL == 1 ? lane + 2 * i * tpr : (lane + i * tpr) * VL;
+    in = c < n;
+    hop = VL == 1 && c + tpr < n ? tpr : 0;
+  }
+  // v for both elements of a pair, 0 for the second where that is past the end
+  __device__ __forceinline__ float2 pair(float v) const { return make_float2(v, VL == 1 && !hop ? 0.f : v); }
+};
+
+// A thread's ring: kStages stages of kSlots 16-byte slots, those of a warp side by side.
+template <int kStages, int kSlots>
+struct Ring {
+  uint4* base;
+  __device__ __forceinline__ explicit Ring(void* sm)
+      : base(static_cast<uint4*>(sm) + (threadIdx.x >> 5) * (kStages * kSlots * 32) + (threadIdx.x & 31)) {}
+  __device__ __forceinline__ uint4* slot(int stage, int i) const { return base + (stage * kSlots + i) * 32; }
+};
+template <int kStages, int kSlots>
+constexpr size_t ring_bytes(int threads) {
+  return (size_t)threads * kStages * kSlots * 16;
+}
+
+// The elements of a slot in a weight vector, widened.
 template <class W, int VL, int kPairs>
 __device__ __forceinline__ void ld_pairs(const W* p, int hop, float2 (&f)[kPairs]) {
   if constexpr (VL == 1) {

@@ -32,20 +32,6 @@ struct RowAt {
     if (!on) r = rows - 1;
   }
 };
-// Column and second-element distance of a thread's slot i.
-template <int VL>
-struct SlotAt {
-  int c, hop;
-  bool in;
-  __device__ __forceinline__ SlotAt(int lane, int i, int tpr, int n) {
-    c = VL == 1 ? lane + 2 * i * tpr : (lane + i * tpr) * VL;
-    in = c < n;
-    hop = VL == 1 && c + tpr < n ? tpr : 0;
-  }
-  // v for both elements of a pair, 0 for the second where that is past the end
-  __device__ __forceinline__ float2 pair(float v) const { return make_float2(v, VL == 1 && !hop ? 0.f : v); }
-};
-
 // Sums over a row's threads, the same in all of them: lanes of a warp, or up to 16 whole
 // warps (32 in a block of one row) that meet at barrier `bar`.  Alternating buffers make
 // one barrier per sum enough.
@@ -236,19 +222,6 @@ constexpr int kBwdStreamThreads = 512, kBwdColumns = 16;
 struct StreamShape {
   int tpr, teams;
 };
-
-// A thread's ring: kStages rows of kTensors x NV slots, those of a warp side by side.
-template <int kStages, int kSlots>
-struct Ring {
-  uint4* base;
-  __device__ __forceinline__ explicit Ring(void* sm)
-      : base(static_cast<uint4*>(sm) + (threadIdx.x >> 5) * (kStages * kSlots * 32) + (threadIdx.x & 31)) {}
-  __device__ __forceinline__ uint4* slot(int stage, int i) const { return base + (stage * kSlots + i) * 32; }
-};
-template <int kStages, int kSlots>
-constexpr size_t ring_bytes(int threads) {
-  return (size_t)threads * kStages * kSlots * 16;
-}
 
 // What a thread knows of its columns: slot i starts at column c0 + i * dc, `nv` slots lie
 // inside the row (kFull kernels: all of them do, for every thread).

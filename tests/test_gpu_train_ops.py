@@ -206,7 +206,7 @@ def _balance(logits, ids, offsets, coef=0.01, dloss=None, grad=True, A=1):
     prob = torch.full((A, E), float("nan"), device="cuda")
     dl = torch.full((T, E), float("nan"), device="cuda") if grad else None
     m.moe_lora_balance_loss(d, logits, ids, offsets, coef, loss, counts, prob, sc, dl, dloss)
-    return loss, counts, prob, dl, m.moe_lora_router_get_error(sc)
+    return loss, counts, prob, dl, m.moe_lora_balance_get_error(d, sc)
 
 
 def _check_balance(logits, ids, offsets, got, coef=0.01, dloss=None):
