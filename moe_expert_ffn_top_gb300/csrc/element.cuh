@@ -135,10 +135,15 @@ struct Vec<T, 1> {
   }
 };
 
-// 16-byte asynchronous copies into shared memory.  A thread that reads only what it
+// Asynchronous copies of 16 (or 4) bytes into shared memory.  A thread that reads only what it
 // copied itself needs no barrier: waiting for its own groups is enough.
 __device__ __forceinline__ void async_copy16(void* dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void async_copy4(void* dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),
                "l"(src)
                : "memory");
 }
