@@ -7,10 +7,12 @@
 //
 // Adapters of one group each (small batches): one launch.  A cluster of eight blocks
 // counts the group's ids, meets, and every block has the counts that the gradient needs;
-// the sums meet in distributed shared memory.  Otherwise a first launch counts, one
-// cluster per group, and the second needs no cluster (its blocks fill every SM): the
-// last block of a group to finish adds the group, the last group of an adapter the
-// adapter.  Logits are read once, for the loss and the gradient together.
+// the sums meet in distributed shared memory.  (Adapters of one chunk: no cluster.)
+// Otherwise a first launch counts, a small cluster per group; the second needs no cluster, its
+// blocks fill every SM; a third adds the chunks' sums.  Each is launched while the one
+// before it still runs, and waits for it where it needs its results: the second has then
+// its first logits under way.  Logits are read once, for the loss and the gradient
+// together.
 #include <algorithm>
 
 #include "common.cuh"
@@ -23,12 +25,18 @@ namespace moelora {
 
 namespace {
 
-constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
+// Threads of the main kernel's blocks: many experts fill the registers of 256, up to 64
+// experts (8 a lane) leave room for 512, whose iterations are half as many.
+constexpr int block_threads(int vals) { return vals == 8 ? 512 : 256; }
+constexpr int kSumPad = 16;
 constexpr int kBalMaxE = 1024;
 constexpr int kBalCluster = 8;       // chunks per group
 constexpr int kBalMaxChunk = 4096;   // tokens; a chunk is a multiple of 32 long
 constexpr int kBalMaxGroups = 38;    // 304 blocks, two per SM, unless the chunks get too long
 constexpr int kBalGroupWork = 1 << 18;  // logits worth another group
+constexpr int kBalChunkWork = 1 << 12;  // logits that one chunk takes alone
+constexpr int kCountCluster = 4, kCountThreads = 512;
+constexpr int kSumThreads = 1024;
 constexpr int kBalStages = 3;
 
 struct BalTable {
@@ -46,8 +54,14 @@ int64_t bal_groups(int64_t n, int E) {
   return std::max<int64_t>(1, std::max(by_work, by_size));
 }
 
+// Tokens per chunk of such an adapter: an eighth of a group, or all of a tiny batch.
+int bal_chunk(int64_t n, int64_t groups, int E) {
+  const int64_t chunks = n * E <= kBalChunkWork && n <= kBalMaxChunk ? 1 : groups * kBalCluster;
+  return (int)((n + chunks * 32 - 1) / (chunks * 32)) * 32;
+}
+
 struct BalLayout {
-  size_t err, adone, gdone, live, bad, bits, counts, gpart, part, total;
+  size_t err, tokens, live, bad, bits, counts, part, total;
 };
 BalLayout bal_layout(const moe_lora_dims* d) {
   BalLayout L;
@@ -57,32 +71,29 @@ BalLayout bal_layout(const moe_lora_dims* d) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   L.err = take(sizeof(int) * d->A);
-  L.adone = take(sizeof(int) * d->A);
-  L.gdone = take(sizeof(int) * groups);
+  L.tokens = take(sizeof(int) * d->A);
   L.live = take(sizeof(int) * groups);
   L.bad = take(sizeof(int) * groups);
   L.bits = take(sizeof(uint32_t) * (d->T / 32 + 1));
   L.counts = take(sizeof(int) * groups * d->E);
-  L.gpart = take(sizeof(float) * groups * d->E);
   L.part = take(sizeof(float) * groups * kBalCluster * d->E);
   L.total = o;
   return L;
 }
-// Device view of the scratch.  Per adapter: an error word, how many of its groups are
-// done.  Per group: how many of its chunks are done, its live tokens, error bits, counts
-// [E], sums of probabilities [E]; per chunk such sums.  A bit per token: it is live.
+// Device view of the scratch.  Per adapter: an error word, its live tokens.  Per group: its
+// live tokens, error bits, counts [E].  Per chunk: sums of probabilities [E].  A bit per
+// token: it is live.
 struct BalScratch {
-  int *err, *adone, *gdone, *live, *bad;
+  int *err, *tokens, *live, *bad;
   uint32_t* bits;
   int* counts;
-  float *gpart, *part;
+  float* part;
 };
 BalScratch bal_scratch(const moe_lora_dims* d, void* p) {
   const BalLayout L = bal_layout(d);
   char* c = static_cast<char*>(p);
-  return BalScratch{(int*)(c + L.err),  (int*)(c + L.adone),     (int*)(c + L.gdone),
-                    (int*)(c + L.live), (int*)(c + L.bad),       (uint32_t*)(c + L.bits),
-                    (int*)(c + L.counts), (float*)(c + L.gpart), (float*)(c + L.part)};
+  return BalScratch{(int*)(c + L.err),  (int*)(c + L.tokens),    (int*)(c + L.live), (int*)(c + L.bad),
+                    (uint32_t*)(c + L.bits), (int*)(c + L.counts), (float*)(c + L.part)};
 }
 
 int check_balance_dims(const moe_lora_dims* d) {
@@ -91,15 +102,18 @@ int check_balance_dims(const moe_lora_dims* d) {
   return d->E > kBalMaxE ? MOE_LORA_ERR_UNSUPPORTED : MOE_LORA_OK;
 }
 
-struct Chunk {
-  int a, group, t0, len;  // adapter, group of all, first token, tokens
-  __device__ __forceinline__ explicit Chunk(const BalTable& bt) {
-    group = blockIdx.x / kBalCluster;
-    a = 0;
-    while (a + 1 < bt.n && group >= bt.group0[a + 1]) ++a;
-    const int64_t at = (int64_t)(blockIdx.x - bt.group0[a] * kBalCluster) * bt.chunk[a];
+__device__ __forceinline__ int adapter_of(const BalTable& bt, int group) {
+  int a = 0;
+  while (a + 1 < bt.n && group >= bt.group0[a + 1]) ++a;
+  return a;
+}
+// `chunks` consecutive chunks of an adapter from its chunk c0 on.
+struct Span {
+  int t0, len;  // first token, tokens
+  __device__ __forceinline__ Span(const BalTable& bt, int a, int64_t c0, int chunks) {
+    const int64_t at = c0 * bt.chunk[a], most = (int64_t)chunks * bt.chunk[a];
     const int64_t left = bt.tok_off[a + 1] - bt.tok_off[a] - at;
-    len = left <= 0 ? 0 : (int)(left < bt.chunk[a] ? left : bt.chunk[a]);
+    len = left <= 0 ? 0 : (int)(left < most ? left : most);
     t0 = bt.tok_off[a] + (int)(len ? at : 0);
   }
 };
@@ -111,77 +125,80 @@ __device__ __forceinline__ V from_rank(const V* p, int rank) {
   return reinterpret_cast<const V&>(v);
 }
 
-// What a block learns from the ids of its chunk.
+// What a block learns from the ids of its tokens.
+template <int kTokens>
 struct IdScan {
-  int hist[kBalMaxE];                // routes per expert
-  uint32_t live[kBalMaxChunk / 32];  // tokens with a route
+  int hist[kBalMaxE];           // routes per expert
+  uint32_t live[kTokens / 32];  // tokens with a route
   int nlive, bad;
 };
-__device__ __forceinline__ void scan_ids(IdScan& sc, const Chunk& ch, const int32_t* ids, int k, int E) {
-  constexpr int kAhead = 4;  // loads under way per thread
-  const int32_t* p = ids + (int64_t)ch.t0 * k;
-  const int routes = ch.len * k, words = (ch.len + 31) / 32;
+// A thread takes a token's ids, a warp 32 tokens, whose live bits are then one ballot.
+template <int kThreads, int kTokens>
+__device__ __forceinline__ void scan_ids(IdScan<kTokens>& sc, const Span& sp, const int32_t* ids, int k, int E) {
+  constexpr int kAhead = 8;  // loads under way per thread
+  const int lane = threadIdx.x & 31, words = (sp.len + 31) / 32;
   int id[kAhead];
+  const auto load = [&](int w, int j0) {
+    const int t = w * 32 + lane;
+    const int32_t* p = ids + ((int64_t)sp.t0 + t) * k + j0;
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) {
-    const int i = threadIdx.x + j * kBalThreads;
-    id[j] = i < routes ? p[i] : -1;
-  }
-  for (int e = threadIdx.x; e < E; e += kBalThreads) sc.hist[e] = 0;
-  for (int i = threadIdx.x; i < words; i += kBalThreads) sc.live[i] = 0;
+    for (int j = 0; j < kAhead; ++j) id[j] = t < sp.len && j0 + j < k ? p[j] : -1;
+  };
+  load(threadIdx.x >> 5, 0);
+  for (int e = threadIdx.x; e < E; e += kThreads) sc.hist[e] = 0;
   if (threadIdx.x == 0) sc.nlive = sc.bad = 0;
   __syncthreads();
-  for (int b = 0; b < routes; b += kAhead * kBalThreads) {
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = b + threadIdx.x + j * kBalThreads, e = id[j];
-      if ((unsigned)e < (unsigned)E) {
-        const int t = i / k;
-        atomicAdd(&sc.hist[e], 1);
-        atomicOr(&sc.live[t >> 5], 1u << (t & 31));
-      } else if (e != -1) {
-        sc.bad = MOE_LORA_DEV_BAD_ID;
-      }
-      const int next = i + kAhead * kBalThreads;
-      id[j] = next < routes ? p[next] : -1;
-    }
-  }
-  __syncthreads();
   int n = 0;
-  for (int i = threadIdx.x; i < words; i += kBalThreads) n += __popc(sc.live[i]);
-  n = __reduce_add_sync(0xffffffffu, n);
-  if ((threadIdx.x & 31) == 0 && n) atomicAdd(&sc.nlive, n);
+  for (int w = threadIdx.x >> 5; w < words; w += kThreads / 32) {
+    bool any = false;
+    for (int j0 = 0; j0 < k; j0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if ((unsigned)id[j] < (unsigned)E) {
+          atomicAdd(&sc.hist[id[j]], 1);
+          any = true;
+        } else if (id[j] != -1) {
+          sc.bad = MOE_LORA_DEV_BAD_ID;
+        }
+      }
+      const bool more = j0 + kAhead < k;
+      load(more ? w : w + kThreads / 32, more ? j0 + kAhead : 0);
+    }
+    const uint32_t bits = __ballot_sync(0xffffffffu, any);
+    if (lane == 0) sc.live[w] = bits;
+    n += __popc(bits);
+  }
+  if (lane == 0 && n) atomicAdd(&sc.nlive, n);
 }
 
 // First launch of larger batches: counts, live tokens and error bits of every group, and
-// the tokens' live bits.
-__global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(kBalThreads)
+// the tokens' live bits.  A group is a cluster's, an expert's count its blocks' sum.
+__global__ void __cluster_dims__(kCountCluster, 1, 1) __launch_bounds__(kCountThreads)
     balance_count_kernel(const __grid_constant__ BalTable bt, const int32_t* ids, int k, int E, BalScratch out) {
-  __shared__ IdScan sc;
-  const Chunk ch(bt);
-  const int rank = (int)cluster_rank();
+  constexpr int kChunks = kBalCluster / kCountCluster;
+  __shared__ IdScan<kChunks * kBalMaxChunk> sc;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  scan_ids(sc, ch, ids, k, E);
-  for (int i = threadIdx.x; i < (ch.len + 31) / 32; i += kBalThreads) out.bits[ch.t0 / 32 + i] = sc.live[i];
+  const int group = blockIdx.x / kCountCluster, a = adapter_of(bt, group), rank = (int)cluster_rank();
+  const Span sp(bt, a, (int64_t)(group - bt.group0[a]) * kBalCluster + rank * kChunks, kChunks);
+  scan_ids<kCountThreads>(sc, sp, ids, k, E);
   cluster_sync_all();
-  const int per = (E + kBalCluster - 1) / kBalCluster;
-  for (int e = rank * per + threadIdx.x; e < min(E, (rank + 1) * per); e += kBalThreads) {
+  for (int i = threadIdx.x; i < (sp.len + 31) / 32; i += kCountThreads) out.bits[sp.t0 / 32 + i] = sc.live[i];
+  const int per = (E + kCountCluster - 1) / kCountCluster;
+  for (int e = rank * per + threadIdx.x; e < min(E, (rank + 1) * per); e += kCountThreads) {
     int c = 0;
 #pragma unroll
-    for (int r = 0; r < kBalCluster; ++r) c += from_rank(&sc.hist[e], r);
-    out.counts[(int64_t)ch.group * E + e] = c;
+    for (int r = 0; r < kCountCluster; ++r) c += from_rank(&sc.hist[e], r);
+    out.counts[(int64_t)group * E + e] = c;
   }
   if (rank == 0 && threadIdx.x == 0) {
     int n = 0, b = 0;
 #pragma unroll
-    for (int r = 0; r < kBalCluster; ++r) {
+    for (int r = 0; r < kCountCluster; ++r) {
       n += from_rank(&sc.nlive, r);
       b |= from_rank(&sc.bad, r);
     }
-    out.live[ch.group] = n;
-    out.bad[ch.group] = b;
-    out.gdone[ch.group] = 0;
-    if (ch.group == bt.group0[ch.a]) out.adone[ch.a] = 0;
+    out.live[group] = n;
+    out.bad[group] = b;
   }
   cluster_sync_all();  // nobody leaves while its counts are read
 }
@@ -225,38 +242,60 @@ struct Pairs {
   __device__ __forceinline__ int apart() const { return kMode == kVec16 || (kMode == kWord && sizeof(T) == 2) ? 1 : lpr; }
 };
 
-// Adds in a fixed order over the block: threads of a warp, then warps.  One thread's result.
-__device__ __forceinline__ float block_total(float v, float* sm) {
+// One expert's mean probability, also to the block that adds the loss (rank 0 of a
+// cluster of kC).
+template <int kC>
+__device__ __forceinline__ void finish_prob(const BalArgs& g, int a, int e, float p, float* psm) {
+  g.prob[a * g.E + e] = p;
+  if (kC > 1)
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(psm + e), 0)), "f"(p) : "memory");
+  else
+    psm[e] = p;
+}
+// The loss from all of f and prob: 32 experts by a warp, the warps' sums in order.
+template <int kThreads>
+__device__ __forceinline__ void finish_loss(const BalArgs& g, int a, const float* f, const float* psm, float* tsm) {
+  float t = 0.f;
+  for (int b = 0; b < g.E; b += kThreads) {
+    const int e = b + threadIdx.x;
+    float v = e < g.E ? f[e] * psm[e] : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int w = 0; w < kBalWarps; ++w) v += sm[w];
-  return v;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) tsm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int w = 0; w < min(kThreads, g.E - b + 31) / 32; ++w) t += tsm[w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) g.loss[a] = g.coef * (float)g.E * t;
 }
 
 // Loss, probabilities and the logits' gradient.  `lpr` lanes hold a row (4 to 32, so that
 // a lane has at most kVals logits); a lane has the same experts in every row, whose f and
 // sum of probabilities stay in its registers (kFull: rows fill every lane).
-template <class T, RowMode kMode, int kVals, bool kOne, bool kFull>
-__global__ void __launch_bounds__(kBalThreads, 2)
+// kC: blocks of a cluster when one launch does it all, 0 as the second of three.
+template <class T, RowMode kMode, int kVals, int kC, bool kFull>
+__global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
     balance_kernel(const __grid_constant__ BalTable bt, const __grid_constant__ BalArgs g) {
   constexpr int kP = kVals / 2;
   constexpr int kWords = kVals * (int)sizeof(T) / 4;  // of a lane's row
   constexpr int kRows16 = kMode == kElement ? 1 : kWords / 4;
+  constexpr bool kOne = kC > 0;
+  constexpr int kT = block_threads(kVals);
   extern __shared__ __align__(16) uint8_t ring_sm[];
-  __shared__ IdScan sc;
+  __shared__ IdScan<kBalMaxChunk> sc;
   __shared__ float fsm[kBalMaxE];  // f_e
-  __shared__ float csm[kBalMaxE];  // sums of probabilities: the block's; rank 0 of a cluster: the adapter's
-  __shared__ float tsm[kBalWarps];
-  __shared__ int nsm[2], last, bad;  // R, N of the adapter
-  // per-warp sums of probabilities, half of the experts at a time, where the ring was
-  float(*psm)[kBalMaxE / 2] = reinterpret_cast<float(*)[kBalMaxE / 2]>(ring_sm);
-  const int E = g.E, row = threadIdx.x / g.lpr, rows = kBalThreads / g.lpr;
+  __shared__ float csm[kBalMaxE];  // sums of probabilities: partial ones, then the block's
+  __shared__ float tsm[kT / 32];
+  __shared__ int nsm[2], bad;  // R, N and error bits of the adapter
+  // where the ring was: a row of sums per row group, rows apart so that float4 stores spread over the banks
+  float* psm = reinterpret_cast<float*>(ring_sm);
+  const int pitch = g.E + kSumPad;
+  const int E = g.E, row = threadIdx.x / g.lpr, rows = kT / g.lpr;
   const Pairs<T, kMode> pr{(int)threadIdx.x % g.lpr, g.lpr};
-  const int rank = kOne ? (int)cluster_rank() : 0;
-  const Chunk ch(bt);
+  const int rank = kC > 1 ? (int)cluster_rank() : 0;
+  const int group = kOne ? blockIdx.x / (kC ? kC : 1) : blockIdx.x / kBalCluster, a = adapter_of(bt, group);
+  const Span ch(bt, a, kC == 1 ? 0 : blockIdx.x - (int64_t)bt.group0[a] * kBalCluster, 1);
   const Ring<kBalStages, kRows16> ring(ring_sm);
   const T* logits = static_cast<const T*>(g.logits) + (int64_t)ch.t0 * g.ld;
   const auto in = [&](int e) { return kFull || e < E; };
@@ -285,57 +324,84 @@ __global__ void __launch_bounds__(kBalThreads, 2)
 #pragma unroll
   for (int s = 0; s < kBalStages - 1; ++s) copy_row(row + s * rows, s);
 
-  const int ng = bt.group0[ch.a + 1] - bt.group0[ch.a];
+  const int ng = bt.group0[a + 1] - bt.group0[a];
   if (threadIdx.x < 2) nsm[threadIdx.x] = 0;
+  if (threadIdx.x == 0) bad = 0;
+  int* cnt = reinterpret_cast<int*>(fsm);
   if (kOne) {
-    scan_ids(sc, ch, g.ids, g.k, E);
-    cluster_sync_all();
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = threadIdx.x; i < (ch.len + 31) / 32; i += kBalThreads) sc.live[i] = g.sc.bits[ch.t0 / 32 + i];
-    __syncthreads();
-  }
-  {
-    const int* gc = g.sc.counts + (int64_t)bt.group0[ch.a] * E;
-    int R = 0, N = 0;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {
-      int c = 0;
-      if (kOne) {
+    scan_ids<kT>(sc, ch, g.ids, g.k, E);
+    if (kC > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kT) {
+      int c = kC > 1 ? 0 : sc.hist[e];
 #pragma unroll
-        for (int r = 0; r < kBalCluster; ++r) c += from_rank(&sc.hist[e], r);
-      } else {
-#pragma unroll 8
-        for (int i = 0; i < ng; ++i) c += gc[(int64_t)i * E + e];
+      for (int r = 0; r < (kC > 1 ? kC : 0); ++r) c += from_rank(&sc.hist[e], r);
+      cnt[e] = c;
+    }
+    if (threadIdx.x < kC) {
+      atomicAdd(&nsm[1], kC > 1 ? from_rank(&sc.nlive, threadIdx.x) : sc.nlive);
+      atomicOr(&bad, kC > 1 ? from_rank(&sc.bad, threadIdx.x) : sc.bad);
+    }
+  } else {
+    for (int e = threadIdx.x; e < E; e += kT) cnt[e] = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    for (int i = threadIdx.x; i < (ch.len + 31) / 32; i += kT) sc.live[i] = g.sc.bits[ch.t0 / 32 + i];
+    const int* gc = g.sc.counts + (int64_t)bt.group0[a] * E;
+    // columns (four at a time where E allows) x slices of the groups, so that all loads are under way together
+    const int wide = E % 4 == 0 ? 4 : 1, cols = E / wide, slices = max(1, kT / cols);
+    for (int c = threadIdx.x; c < cols * slices; c += kT) {
+      const int e = c % cols * wide;
+      int4 v = make_int4(0, 0, 0, 0);
+#pragma unroll 12
+      for (int i = c / cols; i < ng; i += slices) {
+        if (wide == 4) {
+          const int4 u = *reinterpret_cast<const int4*>(gc + (int64_t)i * E + e);
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        } else {
+          v.x += gc[(int64_t)i * E + e];
+        }
       }
-      fsm[e] = __int_as_float(c);
-      R += c;
+      atomicAdd(&cnt[e], v.x);
+      if (wide == 4) {
+        atomicAdd(&cnt[e + 1], v.y);
+        atomicAdd(&cnt[e + 2], v.z);
+        atomicAdd(&cnt[e + 3], v.w);
+      }
     }
-    for (int i = threadIdx.x; i < (kOne ? kBalCluster : ng); i += kBalThreads)
-      N += kOne ? from_rank(&sc.nlive, i) : g.sc.live[bt.group0[ch.a] + i];
-    if (kOne && rank == 0 && threadIdx.x == 0) {
-      bad = 0;
-      for (int r = 0; r < kBalCluster; ++r) bad |= from_rank(&sc.bad, r);
-    }
-    R = __reduce_add_sync(0xffffffffu, R);
-    N = __reduce_add_sync(0xffffffffu, N);
-    if ((threadIdx.x & 31) == 0) {
-      if (R) atomicAdd(&nsm[0], R);
-      if (N) atomicAdd(&nsm[1], N);
+    for (int i = threadIdx.x; i < ng; i += kT) {
+      atomicAdd(&nsm[1], g.sc.live[bt.group0[a] + i]);
+      atomicOr(&bad, g.sc.bad[bt.group0[a] + i]);
     }
   }
   __syncthreads();
+  int R = 0;
+  for (int e = threadIdx.x; e < E; e += kT) R += cnt[e];
+  R = __reduce_add_sync(0xffffffffu, R);
+  if ((threadIdx.x & 31) == 0 && R) atomicAdd(&nsm[0], R);
+  __syncthreads();
   const int N = nsm[1];
   const float rR = 1.0f / (float)max(nsm[0], 1), rN = 1.0f / (float)max(N, 1);
-  const bool writes_counts = blockIdx.x == bt.group0[ch.a] * kBalCluster;
-  for (int e = threadIdx.x; e < E; e += kBalThreads) {
-    const int c = __float_as_int(fsm[e]);
+  const bool first = blockIdx.x == (kC == 1 ? group : bt.group0[a] * kBalCluster);  // block of the adapter
+  for (int e = threadIdx.x; e < E; e += kT) {
+    const int c = cnt[e];
     fsm[e] = (float)c * rR;
-    if (writes_counts) g.counts[ch.a * E + e] = c;
+    if (first) g.counts[a * E + e] = c;
+  }
+  if (first && threadIdx.x == 0) {
+    g.sc.err[a] = bad;
+    g.sc.tokens[a] = N;
   }
   __syncthreads();
   // f - 1/E instead of f: the gradient's difference f_e - <p, f> then loses less to cancellation
   const float mean = 1.0f / (float)E;
-  const float up = (g.dlogits && g.dloss ? g.dloss[ch.a] : 1.f) * (g.coef * (float)E) * rN;
+  const float up = (g.dlogits && g.dloss ? g.dloss[a] : 1.f) * (g.coef * (float)E) * rN;
   float2 f[kP], acc[kP];
 #pragma unroll
   for (int p = 0; p < kP; ++p) {
@@ -428,89 +494,110 @@ __global__ void __launch_bounds__(kBalThreads, 2)
   }
   async_wait<0>();
   __syncthreads();
-  // the block's sums: rows of a warp by shuffles, warps in order
+  // the block's sums over its row groups
 #pragma unroll
-  for (int p = 0; p < kP; ++p)
-    for (int o = g.lpr; o < 32; o <<= 1) {
-      acc[p].x += __shfl_xor_sync(0xffffffffu, acc[p].x, o);
-      acc[p].y += __shfl_xor_sync(0xffffffffu, acc[p].y, o);
+  for (int p = 0; p < kP; ++p) {
+    const int e = pr.first(p), e2 = e + pr.apart();
+    if (kMode == kVec16) {
+      if (p % 2 == 0 && in(e))
+        *reinterpret_cast<float4*>(psm + row * pitch + e) = make_float4(acc[p].x, acc[p].y, acc[p + 1].x, acc[p + 1].y);
+    } else {
+      if (in(e)) psm[row * pitch + e] = acc[p].x;
+      if (in(e2)) psm[row * pitch + e2] = acc[p].y;
     }
-  float* my_part = g.sc.part + (int64_t)blockIdx.x * E;
-  for (int h = 0; h < E; h += kBalMaxE / 2) {
-    const auto put = [&](int e, float x) {
-      if (in(e) && (unsigned)(e - h) < kBalMaxE / 2u) psm[threadIdx.x >> 5][e - h] = x;
-    };
-    if ((int)(threadIdx.x & 31) < g.lpr)
+  }
+  __syncthreads();
+  const int slices = min(rows, max(1, kT / E));
+  float* my_part = kOne ? csm : g.sc.part + (int64_t)blockIdx.x * E;
+  if (slices > 1) {
+    const int e = threadIdx.x % E, q = threadIdx.x / E;
+    float p = 0.f;
+    if (q < slices)
+      for (int r = q; r < rows; r += slices) p += psm[r * pitch + e];
+    __syncthreads();
+    if (q < slices) psm[threadIdx.x] = p;
+    __syncthreads();
+    if (q == 0) {
+      for (int i = 1; i < slices; ++i) p += psm[i * E + e];
+      my_part[e] = p;
+    }
+  } else {
+    for (int e = threadIdx.x; e < E; e += kT) {
+      float p = 0.f;
+      for (int r = 0; r < rows; ++r) p += psm[r * pitch + e];
+      my_part[e] = p;
+    }
+  }
+  if (!kOne) return;
+  // the group's sums and the loss; psm: rank 0's, for all probabilities
+  const int per = kC > 1 ? (E + kC - 1) / kC : E;
+  if (kC > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  for (int e = rank * per + threadIdx.x; e < min(E, (rank + 1) * per); e += kT) {
+    float p = kC > 1 ? 0.f : csm[e];
 #pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        put(pr.first(p), acc[p].x);
-        put(pr.first(p) + pr.apart(), acc[p].y);
+    for (int r = 0; r < (kC > 1 ? kC : 0); ++r) p += from_rank(&csm[e], r);
+    finish_prob<kC>(g, a, e, p * rN, psm);
+  }
+  if (kC > 1)
+    cluster_sync_all();  // also: nobody leaves while its shared memory is read
+  else
+    __syncthreads();
+  if (rank == 0) finish_loss<kT>(g, a, fsm, psm, tsm);
+}
+
+// Third launch of larger batches: a cluster of eight blocks per adapter, an eighth of the
+// experts each.  A group's chunks are added in order by one thread, the groups in order
+// by another.
+__global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(kSumThreads)
+    balance_sum_kernel(const __grid_constant__ BalTable bt, const __grid_constant__ BalArgs g) {
+  constexpr int kBatch = 64, kCols = kBalMaxE / kBalCluster;  // groups at a time, columns of a block
+  __shared__ float gsm[kBatch][kCols];
+  __shared__ float fsm[kBalMaxE], psm[kBalMaxE], tsm[kSumThreads / 32];
+  __shared__ int nsm;
+  const int E = g.E, a = blockIdx.x / kBalCluster, rank = (int)cluster_rank();
+  const int per = (E + kBalCluster - 1) / kBalCluster, e0 = rank * per, cols = max(0, min(E - e0, per));
+  const int slices = max(1, kSumThreads / max(cols, 1)), c = threadIdx.x % max(cols, 1), q = threadIdx.x / max(cols, 1);
+  const int g0 = bt.group0[a], ng = bt.group0[a + 1] - g0;
+  if (threadIdx.x == 0) nsm = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
+  int R = 0;
+  for (int e = threadIdx.x; e < E; e += kSumThreads) {
+    const int n = g.counts[a * E + e];
+    fsm[e] = (float)n;
+    R += n;
+  }
+  R = __reduce_add_sync(0xffffffffu, R);
+  if ((threadIdx.x & 31) == 0 && R) atomicAdd(&nsm, R);
+  float p = 0.f;
+  for (int b = 0; b < ng; b += kBatch) {
+    const int m = min(kBatch, ng - b);
+    if (c < cols && q < slices)
+#pragma unroll 2
+      for (int i = q; i < m; i += slices) {
+        const float* cp = g.sc.part + (int64_t)(g0 + b + i) * kBalCluster * E + e0 + c;
+        float v[kBalCluster];
+#pragma unroll
+        for (int r = 0; r < kBalCluster; ++r) v[r] = cp[(int64_t)r * E];
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < kBalCluster; ++r) t += v[r];
+        gsm[i][c] = t;
       }
     __syncthreads();
-    for (int e = h + threadIdx.x; e < min(E, h + kBalMaxE / 2); e += kBalThreads) {
-      float p = 0.f;
-#pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) p += psm[w][e - h];
-      if (kOne)
-        csm[e] = p;
-      else
-        my_part[e] = p;
-    }
+    if (q == 0 && c < cols)
+      for (int i = 0; i < m; ++i) p += gsm[i][c];
     __syncthreads();
   }
-  // the group's, then the adapter's sums, and the loss
-  float part = 0.f;
-  if (kOne) {
-    cluster_sync_all();
-    const int per = (E + kBalCluster - 1) / kBalCluster;
-    for (int e = rank * per + threadIdx.x; e < min(E, (rank + 1) * per); e += kBalThreads) {
-      float p = 0.f;
-#pragma unroll
-      for (int r = 0; r < kBalCluster; ++r) p += from_rank(&csm[e], r);
-      p *= rN;
-      g.prob[ch.a * E + e] = p;
-      // rank 0 needs them all; its psm is free
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&psm[0][0] + e), 0)), "f"(p) : "memory");
-    }
-    cluster_sync_all();  // also: nobody leaves while its shared memory is read
-    if (rank != 0) return;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) part = fmaf(fsm[e], (&psm[0][0])[e], part);
-  } else {
-    // the last block of the group, then the last group of the adapter, go on
-    const auto is_last = [&](int* counter, int of) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) last = atomicAdd(counter, 1) == of - 1;
-      __syncthreads();
-      __threadfence();
-      return last != 0;
-    };
-    if (!is_last(g.sc.gdone + ch.group, kBalCluster)) return;
-    const float* cp = g.sc.part + (int64_t)ch.group * kBalCluster * E;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {
-      float p = 0.f;
-#pragma unroll
-      for (int r = 0; r < kBalCluster; ++r) p += __ldcg(cp + (int64_t)r * E + e);
-      g.sc.gpart[(int64_t)ch.group * E + e] = p;
-    }
-    if (!is_last(g.sc.adone + ch.a, ng)) return;
-    const float* gp = g.sc.gpart + (int64_t)bt.group0[ch.a] * E;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {
-      float p = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < ng; ++i) p += __ldcg(gp + (int64_t)i * E + e);
-      p *= rN;
-      g.prob[ch.a * E + e] = p;
-      part = fmaf(fsm[e], p, part);
-    }
-  }
-  part = block_total(part, tsm);
-  if (threadIdx.x == 0) {
-    g.loss[ch.a] = g.coef * (float)E * part;
-    int b = kOne ? bad : 0;
-    for (int i = 0; !kOne && i < ng; ++i) b |= g.sc.bad[bt.group0[ch.a] + i];
-    g.sc.err[ch.a] = b;
-  }
+  const float rR = 1.0f / (float)max(nsm, 1), rN = 1.0f / (float)max(g.sc.tokens[a], 1);
+  for (int e = threadIdx.x; e < E; e += kSumThreads) fsm[e] *= rR;
+  cluster_sync_all();  // rank 0 runs, its psm may be written
+  if (q == 0 && c < cols) finish_prob<kBalCluster>(g, a, e0 + c, p * rN, psm);
+  cluster_sync_all();
+  if (rank == 0) finish_loss<kSumThreads>(g, a, fsm, psm, tsm);
 }
 
 #define LAUNCH(call)                                     \
@@ -518,43 +605,62 @@ __global__ void __launch_bounds__(kBalThreads, 2)
     if ((call) != cudaSuccess) return MOE_LORA_ERR_CUDA; \
   } while (0)
 
-template <class T, RowMode kMode, int kVals, bool kOne>
-int launch_balance(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
-  const auto kernel = kMode == kVec16 && a.E == a.lpr * kVals ? balance_kernel<T, kMode, kVals, kOne, kMode == kVec16>
-                                                              : balance_kernel<T, kMode, kVals, kOne, false>;
-  const size_t ring = kMode == kElement ? 0 : (size_t)kBalThreads * kBalStages * kVals * sizeof(T);
-  const size_t smem = std::max(ring, sizeof(float) * kBalWarps * (kBalMaxE / 2));
-  LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+// A launch as a cluster, or overlapping the launch before it in the stream.
+struct BalLaunch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
-  if (kOne) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kBalCluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  } else {  // overlaps the counting launch before it
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+  BalLaunch(int64_t grid, int threads, size_t smem, int cluster, bool overlap, cudaStream_t s) {
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    if (overlap) {
+      at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.numAttrs = 1;
+    } else if (cluster > 1) {
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = cluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.numAttrs = 1;
+    }
   }
-  cfg.gridDim = dim3((unsigned)bt.group0[bt.n] * kBalCluster);
-  cfg.blockDim = dim3(kBalThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+};
+
+template <class T, RowMode kMode, int kVals, int kC>
+int launch_balance(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
+  const auto kernel = kMode == kVec16 && a.E == a.lpr * kVals ? balance_kernel<T, kMode, kVals, kC, kMode == kVec16>
+                                                              : balance_kernel<T, kMode, kVals, kC, false>;
+  constexpr int kT = block_threads(kVals);
+  const size_t ring = kMode == kElement ? 0 : (size_t)kT * kBalStages * kVals * sizeof(T);
+  const size_t smem = std::max(ring, sizeof(float) * (kT / a.lpr) * (a.E + kSumPad));
+  LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  const BalLaunch l((int64_t)bt.group0[bt.n] * (kC == 1 ? 1 : kBalCluster), kT, smem, kC, kC == 0, s);
   prof_begin(K_BAL_LOSS, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, bt, a);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, bt, a);
   prof_end(K_BAL_LOSS, s);
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
 template <class T, RowMode kMode, int kVals>
 int pick_groups(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
-  if (bt.group0[bt.n] == bt.n) return launch_balance<T, kMode, kVals, true>(bt, a, s);
+  if (bt.group0[bt.n] == bt.n) {
+    bool one_chunk = true;
+    for (int i = 0; i < bt.n; ++i) one_chunk &= bt.tok_off[i + 1] - bt.tok_off[i] <= bt.chunk[i];
+    return one_chunk ? launch_balance<T, kMode, kVals, 1>(bt, a, s) : launch_balance<T, kMode, kVals, kBalCluster>(bt, a, s);
+  }
   prof_begin(K_BAL_COUNT, s);
-  balance_count_kernel<<<bt.group0[bt.n] * kBalCluster, kBalThreads, 0, s>>>(bt, a.ids, a.k, a.E, a.sc);
+  balance_count_kernel<<<bt.group0[bt.n] * kCountCluster, kCountThreads, 0, s>>>(bt, a.ids, a.k, a.E, a.sc);
   prof_end(K_BAL_COUNT, s);
   LAUNCH(cudaGetLastError());
-  return launch_balance<T, kMode, kVals, false>(bt, a, s);
+  const int rc = launch_balance<T, kMode, kVals, 0>(bt, a, s);
+  if (rc) return rc;
+  const BalLaunch l((int64_t)bt.n * kBalCluster, kSumThreads, 0, 0, true, s);
+  prof_begin(K_BAL_SUM, s);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, balance_sum_kernel, bt, a);
+  prof_end(K_BAL_SUM, s);
+  return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
 template <class T, RowMode kMode>
@@ -603,7 +709,7 @@ extern "C" int moe_lora_balance_loss(const moe_lora_dims* d, const void* logits,
   for (int a = 0; a < d->A; ++a) {
     const int64_t n = at.tok_off[a + 1] - at.tok_off[a], groups = bal_groups(n, d->E);
     bt.tok_off[a] = at.tok_off[a];
-    bt.chunk[a] = (int)((n + groups * kBalCluster * 32 - 1) / (groups * kBalCluster * 32)) * 32;
+    bt.chunk[a] = bal_chunk(n, groups, d->E);
     bt.group0[a + 1] = bt.group0[a] + (int)groups;
   }
   bt.tok_off[d->A] = at.tok_off[d->A];

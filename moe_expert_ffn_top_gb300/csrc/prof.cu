@@ -44,7 +44,7 @@ const char* prof_name(int slot) {
       "dy_b2", "dB2", "gather_bwd", "w2_dgrad_swiglu_bwd", "dw_reduce", "dA2", "w13_dgrad_b13", "dB13",
       "dy13_combine", "a13_expand", "combine_dx", "dA13", "dequant_mxfp4", "split_reduce", "selftest_gemm",
       "router_topk", "router_dlogits", "router_dx", "router_dWr", "w13_native", "w2_native", "dw_native",
-      "norm_fwd", "norm_bwd", "norm_wgrad", "balance_counts", "balance_loss", "adamw"};
+      "norm_fwd", "norm_bwd", "norm_wgrad", "balance_counts", "balance_loss", "balance_sum", "adamw"};
   return (slot >= 0 && slot < K_NUM_SLOTS) ? names[slot] : "?";
 }
 

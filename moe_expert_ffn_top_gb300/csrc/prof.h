@@ -13,7 +13,7 @@ enum ProfSlot {
   K_DEQUANT, K_SPLIT_REDUCE, K_SELFTEST,
   K_ROUTER_FWD, K_ROUTER_DL, K_ROUTER_DX, K_ROUTER_DW,
   K_W13_NV, K_W2_NV, K_DW_NV,  // native FP4 forward
-  K_NORM_FWD, K_NORM_BWD, K_NORM_WGRAD, K_BAL_COUNT, K_BAL_LOSS, K_ADAMW,  // training step
+  K_NORM_FWD, K_NORM_BWD, K_NORM_WGRAD, K_BAL_COUNT, K_BAL_LOSS, K_BAL_SUM, K_ADAMW,  // training step
   K_NUM_SLOTS
 };
 
