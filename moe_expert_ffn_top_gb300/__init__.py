@@ -14,6 +14,7 @@ gradients.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -442,24 +443,36 @@ def _dtype(t: torch.Tensor, name: str) -> int:
 
 
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
-    """Pointer and row stride of a [rows, n] tensor whose rows are contiguous."""
+    """Pointer and row stride (0 = dense) of a [rows, n] tensor whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [rows, n] with n >= 1")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+    if like is None:
+        if t.dim() != 2 or t.size(1) < 1:
+            raise ValueError(f"{name} must be [rows, n] with n >= 1")
+    elif t.shape != like.shape or t.dtype is not like.dtype:
         raise ValueError(f"{name} must be {tuple(like.shape)} {like.dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     rows, n = t.shape
     ld, step = t.stride()
     if (n > 1 and step != 1) or (rows > 1 and ld < n):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), ld if rows > 1 else n
+    return t.data_ptr(), ld if rows > 1 else 0
 
 
 def _vec(t: Optional[torch.Tensor], n: int, name: str, dtype=None) -> Optional[int]:
-    if t is not None and t.numel() != n:
+    """Pointer of a contiguous CUDA tensor of n elements (None passes through)."""
+    if t is None:
+        return None
+    if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-    return _ptr(t, dtype, name)
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def moe_lora_layernorm_forward(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
@@ -527,14 +540,14 @@ def moe_lora_balance_loss(dims: Dims, logits: torch.Tensor, topk_ids: torch.Tens
     moe_lora_balance_get_error(dims, scratch) reads the device error bits."""
     pl, ld = _rows(logits, "logits")
     T, E, A = dims.T, dims.E, dims.A
-    if logits.shape[0] != T or logits.shape[1] != E:
+    if logits.size(0) != T or logits.size(1) != E:
         raise ValueError(f"logits must be [{T}, {E}], got {tuple(logits.shape)}")
-    offs = _offsets(adapter_offsets)
+    offs = None if adapter_offsets is None else array.array("q", adapter_offsets)
     if offs is not None and len(offs) != A + 1:
         raise ValueError(f"adapter_offsets must have {A + 1} entries")
     rc = lib().moe_lora_balance_loss(dims, pl, _dtype(logits, "logits"), ld,
                                      _vec(topk_ids, T * dims.k, "topk_ids", torch.int32),
-                                     offs, coef, _vec(dloss, A, "dloss", torch.float32),
+                                     None if offs is None else offs.buffer_info()[0], coef, _vec(dloss, A, "dloss", torch.float32),
                                      _vec(loss, A, "loss", torch.float32), _vec(counts, A * E, "counts", torch.int32),
                                      _vec(prob, A * E, "prob", torch.float32),
                                      _vec(dlogits, T * E, "dlogits", torch.float32),

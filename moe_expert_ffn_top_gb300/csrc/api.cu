@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -98,16 +99,23 @@ int tmap_fp4_unpacked(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1
 
 // ------------------------------------------------------------------ device
 // Requires the current device to be an sm_103 GPU; returns its SM count (or the
-// MOELORA_NUM_SMS override, for running beside other work).
+// MOELORA_NUM_SMS override, for running beside other work).  A device's SM count is
+// asked for once.
 int device_sms(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];  // 0: not asked yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_LORA_ERR_DEVICE;
-  int major = 0, minor = 0, n = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MOE_LORA_ERR_DEVICE;
-  if (major != 10 || minor != 3) return MOE_LORA_ERR_DEVICE;
+  int n = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MOE_LORA_ERR_DEVICE;
+    if (major != 10 || minor != 3) return MOE_LORA_ERR_DEVICE;
+    if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
+  }
   if (const char* env = std::getenv("MOELORA_NUM_SMS")) {
     const int v = std::atoi(env);
     if (v > 0 && v < n) n = v;

@@ -635,7 +635,8 @@ int launch_balance(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
   constexpr int kT = block_threads(kVals);
   const size_t ring = kMode == kElement ? 0 : (size_t)kT * kBalStages * kVals * sizeof(T);
   const size_t smem = std::max(ring, sizeof(float) * (kT / a.lpr) * (a.E + kSumPad));
-  LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  if (smem > 32 * 1024)  // with the static part above what a launch may use without asking
+    LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   const BalLaunch l((int64_t)bt.group0[bt.n] * (kC == 1 ? 1 : kBalCluster), kT, smem, kC, kC == 0, s);
   prof_begin(K_BAL_LOSS, s);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, bt, a);
