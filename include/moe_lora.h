@@ -343,7 +343,7 @@ MOE_LORA_API int moe_lora_layernorm_forward(const moe_lora_norm* nm, const void*
  *   dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy      [n] fp32; each may be NULL
  * dx may be dy or dres (same stride); sums over rows run in a fixed order, so equal calls give
  * equal bits.  scratch: device buffer of moe_lora_layernorm_scratch_bytes(nm) bytes (0 for bad
- * sizes); may be NULL when both weight gradients are. */
+ * sizes); may be NULL when both weight gradients are and n <= 8192. */
 MOE_LORA_API size_t moe_lora_layernorm_scratch_bytes(const moe_lora_norm* nm);
 MOE_LORA_API int moe_lora_layernorm_backward(const moe_lora_norm* nm, const void* x, const void* gamma,
                                              const float* mean, const float* rstd, const void* dy, const void* dres,

@@ -142,6 +142,12 @@ __device__ __forceinline__ void async_copy16(void* dst_smem, const void* src) {
                "l"(src)
                : "memory");
 }
+// the first `bytes` of 16, the rest as zeros
+__device__ __forceinline__ void async_copy16_part(void* dst_smem, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void async_copy4(void* dst_smem, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst_smem))),
                "l"(src)
@@ -164,6 +170,12 @@ struct SlotAt {
     in = c < n;
     hop = VL == 1 && c + tpr < n ? tpr : 0;
   }
+  // the same slot of a slice that starts at column `first`
+  __device__ __forceinline__ SlotAt shifted(int first) const {
+    SlotAt s = *this;
+    s.c += first;
+    return s;
+  }
   // v for both elements of a pair, 0 for the second where that is past the end
   __device__ __forceinline__ float2 pair(float v) const { return make_float2(v, VL == 1 && !hop ? 0.f : v); }
 };
@@ -185,7 +197,8 @@ constexpr size_t ring_bytes(int threads) {
 template <class W, int VL, int kPairs>
 __device__ __forceinline__ void ld_pairs(const W* p, int hop, float2 (&f)[kPairs]) {
   if constexpr (VL == 1) {
-    f[0] = make_float2(to_f32(*p), hop ? to_f32(p[hop]) : 0.f);
+    const float a = to_f32(*p), b = to_f32(p[hop]);  // hop 0: the same element again, and no branch
+    f[0] = make_float2(a, hop ? b : 0.f);
   } else if constexpr (sizeof(W) == 4) {
 #pragma unroll
     for (int i = 0; i < kPairs; i += 2) {

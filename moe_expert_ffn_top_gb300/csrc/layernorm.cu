@@ -15,7 +15,6 @@ namespace {
 // i + tpr, ... of the row, NV of them, in registers as loaded: a slot is 16 bytes, or
 // (VL = 1) two single elements tpr columns apart.
 constexpr int kFwdThreads = 512;
-constexpr int kBwdThreads = 768;  // 80 registers a thread
 constexpr int kNormParts = 152;   // most partial rows of the weight gradients: one per block
 
 struct RowShape {
@@ -62,10 +61,7 @@ struct RowSum {
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int k = 0; k < N; ++k) r[(threadIdx.x % tpr >> 5) * N + k] = v[k];
-    if (bar < 0)
-      __syncthreads();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+    meet();
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.f;
     int w = 0;
@@ -82,6 +78,15 @@ struct RowSum {
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] += r[w * N + k];
   }
+  // all threads of the row
+  __device__ __forceinline__ void meet() const {
+    if (tpr <= 32)
+      __syncwarp();
+    else if (bar < 0)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
+  }
   __device__ __forceinline__ float operator()(float x) {
     float v[1] = {x};
     (*this)(v);
@@ -96,39 +101,41 @@ struct RowSum {
 constexpr int kMaxTeams = 15;  // of several warps: one named barrier each
 
 // gamma or beta: NULL, or n elements of a type that is known at run time only (a uniform
-// branch at each load, against three times the kernels).
+// branch per load of a row's slots, against three times the kernels).
 struct Weight {
   const void* p;
   int dtype;
-  // elements of a slot, `none` where there are no weights
-  template <int VL, int kP>
-  __device__ __forceinline__ void slot(const SlotAt<VL>& at, float none, float2 (&f)[kP]) const {
-    if (!p) {
+  // The elements of N slots, `none` where there are no weights; place(i): slot i.  One
+  // branch and no condition inside: all loads are under way together (with a branch per
+  // slot their latencies add up, 10 us ahead of the first row).
+  template <class W, int VL, int N, int kP, class Place>
+  __device__ __forceinline__ void load_as(float2 (&f)[N][kP], const Place& place) const {
 #pragma unroll
-      for (int j = 0; j < kP; ++j) f[j] = both(none);
-    } else if (dtype == MOE_LORA_F32) {
-      ld_pairs<float, VL>(static_cast<const float*>(p) + at.c, at.hop, f);
-    } else if (dtype == MOE_LORA_BF16) {
-      ld_pairs<__nv_bfloat16, VL>(static_cast<const __nv_bfloat16*>(p) + at.c, at.hop, f);
-    } else {
-      ld_pairs<__half, VL>(static_cast<const __half*>(p) + at.c, at.hop, f);
+    for (int i = 0; i < N; ++i) {
+      const SlotAt<VL> at = place(i);
+      ld_pairs<W, VL>(static_cast<const W*>(p) + (at.in ? at.c : 0), at.in ? at.hop : 0, f[i]);
     }
   }
-  template <int VL, int kP>
-  __device__ __forceinline__ void vec(int c, float none, float2 (&f)[kP]) const {
-    SlotAt<VL> at(0, 0, 0, 1);
-    at.c = c;
-    slot(at, none, f);
+  template <int VL, int N, int kP, class Place>
+  __device__ __forceinline__ void load(float2 (&f)[N][kP], float none, const Place& place) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < kP; ++j) f[i][j] = both(none);
+    } else if (dtype == MOE_LORA_F32) {
+      load_as<float, VL>(f, place);
+    } else if (dtype == MOE_LORA_BF16) {
+      load_as<__nv_bfloat16, VL>(f, place);
+    } else {
+      load_as<__half, VL>(f, place);
+    }
   }
   __device__ __forceinline__ float at(int64_t c, float none) const {
     return !p                        ? none
            : dtype == MOE_LORA_F32  ? static_cast<const float*>(p)[c]
            : dtype == MOE_LORA_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[c])
                                     : to_f32(static_cast<const __half*>(p)[c]);
-  }
-  // the whole vector, widened, into shared memory
-  __device__ __forceinline__ void stage(float* sm, int n, float none) const {
-    for (int c = threadIdx.x; c < n; c += blockDim.x) sm[c] = at(c, none);
   }
 };
 
@@ -158,16 +165,14 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
       else
         v[i].clear();
     }
-    float2 g[NV > kAhead ? 1 : NV][kP], b[NV > kAhead ? 1 : NV][kP];
-    if (NV <= kAhead)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const SlotAt<VL> at(lane, i, rs.tpr, n);
-        if (at.in) {
-          gamma.slot(at, 1.f, g[i]);
-          beta.slot(at, 0.f, b[i]);
-        }
-      }
+    constexpr int kW = NV < kAhead ? NV : kAhead;
+    float2 g[kW][kP], b[kW][kP];
+    const auto weights = [&](int i0) {
+      const auto place = [&](int i) { return SlotAt<VL>(lane, i0 + i, rs.tpr, n); };
+      gamma.load<VL>(g, 1.f, place);
+      beta.load<VL>(b, 0.f, place);
+    };
+    if (NV <= kAhead) weights(0);
     float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -190,12 +195,9 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const SlotAt<VL> at(lane, i, rs.tpr, n);
+      if (NV > kAhead && i % kW == 0) weights(i);
       if (at.in && row.on) {
-        if (NV > kAhead) {
-          gamma.slot(at, 1.f, g[0]);
-          beta.slot(at, 0.f, b[0]);
-        }
-        const auto &gi = g[NV > kAhead ? 0 : i], &bi = b[NV > kAhead ? 0 : i];
+        const auto &gi = g[i % kW], &bi = b[i % kW];
         Vec<T, VL> o;
 #pragma unroll
         for (int j = 0; j < kP; ++j) o.put(j, fma2(mul2(add2(v[i].get(j), both(-mu)), both(rt)), gi[j], bi[j]));
@@ -219,6 +221,8 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
 // us against 179 us, and 253 us at 16).  Backward: 16 columns and their two sums.
 constexpr int kFwdStreamThreads = 256, kFwdColumns = 64;
 constexpr int kBwdStreamThreads = 512, kBwdColumns = 16;
+constexpr int kOddThreads = 512, kOddFwdColumns = 32;
+constexpr int kOddRows = 256;  // from here on the staged forward
 struct StreamShape {
   int tpr, teams;
 };
@@ -263,12 +267,9 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
   float2 g[NV][kP], b[NV][kP];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (kFull || cl.in(i)) {
-      gamma.vec<VL>(cl.col(i), 1.f, g[i]);
-      beta.vec<VL>(cl.col(i), 0.f, b[i]);
-    }
+  const auto place = [&](int i) { return SlotAt<VL>(lane, i, ss.tpr, n); };
+  gamma.load<VL>(g, 1.f, place);
+  beta.load<VL>(b, 0.f, place);
   int s = 0;
   // all teams of the block leave together: one without a row works on what its slots hold
   for (int64_t r = first; r - team < nm.rows; r += step) {
@@ -323,21 +324,66 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
 // block * part_ld (the partial rows, or the outputs themselves when one block has all
 // rows).  Same streaming; dx needs one sum (of two values) per row, the weight gradients
 // stay in registers until the block's rows are done.
-template <class T, int NV, int kStages>
+//
+// Rows wider than kBwdSlice are worked on in slices (blockIdx.y) by two launches: kSums
+// leaves every slice's part of a row's sums in `sums` [rows][slices], kApply adds them.
+enum BwdMode { kWhole, kSums, kApply };
+constexpr int kBwdSlice = kBwdStreamThreads * kBwdColumns;
+// Slice blockIdx.y of a row of n.
+struct Slice {
+  int first, n;
+  __device__ __forceinline__ explicit Slice(int all) : first(blockIdx.y * kBwdSlice), n(min(kBwdSlice, all - first)) {}
+};
+// A row's two sums over all slices, from this slice's; false: the row is done (kSums).
+template <BwdMode kMode, class Sum>
+__device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, float2* sums, int64_t r, bool on, int lane) {
+  if (kMode == kApply) {
+    all = both(0.f);
+    if (on)
+      for (int i = 0; i < (int)gridDim.y; ++i) all = add2(all, sums[r * gridDim.y + i]);
+    return true;
+  }
+  all = sum(mine);
+  if (kMode == kWhole) return true;
+  if (on && lane == 0) sums[r * gridDim.y + blockIdx.y] = all;
+  return false;
+}
+// A block's sums of the weight gradients from its teams' [teams][2][n] in shared memory
+// (`acc`, 16 columns of either per thread), teams in order.
+__device__ __forceinline__ void store_wgrad(const float* acc, int teams, int n, float* dgamma, float* dbeta) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * n; i += blockDim.x) {
+    float v = acc[i];
+    for (int k = 1; k < teams; ++k) v += acc[(int64_t)k * 2 * n + i];
+    if (i < n) {
+      if (dgamma) dgamma[i] = v;
+    } else if (dbeta) {
+      dbeta[i - n] = v;
+    }
+  }
+}
+
+template <class T, int NV, int kStages, BwdMode kMode>
 __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
                                                                             Weight gamma, const float* mean,
                                                                             const float* rstd, const T* dy,
                                                                             const T* dres, T* dx, float* dgamma,
-                                                                            float* dbeta, int64_t part_ld) {
+                                                                            float* dbeta, int64_t part_ld,
+                                                                            float2* sums) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
-  extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [2][n]
+  extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const int n = nm.n;
+  const Slice sl(nm.n);
+  const int n = sl.n;
+  x += sl.first;
+  dy += sl.first;
+  dres += dres ? sl.first : 0;
+  dx += sl.first;
   const Ring<kStages, 3 * NV> ring(ring_sm);
   const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
   const Columns cl(lane, ss.tpr, n, VL);
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
-  const float rn = 1.0f / n;
+  const float rn = 1.0f / nm.n;
   const int64_t step = (int64_t)gridDim.x * ss.teams;
   const auto copy_row = [&](int64_t r, int s) {
     if (r < nm.rows) {
@@ -347,7 +393,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
         if (cl.in(i)) {
           async_copy16(ring.slot(s, i), xr + cl.col(i));
           async_copy16(ring.slot(s, NV + i), gr + cl.col(i));
-          if (dres) async_copy16(ring.slot(s, 2 * NV + i), er + cl.col(i));
+          if (kMode != kSums && dres) async_copy16(ring.slot(s, 2 * NV + i), er + cl.col(i));
         }
     }
     async_commit();
@@ -356,12 +402,11 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
   float2 g[NV][kP], dg[NV][kP], db[NV][kP];
+  gamma.load<VL>(g, 1.f, [&](int i) { return SlotAt<VL>(lane, i, ss.tpr, n).shifted(sl.first); });
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (cl.in(i)) gamma.vec<VL>(cl.col(i), 1.f, g[i]);
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < kP; ++j) dg[i][j] = db[i][j] = both(0.f);
-  }
   const auto stat = [&](const float* p, int64_t r) { return r < nm.rows ? p[r] : 0.f; };
   float mu = stat(mean, first), rt = stat(rstd, first);
   int s = 0;
@@ -390,9 +435,10 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
             db[i][j] = add2(db[i][j], d);
           }
         }
-    const float2 t = sum(make_float2(su.x + su.y, sh.x + sh.y));
+    float2 t;
+    const bool more = row_sums<kMode>(sum, make_float2(su.x + su.y, sh.x + sh.y), t, sums, r, on, lane);
     const float2 na = both(-t.x * rn), nb = both(-t.y * rn);
-    if (on) {
+    if (on && more) {
       T* dr = dx + r * nm.lddx;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -411,142 +457,222 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
     rt = rt1;
     s = s == kStages - 1 ? 0 : s + 1;
   }
-  if (!dgamma && !dbeta) return;
+  if (kMode == kSums || (!dgamma && !dbeta)) return;
   async_wait<0>();
   __syncthreads();
   float* acc = reinterpret_cast<float*>(ring_sm);
-  // the teams are added in order, the last one stores
-  for (int k = 0; k < ss.teams; ++k) {
-    if (team == k) {
+  float *ag = acc + team * 2 * n, *ab = ag + n;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (cl.in(i))
+  for (int i = 0; i < NV; ++i)
+    if (cl.in(i))
 #pragma unroll
-          for (int j = 0; j < kP; ++j) {
-            const int e = cl.col(i) + 2 * j;
-            float2 *ag = reinterpret_cast<float2*>(acc + e), *ab = reinterpret_cast<float2*>(acc + n + e);
-            if (k > 0) {
-              dg[i][j] = add2(dg[i][j], *ag);
-              db[i][j] = add2(db[i][j], *ab);
-            }
-            if (k < ss.teams - 1) {
-              *ag = dg[i][j];
-              *ab = db[i][j];
-            } else {
-              if (dgamma) *reinterpret_cast<float2*>(dgamma + blockIdx.x * part_ld + e) = dg[i][j];
-              if (dbeta) *reinterpret_cast<float2*>(dbeta + blockIdx.x * part_ld + e) = db[i][j];
-            }
-          }
+      for (int j = 0; j < kP; j += 2) {
+        const int e = cl.col(i) + 2 * j;
+        *reinterpret_cast<float4*>(ag + e) = make_float4(dg[i][j].x, dg[i][j].y, dg[i][j + 1].x, dg[i][j + 1].y);
+        *reinterpret_cast<float4*>(ab + e) = make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
+      }
+  const int64_t at = blockIdx.x * part_ld + sl.first;
+  store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at : nullptr, dbeta ? dbeta + at : nullptr);
+}
+
+// Rows that 16-byte vectors do not fit (a length, stride or type off the 16-byte grid).  A
+// team copies the aligned 16-byte pieces that cover a row, what lies before its start in
+// the first piece included (never before the tensor's: that start is aligned), nothing
+// past its end; then every thread reads its elements, tpr columns apart.  Pieces are read
+// by other threads than copied them, so a team meets when a row has come, and a stage is
+// refilled only after the sums of the next row, which all of the team have to reach.
+template <class T>
+struct OddStage {
+  char* base;  // of this team; stages of `tensors` pieces of `cap` bytes
+  int cap, tensors;
+  // asynchronous copy of n elements from p
+  __device__ __forceinline__ void copy(int stage, int k, const T* p, int n, int lane, int tpr) const {
+    const int o = (int)(reinterpret_cast<uintptr_t>(p) & 15), bytes = o + n * (int)sizeof(T);
+    const char* src = reinterpret_cast<const char*>(p) - o;
+    char* dst = base + (stage * tensors + k) * cap;
+    for (int c = lane * 16; c < bytes; c += tpr * 16) async_copy16_part(dst + c, src + c, min(16, bytes - c));
+  }
+  __device__ __forceinline__ const T* row(int stage, int k, const T* p) const {
+    return reinterpret_cast<const T*>(base + (stage * tensors + k) * cap + (reinterpret_cast<uintptr_t>(p) & 15));
+  }
+};
+inline int odd_cap(int n, int size) { return (n * size + 15 + 15) / 16 * 16; }
+__device__ __forceinline__ int odd_cap_device(int n, int size) { return (n * size + 15 + 15) / 16 * 16; }
+// The two elements of slot `at` of a staged row.
+template <class T>
+__device__ __forceinline__ float2 odd_pair(const T* row, const SlotAt<1>& at) {
+  return make_float2(to_f32(row[at.c]), at.hop ? to_f32(row[at.c + at.hop]) : 0.f);
+}
+
+template <class T, int NP, int kStages>
+__global__ void __launch_bounds__(kOddThreads, 1) norm_fwd_odd_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
+                                                                      Weight gamma, Weight beta, T* y, float* mean,
+                                                                      float* rstd) {
+  extern __shared__ __align__(16) char stage_sm[];
+  __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
+  const int n = nm.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
+  const int cap = odd_cap_device(n, sizeof(T));
+  const OddStage<T> st{stage_sm + (size_t)team * kStages * cap, cap, 1};
+  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
+  const float rn = 1.0f / n;
+  const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
+  const auto copy_row = [&](int64_t r, int s) {
+    if (r < nm.rows) st.copy(s, 0, x + r * nm.ldx, n, lane, ss.tpr);
+    async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
+  float2 g[NP][1], b[NP][1];
+  const auto place = [&](int i) { return SlotAt<1>(lane, i, ss.tpr, n); };
+  gamma.load<1>(g, 1.f, place);
+  beta.load<1>(b, 0.f, place);
+  int s = 0;
+  for (int64_t r = first; r - team < nm.rows; r += step) {
+    async_wait<kStages - 2>();
+    sum.meet();
+    const bool on = r < nm.rows;
+    const T* row = st.row(s, 0, x + (on ? r : 0) * nm.ldx);
+    float2 v[NP], t = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const SlotAt<1> at(lane, i, ss.tpr, n);
+      if (at.in) {
+        v[i] = odd_pair(row, at);
+        t = add2(t, v[i]);
+      }
     }
-    __syncthreads();
+    const float mu = sum(t.x + t.y) * rn;
+    copy_row(r + (kStages - 1) * step, s == 0 ? kStages - 1 : s - 1);
+    t = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const SlotAt<1> at(lane, i, ss.tpr, n);
+      if (at.in) {
+        v[i] = add2(v[i], at.pair(-mu));
+        t = fma2(v[i], v[i], t);
+      }
+    }
+    const float rt = rsqrtf(sum(t.x + t.y) * rn + nm.eps);
+    if (on) {
+      T* yr = y + r * nm.ldy;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const SlotAt<1> at(lane, i, ss.tpr, n);
+        if (at.in) {
+          const float2 o = fma2(mul2(v[i], both(rt)), g[i][0], b[i][0]);
+          yr[at.c] = from_f32<T>(o.x);
+          if (at.hop) yr[at.c + at.hop] = from_f32<T>(o.y);
+        }
+      }
+      if (mean && lane == 0) {
+        mean[r] = mu;
+        rstd[r] = rt;
+      }
+    }
+    s = s == kStages - 1 ? 0 : s + 1;
   }
 }
 
-// The same for rows that 16-byte vectors do not fit (VL = 1), rows in registers.
-template <class T, int VL, int NV, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(moe_lora_norm nm, RowShape rs, const T* x, Weight gamma,
-                                                               const float* mean, const float* rstd, const T* dy,
-                                                               const T* dres, T* dx, float* dgamma, float* dbeta,
-                                                               int64_t part_ld) {
-  extern __shared__ __align__(16) float wsm[];  // gamma; then, where a block has several groups, their sums [2][n]
+template <class T, int NP, int kStages, BwdMode kMode>
+__global__ void __launch_bounds__(kOddThreads, 1) norm_bwd_odd_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
+                                                                      Weight gamma, const float* mean,
+                                                                      const float* rstd, const T* dy, const T* dres,
+                                                                      T* dx, float* dgamma, float* dbeta,
+                                                                      int64_t part_ld, float2* sums) {
+  extern __shared__ __align__(16) char stage_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  constexpr int kP = Vec<T, VL>::kPairs;
-  const int n = nm.n;
-  const int lane = threadIdx.x % rs.tpr, group = threadIdx.x / rs.tpr;
-  RowSum sum{rs.tpr, group + 1, red + (rs.tpr > 32 ? group * 2 * RowSum::kRedWords : 0)};
-  const float rn = 1.0f / n;
-  gamma.stage(wsm, n, 1.f);
+  const Slice sl(nm.n);
+  const int n = sl.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr, tensors = kMode != kSums && dres ? 3 : 2;
+  x += sl.first;
+  dy += sl.first;
+  dres += dres ? sl.first : 0;
+  dx += sl.first;
+  const int cap = odd_cap_device(n, sizeof(T));
+  const OddStage<T> st{stage_sm + (size_t)team * kStages * tensors * cap, cap, tensors};
+  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
+  const float rn = 1.0f / nm.n;
+  const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
+  const auto copy_row = [&](int64_t r, int s) {
+    if (r < nm.rows) {
+      st.copy(s, 0, x + r * nm.ldx, n, lane, ss.tpr);
+      st.copy(s, 1, dy + r * nm.ldy, n, lane, ss.tpr);
+      if (tensors == 3) st.copy(s, 2, dres + r * nm.lddres, n, lane, ss.tpr);
+    }
+    async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
+  float2 g[NP][1], dg[NP], db[NP];
+  gamma.load<1>(g, 1.f, [&](int i) { return SlotAt<1>(lane, i, ss.tpr, n).shifted(sl.first); });
+#pragma unroll
+  for (int i = 0; i < NP; ++i) dg[i] = db[i] = both(0.f);
+  const auto stat = [&](const float* p, int64_t r) { return r < nm.rows ? p[r] : 0.f; };
+  float mu = stat(mean, first), rt = stat(rstd, first);
+  int s = 0;
+  for (int64_t r = first; r - team < nm.rows; r += step) {
+    const float mu1 = stat(mean, r + step), rt1 = stat(rstd, r + step);
+    async_wait<kStages - 2>();
+    sum.meet();
+    const bool on = r < nm.rows;
+    const int64_t ra = on ? r : 0;
+    const T *xr = st.row(s, 0, x + ra * nm.ldx), *gr = st.row(s, 1, dy + ra * nm.ldy);
+    float2 h[NP], u[NP], su = both(0.f), sh = both(0.f);
+    if (on)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const SlotAt<1> at(lane, i, ss.tpr, n);
+        if (at.in) {
+          const float2 d = odd_pair(gr, at);
+          h[i] = mul2(add2(odd_pair(xr, at), at.pair(-mu)), both(rt));
+          u[i] = mul2(d, g[i][0]);
+          su = add2(su, u[i]);
+          sh = fma2(u[i], h[i], sh);
+          dg[i] = fma2(d, h[i], dg[i]);
+          db[i] = add2(db[i], d);
+        }
+      }
+    float2 t;
+    const bool more = row_sums<kMode>(sum, make_float2(su.x + su.y, sh.x + sh.y), t, sums, r, on, lane);
+    if (kMode == kApply) sum.meet();  // no sum to meet at: the stage before this one is read by nobody any more
+    copy_row(r + (kStages - 1) * step, s == 0 ? kStages - 1 : s - 1);
+    const float2 na = both(-t.x * rn), nb = both(-t.y * rn);
+    if (on && more) {
+      T* dr = dx + r * nm.lddx;
+      const T* er = tensors == 3 ? st.row(s, 2, dres + r * nm.lddres) : nullptr;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const SlotAt<1> at(lane, i, ss.tpr, n);
+        if (at.in) {
+          const float2 w = fma2(h[i], nb, add2(u[i], na));
+          const float2 o = er ? fma2(w, both(rt), odd_pair(er, at)) : mul2(w, both(rt));
+          dr[at.c] = from_f32<T>(o.x);
+          if (at.hop) dr[at.c + at.hop] = from_f32<T>(o.y);
+        }
+      }
+    }
+    mu = mu1;
+    rt = rt1;
+    s = s == kStages - 1 ? 0 : s + 1;
+  }
+  if (kMode == kSums || (!dgamma && !dbeta)) return;
+  async_wait<0>();
   __syncthreads();
-  float2 dg[NV][kP], db[NV][kP];
+  float* acc = reinterpret_cast<float*>(stage_sm);
+  float *ag = acc + team * 2 * n, *ab = ag + n;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < kP; ++j) dg[i][j] = db[i][j] = both(0.f);
-  for (int64_t st = blockIdx.x; st < rs.steps; st += gridDim.x) {
-    const RowAt row(rs, nm.rows, st, group);
-    const T *xr = x + row.r * nm.ldx, *gr = dy + row.r * nm.ldy, *er = dres + row.r * nm.lddres;
-    Vec<T, VL> xv[NV], gv[NV], ev[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const SlotAt<VL> at(lane, i, rs.tpr, n);
-      if (at.in) {
-        xv[i].load(xr + at.c, at.hop);
-        gv[i].load(gr + at.c, at.hop);
-        if (dres) ev[i].load(er + at.c, at.hop);
-      }
+  for (int i = 0; i < NP; ++i) {
+    const SlotAt<1> at(lane, i, ss.tpr, n);
+    if (at.in) {
+      ag[at.c] = dg[i].x;
+      ab[at.c] = db[i].x;
     }
-    const float mu = mean[row.r], rt = rstd[row.r];
-    float2 su = both(0.f), sh = both(0.f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const SlotAt<VL> at(lane, i, rs.tpr, n);
-      if (at.in) {
-        float2 g[kP];
-        ld_pairs<float, VL>(wsm + at.c, at.hop, g);
-#pragma unroll
-        for (int j = 0; j < kP; ++j) {
-          const float2 d = gv[i].get(j), h = mul2(add2(xv[i].get(j), at.pair(-mu)), both(rt)), u = mul2(d, g[j]);
-          su = add2(su, u);
-          sh = fma2(u, h, sh);
-          if (row.on) {
-            dg[i][j] = fma2(d, h, dg[i][j]);
-            db[i][j] = add2(db[i][j], d);
-          }
-        }
-      }
-    }
-    const float2 s = sum(make_float2(su.x + su.y, sh.x + sh.y));
-    const float2 na = both(-s.x * rn), nb = both(-s.y * rn);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const SlotAt<VL> at(lane, i, rs.tpr, n);
-      if (at.in && row.on) {
-        float2 g[kP];
-        ld_pairs<float, VL>(wsm + at.c, at.hop, g);
-        Vec<T, VL> o;
-#pragma unroll
-        for (int j = 0; j < kP; ++j) {
-          const float2 h = mul2(add2(xv[i].get(j), at.pair(-mu)), both(rt));
-          float2 t = fma2(h, nb, fma2(gv[i].get(j), g[j], na));
-          t = dres ? fma2(t, both(rt), ev[i].get(j)) : mul2(t, both(rt));
-          o.put(j, t);
-        }
-        o.store(dx + row.r * nm.lddx + at.c, at.hop);
-      }
+    if (at.hop) {
+      ag[at.c + at.hop] = dg[i].y;
+      ab[at.c + at.hop] = db[i].y;
     }
   }
-  if (!dgamma && !dbeta) return;
-  float* acc_sm = wsm + n;
-  // the block's groups are added in order, the last one stores
-  for (int k = 0; k < rs.groups; ++k) {
-    if (group == k) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const SlotAt<VL> at(lane, i, rs.tpr, n);
-        if (at.in)
-#pragma unroll
-          for (int j = 0; j < kP; ++j)
-#pragma unroll
-            for (int l = 0; l < 2; ++l) {
-              if (VL == 1 && l == 1 && !at.hop) continue;
-              const int e = VL == 1 ? at.c + l * at.hop : at.c + 2 * j + l;
-              float a = l ? dg[i][j].y : dg[i][j].x, b = l ? db[i][j].y : db[i][j].x;
-              if (k > 0) {
-                a += acc_sm[e];
-                b += acc_sm[n + e];
-              }
-              if (k < rs.groups - 1) {
-                acc_sm[e] = a;
-                acc_sm[n + e] = b;
-              } else {
-                if (dgamma) dgamma[blockIdx.x * part_ld + e] = a;
-                if (dbeta) dbeta[blockIdx.x * part_ld + e] = b;
-              }
-            }
-      }
-    }
-    __syncthreads();
-  }
+  const int64_t at0 = blockIdx.x * part_ld + sl.first;
+  store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at0 : nullptr, dbeta ? dbeta + at0 : nullptr);
 }
 
 // dgamma and dbeta (blockIdx.y) from the blocks' partial rows: 32 columns per block,
@@ -610,45 +736,11 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(moe_lora_no
     }
   }
 }
-template <class T>
-__global__ void __launch_bounds__(kLongThreads) norm_bwd_long_kernel(moe_lora_norm nm, const T* x, Weight gamma,
-                                                                     const float* mean, const float* rstd,
-                                                                     const T* dy, const T* dres, T* dx) {
-  __shared__ float sm[32];
-  const int n = nm.n;
-  for (int64_t r = blockIdx.x; r < nm.rows; r += gridDim.x) {
-    const T *xr = x + r * nm.ldx, *gr = dy + r * nm.ldy;
-    const float mu = mean[r], rs = rstd[r];
-    float a = 0.f, b = 0.f;
-    for (int c = threadIdx.x; c < n; c += blockDim.x) {
-      const float u = to_f32(gr[c]) * gamma.at(c, 1.f);
-      a += u;
-      b += u * ((to_f32(xr[c]) - mu) * rs);
-    }
-    a = block_sum(a, sm) / n;
-    b = block_sum(b, sm) / n;
-    for (int c = threadIdx.x; c < n; c += blockDim.x) {
-      const float u = to_f32(gr[c]) * gamma.at(c, 1.f), h = (to_f32(xr[c]) - mu) * rs;
-      const float d = rs * (u - a - h * b) + (dres ? to_f32(dres[r * nm.lddres + c]) : 0.f);
-      dx[r * nm.lddx + c] = from_f32<T>(d);
-    }
-  }
-}
-template <class T>
-__global__ void __launch_bounds__(256) norm_part_long_kernel(moe_lora_norm nm, const T* x, const float* mean,
-                                                             const float* rstd, const T* dy, float* part) {
-  const int n = nm.n, c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= n) return;
-  const int64_t per = (nm.rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * per;
-  const int64_t r1 = r0 + per < nm.rows ? r0 + per : nm.rows;
-  float dg = 0.f, db = 0.f;
-  for (int64_t r = r0; r < r1; ++r) {
-    const float d = to_f32(dy[r * nm.ldy + c]);
-    dg += d * ((to_f32(x[r * nm.ldx + c]) - mean[r]) * rstd[r]);
-    db += d;
-  }
-  part[(int64_t)blockIdx.y * 2 * n + c] = dg;
-  part[(int64_t)blockIdx.y * 2 * n + n + c] = db;
+// Scratch of the backward: partial rows of the weight gradients, then the slices' row
+// sums (wide rows).
+size_t part_bytes(const moe_lora_norm& nm) { return (size_t)kNormParts * 2 * nm.n * sizeof(float); }
+size_t sums_bytes(const moe_lora_norm& nm) {
+  return nm.n > kBwdSlice ? sizeof(float2) * (size_t)nm.rows * ((nm.n + kBwdSlice - 1) / kBwdSlice) : 0;
 }
 
 int check_ld(int64_t* ld, int n) {
@@ -710,6 +802,8 @@ int launch_fwd(const FwdArgs& a, const RowShape& rs) {
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
+constexpr size_t kMaxSmem = 216 * 1024;  // dynamic, beside the kernels' static 8 KB
+
 // Stages of the rings: three rows of copies under way per team (two in fp32), 96 KB per SM
 // at full width; an SM needs about 45 KB to hide the memory's latency.
 template <class T>
@@ -751,6 +845,34 @@ int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss) {
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
+int slices_of(int n) { return (n + kBwdSlice - 1) / kBwdSlice; }
+
+// Shared memory of the staged kernels: as many teams as fit.
+template <class T>
+size_t odd_shape(StreamShape* ss, int n, int columns, int stages, int tensors) {
+  ss->tpr = row_threads((n + 1) / 2, columns / 2);
+  const size_t team = (size_t)stages * tensors * odd_cap(n, sizeof(T));
+  const int fit = (int)(kMaxSmem / team), unit = ss->tpr < 32 ? 32 / ss->tpr : 1;
+  ss->teams = std::max(unit, std::min(kOddThreads / ss->tpr, fit) / unit * unit);
+  return team * ss->teams;
+}
+
+template <class T>
+int launch_fwd_odd(const FwdArgs& a) {
+  constexpr int kS = sizeof(T) == 2 ? 4 : 3;
+  const auto kernel = norm_fwd_odd_kernel<T, kOddFwdColumns / 2, kS>;
+  StreamShape ss;
+  const size_t smem = odd_shape<T>(&ss, a.nm.n, kOddFwdColumns, kS, 1);
+  if (smem > 32 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_LORA_ERR_CUDA;
+  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), a.sms);
+  prof_begin(K_NORM_FWD, a.s);
+  kernel<<<grid, ss.tpr * ss.teams, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd);
+  prof_end(K_NORM_FWD, a.s);
+  return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+}
+
 template <class T, int VL>
 int pick_fwd(const FwdArgs& a) {
   const int slots = (int)ceil_div(a.nm.n, VL == 1 ? 2 : VL);
@@ -774,6 +896,8 @@ int pick_fwd(const FwdArgs& a) {
              : nv == 2      ? launch_fwd_stream<T, 2>(a, ss)
                             : launch_fwd_stream<T, 1>(a, ss);
   }
+  if constexpr (VL == 1)
+    if (a.nm.n <= kOddThreads * kOddFwdColumns && a.nm.rows >= kOddRows) return launch_fwd_odd<T>(a);
   // few rows want many threads
   int nv = 16;
   while (nv > 1 && (slots <= 8 * (nv / 2) || (a.nm.rows * ceil_div(slots, nv) < 512LL * a.sms &&
@@ -820,104 +944,78 @@ struct BwdArgs {
   const void *dy, *dres;
   void* dx;
   float *dgamma, *dbeta, *part;
+  float2* sums;
   int sms;
   cudaStream_t s;
 };
 
-// Where a backward kernel of `grid` blocks leaves its sums: in the outputs, or as partial
-// rows for the kernel that adds them.
-struct WgradTo {
-  float *dgamma, *dbeta;
-  bool parts;
-  WgradTo(const BwdArgs& a, int grid) {
-    parts = (a.dgamma || a.dbeta) && grid > 1;
-    dgamma = parts ? a.part : a.dgamma;
-    dbeta = parts ? a.part + a.nm.n : a.dbeta;
-  }
-};
-int finish_bwd(const BwdArgs& a, const WgradTo& to, int grid) {
-  if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
-  return to.parts ? launch_wgrad(a.nm.n, grid, a.part, a.dgamma, a.dbeta, a.s) : MOE_LORA_OK;
-}
-
-template <class T, int NV>
-int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss) {
-  const auto kernel = norm_bwd_stream_kernel<T, NV, bwd_stages<T>()>;
-  const int threads = ss.tpr * ss.teams;
-  const size_t ring = ring_bytes<bwd_stages<T>(), 3 * NV>(threads), sums = 2 * sizeof(float) * (size_t)a.nm.n;
-  const size_t smem = std::max(ring, sums);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_LORA_ERR_CUDA;
-  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), std::min(a.sms, kNormParts));
-  const WgradTo to(a, grid);
-  prof_begin(K_NORM_BWD, a.s);
-  kernel<<<grid, threads, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.mean, a.rstd, (const T*)a.dy,
-                                       (const T*)a.dres, (T*)a.dx, to.dgamma, to.dbeta, 2LL * a.nm.n);
-  prof_end(K_NORM_BWD, a.s);
-  return finish_bwd(a, to, grid);
-}
-
-template <class T, int NV, int kThreads>
-int launch_bwd_odd(const BwdArgs& a, const RowShape& rs) {
-  const auto kernel = norm_bwd_kernel<T, 1, NV, kThreads>;
-  const int64_t n = a.nm.n;
-  const int grid = (int)std::min<int64_t>(rs.steps, std::min(a.sms, kNormParts));
-  const WgradTo to(a, grid);
-  const size_t smem = sizeof(float) * n * (to.dgamma || to.dbeta ? 3 : 1);
-  if (smem > 40 * 1024 &&
+// One kernel over all rows (of one slice, or of every slice).
+template <class T, BwdMode kMode, class Kernel>
+int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t smem, bool* parts, int* blocks) {
+  const int slices = slices_of(a.nm.n);
+  const int most = std::max(1, std::min(a.sms, kNormParts) / slices);
+  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), most);
+  const bool wgrad = kMode != kSums && (a.dgamma || a.dbeta);
+  *parts = wgrad && grid > 1;
+  *blocks = grid;
+  float* dg = !wgrad ? nullptr : *parts ? a.part : a.dgamma;
+  float* db = !wgrad ? nullptr : *parts ? a.part + a.nm.n : a.dbeta;
+  smem = std::max(smem, wgrad ? 2 * sizeof(float) * ss.teams * std::min(a.nm.n, kBwdSlice) : 0);
+  if (smem > 32 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_LORA_ERR_CUDA;
   prof_begin(K_NORM_BWD, a.s);
-  kernel<<<grid, rs.threads, smem, a.s>>>(a.nm, rs, (const T*)a.x, a.gamma, a.mean, a.rstd, (const T*)a.dy,
-                                          (const T*)a.dres, (T*)a.dx, to.dgamma, to.dbeta, 2 * n);
-  prof_end(K_NORM_BWD, a.s);
-  return finish_bwd(a, to, grid);
-}
-
-template <class T>
-int launch_bwd_long(const BwdArgs& a) {
-  if (a.dgamma || a.dbeta) {  // before dx, which may overwrite dy
-    prof_begin(K_NORM_WGRAD, a.s);
-    norm_part_long_kernel<T><<<dim3((unsigned)ceil_div(a.nm.n, 256), kNormParts), 256, 0, a.s>>>(
-        a.nm, (const T*)a.x, a.mean, a.rstd, (const T*)a.dy, a.part);
-    prof_end(K_NORM_WGRAD, a.s);
-    if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
-    const int rc = launch_wgrad(a.nm.n, kNormParts, a.part, a.dgamma, a.dbeta, a.s);
-    if (rc) return rc;
-  }
-  const int grid = (int)std::min<int64_t>(a.nm.rows, 4LL * a.sms);
-  prof_begin(K_NORM_BWD, a.s);
-  norm_bwd_long_kernel<T><<<grid, kLongThreads, 0, a.s>>>(a.nm, (const T*)a.x, a.gamma, a.mean, a.rstd,
-                                                            (const T*)a.dy, (const T*)a.dres, (T*)a.dx);
+  kernel<<<dim3(grid, slices), ss.tpr * ss.teams, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.mean, a.rstd,
+                                                              (const T*)a.dy, (const T*)a.dres, (T*)a.dx, dg, db,
+                                                              2LL * a.nm.n, a.sums);
   prof_end(K_NORM_BWD, a.s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+}
+
+// kKernel<mode> for rows of one slice, or sums first and then the rest.
+#define BWD_MODES(KERNEL, SMEM)                                                                      \
+  do {                                                                                               \
+    if (slices_of(a.nm.n) == 1) return launch_bwd<T, kWhole>(a, KERNEL(kWhole), ss, SMEM, parts, blocks); \
+    const int rc = launch_bwd<T, kSums>(a, KERNEL(kSums), ss, SMEM, parts, blocks);                  \
+    return rc ? rc : launch_bwd<T, kApply>(a, KERNEL(kApply), ss, SMEM, parts, blocks);              \
+  } while (0)
+
+template <class T, int NV>
+int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, bool* parts, int* blocks) {
+  constexpr int kS = bwd_stages<T>();
+#define KERNEL(MODE) norm_bwd_stream_kernel<T, NV, kS, MODE>
+  BWD_MODES(KERNEL, (ring_bytes<kS, 3 * NV>(ss.tpr * ss.teams)));
+#undef KERNEL
+}
+
+template <class T, int kS>
+int launch_bwd_odd(const BwdArgs& a, bool* parts, int* blocks) {
+  constexpr int kNP = kBwdColumns / 2;
+  StreamShape ss;
+  const size_t smem = odd_shape<T>(&ss, std::min(a.nm.n, kBwdSlice), kBwdColumns, kS, a.dres ? 3 : 2);
+#define KERNEL(MODE) norm_bwd_odd_kernel<T, kNP, kS, MODE>
+  BWD_MODES(KERNEL, smem);
+#undef KERNEL
 }
 
 template <class T>
 int run_bwd(const BwdArgs& a) {
   const int n = a.nm.n;
+  bool parts = false;
+  int blocks = 0, rc;
   if (rows_aligned(a.nm, true, a.dres != nullptr)) {
     constexpr int VL = 16 / sizeof(T), kNV = kBwdColumns / VL;
-    const int slots = n / VL;
-    if (slots > kBwdStreamThreads * kNV) return launch_bwd_long<T>(a);
     const int nvs[] = {kNV, kNV / 2, 1};
     int nv;
-    const StreamShape ss = stream_shape(slots, nvs, kBwdStreamThreads, &nv);
-    return nv == kNV       ? launch_bwd_stream<T, kNV>(a, ss)
-           : nv == kNV / 2 ? launch_bwd_stream<T, kNV / 2>(a, ss)
-                           : launch_bwd_stream<T, 1>(a, ss);
+    const StreamShape ss = stream_shape(std::min(n, kBwdSlice) / VL, nvs, kBwdStreamThreads, &nv);
+    rc = nv == kNV       ? launch_bwd_stream<T, kNV>(a, ss, &parts, &blocks)
+         : nv == kNV / 2 ? launch_bwd_stream<T, kNV / 2>(a, ss, &parts, &blocks)
+                         : launch_bwd_stream<T, 1>(a, ss, &parts, &blocks);
+  } else {
+    // three stages of the widest slice of fp32 rows are more than shared memory holds
+    rc = sizeof(T) == 4 && n > 4096 ? launch_bwd_odd<T, 2>(a, &parts, &blocks) : launch_bwd_odd<T, 3>(a, &parts, &blocks);
   }
-  constexpr int kNV = 8;  // two columns each
-  const int slots = (n + 1) / 2;
-  if (slots > 1024 * kNV) return launch_bwd_long<T>(a);
-  const int tpr = row_threads(slots, kNV);
-  // groups that share a block share its partial row; but every SM gets rows first
-  int groups = std::max(1, kBwdThreads / tpr);
-  while (groups > std::max(1, 32 / tpr) && ceil_div(a.nm.rows, groups) < a.sms) groups = (groups + 1) / 2;
-  if (tpr < 32) groups = (int)ceil_div(groups, 32 / tpr) * (32 / tpr);
-  if (tpr > 32) groups = std::min(groups, kMaxTeams);
-  const RowShape rs = row_shape(a.nm.rows, tpr, groups);
-  return tpr > kBwdThreads ? launch_bwd_odd<T, kNV, 1024>(a, rs) : launch_bwd_odd<T, kNV, kBwdThreads>(a, rs);
+  return rc || !parts ? rc : launch_wgrad(n, blocks, a.part, a.dgamma, a.dbeta, a.s);
 }
 
 // CALL<T>(args) for the element type of nm.
@@ -953,7 +1051,7 @@ int moe_lora_layernorm_forward(const moe_lora_norm* in, const void* x, const voi
 
 size_t moe_lora_layernorm_scratch_bytes(const moe_lora_norm* in) {
   moe_lora_norm nm;
-  return check_norm(in, &nm) ? 0 : (size_t)kNormParts * 2 * nm.n * sizeof(float);
+  return check_norm(in, &nm) ? 0 : part_bytes(nm) + sums_bytes(nm);
 }
 
 int moe_lora_layernorm_backward(const moe_lora_norm* in, const void* x, const void* gamma, const float* mean,
@@ -965,7 +1063,7 @@ int moe_lora_layernorm_backward(const moe_lora_norm* in, const void* x, const vo
   if ((rc = check_opt(gamma)) || (rc = check_opt(dres)) || (rc = check_opt(dgamma)) || (rc = check_opt(dbeta)))
     return rc;
   const bool wgrad = dgamma || dbeta;
-  if (wgrad) {
+  if (wgrad || (nm.n > kBwdSlice && nm.rows > 0)) {
     if ((rc = check_ptr(scratch))) return rc;
     if (scratch_bytes < moe_lora_layernorm_scratch_bytes(in)) return MOE_LORA_ERR_WORKSPACE;
   }
@@ -982,8 +1080,9 @@ int moe_lora_layernorm_backward(const moe_lora_norm* in, const void* x, const vo
       (rc = check_ptr(dx)))
     return rc;
   if ((rc = device_sms(&sms))) return rc;
-  const BwdArgs a{nm, x, {gamma, nm.wdtype}, mean, rstd, dy, dres, dx, dgamma, dbeta, static_cast<float*>(scratch), sms,
-                  static_cast<cudaStream_t>(stream)};
+  const BwdArgs a{nm,     x,     {gamma, nm.wdtype}, mean, rstd, dy, dres, dx, dgamma, dbeta,
+                  static_cast<float*>(scratch), reinterpret_cast<float2*>(static_cast<char*>(scratch) + part_bytes(nm)),
+                  sms,    static_cast<cudaStream_t>(stream)};
   return NORM_DISPATCH(run_bwd, a);
 }
 
