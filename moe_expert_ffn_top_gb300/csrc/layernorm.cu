@@ -131,6 +131,34 @@ struct Weight {
       load_as<__half, VL>(f, place);
     }
   }
+  // N vectors of 2 kP elements from any column, element by element; columns outside [0, n)
+  // give some weight.
+  template <class W, int N, int kP, class Col>
+  __device__ __forceinline__ void load_any_as(float2 (&f)[N][kP], int first, int n, const Col& col) const {
+    const W* w = static_cast<const W*>(p) + first;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        const int c = col(i) + 2 * j;
+        f[i][j] = make_float2(to_f32(w[min(max(c, 0), n - 1)]), to_f32(w[min(max(c + 1, 0), n - 1)]));
+      }
+  }
+  template <int N, int kP, class Col>
+  __device__ __forceinline__ void load_any(float2 (&f)[N][kP], float none, int first, int n, const Col& col) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < kP; ++j) f[i][j] = both(none);
+    } else if (dtype == MOE_LORA_F32) {
+      load_any_as<float>(f, first, n, col);
+    } else if (dtype == MOE_LORA_BF16) {
+      load_any_as<__nv_bfloat16>(f, first, n, col);
+    } else {
+      load_any_as<__half>(f, first, n, col);
+    }
+  }
   __device__ __forceinline__ float at(int64_t c, float none) const {
     return !p                        ? none
            : dtype == MOE_LORA_F32  ? static_cast<const float*>(p)[c]
@@ -221,26 +249,73 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
 // us against 179 us, and 253 us at 16).  Backward: 16 columns and their two sums.
 constexpr int kFwdStreamThreads = 256, kFwdColumns = 64;
 constexpr int kBwdStreamThreads = 512, kBwdColumns = 16;
-constexpr int kOddThreads = 512, kOddFwdColumns = 32;
-constexpr int kOddRows = 256;  // from here on the staged forward
+constexpr int kOddThreads = 512;
+constexpr int kShiftRows = 256;  // from here on the streamed forward of shifted rows
 struct StreamShape {
   int tpr, teams;
 };
 
+// How rows lie on the 16-byte grid: they fill every slot of every thread (no bounds
+// checks); they are whole vectors; or (kShift) they begin and end anywhere.  A shifted row
+// is taken in the aligned vectors that cover it, so that its first column is `shift`
+// elements into the first vector (what lies before it belongs to the row before: the
+// tensor itself starts aligned).  shift = r * ld mod VL depends on the row; the grid is
+// such that all rows of a team have the same, which keeps a thread's columns, its weights
+// and its sums in place.
+enum RowFit { kFull, kPart, kShift };
 // What a thread knows of its columns: slot i starts at column c0 + i * dc, `nv` slots lie
-// inside the row (kFull kernels: all of them do, for every thread).
+// (in part) inside the row.
+template <RowFit kFit>
 struct Columns {
-  int c0, dc, nv;
-  __device__ __forceinline__ Columns(int lane, int tpr, int n, int vl) {
-    c0 = lane * vl;
+  int c0, dc, nv, n;
+  __device__ __forceinline__ Columns(int lane, int tpr, int n, int vl, int shift) : n(n) {
+    c0 = lane * vl - (kFit == kShift ? shift : 0);
     dc = tpr * vl;
     nv = c0 < n ? (n - c0 + dc - 1) / dc : 0;
   }
-  __device__ __forceinline__ bool in(int i) const { return i < nv; }
+  __device__ __forceinline__ bool in(int i) const { return kFit == kFull || i < nv; }
   __device__ __forceinline__ int col(int i) const { return c0 + i * dc; }
+  template <int kP>
+  __device__ __forceinline__ bool edge(int i) const {
+    return kFit == kShift && (col(i) < 0 || col(i) + 2 * kP > n);
+  }
+  // 0 for what is not the row's
+  template <int kP>
+  __device__ __forceinline__ void clip(int i, float2 (&v)[kP]) const {
+    if (kFit != kShift || !edge<kP>(i)) return;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      if ((unsigned)(col(i) + 2 * j) >= (unsigned)n) v[j].x = 0.f;
+      if ((unsigned)(col(i) + 2 * j + 1) >= (unsigned)n) v[j].y = 0.f;
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void copy(uint4* slot, const T* row, int i) const {
+    if (kFit == kShift)
+      async_copy16_part(slot, row + col(i), min(16, (n - col(i)) * (int)sizeof(T)));
+    else
+      async_copy16(slot, row + col(i));
+  }
+  // a slot's results; `fits`: the output's rows lie on the grid as the input's do
+  template <class T, int VL, int kP>
+  __device__ __forceinline__ void store(T* row, int i, const float2 (&v)[kP], bool fits) const {
+    if (kFit != kShift || (fits && !edge<kP>(i))) {
+      Vec<T, VL> o;
+#pragma unroll
+      for (int j = 0; j < kP; ++j) o.put(j, v[j]);
+      o.store(row + col(i), 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        const int c = col(i) + 2 * j;
+        if ((unsigned)c < (unsigned)n) row[c] = from_f32<T>(v[j].x);
+        if ((unsigned)(c + 1) < (unsigned)n) row[c + 1] = from_f32<T>(v[j].y);
+      }
+    }
+  }
 };
 
-template <class T, int NV, int kStages, bool kFull>
+template <class T, int NV, int kStages, RowFit kFit>
 __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
                                                                             Weight gamma, Weight beta, T* y,
                                                                             float* mean, float* rstd) {
@@ -250,26 +325,32 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
   const int n = nm.n;
   const Ring<kStages, NV> ring(ring_sm);
   const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
-  const Columns cl(lane, ss.tpr, n, VL);
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / n;
-  const int64_t step = (int64_t)gridDim.x * ss.teams;
+  const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
+  const Columns<kFit> cl(lane, ss.tpr, n, VL, (int)(first * nm.ldx & (VL - 1)));
+  const bool y_fits = ((nm.ldx ^ nm.ldy) & (VL - 1)) == 0;
   const auto copy_row = [&](int64_t r, int s) {
     if (r < nm.rows) {
       const T* xr = x + r * nm.ldx;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (kFull || cl.in(i)) async_copy16(ring.slot(s, i), xr + cl.col(i));
+        if (cl.in(i)) cl.copy(ring.slot(s, i), xr, i);
     }
     async_commit();
   };
-  const int64_t first = blockIdx.x * (int64_t)ss.teams + team;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
   float2 g[NV][kP], b[NV][kP];
-  const auto place = [&](int i) { return SlotAt<VL>(lane, i, ss.tpr, n); };
-  gamma.load<VL>(g, 1.f, place);
-  beta.load<VL>(b, 0.f, place);
+  if (kFit == kShift) {
+    const auto col = [&](int i) { return cl.col(i); };
+    gamma.load_any(g, 1.f, 0, n, col);
+    beta.load_any(b, 0.f, 0, n, col);
+  } else {
+    const auto place = [&](int i) { return SlotAt<VL>(lane, i, ss.tpr, n); };
+    gamma.load<VL>(g, 1.f, place);
+    beta.load<VL>(b, 0.f, place);
+  }
   int s = 0;
   // all teams of the block leave together: one without a row works on what its slots hold
   for (int64_t r = first; r - team < nm.rows; r += step) {
@@ -279,37 +360,38 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
     float2 t[2] = {both(0.f), both(0.f)};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (kFull || cl.in(i)) {
+      if (cl.in(i)) {
         Vec<T, VL> w;
         w.from_smem(ring.slot(s, i));
 #pragma unroll
-        for (int j = 0; j < kP; ++j) {
-          v[i][j] = w.get(j);
-          t[j & 1] = add2(t[j & 1], v[i][j]);
-        }
+        for (int j = 0; j < kP; ++j) v[i][j] = w.get(j);
+        cl.clip(i, v[i]);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) t[j & 1] = add2(t[j & 1], v[i][j]);
       }
     t[0] = add2(t[0], t[1]);
     const float mu = sum(t[0].x + t[0].y) * rn;
     t[0] = t[1] = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (kFull || cl.in(i))
+      if (cl.in(i)) {
 #pragma unroll
-        for (int j = 0; j < kP; ++j) {
-          v[i][j] = add2(v[i][j], both(-mu));
-          t[j & 1] = fma2(v[i][j], v[i][j], t[j & 1]);
-        }
+        for (int j = 0; j < kP; ++j) v[i][j] = add2(v[i][j], both(-mu));
+        cl.clip(i, v[i]);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) t[j & 1] = fma2(v[i][j], v[i][j], t[j & 1]);
+      }
     t[0] = add2(t[0], t[1]);
     const float rt = rsqrtf(sum(t[0].x + t[0].y) * rn + nm.eps);
     if (r < nm.rows) {
       T* yr = y + r * nm.ldy;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (kFull || cl.in(i)) {
-          Vec<T, VL> o;
+        if (cl.in(i)) {
+          float2 o[kP];
 #pragma unroll
-          for (int j = 0; j < kP; ++j) o.put(j, fma2(mul2(v[i][j], both(rt)), g[i][j], b[i][j]));
-          o.store(yr + cl.col(i), 0);
+          for (int j = 0; j < kP; ++j) o[j] = fma2(mul2(v[i][j], both(rt)), g[i][j], b[i][j]);
+          cl.template store<T, VL>(yr, i, o, y_fits);
         }
       if (mean && lane == 0) {
         mean[r] = mu;
@@ -329,10 +411,12 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
 // leaves every slice's part of a row's sums in `sums` [rows][slices], kApply adds them.
 enum BwdMode { kWhole, kSums, kApply };
 constexpr int kBwdSlice = kBwdStreamThreads * kBwdColumns;
-// Slice blockIdx.y of a row of n.
+// Slice blockIdx.y of a row of n (of one slice, kWhole).
+template <BwdMode kMode>
 struct Slice {
   int first, n;
-  __device__ __forceinline__ explicit Slice(int all) : first(blockIdx.y * kBwdSlice), n(min(kBwdSlice, all - first)) {}
+  __device__ __forceinline__ explicit Slice(int all)
+      : first(kMode == kWhole ? 0 : blockIdx.y * kBwdSlice), n(kMode == kWhole ? all : min(kBwdSlice, all - first)) {}
 };
 // A row's two sums over all slices, from this slice's; false: the row is done (kSums).
 template <BwdMode kMode, class Sum>
@@ -363,7 +447,7 @@ __device__ __forceinline__ void store_wgrad(const float* acc, int teams, int n, 
   }
 }
 
-template <class T, int NV, int kStages, BwdMode kMode>
+template <class T, int NV, int kStages, BwdMode kMode, RowFit kFit>
 __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
                                                                             Weight gamma, const float* mean,
                                                                             const float* rstd, const T* dy,
@@ -373,36 +457,41 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const Slice sl(nm.n);
+  const Slice<kMode> sl(nm.n);
   const int n = sl.n;
-  x += sl.first;
-  dy += sl.first;
-  dres += dres ? sl.first : 0;
-  dx += sl.first;
+  if (kMode != kWhole) {
+    x += sl.first;
+    dy += sl.first;
+    dres += dres ? sl.first : 0;
+    dx += sl.first;
+  }
   const Ring<kStages, 3 * NV> ring(ring_sm);
   const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
-  const Columns cl(lane, ss.tpr, n, VL);
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / nm.n;
-  const int64_t step = (int64_t)gridDim.x * ss.teams;
+  const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
+  const Columns<kFit> cl(lane, ss.tpr, n, VL, (int)(first * nm.ldx & (VL - 1)));
+  const bool dx_fits = ((nm.ldx ^ nm.lddx) & (VL - 1)) == 0;
   const auto copy_row = [&](int64_t r, int s) {
     if (r < nm.rows) {
       const T *xr = x + r * nm.ldx, *gr = dy + r * nm.ldy, *er = dres + r * nm.lddres;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (cl.in(i)) {
-          async_copy16(ring.slot(s, i), xr + cl.col(i));
-          async_copy16(ring.slot(s, NV + i), gr + cl.col(i));
-          if (kMode != kSums && dres) async_copy16(ring.slot(s, 2 * NV + i), er + cl.col(i));
+          cl.copy(ring.slot(s, i), xr, i);
+          cl.copy(ring.slot(s, NV + i), gr, i);
+          if (kMode != kSums && dres) cl.copy(ring.slot(s, 2 * NV + i), er, i);
         }
     }
     async_commit();
   };
-  const int64_t first = blockIdx.x * (int64_t)ss.teams + team;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
   float2 g[NV][kP], dg[NV][kP], db[NV][kP];
-  gamma.load<VL>(g, 1.f, [&](int i) { return SlotAt<VL>(lane, i, ss.tpr, n).shifted(sl.first); });
+  if (kFit == kShift)
+    gamma.load_any(g, 1.f, sl.first, n, [&](int i) { return cl.col(i); });
+  else
+    gamma.load<VL>(g, 1.f, [&](int i) { return SlotAt<VL>(lane, i, ss.tpr, n).shifted(sl.first); });
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -424,15 +513,21 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
           Vec<T, VL> xv, gv;
           xv.from_smem(ring.slot(s, i));
           gv.from_smem(ring.slot(s, NV + i));
+          float2 d[kP];
 #pragma unroll
           for (int j = 0; j < kP; ++j) {
-            const float2 d = gv.get(j);
+            d[j] = gv.get(j);
             h[i][j] = mul2(add2(xv.get(j), both(-mu)), both(rt));
-            u[i][j] = mul2(d, g[i][j]);
+          }
+          cl.clip(i, d);
+          cl.clip(i, h[i]);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) {
+            u[i][j] = mul2(d[j], g[i][j]);
             su = add2(su, u[i][j]);
             sh = fma2(u[i][j], h[i][j], sh);
-            dg[i][j] = fma2(d, h[i][j], dg[i][j]);
-            db[i][j] = add2(db[i][j], d);
+            dg[i][j] = fma2(d[j], h[i][j], dg[i][j]);
+            db[i][j] = add2(db[i][j], d[j]);
           }
         }
     float2 t;
@@ -443,14 +538,15 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (cl.in(i)) {
-          Vec<T, VL> o, ev;
+          Vec<T, VL> ev;
+          float2 o[kP];
           if (dres) ev.from_smem(ring.slot(s, 2 * NV + i));
 #pragma unroll
           for (int j = 0; j < kP; ++j) {
             const float2 w = fma2(h[i][j], nb, add2(u[i][j], na));
-            o.put(j, dres ? fma2(w, both(rt), ev.get(j)) : mul2(w, both(rt)));
+            o[j] = dres ? fma2(w, both(rt), ev.get(j)) : mul2(w, both(rt));
           }
-          o.store(dr + cl.col(i), 0);
+          cl.template store<T, VL>(dr, i, o, dx_fits);
         }
     }
     mu = mu1;
@@ -468,6 +564,17 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
 #pragma unroll
       for (int j = 0; j < kP; j += 2) {
         const int e = cl.col(i) + 2 * j;
+        if (kFit == kShift) {  // the columns of the row, one by one
+          const float vg[4] = {dg[i][j].x, dg[i][j].y, dg[i][j + 1].x, dg[i][j + 1].y};
+          const float vb[4] = {db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y};
+#pragma unroll
+          for (int l = 0; l < 4; ++l)
+            if ((unsigned)(e + l) < (unsigned)n) {
+              ag[e + l] = vg[l];
+              ab[e + l] = vb[l];
+            }
+          continue;
+        }
         *reinterpret_cast<float4*>(ag + e) = make_float4(dg[i][j].x, dg[i][j].y, dg[i][j + 1].x, dg[i][j + 1].y);
         *reinterpret_cast<float4*>(ab + e) = make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
       }
@@ -475,8 +582,8 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
   store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at : nullptr, dbeta ? dbeta + at : nullptr);
 }
 
-// Rows that 16-byte vectors do not fit (a length, stride or type off the 16-byte grid).  A
-// team copies the aligned 16-byte pieces that cover a row, what lies before its start in
+// The backward where the tensors' rows lie on the 16-byte grid in different ways, or wide
+// rows off it.  A team copies the aligned 16-byte pieces that cover a row, what lies before its start in
 // the first piece included (never before the tensor's: that start is aligned), nothing
 // past its end; then every thread reads its elements, tpr columns apart.  Pieces are read
 // by other threads than copied them, so a team meets when a row has come, and a stage is
@@ -504,75 +611,6 @@ __device__ __forceinline__ float2 odd_pair(const T* row, const SlotAt<1>& at) {
   return make_float2(to_f32(row[at.c]), at.hop ? to_f32(row[at.c + at.hop]) : 0.f);
 }
 
-template <class T, int NP, int kStages>
-__global__ void __launch_bounds__(kOddThreads, 1) norm_fwd_odd_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
-                                                                      Weight gamma, Weight beta, T* y, float* mean,
-                                                                      float* rstd) {
-  extern __shared__ __align__(16) char stage_sm[];
-  __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const int n = nm.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
-  const int cap = odd_cap_device(n, sizeof(T));
-  const OddStage<T> st{stage_sm + (size_t)team * kStages * cap, cap, 1};
-  RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
-  const float rn = 1.0f / n;
-  const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
-  const auto copy_row = [&](int64_t r, int s) {
-    if (r < nm.rows) st.copy(s, 0, x + r * nm.ldx, n, lane, ss.tpr);
-    async_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) copy_row(first + s * step, s);
-  float2 g[NP][1], b[NP][1];
-  const auto place = [&](int i) { return SlotAt<1>(lane, i, ss.tpr, n); };
-  gamma.load<1>(g, 1.f, place);
-  beta.load<1>(b, 0.f, place);
-  int s = 0;
-  for (int64_t r = first; r - team < nm.rows; r += step) {
-    async_wait<kStages - 2>();
-    sum.meet();
-    const bool on = r < nm.rows;
-    const T* row = st.row(s, 0, x + (on ? r : 0) * nm.ldx);
-    float2 v[NP], t = both(0.f);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const SlotAt<1> at(lane, i, ss.tpr, n);
-      if (at.in) {
-        v[i] = odd_pair(row, at);
-        t = add2(t, v[i]);
-      }
-    }
-    const float mu = sum(t.x + t.y) * rn;
-    copy_row(r + (kStages - 1) * step, s == 0 ? kStages - 1 : s - 1);
-    t = both(0.f);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const SlotAt<1> at(lane, i, ss.tpr, n);
-      if (at.in) {
-        v[i] = add2(v[i], at.pair(-mu));
-        t = fma2(v[i], v[i], t);
-      }
-    }
-    const float rt = rsqrtf(sum(t.x + t.y) * rn + nm.eps);
-    if (on) {
-      T* yr = y + r * nm.ldy;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const SlotAt<1> at(lane, i, ss.tpr, n);
-        if (at.in) {
-          const float2 o = fma2(mul2(v[i], both(rt)), g[i][0], b[i][0]);
-          yr[at.c] = from_f32<T>(o.x);
-          if (at.hop) yr[at.c + at.hop] = from_f32<T>(o.y);
-        }
-      }
-      if (mean && lane == 0) {
-        mean[r] = mu;
-        rstd[r] = rt;
-      }
-    }
-    s = s == kStages - 1 ? 0 : s + 1;
-  }
-}
-
 template <class T, int NP, int kStages, BwdMode kMode>
 __global__ void __launch_bounds__(kOddThreads, 1) norm_bwd_odd_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
                                                                       Weight gamma, const float* mean,
@@ -581,12 +619,14 @@ __global__ void __launch_bounds__(kOddThreads, 1) norm_bwd_odd_kernel(moe_lora_n
                                                                       int64_t part_ld, float2* sums) {
   extern __shared__ __align__(16) char stage_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const Slice sl(nm.n);
+  const Slice<kMode> sl(nm.n);
   const int n = sl.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr, tensors = kMode != kSums && dres ? 3 : 2;
-  x += sl.first;
-  dy += sl.first;
-  dres += dres ? sl.first : 0;
-  dx += sl.first;
+  if (kMode != kWhole) {
+    x += sl.first;
+    dy += sl.first;
+    dres += dres ? sl.first : 0;
+    dx += sl.first;
+  }
   const int cap = odd_cap_device(n, sizeof(T));
   const OddStage<T> st{stage_sm + (size_t)team * kStages * tensors * cap, cap, tensors};
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
@@ -809,7 +849,7 @@ constexpr size_t kMaxSmem = 216 * 1024;  // dynamic, beside the kernels' static 
 template <class T>
 constexpr int fwd_stages() { return sizeof(T) == 2 ? 4 : 3; }
 template <class T>
-constexpr int bwd_stages() { return sizeof(T) == 2 ? 4 : 2; }
+constexpr int bwd_stages() { return sizeof(T) == 2 ? 3 : 2; }
 
 // Slots per thread (one of `nvs`, descending) and threads of a row: the most slots that
 // every thread fills completely (no bounds checks), else the fewest threads.
@@ -829,16 +869,26 @@ StreamShape stream_shape(int slots, const int (&nvs)[N], int threads, int* nv) {
   return ss;
 }
 
+// Blocks of a streamed kernel: rows whose vectors are shifted need teams that step by a
+// multiple of VL rows, unless no team has a second row.
+int stream_grid(int64_t rows, int teams, int most, bool shift) {
+  int64_t grid = ceil_div(rows, teams);
+  if (grid <= most) return (int)grid;
+  return shift ? most / 8 * 8 : most;
+}
+
 template <class T, int NV>
-int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss) {
-  const bool full = a.nm.n == ss.tpr * NV * 16 / (int)sizeof(T);
-  const auto kernel = full ? norm_fwd_stream_kernel<T, NV, fwd_stages<T>(), true>
-                           : norm_fwd_stream_kernel<T, NV, fwd_stages<T>(), false>;
+int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss, bool shift) {
+  const bool full = !shift && a.nm.n == ss.tpr * NV * 16 / (int)sizeof(T);
+  constexpr int kS = fwd_stages<T>();
+  const auto kernel = full    ? norm_fwd_stream_kernel<T, NV, kS, kFull>
+                      : shift ? norm_fwd_stream_kernel<T, NV, kS, kShift>
+                              : norm_fwd_stream_kernel<T, NV, kS, kPart>;
   const int threads = ss.tpr * ss.teams;
   const size_t smem = ring_bytes<fwd_stages<T>(), NV>(threads);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_LORA_ERR_CUDA;
-  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), a.sms);
+  const int grid = stream_grid(a.nm.rows, ss.teams, a.sms, shift);
   prof_begin(K_NORM_FWD, a.s);
   kernel<<<grid, threads, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd);
   prof_end(K_NORM_FWD, a.s);
@@ -857,20 +907,24 @@ size_t odd_shape(StreamShape* ss, int n, int columns, int stages, int tensors) {
   return team * ss->teams;
 }
 
+// The streamed forward, where a row fits a block and the rows are enough; false: not.
 template <class T>
-int launch_fwd_odd(const FwdArgs& a) {
-  constexpr int kS = sizeof(T) == 2 ? 4 : 3;
-  const auto kernel = norm_fwd_odd_kernel<T, kOddFwdColumns / 2, kS>;
-  StreamShape ss;
-  const size_t smem = odd_shape<T>(&ss, a.nm.n, kOddFwdColumns, kS, 1);
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_LORA_ERR_CUDA;
-  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), a.sms);
-  prof_begin(K_NORM_FWD, a.s);
-  kernel<<<grid, ss.tpr * ss.teams, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd);
-  prof_end(K_NORM_FWD, a.s);
-  return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+bool stream_fwd(const FwdArgs& a, bool shift, int* rc) {
+  constexpr int VL = 16 / sizeof(T);
+  // a shifted row may touch one vector more than its length has
+  const int slots = (int)ceil_div(a.nm.n + (shift ? VL - 1 : 0), VL);
+  constexpr int nvs[] = {kFwdColumns / VL, sizeof(T) == 2 ? 6 : 12, kFwdColumns / VL / 2, kFwdColumns / VL / 4, 2, 1};
+  int nv;
+  const StreamShape ss = stream_shape(slots, nvs, kFwdStreamThreads, &nv);
+  if (ss.teams < 1 || (shift && a.sms < 8)) return false;
+  if (a.nm.rows < (shift ? kShiftRows : 4LL * ss.teams * a.sms)) return false;
+  *rc = nv == nvs[0]   ? launch_fwd_stream<T, nvs[0]>(a, ss, shift)
+        : nv == nvs[1] ? launch_fwd_stream<T, nvs[1]>(a, ss, shift)
+        : nv == nvs[2] ? launch_fwd_stream<T, nvs[2]>(a, ss, shift)
+        : nv == nvs[3] ? launch_fwd_stream<T, nvs[3]>(a, ss, shift)
+        : nv == 2      ? launch_fwd_stream<T, 2>(a, ss, shift)
+                       : launch_fwd_stream<T, 1>(a, ss, shift);
+  return true;
 }
 
 template <class T, int VL>
@@ -884,20 +938,8 @@ int pick_fwd(const FwdArgs& a) {
     prof_end(K_NORM_FWD, a.s);
     return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
   }
-  if constexpr (VL > 1) {
-    constexpr int nvs[] = {kFwdColumns / VL, sizeof(T) == 2 ? 6 : 12, kFwdColumns / VL / 2, kFwdColumns / VL / 4, 2, 1};
-    int nv;
-    const StreamShape ss = stream_shape(slots, nvs, kFwdStreamThreads, &nv);
-    if (ss.teams > 0 && a.nm.rows >= 4LL * ss.teams * a.sms)
-      return nv == nvs[0]   ? launch_fwd_stream<T, nvs[0]>(a, ss)
-             : nv == nvs[1] ? launch_fwd_stream<T, nvs[1]>(a, ss)
-             : nv == nvs[2] ? launch_fwd_stream<T, nvs[2]>(a, ss)
-             : nv == nvs[3] ? launch_fwd_stream<T, nvs[3]>(a, ss)
-             : nv == 2      ? launch_fwd_stream<T, 2>(a, ss)
-                            : launch_fwd_stream<T, 1>(a, ss);
-  }
-  if constexpr (VL == 1)
-    if (a.nm.n <= kOddThreads * kOddFwdColumns && a.nm.rows >= kOddRows) return launch_fwd_odd<T>(a);
+  int rc = 0;
+  if (stream_fwd<T>(a, VL == 1, &rc)) return rc;
   // few rows want many threads
   int nv = 16;
   while (nv > 1 && (slots <= 8 * (nv / 2) || (a.nm.rows * ceil_div(slots, nv) < 512LL * a.sms &&
@@ -951,10 +993,11 @@ struct BwdArgs {
 
 // One kernel over all rows (of one slice, or of every slice).
 template <class T, BwdMode kMode, class Kernel>
-int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t smem, bool* parts, int* blocks) {
+int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t smem, bool shift, bool* parts,
+               int* blocks) {
   const int slices = slices_of(a.nm.n);
   const int most = std::max(1, std::min(a.sms, kNormParts) / slices);
-  const int grid = (int)std::min<int64_t>(ceil_div(a.nm.rows, ss.teams), most);
+  const int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
   const bool wgrad = kMode != kSums && (a.dgamma || a.dbeta);
   *parts = wgrad && grid > 1;
   *blocks = grid;
@@ -975,15 +1018,15 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t sm
 // kKernel<mode> for rows of one slice, or sums first and then the rest.
 #define BWD_MODES(KERNEL, SMEM)                                                                      \
   do {                                                                                               \
-    if (slices_of(a.nm.n) == 1) return launch_bwd<T, kWhole>(a, KERNEL(kWhole), ss, SMEM, parts, blocks); \
-    const int rc = launch_bwd<T, kSums>(a, KERNEL(kSums), ss, SMEM, parts, blocks);                  \
-    return rc ? rc : launch_bwd<T, kApply>(a, KERNEL(kApply), ss, SMEM, parts, blocks);              \
+    if (slices_of(a.nm.n) == 1) return launch_bwd<T, kWhole>(a, KERNEL(kWhole), ss, SMEM, shift, parts, blocks); \
+    const int rc = launch_bwd<T, kSums>(a, KERNEL(kSums), ss, SMEM, shift, parts, blocks);                  \
+    return rc ? rc : launch_bwd<T, kApply>(a, KERNEL(kApply), ss, SMEM, shift, parts, blocks);              \
   } while (0)
 
-template <class T, int NV>
+template <class T, int NV, bool shift>
 int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, bool* parts, int* blocks) {
   constexpr int kS = bwd_stages<T>();
-#define KERNEL(MODE) norm_bwd_stream_kernel<T, NV, kS, MODE>
+#define KERNEL(MODE) norm_bwd_stream_kernel<T, NV, kS, MODE, shift ? kShift : kPart>
   BWD_MODES(KERNEL, (ring_bytes<kS, 3 * NV>(ss.tpr * ss.teams)));
 #undef KERNEL
 }
@@ -991,6 +1034,7 @@ int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, bool* parts, int*
 template <class T, int kS>
 int launch_bwd_odd(const BwdArgs& a, bool* parts, int* blocks) {
   constexpr int kNP = kBwdColumns / 2;
+  constexpr bool shift = false;
   StreamShape ss;
   const size_t smem = odd_shape<T>(&ss, std::min(a.nm.n, kBwdSlice), kBwdColumns, kS, a.dres ? 3 : 2);
 #define KERNEL(MODE) norm_bwd_odd_kernel<T, kNP, kS, MODE>
@@ -998,23 +1042,33 @@ int launch_bwd_odd(const BwdArgs& a, bool* parts, int* blocks) {
 #undef KERNEL
 }
 
+template <class T, bool shift>
+int pick_bwd_stream(const BwdArgs& a, bool* parts, int* blocks) {
+  constexpr int VL = 16 / sizeof(T), kNV = kBwdColumns / VL;
+  const int nvs[] = {kNV, kNV / 2, 1};
+  int nv;
+  const int slots = (int)ceil_div(std::min(a.nm.n, kBwdSlice) + (shift ? VL - 1 : 0), VL);
+  const StreamShape ss = stream_shape(slots, nvs, kBwdStreamThreads, &nv);
+  return nv == kNV       ? launch_bwd_stream<T, kNV, shift>(a, ss, parts, blocks)
+         : nv == kNV / 2 ? launch_bwd_stream<T, kNV / 2, shift>(a, ss, parts, blocks)
+                         : launch_bwd_stream<T, 1, shift>(a, ss, parts, blocks);
+}
+
 template <class T>
 int run_bwd(const BwdArgs& a) {
   const int n = a.nm.n;
+  constexpr int64_t kMask = 16 / sizeof(T) - 1;
   bool parts = false;
   int blocks = 0, rc;
-  if (rows_aligned(a.nm, true, a.dres != nullptr)) {
-    constexpr int VL = 16 / sizeof(T), kNV = kBwdColumns / VL;
-    const int nvs[] = {kNV, kNV / 2, 1};
-    int nv;
-    const StreamShape ss = stream_shape(std::min(n, kBwdSlice) / VL, nvs, kBwdStreamThreads, &nv);
-    rc = nv == kNV       ? launch_bwd_stream<T, kNV>(a, ss, &parts, &blocks)
-         : nv == kNV / 2 ? launch_bwd_stream<T, kNV / 2>(a, ss, &parts, &blocks)
-                         : launch_bwd_stream<T, 1>(a, ss, &parts, &blocks);
-  } else {
-    // three stages of the widest slice of fp32 rows are more than shared memory holds
+  const bool alike = !((a.nm.ldx ^ a.nm.ldy) & kMask) && !(a.dres && (a.nm.ldx ^ a.nm.lddres) & kMask);
+  // one vector more than a slice's has to fit in a block
+  const bool fits = std::min(n, kBwdSlice) + kMask <= kBwdSlice && a.sms >= 8;
+  if (rows_aligned(a.nm, true, a.dres != nullptr))
+    rc = pick_bwd_stream<T, false>(a, &parts, &blocks);
+  else if (alike && fits)
+    rc = pick_bwd_stream<T, true>(a, &parts, &blocks);
+  else  // three stages of the widest slice of fp32 rows are more than shared memory holds
     rc = sizeof(T) == 4 && n > 4096 ? launch_bwd_odd<T, 2>(a, &parts, &blocks) : launch_bwd_odd<T, 3>(a, &parts, &blocks);
-  }
   return rc || !parts ? rc : launch_wgrad(n, blocks, a.part, a.dgamma, a.dbeta, a.s);
 }
 
