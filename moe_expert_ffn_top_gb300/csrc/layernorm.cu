@@ -255,17 +255,21 @@ struct StreamShape {
   int tpr, teams;
 };
 
-// How rows lie on the 16-byte grid: they fill every slot of every thread (no bounds
-// checks); they are whole vectors; or (kShift) they begin and end anywhere.  A shifted row
+// How rows lie on the 16-byte grid: as whole vectors that fill every slot of every thread
+// (kFull, no bounds checks: 65,536 x 4,096 bf16 forward 161 us against 176 us), as whole
+// vectors, or (kShift) they begin and end anywhere.  A shifted row
 // is taken in the aligned vectors that cover it, so that its first column is `shift`
 // elements into the first vector (what lies before it belongs to the row before: the
 // tensor itself starts aligned).  shift = r * ld mod VL depends on the row; the grid is
 // such that all rows of a team have the same, which keeps a thread's columns, its weights
 // and its sums in place.
-enum RowFit { kFull, kPart, kShift };
+enum RowFit { kFull, kAligned, kShift };
 // What a thread knows of its columns: slot i starts at column c0 + i * dc, `nv` slots lie
-// (in part) inside the row.
-template <RowFit kFit>
+// (in part) inside the row.  NV is the number that the row needs, or one more: all but
+// the last two slots are inside for every thread, and only the first and the last three
+// can hold an end of the row, so that the others carry no checks.
+// (kExact false: the row may be any shorter, as the last slice of a wide one.)
+template <RowFit kFit, int NV, bool kExact = true>
 struct Columns {
   int c0, dc, nv, n;
   __device__ __forceinline__ Columns(int lane, int tpr, int n, int vl, int shift) : n(n) {
@@ -273,25 +277,28 @@ struct Columns {
     dc = tpr * vl;
     nv = c0 < n ? (n - c0 + dc - 1) / dc : 0;
   }
-  __device__ __forceinline__ bool in(int i) const { return kFit == kFull || i < nv; }
+  __device__ __forceinline__ bool in(int i) const { return kFit == kFull || (kExact && i < NV - 2) || i < nv; }
   __device__ __forceinline__ int col(int i) const { return c0 + i * dc; }
   template <int kP>
   __device__ __forceinline__ bool edge(int i) const {
-    return kFit == kShift && (col(i) < 0 || col(i) + 2 * kP > n);
+    static_assert(kFit != kShift || kExact, "ends are looked for in the last slots only");
+    return kFit == kShift && ((i == 0 && col(i) < 0) || (i >= NV - 3 && col(i) + 2 * kP > n));
   }
   // 0 for what is not the row's
   template <int kP>
   __device__ __forceinline__ void clip(int i, float2 (&v)[kP]) const {
-    if (kFit != kShift || !edge<kP>(i)) return;
+    if constexpr (kFit == kShift) {
+      if (!edge<kP>(i)) return;
 #pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      if ((unsigned)(col(i) + 2 * j) >= (unsigned)n) v[j].x = 0.f;
-      if ((unsigned)(col(i) + 2 * j + 1) >= (unsigned)n) v[j].y = 0.f;
+      for (int j = 0; j < kP; ++j) {
+        if ((unsigned)(col(i) + 2 * j) >= (unsigned)n) v[j].x = 0.f;
+        if ((unsigned)(col(i) + 2 * j + 1) >= (unsigned)n) v[j].y = 0.f;
+      }
     }
   }
   template <class T>
   __device__ __forceinline__ void copy(uint4* slot, const T* row, int i) const {
-    if (kFit == kShift)
+    if (kFit == kShift && i >= NV - 3)
       async_copy16_part(slot, row + col(i), min(16, (n - col(i)) * (int)sizeof(T)));
     else
       async_copy16(slot, row + col(i));
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / n;
   const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
-  const Columns<kFit> cl(lane, ss.tpr, n, VL, (int)(first * nm.ldx & (VL - 1)));
+  const Columns<kFit, NV> cl(lane, ss.tpr, n, VL, (int)(first * nm.ldx & (VL - 1)));
   const bool y_fits = ((nm.ldx ^ nm.ldy) & (VL - 1)) == 0;
   const auto copy_row = [&](int64_t r, int s) {
     if (r < nm.rows) {
@@ -470,8 +477,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
   const float rn = 1.0f / nm.n;
   const int64_t step = (int64_t)gridDim.x * ss.teams, first = blockIdx.x * (int64_t)ss.teams + team;
-  const Columns<kFit> cl(lane, ss.tpr, n, VL, (int)(first * nm.ldx & (VL - 1)));
-  const bool dx_fits = ((nm.ldx ^ nm.lddx) & (VL - 1)) == 0;
+  const Columns<kFit, NV, kMode == kWhole> cl(lane, ss.tpr, n, VL, (int)(first * nm.ldx & (VL - 1)));
   const auto copy_row = [&](int64_t r, int s) {
     if (r < nm.rows) {
       const T *xr = x + r * nm.ldx, *gr = dy + r * nm.ldy, *er = dres + r * nm.lddres;
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
             const float2 w = fma2(h[i][j], nb, add2(u[i][j], na));
             o[j] = dres ? fma2(w, both(rt), ev.get(j)) : mul2(w, both(rt));
           }
-          cl.template store<T, VL>(dr, i, o, dx_fits);
+          cl.template store<T, VL>(dr, i, o, true);
         }
     }
     mu = mu1;
@@ -851,22 +857,23 @@ constexpr int fwd_stages() { return sizeof(T) == 2 ? 4 : 3; }
 template <class T>
 constexpr int bwd_stages() { return sizeof(T) == 2 ? 3 : 2; }
 
-// Slots per thread (one of `nvs`, descending) and threads of a row: the most slots that
-// every thread fills completely (no bounds checks), else the fewest threads.
-template <int N>
-StreamShape stream_shape(int slots, const int (&nvs)[N], int threads, int* nv) {
-  *nv = 0;
-  for (int v : nvs) {
-    const int t = slots / v;
-    if (!*nv && slots % v == 0 && (t == 8 || t == 16 || t % 32 == 0) && t <= threads) *nv = v;
+// Threads of a row of `slots` slots and, in *nv, slots per thread (`most` at most, even
+// beyond 4 for fp32's many).  What a warp does once per row costs about three slots.
+StreamShape stream_shape(int slots, int most, int threads, int* nv) {
+  StreamShape best = {0, 0};
+  float cost = 0.f;
+  for (int tpr = 8; tpr <= threads; tpr = tpr < 32 ? 2 * tpr : tpr + 32) {
+    int v = (int)ceil_div(slots, tpr);
+    if (v > most) continue;
+    if (most > 8 && v > 4) v += v & 1;
+    const float c = (3.f + v) / (threads / tpr);
+    if (!best.tpr || c < cost) {
+      best = StreamShape{tpr, threads / tpr};
+      cost = c;
+      *nv = v;
+    }
   }
-  if (!*nv)
-    for (int v : nvs)
-      if (!*nv || slots <= 8 * v) *nv = v;
-  StreamShape ss;
-  ss.tpr = row_threads(slots, *nv);
-  ss.teams = threads / ss.tpr;
-  return ss;
+  return best;
 }
 
 // Blocks of a streamed kernel: rows whose vectors are shifted need teams that step by a
@@ -879,11 +886,11 @@ int stream_grid(int64_t rows, int teams, int most, bool shift) {
 
 template <class T, int NV>
 int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss, bool shift) {
-  const bool full = !shift && a.nm.n == ss.tpr * NV * 16 / (int)sizeof(T);
   constexpr int kS = fwd_stages<T>();
+  const bool full = !shift && a.nm.n == ss.tpr * NV * 16 / (int)sizeof(T);
   const auto kernel = full    ? norm_fwd_stream_kernel<T, NV, kS, kFull>
                       : shift ? norm_fwd_stream_kernel<T, NV, kS, kShift>
-                              : norm_fwd_stream_kernel<T, NV, kS, kPart>;
+                              : norm_fwd_stream_kernel<T, NV, kS, kAligned>;
   const int threads = ss.tpr * ss.teams;
   const size_t smem = ring_bytes<fwd_stages<T>(), NV>(threads);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -913,17 +920,26 @@ bool stream_fwd(const FwdArgs& a, bool shift, int* rc) {
   constexpr int VL = 16 / sizeof(T);
   // a shifted row may touch one vector more than its length has
   const int slots = (int)ceil_div(a.nm.n + (shift ? VL - 1 : 0), VL);
-  constexpr int nvs[] = {kFwdColumns / VL, sizeof(T) == 2 ? 6 : 12, kFwdColumns / VL / 2, kFwdColumns / VL / 4, 2, 1};
-  int nv;
-  const StreamShape ss = stream_shape(slots, nvs, kFwdStreamThreads, &nv);
-  if (ss.teams < 1 || (shift && a.sms < 8)) return false;
+  int nv = 0;
+  const StreamShape ss = stream_shape(slots, kFwdColumns / VL, kFwdStreamThreads, &nv);
+  if (!ss.tpr || (shift && a.sms < 8)) return false;
   if (a.nm.rows < (shift ? kShiftRows : 4LL * ss.teams * a.sms)) return false;
-  *rc = nv == nvs[0]   ? launch_fwd_stream<T, nvs[0]>(a, ss, shift)
-        : nv == nvs[1] ? launch_fwd_stream<T, nvs[1]>(a, ss, shift)
-        : nv == nvs[2] ? launch_fwd_stream<T, nvs[2]>(a, ss, shift)
-        : nv == nvs[3] ? launch_fwd_stream<T, nvs[3]>(a, ss, shift)
-        : nv == 2      ? launch_fwd_stream<T, 2>(a, ss, shift)
-                       : launch_fwd_stream<T, 1>(a, ss, shift);
+  switch (nv) {
+    case 1: *rc = launch_fwd_stream<T, 1>(a, ss, shift); break;
+    case 2: *rc = launch_fwd_stream<T, 2>(a, ss, shift); break;
+    case 3: *rc = launch_fwd_stream<T, 3>(a, ss, shift); break;
+    case 4: *rc = launch_fwd_stream<T, 4>(a, ss, shift); break;
+    case 6: *rc = launch_fwd_stream<T, 6>(a, ss, shift); break;
+    case 8: *rc = launch_fwd_stream<T, 8>(a, ss, shift); break;
+    default:
+      if constexpr (sizeof(T) == 2)
+        *rc = nv == 5 ? launch_fwd_stream<T, 5>(a, ss, shift) : launch_fwd_stream<T, 7>(a, ss, shift);
+      else
+        *rc = nv == 10   ? launch_fwd_stream<T, 10>(a, ss, shift)
+              : nv == 12 ? launch_fwd_stream<T, 12>(a, ss, shift)
+              : nv == 14 ? launch_fwd_stream<T, 14>(a, ss, shift)
+                         : launch_fwd_stream<T, 16>(a, ss, shift);
+  }
   return true;
 }
 
@@ -1026,9 +1042,14 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t sm
 template <class T, int NV, bool shift>
 int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, bool* parts, int* blocks) {
   constexpr int kS = bwd_stages<T>();
-#define KERNEL(MODE) norm_bwd_stream_kernel<T, NV, kS, MODE, shift ? kShift : kPart>
-  BWD_MODES(KERNEL, (ring_bytes<kS, 3 * NV>(ss.tpr * ss.teams)));
+  const size_t smem = ring_bytes<kS, 3 * NV>(ss.tpr * ss.teams);
+  if constexpr (shift) {  // of one slice
+    return launch_bwd<T, kWhole>(a, norm_bwd_stream_kernel<T, NV, kS, kWhole, kShift>, ss, smem, shift, parts, blocks);
+  } else {
+#define KERNEL(MODE) norm_bwd_stream_kernel<T, NV, kS, MODE, kAligned>
+    BWD_MODES(KERNEL, smem);
 #undef KERNEL
+  }
 }
 
 template <class T, int kS>
@@ -1045,13 +1066,12 @@ int launch_bwd_odd(const BwdArgs& a, bool* parts, int* blocks) {
 template <class T, bool shift>
 int pick_bwd_stream(const BwdArgs& a, bool* parts, int* blocks) {
   constexpr int VL = 16 / sizeof(T), kNV = kBwdColumns / VL;
-  const int nvs[] = {kNV, kNV / 2, 1};
-  int nv;
   const int slots = (int)ceil_div(std::min(a.nm.n, kBwdSlice) + (shift ? VL - 1 : 0), VL);
-  const StreamShape ss = stream_shape(slots, nvs, kBwdStreamThreads, &nv);
-  return nv == kNV       ? launch_bwd_stream<T, kNV, shift>(a, ss, parts, blocks)
-         : nv == kNV / 2 ? launch_bwd_stream<T, kNV / 2, shift>(a, ss, parts, blocks)
-                         : launch_bwd_stream<T, 1, shift>(a, ss, parts, blocks);
+  int nv = 0;
+  const StreamShape ss = stream_shape(slots, kNV, kBwdStreamThreads, &nv);
+  if constexpr (kNV == 4)
+    if (nv > 2) return nv == 3 ? launch_bwd_stream<T, 3, shift>(a, ss, parts, blocks) : launch_bwd_stream<T, 4, shift>(a, ss, parts, blocks);
+  return nv == 2 ? launch_bwd_stream<T, 2, shift>(a, ss, parts, blocks) : launch_bwd_stream<T, 1, shift>(a, ss, parts, blocks);
 }
 
 template <class T>
@@ -1060,7 +1080,10 @@ int run_bwd(const BwdArgs& a) {
   constexpr int64_t kMask = 16 / sizeof(T) - 1;
   bool parts = false;
   int blocks = 0, rc;
-  const bool alike = !((a.nm.ldx ^ a.nm.ldy) & kMask) && !(a.dres && (a.nm.ldx ^ a.nm.lddres) & kMask);
+  // all rows shifted alike (an output shifted otherwise, stored by single elements, makes this
+  // slower than the staged kernel: 1.7 against 2.8 TB/s at 16,384 x 2,049 bf16)
+  const int64_t differ = (a.nm.ldx ^ a.nm.ldy) | (a.nm.ldx ^ a.nm.lddx) | (a.dres ? a.nm.ldx ^ a.nm.lddres : 0);
+  const bool alike = (differ & kMask) == 0;
   // one vector more than a slice's has to fit in a block
   const bool fits = std::min(n, kBwdSlice) + kMask <= kBwdSlice && a.sms >= 8;
   if (rows_aligned(a.nm, true, a.dres != nullptr))
