@@ -405,8 +405,8 @@ typedef struct moe_lora_adamw_tensor {
   const void* g;       /* [numel] gradient */
   void* m;             /* [numel] fp32, or E4M3 codes */
   void* v;             /* [numel] fp32, or E4M3 codes of r */
-  float* m_scale;      /* state 1: [ceil(numel / 256)] */
-  float* v_scale;      /* state 1: [ceil(numel / 256)] */
+  float* m_scale;      /* state 1: [ceil(numel / 256)]; 4-byte aligned */
+  float* v_scale;      /* state 1: [ceil(numel / 256)]; 4-byte aligned */
   int64_t numel;       /* 0 = skipped */
   int32_t p_dtype, g_dtype; /* MOE_LORA_F32 / _BF16 / _F16 */
   int32_t state;       /* 0 = 32 bits, 1 = 8 bits */

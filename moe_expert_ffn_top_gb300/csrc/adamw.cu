@@ -301,7 +301,10 @@ int check_tensor(const moe_lora_adamw_tensor& t) {
   if ((rc = check_ptr(t.p)) || (rc = check_ptr(t.g)) || (rc = check_ptr(t.m)) || (rc = check_ptr(t.v)) ||
       (rc = check_opt(t.master)))
     return rc;
-  if (t.state == 1 && ((rc = check_ptr(t.m_scale)) || (rc = check_ptr(t.v_scale)))) return rc;
+  if (t.state == 1) {  // the scales are read one by one, and may be slices of larger arrays
+    if (!t.m_scale || !t.v_scale) return MOE_LORA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(t.m_scale) | reinterpret_cast<uintptr_t>(t.v_scale)) & 3u) return MOE_LORA_ERR_ALIGN;
+  }
   return MOE_LORA_OK;
 }
 

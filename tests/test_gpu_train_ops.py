@@ -521,6 +521,26 @@ def test_adamw_many_tensors():
             assert not torch.is_tensor(x[key]) or torch.equal(x[key], y[key])
 
 
+def test_adamw_scales_inside_an_array():
+    """The block scales of several tensors in one array, at any multiple of four bytes."""
+    def make():
+        g = _gen(5)
+        es = [_entry(n, BF, F32, True, True, g) for n in (257, 1000, 300, 64)]
+        return es
+    a, b = make(), make()
+    ms, vs = torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")
+    at = 1
+    for e in b:
+        k = e["m_scale"].numel()
+        e["m_scale"], e["v_scale"] = ms[at:at + k], vs[at:at + k]
+        at += k
+    for step in (1, 2):
+        m.moe_lora_adamw_step(m.AdamWTensors(a), step)
+        m.moe_lora_adamw_step(m.AdamWTensors(b), step)
+    for x, y in zip(a, b):
+        assert all(torch.equal(x[k], y[k]) for k in ("p", "master", "m", "v", "m_scale", "v_scale"))
+
+
 def test_adamw_empty_and_lr():
     e0 = dict(p=torch.empty(0, device="cuda"), g=torch.empty(0, device="cuda"), m=torch.empty(0, device="cuda"),
               v=torch.empty(0, device="cuda"))

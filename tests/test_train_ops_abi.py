@@ -105,7 +105,7 @@ def _tensor(**kw):
     (-2, {}, dict(lr=float("nan"))), (-2, {}, dict(weight_decay=float("inf"))), (-1, {}, dict(p=None)),
     (-1, {}, dict(g=None)), (-1, {}, dict(m=None)), (-1, {}, dict(v=None)), (-1, {}, dict(m_scale=None)),
     (-1, {}, dict(v_scale=None)), (-3, {}, dict(p=FAKE + 2)), (-3, {}, dict(master=FAKE + 4)),
-    (-3, {}, dict(g=FAKE + 8)), (-3, {}, dict(m=FAKE + 1)), (-3, {}, dict(v_scale=FAKE + 4))])
+    (-3, {}, dict(g=FAKE + 8)), (-3, {}, dict(m=FAKE + 1)), (-3, {}, dict(v_scale=FAKE + 2)), (-3, {}, dict(m_scale=FAKE + 1))])
 def test_adamw_rejections(L, code, opt, over):
     o = dict(beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=None)
     o.update(opt)
