@@ -367,7 +367,7 @@ MOE_LORA_API int moe_lora_layernorm_backward(const moe_lora_norm* nm, const void
  * dims gives T, E <= 1024 (else MOE_LORA_ERR_UNSUPPORTED), k and A.  `scratch` is a device buffer
  * of moe_lora_workspace_bytes(.., MOE_LORA_WS_BALANCE_SCRATCH).  Sums run in a fixed order that
  * depends on the adapter's own tokens alone: each adapter's results equal its standalone run bit
- * for bit.  One launch where every adapter has at most 2^18 logits (T_a * E) and 32,768 tokens, three
+ * for bit.  One launch where every adapter has at most 2^19 logits (T_a * E) and 2^13 tokens, three
  * otherwise. */
 MOE_LORA_API int moe_lora_balance_loss(const moe_lora_dims* dims, const void* logits, int32_t dtype, int64_t ld,
                                        const int32_t* topk_ids, const int64_t* adapter_offsets, float coef,

@@ -10,6 +10,8 @@
 // elements with 32-bit moments 130 us (96%).
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "element.cuh"
 #include "launch.h"
@@ -24,7 +26,7 @@ constexpr int kAdamBlock = 256;  // elements of a warp's step = of one scale of 
 constexpr int kAdamChunk = kAdamWarps * kAdamBlock;
 // Tensors per launch.  The table travels in the kernel's parameters (32 KB at most), so
 // nothing is copied to the device ahead of the launch and a graph captures it.
-constexpr int kAdamFew = 40, kAdamMany = 352;
+constexpr int kAdamFew = 40, kAdamSome = 128, kAdamMany = 352;
 
 struct AdamTensor {
   void* p;
@@ -365,9 +367,11 @@ extern "C" int moe_lora_adamw_step(const moe_lora_adamw* o, const moe_lora_adamw
   const AdamHyper h{(float)o->beta1, (float)(1 - o->beta1), (float)o->beta2, (float)(1 - o->beta2),
                     (float)(1 / sqrt(bc2)), (float)o->eps, -0.f, o->grad_scale};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = n <= kAdamFew ? run_adamw<false, kAdamFew>(h, bc1, tensors, n, sms, s)
-                          : run_adamw<false, kAdamMany>(h, bc1, tensors, n, sms, s)))
-    return rc;
-  return n <= kAdamFew ? run_adamw<true, kAdamFew>(h, bc1, tensors, n, sms, s)
-                       : run_adamw<true, kAdamMany>(h, bc1, tensors, n, sms, s);
+  const auto run = [&](auto eight) {
+    return n <= kAdamFew    ? run_adamw<eight, kAdamFew>(h, bc1, tensors, n, sms, s)
+           : n <= kAdamSome ? run_adamw<eight, kAdamSome>(h, bc1, tensors, n, sms, s)
+                            : run_adamw<eight, kAdamMany>(h, bc1, tensors, n, sms, s);
+  };
+  if ((rc = run(std::false_type{}))) return rc;
+  return run(std::true_type{});
 }

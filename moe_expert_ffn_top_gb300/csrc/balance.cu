@@ -1,12 +1,12 @@
 // Balance loss of the routing step with the per-expert counts and its gradient to the
 // logits (definitions in include/moe_lora.h).
 //
-// An adapter's tokens are cut into groups of eight chunks, in numbers that depend on that
+// An adapter's tokens are cut into groups of sixteen chunks, in numbers that depend on that
 // adapter's sizes alone; a block works on a chunk and keeps its sums of probabilities in
 // registers.  The sums of a group's chunks, then the groups', are added in order.
 //
-// Adapters of one group each (small batches): one launch.  A cluster of eight blocks
-// counts the group's ids, meets, and every block has the counts that the gradient needs;
+// Adapters of one group each (small batches): one launch.  A cluster of up to sixteen
+// blocks counts the group's ids, meets, and every block has the counts that the gradient needs;
 // the sums meet in distributed shared memory.  (Adapters of one chunk: no cluster.)
 // Otherwise a first launch counts, a small cluster per group; the second needs no cluster, its
 // blocks fill every SM; a third adds the chunks' sums.  Each is launched while the one
@@ -30,13 +30,15 @@ namespace {
 constexpr int block_threads(int vals) { return vals == 8 ? 512 : 256; }
 constexpr int kSumPad = 16;
 constexpr int kBalMaxE = 1024;
-constexpr int kBalCluster = 8;       // chunks per group
+constexpr int kBalCluster = 16;      // chunks per group
 constexpr int kBalMaxChunk = 4096;   // tokens; a chunk is a multiple of 32 long
-constexpr int kBalMaxGroups = 38;    // 304 blocks, two per SM, unless the chunks get too long
-constexpr int kBalGroupWork = 1 << 18;  // logits worth another group
+constexpr int kBalMaxGroups = 19;    // 304 blocks, two per SM, unless the chunks get too long
+constexpr int kBalGroupWork = 1 << 19;  // logits worth another group
+constexpr int kBalGroupTokens = 1 << 13;  // tokens worth another group
+constexpr int kBalFew = 8, kBalFewWork = 3 << 16, kBalFewTokens = 3 << 9;  // chunks of a small group, logits, tokens
 constexpr int kBalChunkWork = 1 << 12;  // logits that one chunk takes alone
 constexpr int kCountCluster = 4, kCountThreads = 512;
-constexpr int kSumThreads = 1024;
+constexpr int kSumCluster = 8, kSumThreads = 1024;
 constexpr int kBalStages = 3;
 
 struct BalTable {
@@ -46,17 +48,22 @@ struct BalTable {
   int chunk[kMaxAdapters];       // tokens per chunk
 };
 
-// Groups of an adapter of n tokens: one per 2^18 logits up to 38, more only where a
-// chunk would pass its limit.
+// Groups of an adapter of n tokens: one per 2^19 logits and per 2^13 tokens up to 19, more
+// only where a chunk would pass its limit.
 int64_t bal_groups(int64_t n, int E) {
-  const int64_t by_work = std::min<int64_t>((n * E + kBalGroupWork - 1) / kBalGroupWork, kBalMaxGroups);
+  const int64_t by_work = std::min<int64_t>(
+      std::max<int64_t>((n * E + kBalGroupWork - 1) / kBalGroupWork, (n + kBalGroupTokens - 1) / kBalGroupTokens),
+      kBalMaxGroups);
   const int64_t by_size = (n + kBalCluster * kBalMaxChunk - 1) / (kBalCluster * kBalMaxChunk);
   return std::max<int64_t>(1, std::max(by_work, by_size));
 }
 
-// Tokens per chunk of such an adapter: an eighth of a group, or all of a tiny batch.
+// Tokens per chunk of such an adapter: a sixteenth of a group; of one group and little
+// work an eighth (16 adapters x 1,024 x 128: 11 us as clusters of eight, 17 us as clusters
+// of sixteen, which do not all run together), of very little all.
 int bal_chunk(int64_t n, int64_t groups, int E) {
-  const int64_t chunks = n * E <= kBalChunkWork && n <= kBalMaxChunk ? 1 : groups * kBalCluster;
+  const int64_t work = std::max(n * E, n * (kBalFewWork / kBalFewTokens));
+  const int64_t chunks = groups > 1 || work > kBalFewWork ? groups * kBalCluster : n * E > kBalChunkWork ? kBalFew : 1;
   return (int)((n + chunks * 32 - 1) / (chunks * 32)) * 32;
 }
 
@@ -66,8 +73,8 @@ struct BalLayout {
 BalLayout bal_layout(const moe_lora_dims* d) {
   BalLayout L;
   // ceil(a) + ceil(b) <= ceil(a + b) + 1, an adapter's groups
-  const int64_t work = d->T * d->E / kBalGroupWork, size = d->T / (kBalCluster * kBalMaxChunk);
-  const int64_t groups = std::min<int64_t>(work, (int64_t)d->A * kBalMaxGroups) + size + 2 * d->A;
+  const int64_t work = d->T * d->E / kBalGroupWork + d->T / kBalGroupTokens, size = d->T / (kBalCluster * kBalMaxChunk);
+  const int64_t groups = std::min<int64_t>(work, (int64_t)d->A * kBalMaxGroups) + size + 3 * d->A;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   L.err = take(sizeof(int) * d->A);
@@ -295,7 +302,8 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
   const Pairs<T, kMode> pr{(int)threadIdx.x % g.lpr, g.lpr};
   const int rank = kC > 1 ? (int)cluster_rank() : 0;
   const int group = kOne ? blockIdx.x / (kC ? kC : 1) : blockIdx.x / kBalCluster, a = adapter_of(bt, group);
-  const Span ch(bt, a, kC == 1 ? 0 : blockIdx.x - (int64_t)bt.group0[a] * kBalCluster, 1);
+  const int64_t chunk = kOne ? blockIdx.x % (kC ? kC : 1) : blockIdx.x - (int64_t)bt.group0[a] * kBalCluster;
+  const Span ch(bt, a, chunk, 1);
   const Ring<kBalStages, kRows16> ring(ring_sm);
   const T* logits = static_cast<const T*>(g.logits) + (int64_t)ch.t0 * g.ld;
   const auto in = [&](int e) { return kFull || e < E; };
@@ -388,7 +396,7 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
   __syncthreads();
   const int N = nsm[1];
   const float rR = 1.0f / (float)max(nsm[0], 1), rN = 1.0f / (float)max(N, 1);
-  const bool first = blockIdx.x == (kC == 1 ? group : bt.group0[a] * kBalCluster);  // block of the adapter
+  const bool first = chunk == 0;  // block of the adapter
   for (int e = threadIdx.x; e < E; e += kT) {
     const int c = cnt[e];
     fsm[e] = (float)c * rR;
@@ -551,14 +559,14 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
 // Third launch of larger batches: a cluster of eight blocks per adapter, an eighth of the
 // experts each.  A group's chunks are added in order by one thread, the groups in order
 // by another.
-__global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(kSumThreads)
+__global__ void __cluster_dims__(kSumCluster, 1, 1) __launch_bounds__(kSumThreads)
     balance_sum_kernel(const __grid_constant__ BalTable bt, const __grid_constant__ BalArgs g) {
-  constexpr int kBatch = 64, kCols = kBalMaxE / kBalCluster;  // groups at a time, columns of a block
+  constexpr int kBatch = 64, kCols = kBalMaxE / kSumCluster;  // groups at a time, columns of a block
   __shared__ float gsm[kBatch][kCols];
   __shared__ float fsm[kBalMaxE], psm[kBalMaxE], tsm[kSumThreads / 32];
   __shared__ int nsm;
-  const int E = g.E, a = blockIdx.x / kBalCluster, rank = (int)cluster_rank();
-  const int per = (E + kBalCluster - 1) / kBalCluster, e0 = rank * per, cols = max(0, min(E - e0, per));
+  const int E = g.E, a = blockIdx.x / kSumCluster, rank = (int)cluster_rank();
+  const int per = (E + kSumCluster - 1) / kSumCluster, e0 = rank * per, cols = max(0, min(E - e0, per));
   const int slices = max(1, kSumThreads / max(cols, 1)), c = threadIdx.x % max(cols, 1), q = threadIdx.x / max(cols, 1);
   const int g0 = bt.group0[a], ng = bt.group0[a + 1] - g0;
   if (threadIdx.x == 0) nsm = 0;
@@ -595,7 +603,7 @@ __global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(kSumThread
   const float rR = 1.0f / (float)max(nsm, 1), rN = 1.0f / (float)max(g.sc.tokens[a], 1);
   for (int e = threadIdx.x; e < E; e += kSumThreads) fsm[e] *= rR;
   cluster_sync_all();  // rank 0 runs, its psm may be written
-  if (q == 0 && c < cols) finish_prob<kBalCluster>(g, a, e0 + c, p * rN, psm);
+  if (q == 0 && c < cols) finish_prob<kSumCluster>(g, a, e0 + c, p * rN, psm);
   cluster_sync_all();
   if (rank == 0) finish_loss<kSumThreads>(g, a, fsm, psm, tsm);
 }
@@ -637,7 +645,8 @@ int launch_balance(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
   const size_t smem = std::max(ring, sizeof(float) * (kT / a.lpr) * (a.E + kSumPad));
   if (smem > 32 * 1024)  // with the static part above what a launch may use without asking
     LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  const BalLaunch l((int64_t)bt.group0[bt.n] * (kC == 1 ? 1 : kBalCluster), kT, smem, kC, kC == 0, s);
+  if (kC > 8) LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  const BalLaunch l((int64_t)bt.group0[bt.n] * (kC ? kC : kBalCluster), kT, smem, kC, kC == 0, s);
   prof_begin(K_BAL_LOSS, s);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, bt, a);
   prof_end(K_BAL_LOSS, s);
@@ -647,9 +656,12 @@ int launch_balance(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
 template <class T, RowMode kMode, int kVals>
 int pick_groups(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
   if (bt.group0[bt.n] == bt.n) {
-    bool one_chunk = true;
-    for (int i = 0; i < bt.n; ++i) one_chunk &= bt.tok_off[i + 1] - bt.tok_off[i] <= bt.chunk[i];
-    return one_chunk ? launch_balance<T, kMode, kVals, 1>(bt, a, s) : launch_balance<T, kMode, kVals, kBalCluster>(bt, a, s);
+    int most = 1;  // chunks of an adapter
+    for (int i = 0; i < bt.n; ++i)
+      if (bt.chunk[i]) most = std::max(most, (bt.tok_off[i + 1] - bt.tok_off[i] + bt.chunk[i] - 1) / bt.chunk[i]);
+    return most == 1          ? launch_balance<T, kMode, kVals, 1>(bt, a, s)
+           : most <= kBalFew ? launch_balance<T, kMode, kVals, kBalFew>(bt, a, s)
+                             : launch_balance<T, kMode, kVals, kBalCluster>(bt, a, s);
   }
   prof_begin(K_BAL_COUNT, s);
   balance_count_kernel<<<bt.group0[bt.n] * kCountCluster, kCountThreads, 0, s>>>(bt, a.ids, a.k, a.E, a.sc);
@@ -657,7 +669,7 @@ int pick_groups(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
   LAUNCH(cudaGetLastError());
   const int rc = launch_balance<T, kMode, kVals, 0>(bt, a, s);
   if (rc) return rc;
-  const BalLaunch l((int64_t)bt.n * kBalCluster, kSumThreads, 0, 0, true, s);
+  const BalLaunch l((int64_t)bt.n * kSumCluster, kSumThreads, 0, 0, true, s);
   prof_begin(K_BAL_SUM, s);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, balance_sum_kernel, bt, a);
   prof_end(K_BAL_SUM, s);
