@@ -5,6 +5,7 @@
 #include "element.cuh"
 #include "launch.h"
 #include "prof.h"
+#include "sm100_ptx.cuh"
 
 namespace moelora {
 
@@ -253,6 +254,7 @@ constexpr int kOddThreads = 512;
 constexpr int kShiftRows = 256;  // from here on the streamed forward of shifted rows
 struct StreamShape {
   int tpr, teams;
+  int slice = 0;  // columns of a slice (backward)
 };
 
 // How rows lie on the 16-byte grid: as whole vectors that fill every slot of every thread
@@ -281,8 +283,7 @@ struct Columns {
   __device__ __forceinline__ int col(int i) const { return c0 + i * dc; }
   template <int kP>
   __device__ __forceinline__ bool edge(int i) const {
-    static_assert(kFit != kShift || kExact, "ends are looked for in the last slots only");
-    return kFit == kShift && ((i == 0 && col(i) < 0) || (i >= NV - 3 && col(i) + 2 * kP > n));
+    return kFit == kShift && (((!kExact || i == 0) && col(i) < 0) || ((!kExact || i >= NV - 3) && col(i) + 2 * kP > n));
   }
   // 0 for what is not the row's
   template <int kP>
@@ -298,7 +299,7 @@ struct Columns {
   }
   template <class T>
   __device__ __forceinline__ void copy(uint4* slot, const T* row, int i) const {
-    if (kFit == kShift && i >= NV - 3)
+    if (kFit == kShift && (!kExact || i >= NV - 3))
       async_copy16_part(slot, row + col(i), min(16, (n - col(i)) * (int)sizeof(T)));
     else
       async_copy16(slot, row + col(i));
@@ -414,20 +415,30 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
 // rows).  Same streaming; dx needs one sum (of two values) per row, the weight gradients
 // stay in registers until the block's rows are done.
 //
-// Rows wider than kBwdSlice are worked on in slices (blockIdx.y) by two launches: kSums
-// leaves every slice's part of a row's sums in `sums` [rows][slices], kApply adds them.
-enum BwdMode { kWhole, kSums, kApply };
+// Rows wider than kBwdSlice are worked on in slices (blockIdx.y).  Up to eight slices are
+// a cluster (kCluster): its blocks exchange a row's sums through distributed shared
+// memory.  More take two launches: kSums leaves every slice's part of a row's sums in
+// `sums` [rows][slices], kApply adds them (and reads x and dy again: 16,384 columns bf16
+// 2.5 TB/s in two launches).
+enum BwdMode { kWhole, kCluster, kSums, kApply };
 constexpr int kBwdSlice = kBwdStreamThreads * kBwdColumns;
-// Slice blockIdx.y of a row of n (of one slice, kWhole).
+constexpr int kBwdCluster = 8;
+// Slice blockIdx.y, `width` columns, of a row of n (of one slice, kWhole).
 template <BwdMode kMode>
 struct Slice {
   int first, n;
-  __device__ __forceinline__ explicit Slice(int all)
-      : first(kMode == kWhole ? 0 : blockIdx.y * kBwdSlice), n(kMode == kWhole ? all : min(kBwdSlice, all - first)) {}
+  __device__ __forceinline__ Slice(int all, int width)
+      : first(kMode == kWhole ? 0 : blockIdx.y * width), n(kMode == kWhole ? all : min(width, all - first)) {}
+};
+// The slices' parts of the rows that a cluster's teams work on, in two buffers: a block
+// writes the second time into one only after all have read it (they meet in between).
+struct SliceSums {
+  float2 v[2][kMaxTeams][kBwdCluster];
 };
 // A row's two sums over all slices, from this slice's; false: the row is done (kSums).
 template <BwdMode kMode, class Sum>
-__device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, float2* sums, int64_t r, bool on, int lane) {
+__device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, float2* sums, int64_t r, bool on, int lane,
+                                         SliceSums* sm = nullptr, int team = 0, int buf = 0) {
   if (kMode == kApply) {
     all = both(0.f);
     if (on)
@@ -436,6 +447,17 @@ __device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, flo
   }
   all = sum(mine);
   if (kMode == kWhole) return true;
+  if (kMode == kCluster) {
+    const int slices = gridDim.y;
+    if (lane < slices) {
+      const uint32_t to = mapa_shared(smem_u32(&sm->v[buf][team][blockIdx.y]), lane);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(all.x), "f"(all.y) : "memory");
+    }
+    cluster_sync_all();
+    all = both(0.f);
+    for (int i = 0; i < slices; ++i) all = add2(all, sm->v[buf][team][i]);
+    return true;
+  }
   if (on && lane == 0) sums[r * gridDim.y + blockIdx.y] = all;
   return false;
 }
@@ -464,7 +486,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const Slice<kMode> sl(nm.n);
+  const Slice<kMode> sl(nm.n, ss.slice);
   const int n = sl.n;
   if (kMode != kWhole) {
     x += sl.first;
@@ -472,6 +494,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
     dres += dres ? sl.first : 0;
     dx += sl.first;
   }
+  __shared__ SliceSums slice_sm;
   const Ring<kStages, 3 * NV> ring(ring_sm);
   const int lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
   RowSum sum{ss.tpr, team + 1, red + (ss.tpr > 32 ? team * 2 * RowSum::kRedWords : 0)};
@@ -504,7 +527,8 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
     for (int j = 0; j < kP; ++j) dg[i][j] = db[i][j] = both(0.f);
   const auto stat = [&](const float* p, int64_t r) { return r < nm.rows ? p[r] : 0.f; };
   float mu = stat(mean, first), rt = stat(rstd, first);
-  int s = 0;
+  int s = 0, buf = 0;
+  if (kMode == kCluster) cluster_sync_all();  // all of the cluster run before one writes into another
   for (int64_t r = first; r - team < nm.rows; r += step) {
     copy_row(r + (kStages - 1) * step, s == 0 ? kStages - 1 : s - 1);
     const float mu1 = stat(mean, r + step), rt1 = stat(rstd, r + step);
@@ -537,7 +561,8 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
           }
         }
     float2 t;
-    const bool more = row_sums<kMode>(sum, make_float2(su.x + su.y, sh.x + sh.y), t, sums, r, on, lane);
+    const bool more = row_sums<kMode>(sum, make_float2(su.x + su.y, sh.x + sh.y), t, sums, r, on, lane, &slice_sm, team, buf);
+    buf ^= 1;
     const float2 na = both(-t.x * rn), nb = both(-t.y * rn);
     if (on && more) {
       T* dr = dx + r * nm.lddx;
@@ -625,7 +650,7 @@ __global__ void __launch_bounds__(kOddThreads, 1) norm_bwd_odd_kernel(moe_lora_n
                                                                       int64_t part_ld, float2* sums) {
   extern __shared__ __align__(16) char stage_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const Slice<kMode> sl(nm.n);
+  const Slice<kMode> sl(nm.n, ss.slice);
   const int n = sl.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr, tensors = kMode != kSums && dres ? 3 : 2;
   if (kMode != kWhole) {
     x += sl.first;
@@ -786,7 +811,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(moe_lora_no
 // sums (wide rows).
 size_t part_bytes(const moe_lora_norm& nm) { return (size_t)kNormParts * 2 * nm.n * sizeof(float); }
 size_t sums_bytes(const moe_lora_norm& nm) {
-  return nm.n > kBwdSlice ? sizeof(float2) * (size_t)nm.rows * ((nm.n + kBwdSlice - 1) / kBwdSlice) : 0;
+  return nm.n > kBwdSlice ? sizeof(float2) * (size_t)nm.rows * ((nm.n + kBwdSlice - 9) / (kBwdSlice - 8)) : 0;
 }
 
 int check_ld(int64_t* ld, int n) {
@@ -860,7 +885,8 @@ constexpr int bwd_stages() { return sizeof(T) == 2 ? 3 : 2; }
 // Threads of a row of `slots` slots and, in *nv, slots per thread (`most` at most, even
 // beyond 4 for fp32's many).  What a warp does once per row costs about three slots.
 StreamShape stream_shape(int slots, int most, int threads, int* nv) {
-  StreamShape best = {0, 0};
+  StreamShape best;
+  best.tpr = best.teams = 0;
   float cost = 0.f;
   for (int tpr = 8; tpr <= threads; tpr = tpr < 32 ? 2 * tpr : tpr + 32) {
     int v = (int)ceil_div(slots, tpr);
@@ -868,7 +894,8 @@ StreamShape stream_shape(int slots, int most, int threads, int* nv) {
     if (most > 8 && v > 4) v += v & 1;
     const float c = (3.f + v) / (threads / tpr);
     if (!best.tpr || c < cost) {
-      best = StreamShape{tpr, threads / tpr};
+      best.tpr = tpr;
+      best.teams = threads / tpr;
       cost = c;
       *nv = v;
     }
@@ -881,7 +908,7 @@ StreamShape stream_shape(int slots, int most, int threads, int* nv) {
 int stream_grid(int64_t rows, int teams, int most, bool shift) {
   int64_t grid = ceil_div(rows, teams);
   if (grid <= most) return (int)grid;
-  return shift ? most / 8 * 8 : most;
+  return shift ? std::max(8, most / 8 * 8) : most;
 }
 
 template <class T, int NV>
@@ -901,8 +928,6 @@ int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss, bool shift) {
   prof_end(K_NORM_FWD, a.s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
-
-int slices_of(int n) { return (n + kBwdSlice - 1) / kBwdSlice; }
 
 // Shared memory of the staged kernels: as many teams as fit.
 template <class T>
@@ -1011,67 +1036,93 @@ struct BwdArgs {
 template <class T, BwdMode kMode, class Kernel>
 int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t smem, bool shift, bool* parts,
                int* blocks) {
-  const int slices = slices_of(a.nm.n);
-  const int most = std::max(1, std::min(a.sms, kNormParts) / slices);
-  const int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
+  const int slices = (int)ceil_div(a.nm.n, ss.slice);
   const bool wgrad = kMode != kSums && (a.dgamma || a.dbeta);
+  smem = std::max(smem, wgrad ? 2 * sizeof(float) * ss.teams * std::min(a.nm.n, ss.slice) : 0);
+  if (smem > 32 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_LORA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(1, slices);
+  cfg.blockDim = dim3(ss.tpr * ss.teams);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.s;
+  int most = std::max(1, std::min(a.sms, kNormParts) / slices);
+  if (kMode == kCluster) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.y = slices;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    // as many clusters as run together (fewer than blocks would: a cluster stays inside one
+    // processing cluster); one more is a second wave as long as the first
+    int together = 0;
+    if (cudaOccupancyMaxActiveClusters(&together, kernel, &cfg) != cudaSuccess) return MOE_LORA_ERR_CUDA;
+    most = std::max(1, std::min(most, together));
+  }
+  const int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
+  cfg.gridDim.x = grid;
   *parts = wgrad && grid > 1;
   *blocks = grid;
   float* dg = !wgrad ? nullptr : *parts ? a.part : a.dgamma;
   float* db = !wgrad ? nullptr : *parts ? a.part + a.nm.n : a.dbeta;
-  smem = std::max(smem, wgrad ? 2 * sizeof(float) * ss.teams * std::min(a.nm.n, kBwdSlice) : 0);
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_LORA_ERR_CUDA;
   prof_begin(K_NORM_BWD, a.s);
-  kernel<<<dim3(grid, slices), ss.tpr * ss.teams, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.mean, a.rstd,
-                                                              (const T*)a.dy, (const T*)a.dres, (T*)a.dx, dg, db,
-                                                              2LL * a.nm.n, a.sums);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kernel, a.nm, ss, static_cast<const T*>(a.x), a.gamma, a.mean, a.rstd,
+                         static_cast<const T*>(a.dy), static_cast<const T*>(a.dres), static_cast<T*>(a.dx), dg, db,
+                         (int64_t)2 * a.nm.n, a.sums);
   prof_end(K_NORM_BWD, a.s);
-  return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+  return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-// kKernel<mode> for rows of one slice, or sums first and then the rest.
-#define BWD_MODES(KERNEL, SMEM)                                                                      \
-  do {                                                                                               \
-    if (slices_of(a.nm.n) == 1) return launch_bwd<T, kWhole>(a, KERNEL(kWhole), ss, SMEM, shift, parts, blocks); \
-    const int rc = launch_bwd<T, kSums>(a, KERNEL(kSums), ss, SMEM, shift, parts, blocks);                  \
-    return rc ? rc : launch_bwd<T, kApply>(a, KERNEL(kApply), ss, SMEM, shift, parts, blocks);              \
-  } while (0)
-
-template <class T, int NV, bool shift>
+template <class T, int NV, RowFit kFit>
 int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, bool* parts, int* blocks) {
   constexpr int kS = bwd_stages<T>();
+  constexpr bool shift = kFit == kShift;
   const size_t smem = ring_bytes<kS, 3 * NV>(ss.tpr * ss.teams);
-  if constexpr (shift) {  // of one slice
-    return launch_bwd<T, kWhole>(a, norm_bwd_stream_kernel<T, NV, kS, kWhole, kShift>, ss, smem, shift, parts, blocks);
-  } else {
-#define KERNEL(MODE) norm_bwd_stream_kernel<T, NV, kS, MODE, kAligned>
-    BWD_MODES(KERNEL, smem);
-#undef KERNEL
-  }
+  const int64_t slices = ceil_div(a.nm.n, ss.slice);
+  if (slices == 1)
+    return launch_bwd<T, kWhole>(a, norm_bwd_stream_kernel<T, NV, kS, kWhole, kFit>, ss, smem, shift, parts, blocks);
+  if (slices <= kBwdCluster)
+    return launch_bwd<T, kCluster>(a, norm_bwd_stream_kernel<T, NV, kS, kCluster, kFit>, ss, smem, shift, parts, blocks);
+  const int rc = launch_bwd<T, kSums>(a, norm_bwd_stream_kernel<T, NV, kS, kSums, kFit>, ss, smem, shift, parts, blocks);
+  return rc ? rc
+            : launch_bwd<T, kApply>(a, norm_bwd_stream_kernel<T, NV, kS, kApply, kFit>, ss, smem, shift, parts, blocks);
 }
 
 template <class T, int kS>
 int launch_bwd_odd(const BwdArgs& a, bool* parts, int* blocks) {
   constexpr int kNP = kBwdColumns / 2;
-  constexpr bool shift = false;
   StreamShape ss;
   const size_t smem = odd_shape<T>(&ss, std::min(a.nm.n, kBwdSlice), kBwdColumns, kS, a.dres ? 3 : 2);
-#define KERNEL(MODE) norm_bwd_odd_kernel<T, kNP, kS, MODE>
-  BWD_MODES(KERNEL, smem);
-#undef KERNEL
+  ss.slice = kBwdSlice;
+  if (a.nm.n <= kBwdSlice)
+    return launch_bwd<T, kWhole>(a, norm_bwd_odd_kernel<T, kNP, kS, kWhole>, ss, smem, false, parts, blocks);
+  const int rc = launch_bwd<T, kSums>(a, norm_bwd_odd_kernel<T, kNP, kS, kSums>, ss, smem, false, parts, blocks);
+  return rc ? rc : launch_bwd<T, kApply>(a, norm_bwd_odd_kernel<T, kNP, kS, kApply>, ss, smem, false, parts, blocks);
 }
 
-template <class T, bool shift>
+template <class T, RowFit kFit>
 int pick_bwd_stream(const BwdArgs& a, bool* parts, int* blocks) {
   constexpr int VL = 16 / sizeof(T), kNV = kBwdColumns / VL;
-  const int slots = (int)ceil_div(std::min(a.nm.n, kBwdSlice) + (shift ? VL - 1 : 0), VL);
+  // equal slices of whole vectors; a shifted one may touch one vector more than it has
+  const int64_t room = kBwdSlice - (kFit == kShift ? VL : 0), slices = ceil_div(a.nm.n, room);
+  const int slice = (int)ceil_div(ceil_div(a.nm.n, slices), VL) * VL;
+  const int slots = (int)ceil_div(std::min(slice, a.nm.n) + (kFit == kShift ? VL - 1 : 0), VL);
   int nv = 0;
-  const StreamShape ss = stream_shape(slots, kNV, kBwdStreamThreads, &nv);
+  StreamShape ss = stream_shape(slots, kNV, kBwdStreamThreads, &nv);
+  ss.slice = slice;
   if constexpr (kNV == 4)
-    if (nv > 2) return nv == 3 ? launch_bwd_stream<T, 3, shift>(a, ss, parts, blocks) : launch_bwd_stream<T, 4, shift>(a, ss, parts, blocks);
-  return nv == 2 ? launch_bwd_stream<T, 2, shift>(a, ss, parts, blocks) : launch_bwd_stream<T, 1, shift>(a, ss, parts, blocks);
+    if (nv > 2)
+      return nv == 3 ? launch_bwd_stream<T, 3, kFit>(a, ss, parts, blocks) : launch_bwd_stream<T, 4, kFit>(a, ss, parts, blocks);
+  return nv == 2 ? launch_bwd_stream<T, 2, kFit>(a, ss, parts, blocks) : launch_bwd_stream<T, 1, kFit>(a, ss, parts, blocks);
+}
+
+// The teams of shifted rows step by whole multiples of eight blocks, which there must be
+// (of clusters, where the rows are wide).
+bool shifted_rows_fit(const BwdArgs& a) {
+  return std::min(a.sms, kNormParts) / ceil_div(a.nm.n, kBwdSlice - 8) >= 8;
 }
 
 template <class T>
@@ -1084,12 +1135,10 @@ int run_bwd(const BwdArgs& a) {
   // slower than the staged kernel: 1.7 against 2.8 TB/s at 16,384 x 2,049 bf16)
   const int64_t differ = (a.nm.ldx ^ a.nm.ldy) | (a.nm.ldx ^ a.nm.lddx) | (a.dres ? a.nm.ldx ^ a.nm.lddres : 0);
   const bool alike = (differ & kMask) == 0;
-  // one vector more than a slice's has to fit in a block
-  const bool fits = std::min(n, kBwdSlice) + kMask <= kBwdSlice && a.sms >= 8;
   if (rows_aligned(a.nm, true, a.dres != nullptr))
-    rc = pick_bwd_stream<T, false>(a, &parts, &blocks);
-  else if (alike && fits)
-    rc = pick_bwd_stream<T, true>(a, &parts, &blocks);
+    rc = pick_bwd_stream<T, kAligned>(a, &parts, &blocks);
+  else if (alike && shifted_rows_fit(a))
+    rc = pick_bwd_stream<T, kShift>(a, &parts, &blocks);
   else  // three stages of the widest slice of fp32 rows are more than shared memory holds
     rc = sizeof(T) == 4 && n > 4096 ? launch_bwd_odd<T, 2>(a, &parts, &blocks) : launch_bwd_odd<T, 3>(a, &parts, &blocks);
   return rc || !parts ? rc : launch_wgrad(n, blocks, a.part, a.dgamma, a.dbeta, a.s);

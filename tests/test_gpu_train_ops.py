@@ -50,7 +50,8 @@ NORM = [  # rows, n, dtype, weight type, gamma, beta, extra columns between rows
     (29, 1024, HF, F32, False, False, 8), (17, 1027, BF, BF, True, True, 5), (300, 2048, BF, F32, True, True, 8),
     (41, 2049, HF, F32, True, True, 6), (64, 4096, F32, F32, True, True, 0), (9, 8192, BF, BF, False, True, 0),
     (3, 12000, HF, HF, True, True, 0), (2, 16384, BF, BF, True, True, 16), (4, 16385, BF, F32, True, True, 0),
-    (2, 40000, F32, F32, True, True, 0), (700, 256, F32, BF, True, True, 0), (1500, 96, BF, HF, True, True, 4),
+    (2, 40000, F32, F32, True, True, 0), (3, 70000, BF, F32, True, True, 0), (2, 70001, HF, BF, True, True, 0),
+    (400, 9858, BF, BF, True, True, 8), (330, 8185, HF, F32, True, True, 7), (1300, 130, BF, F32, True, True, 1), (700, 256, F32, BF, True, True, 0), (1500, 96, BF, HF, True, True, 4),
 ]
 
 
