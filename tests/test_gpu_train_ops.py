@@ -630,3 +630,19 @@ def test_training_calls_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(out[n], want[n]) for n in out)
     assert math.isfinite(float(want["loss"]))
+
+
+def test_training_example_learns():
+    """The example's block: the loss falls, two runs agree bit for bit."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_block.py")
+    spec = importlib.util.spec_from_file_location("train_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    shp = ex.Shape(T=300, H=512, I=256, E=16, k=2, r=16)
+    losses, aux = ex.train(shp, 60)
+    assert all(math.isfinite(v) for v in losses + aux)
+    assert losses[-1] < 0.5 * losses[0], (losses[0], losses[-1])
+    again, _ = ex.train(shp, 5)
+    assert again == losses[:5]
