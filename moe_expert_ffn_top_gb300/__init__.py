@@ -547,7 +547,8 @@ def moe_lora_balance_loss(dims: Dims, logits: torch.Tensor, topk_ids: torch.Tens
         raise ValueError(f"adapter_offsets must have {A + 1} entries")
     rc = lib().moe_lora_balance_loss(dims, pl, _dtype(logits, "logits"), ld,
                                      _vec(topk_ids, T * dims.k, "topk_ids", torch.int32),
-                                     None if offs is None else offs.buffer_info()[0], coef, _vec(dloss, A, "dloss", torch.float32),
+                                     None if offs is None else offs.buffer_info()[0], coef,
+                                     _vec(dloss, A, "dloss", torch.float32),
                                      _vec(loss, A, "loss", torch.float32), _vec(counts, A * E, "counts", torch.int32),
                                      _vec(prob, A * E, "prob", torch.float32),
                                      _vec(dlogits, T * E, "dlogits", torch.float32),

@@ -305,7 +305,8 @@ int check_tensor(const moe_lora_adamw_tensor& t) {
     return rc;
   if (t.state == 1) {  // the scales are read one by one, and may be slices of larger arrays
     if (!t.m_scale || !t.v_scale) return MOE_LORA_ERR_NULL;
-    if ((reinterpret_cast<uintptr_t>(t.m_scale) | reinterpret_cast<uintptr_t>(t.v_scale)) & 3u) return MOE_LORA_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(t.m_scale) | reinterpret_cast<uintptr_t>(t.v_scale)) & 3u)
+      return MOE_LORA_ERR_ALIGN;
   }
   return MOE_LORA_OK;
 }
@@ -355,7 +356,7 @@ extern "C" int moe_lora_adamw_step(const moe_lora_adamw* o, const moe_lora_adamw
                                    void* stream) {
   if (!o || (n > 0 && !tensors)) return MOE_LORA_ERR_NULL;
   if (n < 0 || o->step < 1) return MOE_LORA_ERR_DIMS;
-  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !(o->eps > 0) || !isfinite(o->eps))
+  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !((float)o->eps > 0) || !isfinite((float)o->eps))
     return MOE_LORA_ERR_DIMS;
   int rc;
   if (reinterpret_cast<uintptr_t>(o->grad_scale) & 3u) return MOE_LORA_ERR_ALIGN;  // a scalar, often inside a buffer

@@ -246,7 +246,9 @@ struct Pairs {
     if (kMode == kWord && sizeof(T) == 2) return 2 * (lane + p * lpr);
     return lane + 2 * p * lpr;
   }
-  __device__ __forceinline__ int apart() const { return kMode == kVec16 || (kMode == kWord && sizeof(T) == 2) ? 1 : lpr; }
+  __device__ __forceinline__ int apart() const {
+    return kMode == kVec16 || (kMode == kWord && sizeof(T) == 2) ? 1 : lpr;
+  }
 };
 
 // One expert's mean probability, also to the block that adds the loss (rank 0 of a
@@ -255,7 +257,8 @@ template <int kC>
 __device__ __forceinline__ void finish_prob(const BalArgs& g, int a, int e, float p, float* psm) {
   g.prob[a * g.E + e] = p;
   if (kC > 1)
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(psm + e), 0)), "f"(p) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(psm + e), 0)), "f"(p)
+                 : "memory");
   else
     psm[e] = p;
 }
@@ -278,8 +281,9 @@ __device__ __forceinline__ void finish_loss(const BalArgs& g, int a, const float
 }
 
 // Loss, probabilities and the logits' gradient.  `lpr` lanes hold a row (4 to 32, so that
-// a lane has at most kVals logits); a lane has the same experts in every row, whose f and
-// sum of probabilities stay in its registers (kFull: rows fill every lane).
+// a lane has at most kVals logits and a row's three reductions take few shuffles); a lane
+// has the same experts in every row, whose f and sum of probabilities stay in its
+// registers (kFull: rows fill every lane).
 // kC: blocks of a cluster when one launch does it all, 0 as the second of three.
 template <class T, RowMode kMode, int kVals, int kC, bool kFull>
 __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
@@ -484,7 +488,8 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
       if constexpr (kMode == kVec16) {
 #pragma unroll
         for (int p = 0; p < kP; p += 2)
-          if (in(pr.first(p))) *reinterpret_cast<float4*>(dr + pr.first(p)) = make_float4(v[p].x, v[p].y, v[p + 1].x, v[p + 1].y);
+          if (in(pr.first(p)))
+            *reinterpret_cast<float4*>(dr + pr.first(p)) = make_float4(v[p].x, v[p].y, v[p + 1].x, v[p + 1].y);
       } else if constexpr (kMode == kWord && sizeof(T) == 2) {
 #pragma unroll
         for (int p = 0; p < kP; ++p)
@@ -726,7 +731,8 @@ extern "C" int moe_lora_balance_loss(const moe_lora_dims* d, const void* logits,
     bt.group0[a + 1] = bt.group0[a] + (int)groups;
   }
   bt.tok_off[d->A] = at.tok_off[d->A];
-  const BalArgs a{logits, ld, topk_ids, d->k, d->E, 0, coef, dloss, loss, counts, prob, dlogits, bal_scratch(d, scratch)};
+  const BalArgs a{logits, ld,   topk_ids, d->k, d->E,    0,
+                  coef,   dloss, loss,    counts, prob, dlogits, bal_scratch(d, scratch)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == MOE_LORA_F32    ? run_balance<float>(bt, a, s)
          : dtype == MOE_LORA_BF16 ? run_balance<__nv_bfloat16>(bt, a, s)

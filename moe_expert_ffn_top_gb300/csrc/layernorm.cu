@@ -1,5 +1,20 @@
 // Layer norm over rows of [rows, n], forward and backward (definitions in
 // include/moe_lora.h).
+//
+// Forward: mean, then the sum of squared deviations from it, both from the row in
+// registers (one pass over memory; a one-pass variance would cancel where the mean is
+// large).  Backward: with h = (x - mean) rstd and u = dy gamma, dx needs avg u and
+// avg(u h); dgamma = sum dy h and dbeta = sum dy run down the columns.  HBM is the bound:
+// 2 x 8 KB per 4,096-column bf16 row forward, 4 x 8 KB backward with the residual's
+// gradient.  Measured on one GB300 (copy bandwidth 6.78 TB/s): 65,536 x 4,096 bf16 forward
+// 160 us (6.7 TB/s, 99%), backward with dres and both weight gradients 325 us (6.6 TB/s,
+// 97%); one row of 4,096 2.7 us; 347 x 577 fp32 backward 7.0 us (two launches).
+//
+// Which kernel: rows that stream (norm_*_stream_kernel) when there are enough of them, or
+// always backward; norm_fwd_kernel for few rows, where a row spread over many threads is
+// faster than a ring that never fills (one row of 4,096 2.7 us; 1,024 rows 6.7 us); the
+// staged backward (norm_bwd_odd_kernel) where the tensors' strides differ modulo 16 bytes;
+// norm_fwd_long_kernel for forward rows beyond 8,192 vectors of a block's registers.
 #include <algorithm>
 
 #include "element.cuh"
@@ -247,14 +262,16 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
 // thread has the same columns in every row, so its weights stay in its registers.
 // Forward: 64 columns a thread, 255 registers: what a warp does once per row (sums,
 // addresses, waits) is half of the instructions at 32 columns (65,536 x 4,096 bf16: 163
-// us against 179 us, and 253 us at 16).  Backward: 16 columns and their two sums.
+// us against 179 us, and 253 us at 16).  Backward: 16 columns and their two sums (32
+// columns in 256 threads: 351 us against 328 us).
 constexpr int kFwdStreamThreads = 256, kFwdColumns = 64;
 constexpr int kBwdStreamThreads = 512, kBwdColumns = 16;
 constexpr int kOddThreads = 512;
-constexpr int kShiftRows = 256;  // from here on the streamed forward of shifted rows
+// From here on shifted rows stream forward (577 columns: 150 rows 3.3 us in registers, 256
+// rows 4.8 us streamed, 1,024 rows 5.0 us).
+constexpr int kShiftRows = 256;
 struct StreamShape {
   int tpr, teams;
-  int slice = 0;  // columns of a slice (backward)
 };
 
 // How rows lie on the 16-byte grid: as whole vectors that fill every slot of every thread
@@ -324,9 +341,9 @@ struct Columns {
 };
 
 template <class T, int NV, int kStages, RowFit kFit>
-__global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
-                                                                            Weight gamma, Weight beta, T* y,
-                                                                            float* mean, float* rstd) {
+__global__ void __launch_bounds__(kFwdStreamThreads, 1)
+    norm_fwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x, Weight gamma, Weight beta, T* y, float* mean,
+                           float* rstd) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   extern __shared__ __align__(16) uint8_t ring_sm[];
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
@@ -418,8 +435,8 @@ __global__ void __launch_bounds__(kFwdStreamThreads, 1) norm_fwd_stream_kernel(m
 // Rows wider than kBwdSlice are worked on in slices (blockIdx.y).  Up to eight slices are
 // a cluster (kCluster): its blocks exchange a row's sums through distributed shared
 // memory.  More take two launches: kSums leaves every slice's part of a row's sums in
-// `sums` [rows][slices], kApply adds them (and reads x and dy again: 16,384 columns bf16
-// 2.5 TB/s in two launches).
+// `sums` [rows][slices], kApply adds them and reads x and dy again (4,096 x 16,384 bf16:
+// 2.5 TB/s in two launches, 3.4 TB/s as clusters; fp32 3.5 and 5.4 TB/s).
 enum BwdMode { kWhole, kCluster, kSums, kApply };
 constexpr int kBwdSlice = kBwdStreamThreads * kBwdColumns;
 constexpr int kBwdCluster = 8;
@@ -437,8 +454,8 @@ struct SliceSums {
 };
 // A row's two sums over all slices, from this slice's; false: the row is done (kSums).
 template <BwdMode kMode, class Sum>
-__device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, float2* sums, int64_t r, bool on, int lane,
-                                         SliceSums* sm = nullptr, int team = 0, int buf = 0) {
+__device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, float2* sums, int64_t r, bool on,
+                                         int lane, SliceSums* sm = nullptr, int team = 0, int buf = 0) {
   if (kMode == kApply) {
     all = both(0.f);
     if (on)
@@ -477,16 +494,14 @@ __device__ __forceinline__ void store_wgrad(const float* acc, int teams, int n, 
 }
 
 template <class T, int NV, int kStages, BwdMode kMode, RowFit kFit>
-__global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
-                                                                            Weight gamma, const float* mean,
-                                                                            const float* rstd, const T* dy,
-                                                                            const T* dres, T* dx, float* dgamma,
-                                                                            float* dbeta, int64_t part_ld,
-                                                                            float2* sums) {
+__global__ void __launch_bounds__(kBwdStreamThreads, 1)
+    norm_bwd_stream_kernel(moe_lora_norm nm, StreamShape ss, const T* x, Weight gamma, const float* mean,
+                           const float* rstd, const T* dy, const T* dres, T* dx, float* dgamma, float* dbeta,
+                           int64_t part_ld, float2* sums, int slice) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   extern __shared__ __align__(16) uint8_t ring_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const Slice<kMode> sl(nm.n, ss.slice);
+  const Slice<kMode> sl(nm.n, slice);
   const int n = sl.n;
   if (kMode != kWhole) {
     x += sl.first;
@@ -561,7 +576,8 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
           }
         }
     float2 t;
-    const bool more = row_sums<kMode>(sum, make_float2(su.x + su.y, sh.x + sh.y), t, sums, r, on, lane, &slice_sm, team, buf);
+    const bool more =
+        row_sums<kMode>(sum, make_float2(su.x + su.y, sh.x + sh.y), t, sums, r, on, lane, &slice_sm, team, buf);
     buf ^= 1;
     const float2 na = both(-t.x * rn), nb = both(-t.y * rn);
     if (on && more) {
@@ -613,12 +629,14 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1) norm_bwd_stream_kernel(m
   store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at : nullptr, dbeta ? dbeta + at : nullptr);
 }
 
-// The backward where the tensors' rows lie on the 16-byte grid in different ways, or wide
-// rows off it.  A team copies the aligned 16-byte pieces that cover a row, what lies before its start in
-// the first piece included (never before the tensor's: that start is aligned), nothing
-// past its end; then every thread reads its elements, tpr columns apart.  Pieces are read
-// by other threads than copied them, so a team meets when a row has come, and a stage is
-// refilled only after the sums of the next row, which all of the team have to reach.
+// The backward where the tensors' rows lie on the 16-byte grid in different ways, so that
+// no vector of one matches a vector of the others.  A team copies the aligned 16-byte
+// pieces that cover a row, what lies before its start in the first piece included (never
+// before the tensor's: that start is aligned), nothing past its end; then every thread
+// reads its elements, tpr columns apart.  Pieces are read by other threads than copied
+// them, so a team meets when a row has come, and a stage is refilled only after the sums
+// of the next row, which all of the team have to reach.  2.4-3.5 TB/s at 1,024 to 4,096
+// columns bf16, bound by instructions.
 template <class T>
 struct OddStage {
   char* base;  // of this team; stages of `tensors` pieces of `cap` bytes
@@ -643,15 +661,15 @@ __device__ __forceinline__ float2 odd_pair(const T* row, const SlotAt<1>& at) {
 }
 
 template <class T, int NP, int kStages, BwdMode kMode>
-__global__ void __launch_bounds__(kOddThreads, 1) norm_bwd_odd_kernel(moe_lora_norm nm, StreamShape ss, const T* x,
-                                                                      Weight gamma, const float* mean,
-                                                                      const float* rstd, const T* dy, const T* dres,
-                                                                      T* dx, float* dgamma, float* dbeta,
-                                                                      int64_t part_ld, float2* sums) {
+__global__ void __launch_bounds__(kOddThreads, 1)
+    norm_bwd_odd_kernel(moe_lora_norm nm, StreamShape ss, const T* x, Weight gamma, const float* mean,
+                        const float* rstd, const T* dy, const T* dres, T* dx, float* dgamma, float* dbeta,
+                        int64_t part_ld, float2* sums, int slice) {
   extern __shared__ __align__(16) char stage_sm[];  // afterwards: the teams' sums [teams][2][n]
   __shared__ __align__(16) float red[kMaxTeams * 2 * RowSum::kRedWords];
-  const Slice<kMode> sl(nm.n, ss.slice);
-  const int n = sl.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr, tensors = kMode != kSums && dres ? 3 : 2;
+  const Slice<kMode> sl(nm.n, slice);
+  const int n = sl.n, lane = threadIdx.x % ss.tpr, team = threadIdx.x / ss.tpr;
+  const int tensors = kMode != kSums && dres ? 3 : 2;
   if (kMode != kWhole) {
     x += sl.first;
     dy += sl.first;
@@ -875,8 +893,9 @@ int launch_fwd(const FwdArgs& a, const RowShape& rs) {
 
 constexpr size_t kMaxSmem = 216 * 1024;  // dynamic, beside the kernels' static 8 KB
 
-// Stages of the rings: three rows of copies under way per team (two in fp32), 96 KB per SM
-// at full width; an SM needs about 45 KB to hide the memory's latency.
+// Stages of the rings: 64 to 128 KB of copies under way per SM at full width, where an SM
+// needs about 45 KB to hide the memory's latency (65,536 x 4,096 bf16 backward: three
+// stages 328 us, four 331 us; forward: two 173 us, three 164-168 us, four 161 us).
 template <class T>
 constexpr int fwd_stages() { return sizeof(T) == 2 ? 4 : 3; }
 template <class T>
@@ -885,8 +904,7 @@ constexpr int bwd_stages() { return sizeof(T) == 2 ? 3 : 2; }
 // Threads of a row of `slots` slots and, in *nv, slots per thread (`most` at most, even
 // beyond 4 for fp32's many).  What a warp does once per row costs about three slots.
 StreamShape stream_shape(int slots, int most, int threads, int* nv) {
-  StreamShape best;
-  best.tpr = best.teams = 0;
+  StreamShape best = {0, 0};
   float cost = 0.f;
   for (int tpr = 8; tpr <= threads; tpr = tpr < 32 ? 2 * tpr : tpr + 32) {
     int v = (int)ceil_div(slots, tpr);
@@ -894,8 +912,7 @@ StreamShape stream_shape(int slots, int most, int threads, int* nv) {
     if (most > 8 && v > 4) v += v & 1;
     const float c = (3.f + v) / (threads / tpr);
     if (!best.tpr || c < cost) {
-      best.tpr = tpr;
-      best.teams = threads / tpr;
+      best = StreamShape{tpr, threads / tpr};
       cost = c;
       *nv = v;
     }
@@ -1034,11 +1051,11 @@ struct BwdArgs {
 
 // One kernel over all rows (of one slice, or of every slice).
 template <class T, BwdMode kMode, class Kernel>
-int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t smem, bool shift, bool* parts,
-               int* blocks) {
-  const int slices = (int)ceil_div(a.nm.n, ss.slice);
+int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, int slice, size_t smem, bool shift,
+               bool* parts, int* blocks) {
+  const int slices = (int)ceil_div(a.nm.n, slice);
   const bool wgrad = kMode != kSums && (a.dgamma || a.dbeta);
-  smem = std::max(smem, wgrad ? 2 * sizeof(float) * ss.teams * std::min(a.nm.n, ss.slice) : 0);
+  smem = std::max(smem, wgrad ? 2 * sizeof(float) * ss.teams * std::min(a.nm.n, slice) : 0);
   if (smem > 32 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_LORA_ERR_CUDA;
@@ -1071,24 +1088,23 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, size_t sm
   const cudaError_t e =
       cudaLaunchKernelEx(&cfg, kernel, a.nm, ss, static_cast<const T*>(a.x), a.gamma, a.mean, a.rstd,
                          static_cast<const T*>(a.dy), static_cast<const T*>(a.dres), static_cast<T*>(a.dx), dg, db,
-                         (int64_t)2 * a.nm.n, a.sums);
+                         (int64_t)2 * a.nm.n, a.sums, slice);
   prof_end(K_NORM_BWD, a.s);
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
 template <class T, int NV, RowFit kFit>
-int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, bool* parts, int* blocks) {
+int launch_bwd_stream(const BwdArgs& a, const StreamShape& ss, int slice, bool* parts, int* blocks) {
   constexpr int kS = bwd_stages<T>();
-  constexpr bool shift = kFit == kShift;
   const size_t smem = ring_bytes<kS, 3 * NV>(ss.tpr * ss.teams);
-  const int64_t slices = ceil_div(a.nm.n, ss.slice);
-  if (slices == 1)
-    return launch_bwd<T, kWhole>(a, norm_bwd_stream_kernel<T, NV, kS, kWhole, kFit>, ss, smem, shift, parts, blocks);
-  if (slices <= kBwdCluster)
-    return launch_bwd<T, kCluster>(a, norm_bwd_stream_kernel<T, NV, kS, kCluster, kFit>, ss, smem, shift, parts, blocks);
-  const int rc = launch_bwd<T, kSums>(a, norm_bwd_stream_kernel<T, NV, kS, kSums, kFit>, ss, smem, shift, parts, blocks);
-  return rc ? rc
-            : launch_bwd<T, kApply>(a, norm_bwd_stream_kernel<T, NV, kS, kApply, kFit>, ss, smem, shift, parts, blocks);
+  const int64_t slices = ceil_div(a.nm.n, slice);
+#define RUN(MODE)                                                                                              \
+  launch_bwd<T, MODE>(a, norm_bwd_stream_kernel<T, NV, kS, MODE, kFit>, ss, slice, smem, kFit == kShift, parts, blocks)
+  if (slices == 1) return RUN(kWhole);
+  if (slices <= kBwdCluster) return RUN(kCluster);
+  const int rc = RUN(kSums);
+  return rc ? rc : RUN(kApply);
+#undef RUN
 }
 
 template <class T, int kS>
@@ -1096,11 +1112,12 @@ int launch_bwd_odd(const BwdArgs& a, bool* parts, int* blocks) {
   constexpr int kNP = kBwdColumns / 2;
   StreamShape ss;
   const size_t smem = odd_shape<T>(&ss, std::min(a.nm.n, kBwdSlice), kBwdColumns, kS, a.dres ? 3 : 2);
-  ss.slice = kBwdSlice;
-  if (a.nm.n <= kBwdSlice)
-    return launch_bwd<T, kWhole>(a, norm_bwd_odd_kernel<T, kNP, kS, kWhole>, ss, smem, false, parts, blocks);
-  const int rc = launch_bwd<T, kSums>(a, norm_bwd_odd_kernel<T, kNP, kS, kSums>, ss, smem, false, parts, blocks);
-  return rc ? rc : launch_bwd<T, kApply>(a, norm_bwd_odd_kernel<T, kNP, kS, kApply>, ss, smem, false, parts, blocks);
+#define RUN(MODE) \
+  launch_bwd<T, MODE>(a, norm_bwd_odd_kernel<T, kNP, kS, MODE>, ss, kBwdSlice, smem, false, parts, blocks)
+  if (a.nm.n <= kBwdSlice) return RUN(kWhole);
+  const int rc = RUN(kSums);
+  return rc ? rc : RUN(kApply);
+#undef RUN
 }
 
 template <class T, RowFit kFit>
@@ -1111,12 +1128,13 @@ int pick_bwd_stream(const BwdArgs& a, bool* parts, int* blocks) {
   const int slice = (int)ceil_div(ceil_div(a.nm.n, slices), VL) * VL;
   const int slots = (int)ceil_div(std::min(slice, a.nm.n) + (kFit == kShift ? VL - 1 : 0), VL);
   int nv = 0;
-  StreamShape ss = stream_shape(slots, kNV, kBwdStreamThreads, &nv);
-  ss.slice = slice;
-  if constexpr (kNV == 4)
-    if (nv > 2)
-      return nv == 3 ? launch_bwd_stream<T, 3, kFit>(a, ss, parts, blocks) : launch_bwd_stream<T, 4, kFit>(a, ss, parts, blocks);
-  return nv == 2 ? launch_bwd_stream<T, 2, kFit>(a, ss, parts, blocks) : launch_bwd_stream<T, 1, kFit>(a, ss, parts, blocks);
+  const StreamShape ss = stream_shape(slots, kNV, kBwdStreamThreads, &nv);
+  if (nv == 1) return launch_bwd_stream<T, 1, kFit>(a, ss, slice, parts, blocks);
+  if constexpr (kNV == 4) {
+    if (nv == 3) return launch_bwd_stream<T, 3, kFit>(a, ss, slice, parts, blocks);
+    if (nv == 4) return launch_bwd_stream<T, 4, kFit>(a, ss, slice, parts, blocks);
+  }
+  return launch_bwd_stream<T, 2, kFit>(a, ss, slice, parts, blocks);
 }
 
 // The teams of shifted rows step by whole multiples of eight blocks, which there must be
@@ -1140,7 +1158,8 @@ int run_bwd(const BwdArgs& a) {
   else if (alike && shifted_rows_fit(a))
     rc = pick_bwd_stream<T, kShift>(a, &parts, &blocks);
   else  // three stages of the widest slice of fp32 rows are more than shared memory holds
-    rc = sizeof(T) == 4 && n > 4096 ? launch_bwd_odd<T, 2>(a, &parts, &blocks) : launch_bwd_odd<T, 3>(a, &parts, &blocks);
+    rc = sizeof(T) == 4 && n > 4096 ? launch_bwd_odd<T, 2>(a, &parts, &blocks)
+                                    : launch_bwd_odd<T, 3>(a, &parts, &blocks);
   return rc || !parts ? rc : launch_wgrad(n, blocks, a.part, a.dgamma, a.dbeta, a.s);
 }
 
