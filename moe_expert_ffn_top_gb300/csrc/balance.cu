@@ -648,12 +648,9 @@ int launch_balance(const BalTable& bt, const BalArgs& a, cudaStream_t s) {
   constexpr int kT = block_threads(kVals);
   const size_t ring = kMode == kElement ? 0 : (size_t)kT * kBalStages * kVals * sizeof(T);
   const size_t smem = std::max(ring, sizeof(float) * (kT / a.lpr) * (a.E + kSumPad));
-  if (smem > 32 * 1024)  // with the static part above what a launch may use without asking
-    LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  if (kC > 8) LAUNCH(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   const BalLaunch l((int64_t)bt.group0[bt.n] * (kC ? kC : kBalCluster), kT, smem, kC, kC == 0, s);
   prof_begin(K_BAL_LOSS, s);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, bt, a);
+  const cudaError_t e = launch_allowed(l.cfg, (kC > 8), kernel, bt, a);
   prof_end(K_BAL_LOSS, s);
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }

@@ -479,18 +479,38 @@ __device__ __forceinline__ bool row_sums(Sum& sum, float2 mine, float2& all, flo
   return false;
 }
 // A block's sums of the weight gradients from its teams' [teams][2][n] in shared memory
-// (`acc`, 16 columns of either per thread), teams in order.
-__device__ __forceinline__ void store_wgrad(const float* acc, int teams, int n, float* dgamma, float* dbeta) {
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * n; i += blockDim.x) {
-    float v = acc[i];
-    for (int k = 1; k < teams; ++k) v += acc[(int64_t)k * 2 * n + i];
+// (`acc`, 16 columns of either per thread), teams in order: to dgamma / dbeta, or, where
+// all blocks are one cluster (`together`), first added over the blocks in order.
+__device__ __forceinline__ void store_wgrad(float* acc, int teams, int n, float* dgamma, float* dbeta, bool together) {
+  const auto store = [&](int i, float v) {
     if (i < n) {
       if (dgamma) dgamma[i] = v;
     } else if (dbeta) {
       dbeta[i - n] = v;
     }
+  };
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * n; i += blockDim.x) {
+    float v = acc[i];
+    for (int k = 1; k < teams; ++k) v += acc[(int64_t)k * 2 * n + i];
+    if (together)
+      acc[i] = v;
+    else
+      store(i, v);
   }
+  if (!together) return;
+  cluster_sync_all();
+  const int ranks = gridDim.x, per = (2 * n + ranks - 1) / ranks, end = min(2 * n, (int)(blockIdx.x + 1) * per);
+  for (int i = blockIdx.x * per + threadIdx.x; i < end; i += blockDim.x) {
+    float v = 0.f;
+    for (int k = 0; k < ranks; ++k) {
+      float u;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(mapa_shared(smem_u32(acc + i), k)) : "memory");
+      v += u;
+    }
+    store(i, v);
+  }
+  cluster_sync_all();  // nobody leaves while its sums are read
 }
 
 template <class T, int NV, int kStages, BwdMode kMode, RowFit kFit>
@@ -626,7 +646,8 @@ __global__ void __launch_bounds__(kBwdStreamThreads, 1)
         *reinterpret_cast<float4*>(ab + e) = make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
       }
   const int64_t at = blockIdx.x * part_ld + sl.first;
-  store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at : nullptr, dbeta ? dbeta + at : nullptr);
+  store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at : nullptr, dbeta ? dbeta + at : nullptr,
+              kMode == kWhole && part_ld == 0);
 }
 
 // The backward where the tensors' rows lie on the 16-byte grid in different ways, so that
@@ -761,7 +782,8 @@ __global__ void __launch_bounds__(kOddThreads, 1)
     }
   }
   const int64_t at0 = blockIdx.x * part_ld + sl.first;
-  store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at0 : nullptr, dbeta ? dbeta + at0 : nullptr);
+  store_wgrad(acc, ss.teams, n, dgamma ? dgamma + at0 : nullptr, dbeta ? dbeta + at0 : nullptr,
+              kMode == kWhole && part_ld == 0);
 }
 
 // dgamma and dbeta (blockIdx.y) from the blocks' partial rows: 32 columns per block,
@@ -937,13 +959,16 @@ int launch_fwd_stream(const FwdArgs& a, const StreamShape& ss, bool shift) {
                               : norm_fwd_stream_kernel<T, NV, kS, kAligned>;
   const int threads = ss.tpr * ss.teams;
   const size_t smem = ring_bytes<fwd_stages<T>(), NV>(threads);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_LORA_ERR_CUDA;
-  const int grid = stream_grid(a.nm.rows, ss.teams, a.sms, shift);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(stream_grid(a.nm.rows, ss.teams, a.sms, shift));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.s;
   prof_begin(K_NORM_FWD, a.s);
-  kernel<<<grid, threads, smem, a.s>>>(a.nm, ss, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd);
+  const cudaError_t e = launch_allowed(cfg, false, kernel, a.nm, ss, static_cast<const T*>(a.x), a.gamma, a.beta,
+                                       static_cast<T*>(a.y), a.mean, a.rstd);
   prof_end(K_NORM_FWD, a.s);
-  return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
+  return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
 // Shared memory of the staged kernels: as many teams as fit.
@@ -1056,9 +1081,6 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, int slice
   const int slices = (int)ceil_div(a.nm.n, slice);
   const bool wgrad = kMode != kSums && (a.dgamma || a.dbeta);
   smem = std::max(smem, wgrad ? 2 * sizeof(float) * ss.teams * std::min(a.nm.n, slice) : 0);
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_LORA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3(1, slices);
@@ -1074,21 +1096,42 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, int slice
     cfg.numAttrs = 1;
     // as many clusters as run together (fewer than blocks would: a cluster stays inside one
     // processing cluster); one more is a second wave as long as the first
-    int together = 0;
-    if (cudaOccupancyMaxActiveClusters(&together, kernel, &cfg) != cudaSuccess) return MOE_LORA_ERR_CUDA;
-    most = std::max(1, std::min(most, together));
+    int fit = 0;
+    if (allow_options(reinterpret_cast<const void*>(kernel), smem, false) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess)
+      return MOE_LORA_ERR_CUDA;
+    most = std::max(1, std::min(most, fit));
   }
-  const int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
+  int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
+  // Few rows: at most sixteen blocks, a cluster, add the weight gradients themselves.  The
+  // second launch that this saves costs the host 2.3 us; a team's second and third row
+  // cost the GPU about 1.2 us each where rows are short (347 x 577 fp32, three rows a team:
+  // a call 9.7 us against 12.0 us, on the GPU alone 9.4 us against 7.2 us), more where they
+  // are long.
+  bool together = false;
+  if (kMode == kWhole && wgrad && grid > 1) {
+    int cluster = 2;
+    while (cluster < 16 && cluster < grid) cluster *= 2;
+    together = ceil_div(a.nm.rows, (int64_t)ss.teams * cluster) <= (ss.teams >= 4 ? 3 : 2);
+    if (together) {
+      grid = cluster;
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = cluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+    }
+  }
   cfg.gridDim.x = grid;
-  *parts = wgrad && grid > 1;
+  *parts = wgrad && grid > 1 && !together;
   *blocks = grid;
   float* dg = !wgrad ? nullptr : *parts ? a.part : a.dgamma;
   float* db = !wgrad ? nullptr : *parts ? a.part + a.nm.n : a.dbeta;
   prof_begin(K_NORM_BWD, a.s);
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, kernel, a.nm, ss, static_cast<const T*>(a.x), a.gamma, a.mean, a.rstd,
-                         static_cast<const T*>(a.dy), static_cast<const T*>(a.dres), static_cast<T*>(a.dx), dg, db,
-                         (int64_t)2 * a.nm.n, a.sums, slice);
+  const cudaError_t e = launch_allowed(
+      cfg, together && grid > 8, kernel, a.nm, ss, static_cast<const T*>(a.x), a.gamma, a.mean, a.rstd,
+      static_cast<const T*>(a.dy), static_cast<const T*>(a.dres), static_cast<T*>(a.dx), dg, db,
+      *parts ? (int64_t)2 * a.nm.n : 0, a.sums, slice);
   prof_end(K_NORM_BWD, a.s);
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
