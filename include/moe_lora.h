@@ -53,7 +53,7 @@ extern "C" {
 #define MOE_LORA_ERR_DIMS (-2)        /* unsupported or inconsistent sizes */
 #define MOE_LORA_ERR_ALIGN (-3)       /* a pointer is not 16-byte aligned */
 #define MOE_LORA_ERR_WORKSPACE (-4)   /* a workspace is smaller than required */
-#define MOE_LORA_ERR_UNSUPPORTED (-5) /* activation / base format not supported */
+#define MOE_LORA_ERR_UNSUPPORTED (-5) /* activation / base format / element type not supported */
 #define MOE_LORA_ERR_CUDA (-6)        /* a CUDA call or kernel launch failed */
 #define MOE_LORA_ERR_DEVICE (-7)      /* current device is not an sm_103 GPU */
 #define MOE_LORA_ERR_SCRATCH_LIMIT (-8) /* sizes exceed moe_lora_plan_noalloc's fixed scratch */

@@ -368,7 +368,7 @@ const char* moe_lora_strerror(int code) {
     case MOE_LORA_ERR_DIMS: return "unsupported or inconsistent sizes";
     case MOE_LORA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case MOE_LORA_ERR_WORKSPACE: return "a workspace is smaller than required";
-    case MOE_LORA_ERR_UNSUPPORTED: return "unsupported activation or base format";
+    case MOE_LORA_ERR_UNSUPPORTED: return "unsupported activation, base format or element type";
     case MOE_LORA_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case MOE_LORA_ERR_DEVICE: return "the current device is not an sm_103 GPU";
     case MOE_LORA_ERR_SCRATCH_LIMIT: return "sizes exceed the fixed scratch of moe_lora_plan_noalloc";

@@ -49,6 +49,19 @@ def test_norm_backward_rejections(L, code, norm, over):
                                          None) == code
 
 
+def test_norm_backward_of_wide_rows_needs_scratch(L):
+    """Beyond 8,192 columns also without weight gradients."""
+    for n, code in ((8192, None), (8193, -1)):
+        nm = _norm(n=n)
+        rc = L.moe_lora_layernorm_backward(nm, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, None, None, None, 0, None)
+        assert rc == -1  # mean is NULL in both
+        if code:
+            assert L.moe_lora_layernorm_backward(nm, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, None, None, None, 0,
+                                                 None) == code
+            assert L.moe_lora_layernorm_backward(nm, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, None, None, FAKE, 64,
+                                                 None) == -4
+
+
 def test_norm_scratch_sizes(L):
     assert L.moe_lora_layernorm_scratch_bytes(_norm()) >= 8 * 64
     assert L.moe_lora_layernorm_scratch_bytes(_norm(n=0)) == 0
