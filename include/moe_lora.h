@@ -415,7 +415,7 @@ typedef struct moe_lora_adamw_tensor {
 
 typedef struct moe_lora_adamw {
   double beta1, beta2; /* in [0, 1) */
-  double eps;          /* > 0, also in fp32 */
+  double eps;          /* >= 2^-126 (a normal number in fp32) */
   int64_t step;        /* 1 for the first step */
   const float* grad_scale; /* DEVICE scalar (e.g. a clipping factor; 4-byte aligned), or NULL for 1 */
 } moe_lora_adamw;

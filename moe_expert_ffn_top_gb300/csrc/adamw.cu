@@ -8,6 +8,7 @@
 // code conversions are half of them).  Measured on one GB300: 203 M elements with 8-bit
 // moments 570 us (6.4 TB/s, 95% of the measured copy bandwidth); 96 tensors of 38.6 M
 // elements with 32-bit moments 130 us (96%).
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -149,7 +150,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float& scale) {
 // -0 changes nothing.  The quotient is
 // the fast one, to 2 units in the last place of the update (203 M elements with 8-bit
 // moments: 570 us against 629 us with the correctly rounded one); its divisor lies
-// between eps and 2^126, the range that the fast one takes.
+// between eps (2^-126 at least) and 2^126, the range that the fast one takes.
 __device__ __forceinline__ void adam_pair(const AdamHyper& h, float decay, float lr, float2 g, float2& m, float2& v,
                                           float2& r, float2& w) {
   const auto mul = [&](float2 a, float2 b) { return fma2(a, b, both(h.minus0)); };
@@ -356,8 +357,9 @@ extern "C" int moe_lora_adamw_step(const moe_lora_adamw* o, const moe_lora_adamw
                                    void* stream) {
   if (!o || (n > 0 && !tensors)) return MOE_LORA_ERR_NULL;
   if (n < 0 || o->step < 1) return MOE_LORA_ERR_DIMS;
-  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !((float)o->eps > 0) || !isfinite((float)o->eps))
-    return MOE_LORA_ERR_DIMS;
+  if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1)) return MOE_LORA_ERR_DIMS;
+  // A subnormal eps would be outside the fast quotient's range: 0 / eps would be NaN.
+  if (!((float)o->eps >= FLT_MIN) || !isfinite((float)o->eps)) return MOE_LORA_ERR_DIMS;
   int rc;
   if (reinterpret_cast<uintptr_t>(o->grad_scale) & 3u) return MOE_LORA_ERR_ALIGN;  // a scalar, often inside a buffer
   for (int i = 0; i < n; ++i)

@@ -113,7 +113,7 @@ def _tensor(**kw):
 
 @pytest.mark.parametrize("code,opt,over", [
     (-2, dict(step=0), {}), (-2, dict(beta1=1.0), {}), (-2, dict(beta2=-0.1), {}), (-2, dict(eps=0.0), {}),
-    (-2, dict(eps=float("nan")), {}), (-2, dict(eps=1e-60), {}), (-3, dict(grad_scale=FAKE + 2), {}), (-2, {}, dict(numel=-1)),
+    (-2, dict(eps=float("nan")), {}), (-2, dict(eps=1e-60), {}), (-2, dict(eps=1e-39), {}), (-3, dict(grad_scale=FAKE + 2), {}), (-2, {}, dict(numel=-1)),
     (-5, {}, dict(p_dtype=4)), (-5, {}, dict(g_dtype=-1)), (-5, {}, dict(state=2)), (-5, {}, dict(p_dtype=0)),
     (-2, {}, dict(lr=float("nan"))), (-2, {}, dict(weight_decay=float("inf"))), (-1, {}, dict(p=None)),
     (-1, {}, dict(g=None)), (-1, {}, dict(m=None)), (-1, {}, dict(v=None)), (-1, {}, dict(m_scale=None)),
