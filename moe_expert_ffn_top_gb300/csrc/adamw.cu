@@ -3,11 +3,12 @@
 //
 // Every element is read and written once: 18 bytes with 8-bit moments, fp32 gradients
 // and master weights and a bf16 copy (and 16 per block for its scales), 22 with 32-bit
-// moments, bf16 weights and gradients.  HBM is the bound, the instructions are
-// close behind (about 60 per element and lane; the square root, the quotient and the
-// code conversions are half of them).  Measured on one GB300: 203 M elements with 8-bit
-// moments 570 us (6.4 TB/s, 95% of the measured copy bandwidth); 96 tensors of 38.6 M
-// elements with 32-bit moments 130 us (96%).
+// moments, bf16 weights and gradients.  HBM is the bound; with 8-bit moments the
+// instructions are close behind (69 per element and lane; the square root and the code
+// conversions are half of them), and lead where weights and gradients have 16 bits.
+// Measured on one GB300: 203 M elements with 8-bit moments 539 us (6.8 TB/s, the measured
+// copy bandwidth); 96 tensors of 38.6 M elements with 32-bit moments 130 us (96% of it);
+// 11.5 M elements of 10 bytes each, 8-bit moments with bf16 weights alone, 32 us (53%).
 #include <float.h>
 #include <math.h>
 
@@ -63,6 +64,16 @@ struct Raw8 {
     const char* q = static_cast<const char*>(p) + (dtype == MOE_LORA_F32 ? 4 : 2) * i;
     a = *reinterpret_cast<const uint4*>(q);
     if (dtype == MOE_LORA_F32) b = *reinterpret_cast<const uint4*>(q + 16);
+  }
+  // this lane's eight of a warp's 256 elements in shared memory, 32 lanes' 16 bytes to a row
+  __device__ __forceinline__ void get(const uint4* row, int dtype) {
+    const int lane = threadIdx.x & 31;
+    if (dtype == MOE_LORA_F32) {
+      a = row[2 * lane];
+      b = row[2 * lane + 1];
+    } else {
+      a = row[lane];
+    }
   }
   __device__ __forceinline__ void widen(int dtype, float (&f)[8]) const {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -124,33 +135,53 @@ __device__ __forceinline__ void block_scale(float top, float& inv, float& scale)
   inv = some ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
   scale = some ? __fmul_rn(top, 1.0f / 448.0f) : 0.f;
 }
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < INFINITY ? a : 0.f;
+__device__ __forceinline__ uint32_t warp_max(float v) {  // v >= 0 or NaN: ordered as its bits, NaN last
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(v));
 }
-__device__ __forceinline__ float warp_top(float v) {  // v >= 0: ordered as its bits
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-}
-// Codes of a warp's block (this lane's eight values) and its scale.  x - x makes the NaN
-// code of what is not finite; the conversion alone would saturate an infinity.
+// Codes of a warp's block (this lane's eight values) and its scale.  All values are as
+// good as always finite: the largest magnitude, NaN above all, tells, and only a block
+// with one that is not looks at its elements one by one, for its scale and for the NaN
+// codes (the conversion would saturate an infinity).
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float& scale) {
-  float top = 0.f, inv, q[8];
+  float t = 0.f, inv;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(x[i]));
-  block_scale(warp_top(top), inv, scale);
+  for (int i = 0; i < 8; i += 2)
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(t) : "f"(t), "f"(x[i]), "f"(x[i + 1]));
+  uint32_t top = warp_max(t), nan[2] = {0, 0};
+  if (top >= 0x7f800000u) {
+    t = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = __fadd_rn(__fmul_rn(x[i], inv), __fsub_rn(x[i], x[i]));
-  return make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
+    for (int i = 0; i < 8; ++i) {
+      if (fabsf(x[i]) < INFINITY)
+        t = fmaxf(t, fabsf(x[i]));
+      else
+        nan[i >> 2] |= 0x7fu << (8 * (i & 3));
+    }
+    top = warp_max(t);
+  }
+  block_scale(__uint_as_float(top), inv, scale);
+  float2 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(inv));
+  return make_uint2(e4m3x2(q[0].x, q[0].y) | e4m3x2(q[1].x, q[1].y) << 16 | nan[0],
+                    e4m3x2(q[2].x, q[2].y) | e4m3x2(q[3].x, q[3].y) << 16 | nan[1]);
+}
+
+// 1 / d to one unit in the last place, for d in [2^-126, 2^126] (0 above it)
+__device__ __forceinline__ float rcp_fast(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
 }
 
 // Two elements: new moments (v as its root r too) and weights.  Every product and sum is
 // rounded on its own, so that the moments, and with them the 8-bit codes, are the
 // formula's in fp32 bit for bit.  The assembler fuses mul.f32x2 with add.f32x2 (seen in
 // results); a product with -0 added, a value it does not know, it leaves alone, and the
-// -0 changes nothing.  The quotient is
-// the fast one, to 2 units in the last place of the update (203 M elements with 8-bit
-// moments: 570 us against 629 us with the correctly rounded one); its divisor lies
-// between eps (2^-126 at least) and 2^126, the range that the fast one takes.
+// -0 changes nothing.  The quotient is a product with the fast reciprocal, to 2 units in
+// the last place of the update (203 M elements with 8-bit moments: 539 us, with
+// __fdividef 546 us, and the correctly rounded quotient was 59 us slower than that); its
+// divisor lies between eps (2^-126 at least) and 2^126, the range that rcp_fast takes.
 __device__ __forceinline__ void adam_pair(const AdamHyper& h, float decay, float lr, float2 g, float2& m, float2& v,
                                           float2& r, float2& w) {
   const auto mul = [&](float2 a, float2 b) { return fma2(a, b, both(h.minus0)); };
@@ -158,68 +189,144 @@ __device__ __forceinline__ void adam_pair(const AdamHyper& h, float decay, float
   v = add2(mul(both(h.b2), v), mul(mul(both(h.c2), g), g));
   r = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
   const float2 d = add2(mul(r, both(h.rbc2)), both(h.eps));
-  const float2 u = make_float2(__fdividef(m.x, d.x), __fdividef(m.y, d.y));
+  const float2 u = mul(m, make_float2(rcp_fast(d.x), rcp_fast(d.y)));
   w = add2(mul(w, both(decay)), mul(both(-lr), u));
 }
 
 // A block takes chunks of eight 256-element blocks of one tensor in turn, a warp one of
 // the eight, a lane eight consecutive elements of it.  The tensor is the same for the
 // whole block: its table entry is read through the uniform path.
+//
+// 8-bit moments: their arithmetic is as long as the memory takes, so a warp's next block is
+// copied into the warp's own shared memory (two stages) while it works on this one.  The 32
+// lanes copy 512 bytes side by side and pick up their own eight elements afterwards; with
+// two copies of 16 bytes a lane, 32 bytes apart, 203 M elements took 810 us.  Measured so,
+// and loaded when needed: 203 M elements with fp32 gradients and master weights 539 and
+// 578 us, 11.5 M with fp16 gradients and bf16 weights alone 32.0 and 32.9 us.  Three blocks
+// an SM: with four the 203 M elements took 633 us (the reads ahead of all of them get in
+// each other's way in memory).  With the stores through shared memory as well: 548 us.
+// 32-bit moments: loaded when needed, four blocks an SM (38.6 M elements 130 us; copied
+// ahead 142 us).
+constexpr int kAdamSlots = 5;  // 16 bytes a lane: gradient, weight (two each), moments
+using AdamRing = Ring<2, kAdamSlots>;
+template <bool kEight>
+constexpr int kAdamPerSm = kEight ? 3 : 4;  // blocks
+template <bool kEight>
+constexpr size_t kAdamSmem = kEight ? ring_bytes<2, kAdamSlots>(kAdamThreads) : 0;
+static_assert(kAdamSmem<true> <= 48 << 10, "no launch option asked for");
+
+// The tensor of chunk c, at or after `ti` in the table.
+template <int kCap>
+__device__ __forceinline__ int adam_tensor(const AdamTable<kCap>& tab, int64_t c, int ti) {
+  if (c < tab.base[ti + 1]) return ti;
+  int lo = ti + 1, hi = tab.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c >= tab.base[mid])
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+// Starts the copy of a warp's block, from element e on, of which `left` are inside the
+// tensor: all whole units of 16 bytes (8 of codes), and so all lanes' whole eights.
+__device__ __forceinline__ void adam_fetch(const AdamRing& ring, int stage, const AdamTensor& t, int64_t e,
+                                           int64_t left) {
+  const int lane = threadIdx.x & 31;
+  const auto vec = [&](const void* p, int dtype, int at) {
+    if (dtype == MOE_LORA_F32) {
+      const float* q = static_cast<const float*>(p) + e + lane * 4;
+      if (lane * 4 + 4 <= left) async_copy16(ring.slot(stage, at), q);
+      if (lane * 4 + 132 <= left) async_copy16(ring.slot(stage, at + 1), q + 128);
+    } else if (lane * 8 + 8 <= left) {
+      async_copy16(ring.slot(stage, at), static_cast<const uint16_t*>(p) + e + lane * 8);
+    }
+  };
+  vec(t.g, t.g_dtype, 0);
+  if (t.master)
+    vec(t.master, MOE_LORA_F32, 2);
+  else
+    vec(t.p, t.p_dtype, 2);
+  if (lane * 8 + 8 <= left) {
+    uint2* q = reinterpret_cast<uint2*>(ring.slot(stage, 4));
+    async_copy8(q, static_cast<const uint8_t*>(t.m) + e + lane * 8);
+    async_copy8(q + 1, static_cast<const uint8_t*>(t.v) + e + lane * 8);
+  }
+}
+
 template <bool kEight, int kCap>
-__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamTable<kCap> tab) {
+__global__ void __launch_bounds__(kAdamThreads, kAdamPerSm<kEight>)
+    adamw_kernel(const __grid_constant__ AdamTable<kCap> tab) {
+  extern __shared__ uint4 adam_smem[];
+  const AdamRing ring(adam_smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const AdamHyper& h = tab.h;
   const float gs = h.gs ? *h.gs : 1.0f;
-  int ti = 0;
-  for (int64_t c = blockIdx.x; c < tab.base[tab.n]; c += gridDim.x) {
-    if (c >= tab.base[ti + 1]) {  // the tensor of chunk c, further on in the table
-      int lo = ti + 1, hi = tab.n - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (c >= tab.base[mid])
-          lo = mid;
-        else
-          hi = mid - 1;
+  const int64_t end = tab.base[tab.n];
+  int ti = 0, next = 0, stage = 0;  // tensor of this chunk and of the next
+  float sm = 0.f, sv = 0.f, next_sm = 0.f, next_sv = 0.f;
+  const auto ahead = [&](int64_t c, int st) {
+    if (c < end) {
+      next = adam_tensor(tab, c, next);
+      const AdamTensor& t = tab.t[next];
+      const int64_t blk = (c - tab.base[next]) * kAdamWarps + warp, e = blk * kAdamBlock;
+      adam_fetch(ring, st, t, e, t.numel - e);
+      if (e < t.numel) {
+        next_sm = t.ms[blk];
+        next_sv = t.vs[blk];
       }
-      ti = lo;
+    }
+    async_commit();
+  };
+  if constexpr (kEight) ahead(blockIdx.x, 0);
+  for (int64_t c = blockIdx.x; c < end; c += gridDim.x, stage ^= 1) {
+    if constexpr (kEight) {
+      ti = next;
+      sm = next_sm;
+      sv = next_sv;
+      __syncwarp();  // all lanes have read the stage that is filled next
+      ahead(c + gridDim.x, stage ^ 1);
+      async_wait<1>();
+      __syncwarp();
+    } else {
+      ti = adam_tensor(tab, c, ti);
     }
     const AdamTensor& t = tab.t[ti];
     const int64_t blk = (c - tab.base[ti]) * kAdamWarps + warp, i = blk * kAdamBlock + lane * 8;
     if (blk * kAdamBlock >= t.numel) continue;
     const bool whole = i + 8 <= t.numel;
-    float g[8], m[8], v[8], w[8], sm = 0.f, sv = 0.f;
-    if (kEight) {
-      sm = t.ms[blk];
-      sv = t.vs[blk];
-    }
+    float g[8], m[8], v[8], w[8];
     if (whole) {
-      Raw8 rg, rw, rm, rv;
-      rg.load(t.g, t.g_dtype, i);
-      if (t.master)
-        rw.load(t.master, MOE_LORA_F32, i);
-      else
-        rw.load(t.p, t.p_dtype, i);
-      uint2 cm, cv;
-      if (kEight) {
-        cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
-        cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
+      Raw8 rg, rw;
+      const int wd = t.master ? MOE_LORA_F32 : t.p_dtype;
+      if constexpr (kEight) {
+        rg.get(ring.slot(stage, 0) - lane, t.g_dtype);
+        rw.get(ring.slot(stage, 2) - lane, wd);
+        const uint4 q = *ring.slot(stage, 4);
+        const uint32_t code[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 a = from_e4m3x2(code[j >> 2] >> (8 * (j & 3)));
+          const float2 b = from_e4m3x2(code[2 + (j >> 2)] >> (8 * (j & 3)));
+          m[j] = a.x;
+          m[j + 1] = a.y;
+          v[j] = b.x;
+          v[j + 1] = b.y;
+        }
+        rg.widen(t.g_dtype, g);
+        rw.widen(wd, w);
       } else {
+        Raw8 rm, rv;
+        rg.load(t.g, t.g_dtype, i);
+        if (t.master)
+          rw.load(t.master, MOE_LORA_F32, i);
+        else
+          rw.load(t.p, t.p_dtype, i);
         rm.load(t.m, MOE_LORA_F32, i);
         rv.load(t.v, MOE_LORA_F32, i);
-      }
-      rg.widen(t.g_dtype, g);
-      rw.widen(t.master ? MOE_LORA_F32 : t.p_dtype, w);
-      if (kEight) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 a = from_e4m3x2((j < 2 ? cm.x : cm.y) >> (16 * (j & 1)));
-          const float2 c = from_e4m3x2((j < 2 ? cv.x : cv.y) >> (16 * (j & 1)));
-          m[2 * j] = a.x;
-          m[2 * j + 1] = a.y;
-          v[2 * j] = c.x;
-          v[2 * j + 1] = c.y;
-        }
-      } else {
+        rg.widen(t.g_dtype, g);
+        rw.widen(wd, w);
         rm.widen(MOE_LORA_F32, m);
         rv.widen(MOE_LORA_F32, v);
       }
@@ -314,13 +421,9 @@ int check_tensor(const moe_lora_adamw_tensor& t) {
 
 template <bool kEight, int kCap>
 int launch_adamw(const AdamTable<kCap>& tab, int sms, cudaStream_t s) {
-  const auto kernel = adamw_kernel<kEight, kCap>;
-  int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kAdamThreads, 0) != cudaSuccess || per < 1)
-    return MOE_LORA_ERR_CUDA;
-  const int64_t want = tab.base[tab.n], most = (int64_t)per * sms;
+  const int64_t want = tab.base[tab.n], most = (int64_t)kAdamPerSm<kEight> * sms;
   prof_begin(K_ADAMW, s);
-  kernel<<<(int)(want < most ? want : most), kAdamThreads, 0, s>>>(tab);
+  adamw_kernel<kEight, kCap><<<(int)(want < most ? want : most), kAdamThreads, kAdamSmem<kEight>, s>>>(tab);
   prof_end(K_ADAMW, s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }

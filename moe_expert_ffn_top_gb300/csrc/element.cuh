@@ -148,6 +148,9 @@ __device__ __forceinline__ void async_copy16_part(void* dst_smem, const void* sr
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(dst_smem)), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void async_copy8(void* dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(shared_address(dst_smem)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void async_copy4(void* dst_smem, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_address(dst_smem)), "l"(src) : "memory");
 }
