@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
   extern __shared__ __align__(16) uint8_t ring_sm[];
   __shared__ IdScan<kBalMaxChunk> sc;
   __shared__ float fsm[kBalMaxE];  // f_e
-  __shared__ float csm[kBalMaxE];  // sums of probabilities: partial ones, then the block's
+  __shared__ float csm[kBalMaxE];  // f_e - 1/E; then the block's sums of probabilities
   __shared__ float tsm[kT / 32];
   __shared__ int nsm[2], bad;  // R, N and error bits of the adapter
   // where the ring was: a row of sums per row group, rows apart so that float4 stores spread over the banks
@@ -401,8 +401,12 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
   const int N = nsm[1];
   const float rR = 1.0f / (float)max(nsm[0], 1), rN = 1.0f / (float)max(N, 1);
   const bool first = chunk == 0;  // block of the adapter
+  // f - 1/E instead of f for the gradient, which is the difference f_e - <p, f>: formed in
+  // whole numbers, so that nothing cancels however even the counts are.
+  const float rRE = rR * (1.0f / (float)E);
   for (int e = threadIdx.x; e < E; e += kT) {
     const int c = cnt[e];
+    csm[e] = (float)((int64_t)c * E - nsm[0]) * rRE;
     fsm[e] = (float)c * rR;
     if (first) g.counts[a * E + e] = c;
   }
@@ -411,14 +415,12 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
     g.sc.tokens[a] = N;
   }
   __syncthreads();
-  // f - 1/E instead of f: the gradient's difference f_e - <p, f> then loses less to cancellation
-  const float mean = 1.0f / (float)E;
   const float up = (g.dlogits && g.dloss ? g.dloss[a] : 1.f) * (g.coef * (float)E) * rN;
   float2 f[kP], acc[kP];
 #pragma unroll
   for (int p = 0; p < kP; ++p) {
     const int e = pr.first(p), e2 = e + pr.apart();
-    f[p] = make_float2(in(e) ? fsm[e] - mean : 0.f, in(e2) ? fsm[e2] - mean : 0.f);
+    f[p] = make_float2(in(e) ? csm[e] : 0.f, in(e2) ? csm[e2] : 0.f);
     acc[p] = both(0.f);
   }
   int s = 0;

@@ -304,6 +304,30 @@ def test_balance_adapters_equal_their_own_runs(dt):
     assert float(got[0][2]) == 0 and (got[3][128:1280] == 0).all()
 
 
+@pytest.mark.parametrize("T,masked", [(256, 0), (256, 0.02), (4096, 0.2), (16_384, 0), (20_824, 0.2)])
+def test_balance_gradient_of_even_counts(T, masked):
+    """Every expert selected: the counts differ by masked routes alone, and the gradient is what their
+    small differences leave.  Its error is relative to those, not to the counts; even counts give 0."""
+    E = 8
+    g = _gen(21)
+    logits = torch.randn(T, E, generator=g, device="cuda").bfloat16()
+    ids = torch.rand(T, E, generator=g, device="cuda").argsort(1).int()
+    ids[torch.rand(T, E, generator=g, device="cuda") < masked] = -1
+    _, counts, _, dl, err = _balance(logits, ids, [0, T])
+    assert err == 0
+    if not masked:
+        assert (counts == T).all() and not dl.any()
+        return
+    _, wc, _, wd = ref.balance(logits.float().cpu(), ids.cpu(), [0, T], 0.01, None)
+    assert torch.equal(counts.cpu(), wc)
+    l = logits.double().cpu()
+    live = (ids >= 0).any(1).cpu()
+    f = (wc[0].double() / wc.sum() - 1 / E).abs()  # dl = g p (f_e - <p, f>) with f less 1/E as well
+    p = torch.softmax(l, 1) * live[:, None]
+    rel = (CHAIN + 4 * l.abs().amax() + 16) * U32  # as in _check_balance
+    _within("dlogits", dl, wd, 2 * rel * 0.01 * E / int(live.sum()) * p * (f + (p * f).sum(1, keepdim=True)) + 1e-30)
+
+
 def test_balance_masked_values():
     """-inf logits have no probability, a row of them nothing at all; rows without a live route are not
     looked at; out-of-range ids are dropped and flagged."""
