@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(block_threads(kVals), kVals == 8 ? 1 : 2)
 #pragma unroll
     for (int p = 0; p < kP; ++p) acc[p] = fma2(v[p], both(rz), acc[p]);
     if (g.dlogits && on) {
-      const float2 w = both(up * rz), nd = both(-ds);
+      // rows without a probability (not live, or -inf throughout) have no gradient, also where dloss is not finite
+      const float2 w = both(zs == 0.f ? 0.f : up * rz), nd = both(-ds);
       float* dr = g.dlogits + (ch.t0 + (int64_t)t) * E;
 #pragma unroll
       for (int p = 0; p < kP; ++p) v[p] = mul2(mul2(v[p], w), add2(f[p], nd));
