@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoelora.so")
 SOURCES = ["api.cu", "plan.cu", "mem_kernels.cu", "forward.cu", "backward.cu", "selftest.cu", "prof.cu", "plan_noalloc.cu", "router.cu",
-           "layernorm.cu", "balance.cu", "adamw.cu"]
+           "layernorm.cu", "balance.cu", "adamw.cu", "options.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -4,7 +4,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
@@ -123,36 +122,6 @@ int device_sms(int* sms) {
   }
   *sms = n;
   return MOE_LORA_OK;
-}
-
-// Kernels and what they were allowed: shared memory in bytes, bit 30 for wide clusters.
-bool options_asked(const void* kernel, size_t smem, bool wide_cluster) {
-  constexpr int kSlots = 1024;  // a few hundred kernels ask
-  static std::atomic<const void*> keys[kSlots];
-  static std::atomic<int> allowed[kSlots];
-  constexpr int kWide = 1 << 30;
-  if (smem <= 32 * 1024 && !wide_cluster) return true;  // with 16 KB of static memory at most: nothing to ask for
-  for (size_t h = (reinterpret_cast<uintptr_t>(kernel) >> 4) % kSlots, n = 0; n < kSlots; ++n, h = (h + 1) % kSlots) {
-    const void* key = keys[h].load(std::memory_order_acquire);
-    if (!key && !keys[h].compare_exchange_strong(key, kernel)) {
-      if (key != kernel) continue;
-    } else if (key && key != kernel) {
-      continue;
-    }
-    const int had = allowed[h].load(std::memory_order_relaxed);
-    const int want = std::max(had & (kWide - 1), (int)smem) | (had & kWide) | (wide_cluster ? kWide : 0);
-    if (want == had) return true;
-    allowed[h].store(want, std::memory_order_relaxed);
-    return false;
-  }
-  return false;
-}
-cudaError_t allow_options(const void* kernel, size_t smem, bool wide_cluster) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 32 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && wide_cluster)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e;
 }
 
 static bool aligned16(const void* p) { return check_opt(p) == MOE_LORA_OK; }

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "options.h"
 
 namespace moelora {
 
@@ -42,27 +43,6 @@ inline int check_opt(const void* p) {
   return reinterpret_cast<uintptr_t>(p) & 15u ? MOE_LORA_ERR_ALIGN : MOE_LORA_OK;
 }
 inline int check_ptr(const void* p) { return p ? check_opt(p) : MOE_LORA_ERR_NULL; }
-
-// Launches that need more than 48 KB of shared memory, or clusters of more than eight
-// blocks, which a kernel has to be allowed once per context (a call of about a
-// microsecond).  options_asked tells whether this process has allowed `kernel` as much
-// before, and notes it; a launch that fails all the same (another context) allows it
-// again and is repeated.
-bool options_asked(const void* kernel, size_t smem, bool wide_cluster);
-cudaError_t allow_options(const void* kernel, size_t smem, bool wide_cluster);
-template <class... P, class... Args>
-cudaError_t launch_allowed(const cudaLaunchConfig_t& cfg, bool wide_cluster, void (*kernel)(P...), Args... args) {
-  const void* k = reinterpret_cast<const void*>(kernel);
-  const bool asked = options_asked(k, cfg.dynamicSmemBytes, wide_cluster);
-  cudaError_t e = asked ? cudaSuccess : allow_options(k, cfg.dynamicSmemBytes, wide_cluster);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  if (e != cudaSuccess && asked) {
-    (void)cudaGetLastError();
-    e = allow_options(k, cfg.dynamicSmemBytes, wide_cluster);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  }
-  return e;
-}
 
 // Bytes of the balance loss's scratch (balance.cu); 0 for sizes it does not take.
 size_t balance_scratch_bytes(const moe_lora_dims* d);

@@ -1097,9 +1097,14 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, int slice
     // as many clusters as run together (fewer than blocks would: a cluster stays inside one
     // processing cluster); one more is a second wave as long as the first
     int fit = 0;
-    if (allow_options(reinterpret_cast<const void*>(kernel), smem, false) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess)
-      return MOE_LORA_ERR_CUDA;
+    const auto ask = [&](bool again) {
+      const cudaError_t e = allow_options(reinterpret_cast<const void*>(kernel), again);
+      return e == cudaSuccess ? cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) : e;
+    };
+    if (ask(false) != cudaSuccess) {
+      (void)cudaGetLastError();
+      if (ask(true) != cudaSuccess) return MOE_LORA_ERR_CUDA;
+    }
     most = std::max(1, std::min(most, fit));
   }
   int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
