@@ -1044,7 +1044,10 @@ int run_fwd(const FwdArgs& a) {
   return rows_aligned(a.nm, false, false) ? pick_fwd<T, 16 / sizeof(T)>(a) : pick_fwd<T, 1>(a);
 }
 
-// The partial rows' sum, launched while the kernel before it still runs.
+// The partial rows' sum.  Its launch is prepared while the kernel before it runs; its blocks
+// start when that kernel's have exited.  (Let in at that kernel's start, to wait on the SMs,
+// they save 0.1 us at 128 x 577 fp32, but 256 x 4,096 bf16 takes 10.4 us instead of 8.7 and
+// 1,024 x 4,096 15.1 instead of 13.6.)
 int launch_wgrad(int n, int parts, const float* part, float* dgamma, float* dbeta, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
@@ -1108,16 +1111,18 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, int slice
     most = std::max(1, std::min(most, fit));
   }
   int grid = stream_grid(a.nm.rows, ss.teams, most, shift);
-  // Few rows: at most sixteen blocks, a cluster, add the weight gradients themselves.  The
-  // second launch that this saves costs the host 2.3 us; a team's second and third row
-  // cost the GPU about 1.2 us each where rows are short (347 x 577 fp32, three rows a team:
-  // a call 9.7 us against 12.0 us, on the GPU alone 9.4 us against 7.2 us), more where they
-  // are long.
+  // Few rows, one a team at most: up to sixteen blocks, a cluster, add the weight gradients
+  // themselves.  The GPU takes as long as with a second launch (128 x 577 fp32 6.2 and 6.5
+  // us, 32 x 4,096 bf16 7.8 and 7.7, 1,024 x 64 bf16 4.1 and 4.7), a call 2 us less of the
+  // host's time (8.5 and 10.4).  With a second and third row a team the cluster is behind:
+  // 192 x 577 fp32 7.7 us on the GPU against 6.8, 347 x 577 9.1 against 7.0, 96 x 4,096 bf16
+  // 10.3 against 8.2; a row of calls takes as long as its GPU work there (347 x 577: 11.5 us
+  // a call against 10.5).
   bool together = false;
   if (kMode == kWhole && wgrad && grid > 1) {
     int cluster = 2;
     while (cluster < 16 && cluster < grid) cluster *= 2;
-    together = ceil_div(a.nm.rows, (int64_t)ss.teams * cluster) <= (ss.teams >= 4 ? 3 : 2);
+    together = a.nm.rows <= (int64_t)ss.teams * cluster;
     if (together) {
       grid = cluster;
       at[0].id = cudaLaunchAttributeClusterDimension;
