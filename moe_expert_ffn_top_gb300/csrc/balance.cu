@@ -59,8 +59,16 @@ int64_t bal_groups(int64_t n, int E) {
 }
 
 // Tokens per chunk of such an adapter: a sixteenth of a group; of one group and little
-// work an eighth (16 adapters x 1,024 x 128: 11 us as clusters of eight, 17 us as clusters
-// of sixteen, which do not all run together), of very little all.
+// work an eighth, of very little all.  The rule sees one adapter's sizes alone, so that its
+// sums do not depend on the others.
+// Clusters of eight against sixteen: one to four adapters of 1,024 x 128 8.5 and 7.6 us, of
+// 2,048 x 128 11.4 and 8.8, of 512 x 16 6.4 and 6.4; sixteen adapters, whose clusters of
+// sixteen do not all run together, 11.2 and 15.7, 15.6 and 20.6, 8.4 and 13.7.
+// One block against a cluster of eight: 128 x 8 5.3 and 6.3 us, 512 x 8 7.5 and 6.9; 256 x 16
+// 5.9 and 6.3, 512 x 16 7.3 and 6.5; 256 x 32 5.9 and 6.4; 64 x 64 5.1 and 6.5, 128 x 64 5.8
+// and 6.4; 64 x 128 5.8 and 6.6.  They are level near 2,700 logits at 8 experts, 6,000 at 16,
+// 10,000 at 32 and more: what one block takes alone is set for the few experts, and costs the
+// others up to 1 us between 4,096 and 8,192 logits.
 int bal_chunk(int64_t n, int64_t groups, int E) {
   const int64_t work = std::max(n * E, n * (kBalFewWork / kBalFewTokens));
   const int64_t chunks = groups > 1 || work > kBalFewWork ? groups * kBalCluster : n * E > kBalChunkWork ? kBalFew : 1;

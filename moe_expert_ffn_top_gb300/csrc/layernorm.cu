@@ -7,7 +7,7 @@
 // avg(u h); dgamma = sum dy h and dbeta = sum dy run down the columns.  HBM is the bound:
 // 2 x 8 KB per 4,096-column bf16 row forward, 4 x 8 KB backward with the residual's
 // gradient.  Measured on one GB300 (copy bandwidth 6.78 TB/s): 65,536 x 4,096 bf16 forward
-// 160 us (6.7 TB/s, 99%), backward with dres and both weight gradients 325 us (6.6 TB/s,
+// 161 us (6.7 TB/s, 98%), backward with dres and both weight gradients 327 us (6.6 TB/s,
 // 97%); one row of 4,096 2.7 us; 347 x 577 fp32 backward 7.0 us (two launches).
 //
 // Which kernel: rows that stream (norm_*_stream_kernel) when there are enough of them, or
@@ -267,8 +267,13 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(moe_lora_norm nm,
 constexpr int kFwdStreamThreads = 256, kFwdColumns = 64;
 constexpr int kBwdStreamThreads = 512, kBwdColumns = 16;
 constexpr int kOddThreads = 512;
-// From here on shifted rows stream forward (577 columns: 150 rows 3.3 us in registers, 256
-// rows 4.8 us streamed, 1,024 rows 5.0 us).
+// From here on shifted rows stream forward.  In registers and streamed, us: 130 columns 2.6
+// and 3.4 at 256 rows, 2.9 and 3.4 at 1,029, 4.5 and 3.5 at 2,048; 577 columns 3.1 and 4.5,
+// 5.1 and 4.5, 6.9 and 4.7; 1,027 bf16 3.4 and 5.5 at 256 rows, 5.5 and 5.5 at 512; 2,049
+// fp16 3.6 and 5.9 at 150, 5.5 and 5.8 at 256, 7.6 and 6.0 at 384; 4,097 bf16 4.9 and 5.7 at
+// 150, 7.7 and 5.6 at 192, 17.4 and 11.0 at 1,029; 8,191 bf16 5.2 and 5.1 up to 150, 8.8 and
+// 6.8 at 256.  One number of rows for all widths: narrow rows would stay in registers for
+// longer (by 1 us), rows of 4,096 and more could stream from 160 rows on (2 us).
 constexpr int kShiftRows = 256;
 struct StreamShape {
   int tpr, teams;
@@ -913,7 +918,7 @@ int launch_fwd(const FwdArgs& a, const RowShape& rs) {
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-constexpr size_t kMaxSmem = 216 * 1024;  // dynamic, beside the kernels' static 8 KB
+constexpr size_t kMaxSmem = 216 * 1024;  // dynamic, beside the kernels' static 9.6 KB at most (227 KB in all)
 
 // Stages of the rings: 64 to 128 KB of copies under way per SM at full width, where an SM
 // needs about 45 KB to hide the memory's latency (65,536 x 4,096 bf16 backward: three
@@ -1116,8 +1121,8 @@ int launch_bwd(const BwdArgs& a, Kernel kernel, const StreamShape& ss, int slice
   // us, 32 x 4,096 bf16 7.8 and 7.7, 1,024 x 64 bf16 4.1 and 4.7), a call 2 us less of the
   // host's time (8.5 and 10.4).  With a second and third row a team the cluster is behind:
   // 192 x 577 fp32 7.7 us on the GPU against 6.8, 347 x 577 9.1 against 7.0, 96 x 4,096 bf16
-  // 10.3 against 8.2; a row of calls takes as long as its GPU work there (347 x 577: 11.5 us
-  // a call against 10.5).
+  // 10.3 against 8.2.  (Calls of 347 x 577 in a row, where host and GPU are about level: 11.2
+  // to 11.5 us as a cluster, 10.5 to 13.1 in two launches.)
   bool together = false;
   if (kMode == kWhole && wgrad && grid > 1) {
     int cluster = 2;
