@@ -22,6 +22,12 @@ def pytest_collection_modifyitems(config, items):
     except Exception:
         has_gpu = False
     if has_gpu:
+        # Answers of a host without a GPU: where there is one, the placeholder addresses of
+        # these calls would reach a kernel and fault.
+        skip = pytest.mark.skip(reason="checks the no-GPU answer")
+        for it in items:
+            if it.name == "test_no_device_is_reported":
+                it.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA GPU")
     for it in items:
