@@ -425,6 +425,162 @@ typedef struct moe_lora_adamw {
 MOE_LORA_API int moe_lora_adamw_step(const moe_lora_adamw* opt, const moe_lora_adamw_tensor* tensors, int32_t n,
                                      void* stream);
 
+/* ---- post-training: the losses on token log probabilities, and Muon ----
+ * What starts the backward pass when adapters are trained on preferences or rewards, and an
+ * optimiser for matrices with one short side, which all factors are.  The pages give none of
+ * them; each is the usual definition, stated below. */
+
+/* Rows of logits over a vocabulary of n entries.  Rows may be farther apart than n: ld and ldd
+ * are the row strides of the logits and of their gradient in elements (0 = n, else >= n), and
+ * rows need not start on 16 bytes.  0 <= rows <= 2^26, 1 <= n <= 2^19 (else
+ * MOE_LORA_ERR_UNSUPPORTED); rows = 0 is a no-op.  inv_temp multiplies the logits (the inverse
+ * of the sampling temperature), 1e-30 <= inv_temp <= 1e30. */
+typedef struct moe_lora_rows {
+  int64_t rows;
+  int64_t ld;
+  int64_t ldd;
+  int32_t n;
+  int32_t dtype; /* logits and their gradient */
+  float inv_temp;
+} moe_lora_rows;
+
+/* With z = inv_temp * logits, for row t with target y = targets[t] in [0, n):
+ *     lse_t = log sum_e exp z_te,   logp_t = z_ty - lse_t,   entropy_t = lse_t - sum_e p_te z_te,
+ * p = exp(z - lse).  Rows with target -1 (prompts, padding) give 0 and their logits are not read;
+ * any other target outside [0, n) counts as -1 and sets MOE_LORA_DEV_BAD_ID in *err.  A logit of
+ * -inf has probability 0; NaN, +inf, or nothing but -inf in a row give NaN log probabilities.
+ *   targets [rows] int32; logp, lse, entropy [rows] fp32, each may be NULL (not all three)
+ *   err     DEVICE word (4-byte aligned) whose bits are set and never cleared, or NULL */
+MOE_LORA_API int moe_lora_token_logp_forward(const moe_lora_rows* r, const void* logits, const int32_t* targets,
+                                             float* logp, float* lse, float* entropy, int32_t* err, void* stream);
+
+/* dlogits_te = inv_temp * dlogp_t * ([e = y_t] - exp(z_te - lse_t)), one rounding to dlogits' type.
+ * Rows without a target, and rows whose dlogp is 0, get zeros and their logits are not read.
+ * lse [rows] as the forward wrote it.  dlogits may be logits (ldd = ld). */
+MOE_LORA_API int moe_lora_token_logp_backward(const moe_lora_rows* r, const void* logits, const int32_t* targets,
+                                              const float* lse, const float* dlogp, void* dlogits, int32_t* err,
+                                              void* stream);
+
+/* Clipped policy loss with a KL term.  For token t (logp as above; targets of -1 take no part):
+ *     rho = exp(logp - old_logp),   d = ref_logp - logp,   kl = exp(d) - 1 - d,
+ *     l = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + kl_coef * kl,   A = advantages[t],
+ *     loss_a = sum over the tokens of adapter a of w_t l_t,
+ * w = weight[t], or 1 / (live tokens of the adapter) where weight is NULL.  A token of weight 0
+ * takes no part either, whatever its values.  Without ref_logp kl is 0.  The gradient passes where
+ * the clip does not take the minimum, its borders included:
+ *     dl/dlogp = -rho A [not clipped] + kl_coef (1 - exp d),
+ *     dlogits_te = dloss_a * w_t * dl/dlogp * inv_temp * ([e = y_t] - p_te), zeros for tokens without part.
+ *   advantages, old_logp, ref_logp (or NULL), weight (or NULL)  [rows] fp32
+ *   adapter_offsets [adapters+1] int64, HOST, first token of each adapter: off[0] = 0, non-decreasing,
+ *            off[adapters] = rows; NULL when adapters == 1.  Any token may start a range.
+ *   dloss [adapters] fp32, the gradient that reaches each loss (NULL = 1); used by dlogits alone
+ *   loss  [adapters] fp32;  stats [adapters,4] fp32: sums over the adapter's tokens of w times kl,
+ *            [clipped], rho, entropy
+ *   logp [rows] fp32 or NULL;  dlogits [rows,n] or NULL for the loss alone; it may be logits (ldd = ld)
+ * Logits are read once, for the loss and the gradient together.  Equal calls give equal bits, and an
+ * adapter's tokens are added in an order of their own; calls with other numbers of rows may cut rows
+ * differently, and differ in the last bits of a token's values.  scratch: moe_lora_policy_scratch_bytes(rows, adapters) bytes (0 for
+ * bad sizes); calls that may run at the same time need one each. */
+typedef struct moe_lora_policy {
+  float clip_low;   /* in [0, 1] */
+  float clip_high;  /* >= 0 */
+  float kl_coef;
+  int32_t adapters; /* 1 .. 64 */
+} moe_lora_policy;
+MOE_LORA_API size_t moe_lora_policy_scratch_bytes(int64_t rows, int32_t adapters);
+MOE_LORA_API int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_policy* opt, const void* logits,
+                                      const int32_t* targets, const float* advantages, const float* old_logp,
+                                      const float* ref_logp, const float* weight, const int64_t* adapter_offsets,
+                                      const float* dloss, float* loss, float* stats, float* logp, void* dlogits,
+                                      int32_t* err, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Preference loss over pairs of packed sequences: sequence 2i is pair i's chosen answer, 2i + 1 its
+ * rejected one; sequence j's tokens are [seq_offsets[j], seq_offsets[j+1]).  With live tokens those
+ * whose target is not negative,
+ *     s_j = sum of logp over j's live tokens (average: divided by their number, at least 1),
+ *     r_j = s_j - ref_j,   h = r_2i - r_2i+1,   x = beta h - margin,
+ *     sigmoid: l = -(1 - label_smoothing) log sigma(x) - label_smoothing log sigma(-x)
+ *     squared: l = (h - 1 / (2 beta))^2        hinge: l = max(0, 1 - x)
+ *     loss_a = mean of l over the pairs of adapter a (0 without pairs),
+ *     dlogp_t = dloss_a / pairs_a * dl/dh * (+1 chosen, -1 rejected) (average: / live tokens of j).
+ *   logp [tokens] fp32, e.g. moe_lora_token_logp_forward's; targets [tokens] int32
+ *   seq_offsets [2 pairs + 1] int64, DEVICE.  An offset below the one before it or above tokens is
+ *            taken as the nearest that is not, and sets MOE_LORA_DEV_BAD_ID in *err.
+ *   ref [2 pairs] fp32, the reference model's s_j (a call without ref writes them), or NULL for 0
+ *   pair_offsets [adapters+1] int64, HOST, as adapter_offsets above, in pairs
+ *   loss [adapters] fp32;  stats [adapters,4] fp32: means of [x > 0], beta r_chosen, beta r_rejected, h
+ *   seq_logp [2 pairs] fp32 (s_j) or NULL
+ *   dlogp [tokens] fp32 or NULL: 0 at the sequences' tokens that are not live; tokens of no sequence
+ *            are left as they were
+ * scratch: moe_lora_preference_scratch_bytes(pairs) bytes; calls that may run at the same time need
+ * one each. */
+#define MOE_LORA_PREF_SIGMOID 0
+#define MOE_LORA_PREF_SQUARED 1
+#define MOE_LORA_PREF_HINGE 2
+typedef struct moe_lora_preference {
+  int64_t tokens;        /* 0 .. 2^40 */
+  int64_t pairs;         /* 0 .. 2^26 */
+  float beta;            /* > 0 */
+  float margin;
+  float label_smoothing; /* in [0, 0.5]; sigmoid only */
+  int32_t kind;          /* MOE_LORA_PREF_* */
+  int32_t average;       /* 0 = sums, 1 = means over live tokens */
+  int32_t adapters;      /* 1 .. 64 */
+} moe_lora_preference;
+MOE_LORA_API size_t moe_lora_preference_scratch_bytes(int64_t pairs);
+MOE_LORA_API int moe_lora_preference_loss(const moe_lora_preference* opt, const float* logp, const int32_t* targets,
+                                          const int64_t* seq_offsets, const float* ref, const int64_t* pair_offsets,
+                                          const float* dloss, float* loss, float* stats, float* seq_logp, float* dlogp,
+                                          int32_t* err, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Muon over n tensors at once.  A tensor is `batch` matrices [rows, cols], one after the other,
+ * min(rows, cols) <= 128 (else MOE_LORA_ERR_UNSUPPORTED): every factor of an adapter is.  With g the
+ * gradient times *grad_scale, in fp32:
+ *     m = momentum * m + (1 - momentum) g,   u = nesterov ? (1 - momentum) g + momentum * m : m,
+ * and for each matrix of u on its own
+ *     X = u / (|u| + eps)  (|u| = sqrt of the sum of squares),
+ *     `steps` times  X = a X + b (X X^T) X + c (X X^T)^2 X   (of X^T where rows > cols),
+ *     w = w (1 - lr weight_decay) - lr * scale * X,   p = w rounded to its type;
+ * w is `master` where that is given, else p.  Products are formed on the tensor cores from operands
+ * in parts, to 2^-22 of their factors; the squares X X^T are formed anew after the first steps, so
+ * that directions that start small keep their precision: X is within about 1e-5 (its 2-norm) of the
+ * definition for usual spectra and 1e-4 for the hardest ones.  It holds for coefficients that keep the
+ * singular values below 4 (the usual ones: below 1.3).  A matrix whose |u| is not finite, or whose
+ * square passes fp32's range, gives NaN in its own m or weights alone; one whose |u| is below 2^-60
+ * counts as 0. */
+typedef struct moe_lora_muon_tensor {
+  void* p;       /* [batch, rows, cols] parameter, read (unless master is given) and written */
+  float* master; /* fp32 parameter of a bf16 / fp16 p, read and written; or NULL */
+  const void* g; /* gradient */
+  float* m;      /* momentum, fp32 */
+  int64_t batch; /* 0 = skipped */
+  int32_t rows, cols;
+  int32_t p_dtype, g_dtype; /* MOE_LORA_F32 / _BF16 / _F16 */
+  double lr, weight_decay, scale;
+} moe_lora_muon_tensor;
+
+typedef struct moe_lora_muon {
+  double momentum;         /* in [0, 1) */
+  double eps;              /* 1e-30 .. 1 */
+  double a, b, c;          /* |a| <= 8, |b|, |c| <= 16; usually 3.4445, -4.775, 2.0315 */
+  int32_t nesterov;
+  int32_t steps;           /* 1 .. 5 (else MOE_LORA_ERR_UNSUPPORTED) */
+  const float* grad_scale; /* DEVICE scalar (4-byte aligned), or NULL for 1 */
+} moe_lora_muon;
+
+/* tensors [n]: HOST array, read before the call returns.  The tensors do not overlap.  scratch:
+ * moe_lora_muon_scratch_bytes(tensors, n) bytes (from batch, rows and cols alone; 0 for bad sizes),
+ * four bytes per element and a little; its first 16 bytes are the device error word, which the caller
+ * clears once and calls only add to.  Calls that may run at the same time need one each.  Sums run in
+ * a fixed order, so equal calls give equal bits.  Five launches per 128 tensors. */
+MOE_LORA_API size_t moe_lora_muon_scratch_bytes(const moe_lora_muon_tensor* tensors, int32_t n);
+MOE_LORA_API int moe_lora_muon_step(const moe_lora_muon* opt, const moe_lora_muon_tensor* tensors, int32_t n,
+                                    void* scratch, size_t scratch_bytes, void* stream);
+
+/* Reads the device error word of a moe_lora_muon_step scratch (MOE_LORA_DEV_* bits); synchronises
+ * `stream`. */
+MOE_LORA_API int moe_lora_muon_get_error(const void* scratch, void* stream);
+
 /* Static description of a return code. */
 MOE_LORA_API const char* moe_lora_strerror(int code);
 

@@ -67,6 +67,33 @@ class AdamW(ctypes.Structure):
                 ("step", ctypes.c_int64), ("grad_scale", ctypes.c_void_p)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ld", ctypes.c_int64), ("ldd", ctypes.c_int64), ("n", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("inv_temp", ctypes.c_float)]
+
+
+class Policy(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("adapters", ctypes.c_int32)]
+
+
+class Preference(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("pairs", ctypes.c_int64), ("beta", ctypes.c_float),
+                ("margin", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("kind", ctypes.c_int32),
+                ("average", ctypes.c_int32), ("adapters", ctypes.c_int32)]
+
+
+class MuonTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "master", "g", "m")] + [
+        ("batch", ctypes.c_int64), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("p_dtype", ctypes.c_int32),
+        ("g_dtype", ctypes.c_int32), ("lr", ctypes.c_double), ("weight_decay", ctypes.c_double), ("scale", ctypes.c_double)]
+
+
+class Muon(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("momentum", "eps", "a", "b", "c")] + [
+        ("nesterov", ctypes.c_int32), ("steps", ctypes.c_int32), ("grad_scale", ctypes.c_void_p)]
+
+
 class Grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dA1", "dA3", "dB1", "dB3", "dA2", "dB2")]
 
@@ -151,6 +178,24 @@ def lib() -> ctypes.CDLL:
                                                    ctypes.c_size_t, P]
         L.moe_lora_adamw_step.restype = ctypes.c_int
         L.moe_lora_adamw_step.argtypes = [ctypes.POINTER(AdamW), P, ctypes.c_int32, P]
+        L.moe_lora_token_logp_forward.restype = ctypes.c_int
+        L.moe_lora_token_logp_forward.argtypes = [ctypes.POINTER(Rows), P, P, P, P, P, P, P]
+        L.moe_lora_token_logp_backward.restype = ctypes.c_int
+        L.moe_lora_token_logp_backward.argtypes = [ctypes.POINTER(Rows), P, P, P, P, P, P, P]
+        L.moe_lora_policy_scratch_bytes.restype = ctypes.c_size_t
+        L.moe_lora_policy_scratch_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32]
+        L.moe_lora_policy_loss.restype = ctypes.c_int
+        L.moe_lora_policy_loss.argtypes = [ctypes.POINTER(Rows), ctypes.POINTER(Policy)] + [P] * 14 + [ctypes.c_size_t, P]
+        L.moe_lora_preference_scratch_bytes.restype = ctypes.c_size_t
+        L.moe_lora_preference_scratch_bytes.argtypes = [ctypes.c_int64]
+        L.moe_lora_preference_loss.restype = ctypes.c_int
+        L.moe_lora_preference_loss.argtypes = [ctypes.POINTER(Preference)] + [P] * 12 + [ctypes.c_size_t, P]
+        L.moe_lora_muon_scratch_bytes.restype = ctypes.c_size_t
+        L.moe_lora_muon_scratch_bytes.argtypes = [P, ctypes.c_int32]
+        L.moe_lora_muon_step.restype = ctypes.c_int
+        L.moe_lora_muon_step.argtypes = [ctypes.POINTER(Muon), P, ctypes.c_int32, P, ctypes.c_size_t, P]
+        L.moe_lora_muon_get_error.restype = ctypes.c_int
+        L.moe_lora_muon_get_error.argtypes = [P, P]
         _lib = L
     return _lib
 
@@ -624,6 +669,183 @@ def moe_lora_adamw_step(tensors: AdamWTensors, step: int, beta1: float = 0.9, be
     opt = AdamW(beta1, beta2, eps, step, _vec(grad_scale, 1, "grad_scale", torch.float32))
     rc = lib().moe_lora_adamw_step(opt, tensors.table, len(tensors.entries), _stream(stream))
     _check(rc, "moe_lora_adamw_step")
+
+
+# ------------------------------------------------------------------ post-training
+def _logit_rows(logits: torch.Tensor, dlogits: Optional[torch.Tensor], inv_temp: float):
+    """The row description of logits [rows, n] and their gradient, and both pointers."""
+    px, ld = _rows(logits, "logits")
+    pd, ldd = (None, 0) if dlogits is None else _rows(dlogits, "dlogits", logits)
+    rows, n = logits.shape
+    return Rows(rows, ld, ldd, n, _dtype(logits, "logits"), inv_temp), px, pd
+
+
+def moe_lora_token_logp_forward(logits: torch.Tensor, targets: torch.Tensor, logp: Optional[torch.Tensor],
+                                lse: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                                inv_temp: float = 1.0, err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Log probability of targets [rows] int32 (-1 = none, gives 0) under softmax(inv_temp * logits) of
+    logits [rows, n] (fp32, bf16 or fp16; rows may be strided), with lse and entropy if given, all
+    [rows] fp32.  err: a device int32 word that collects MOE_LORA_DEV_BAD_ID."""
+    r, px, _ = _logit_rows(logits, None, inv_temp)
+    T = r.rows
+    rc = lib().moe_lora_token_logp_forward(r, px, _vec(targets, T, "targets", torch.int32),
+                                           _vec(logp, T, "logp", torch.float32), _vec(lse, T, "lse", torch.float32),
+                                           _vec(entropy, T, "entropy", torch.float32), _vec(err, 1, "err", torch.int32),
+                                           _stream(stream))
+    _check(rc, "moe_lora_token_logp_forward")
+
+
+def moe_lora_token_logp_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dlogp: torch.Tensor,
+                                 dlogits: torch.Tensor, inv_temp: float = 1.0, err: Optional[torch.Tensor] = None,
+                                 stream=None) -> None:
+    """dlogits [rows, n] (the logits' type; may be logits) of the log probabilities, from the forward's
+    lse [rows] and the gradient dlogp [rows] that reaches them."""
+    r, px, pd = _logit_rows(logits, dlogits, inv_temp)
+    T = r.rows
+    rc = lib().moe_lora_token_logp_backward(r, px, _vec(targets, T, "targets", torch.int32),
+                                            _vec(lse, T, "lse", torch.float32), _vec(dlogp, T, "dlogp", torch.float32),
+                                            pd, _vec(err, 1, "err", torch.int32), _stream(stream))
+    _check(rc, "moe_lora_token_logp_backward")
+
+
+def policy_scratch(rows: int, adapters: int = 1, device="cuda") -> torch.Tensor:
+    """Workspace of moe_lora_policy_loss."""
+    b = int(lib().moe_lora_policy_scratch_bytes(rows, adapters))
+    if b == 0:
+        raise MoeLoraError(-2, "moe_lora_policy_scratch_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def _host_offsets(offsets: Optional[Sequence[int]], adapters: int, name: str):
+    if offsets is None:
+        return None
+    a = array.array("q", offsets)
+    if len(a) != adapters + 1:
+        raise ValueError(f"{name} must have {adapters + 1} entries")
+    return a
+
+
+def moe_lora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, advantages: torch.Tensor, old_logp: torch.Tensor,
+                         ref_logp: Optional[torch.Tensor], loss: torch.Tensor, stats: torch.Tensor,
+                         scratch: torch.Tensor, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                         weight: Optional[torch.Tensor] = None, adapter_offsets: Optional[Sequence[int]] = None,
+                         logp: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                         dloss: Optional[torch.Tensor] = None, inv_temp: float = 1.0,
+                         err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Clipped policy loss [A] with a KL term to ref_logp, for targets [rows] int32 (-1 = none) under
+    logits [rows, n]; advantages, old_logp, ref_logp and weight (None: each adapter's mean) [rows] fp32.
+    stats [A,4]: weighted KL, clipped share, ratio, entropy.  dlogits [rows, n] (may be logits) receives
+    the gradient (for the upstream gradient dloss [A], None = 1) in the same pass if given.
+    adapter_offsets [A+1] (host) splits the tokens between adapters."""
+    r, px, pd = _logit_rows(logits, dlogits, inv_temp)
+    T, A, f32 = r.rows, loss.numel(), torch.float32
+    offs = _host_offsets(adapter_offsets, A, "adapter_offsets")
+    rc = lib().moe_lora_policy_loss(r, Policy(clip_low, clip_high, kl_coef, A), px,
+                                    _vec(targets, T, "targets", torch.int32), _vec(advantages, T, "advantages", f32),
+                                    _vec(old_logp, T, "old_logp", f32), _vec(ref_logp, T, "ref_logp", f32),
+                                    _vec(weight, T, "weight", f32), None if offs is None else offs.buffer_info()[0],
+                                    _vec(dloss, A, "dloss", f32), _vec(loss, A, "loss", f32),
+                                    _vec(stats, 4 * A, "stats", f32), _vec(logp, T, "logp", f32), pd,
+                                    _vec(err, 1, "err", torch.int32), _ptr(scratch, None, "scratch"),
+                                    scratch.numel() * scratch.element_size(), _stream(stream))
+    _check(rc, "moe_lora_policy_loss")
+
+
+PREFERENCE_KINDS = {"sigmoid": 0, "squared": 1, "hinge": 2}
+
+
+def preference_scratch(pairs: int, adapters: int = 1, device="cuda") -> torch.Tensor:
+    """Workspace of moe_lora_preference_loss (its size does not depend on the adapters)."""
+    b = int(lib().moe_lora_preference_scratch_bytes(pairs))
+    if b == 0 or not 1 <= adapters <= 64:
+        raise MoeLoraError(-2, "moe_lora_preference_scratch_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def moe_lora_preference_loss(logp: torch.Tensor, targets: torch.Tensor, seq_offsets: torch.Tensor,
+                             ref: Optional[torch.Tensor], loss: torch.Tensor, stats: torch.Tensor,
+                             scratch: torch.Tensor, beta: float = 0.1, kind: str = "sigmoid",
+                             label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                             pair_offsets: Optional[Sequence[int]] = None, seq_logp: Optional[torch.Tensor] = None,
+                             dlogp: Optional[torch.Tensor] = None, dloss: Optional[torch.Tensor] = None,
+                             err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Preference loss [A] over pairs of packed sequences (2i chosen, 2i + 1 rejected; seq_offsets
+    [2 pairs + 1] int64 on the device) of token log probabilities logp [tokens], live where targets
+    [tokens] int32 is not negative; ref [2 pairs] holds the reference model's sums.  stats [A,4]: share
+    of pairs the right way round, rewards of chosen and rejected, their distance.  dlogp [tokens]
+    receives the gradient, seq_logp [2 pairs] the sums (means with `average`)."""
+    if seq_offsets.numel() % 2 != 1:
+        raise ValueError("seq_offsets must have 2 * pairs + 1 entries")
+    if kind not in PREFERENCE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}, got {kind!r}")
+    P, T, A, f32 = seq_offsets.numel() // 2, logp.numel(), loss.numel(), torch.float32
+    offs = _host_offsets(pair_offsets, A, "pair_offsets")
+    opt = Preference(T, P, beta, margin, label_smoothing, PREFERENCE_KINDS[kind], int(average), A)
+    rc = lib().moe_lora_preference_loss(opt, _vec(logp, T, "logp", f32), _vec(targets, T, "targets", torch.int32),
+                                        _vec(seq_offsets, 2 * P + 1, "seq_offsets", torch.int64),
+                                        _vec(ref, 2 * P, "ref", f32), None if offs is None else offs.buffer_info()[0],
+                                        _vec(dloss, A, "dloss", f32), _vec(loss, A, "loss", f32),
+                                        _vec(stats, 4 * A, "stats", f32), _vec(seq_logp, 2 * P, "seq_logp", f32),
+                                        _vec(dlogp, T, "dlogp", f32), _vec(err, 1, "err", torch.int32),
+                                        _ptr(scratch, None, "scratch"), scratch.numel() * scratch.element_size(),
+                                        _stream(stream))
+    _check(rc, "moe_lora_preference_loss")
+
+
+class MuonTensors:
+    """The tensors of a Muon step, listed once and kept between steps, with their workspace.  Each entry
+    is a dict: p (fp32, bf16 or fp16; its last two axes are a matrix, one of them at most 128, all others
+    count matrices), g of p's shape, m (fp32 momentum, started at zero), and optionally master (fp32, for
+    a 16-bit p), lr (1e-3), weight_decay (0) and scale (sqrt(max(1, rows / cols))), which multiplies the
+    update.  All contiguous; no two overlap.  The entries hold the tensors alive.  Steps that may run at
+    the same time need an object each."""
+
+    def __init__(self, entries: Sequence[Dict]):
+        self.entries = [dict(e) for e in entries]
+        self.table = (MuonTensor * max(1, len(self.entries)))()
+        for d, e in zip(self.table, self.entries):
+            p, n = e["p"], e["p"].numel()
+            if p.dim() < 2:
+                raise ValueError("p must have at least two axes")
+            if e["g"].shape != p.shape:
+                raise ValueError(f"g must be {tuple(p.shape)}, got {tuple(e['g'].shape)}")
+            d.rows, d.cols = p.shape[-2:]
+            d.batch = n // (d.rows * d.cols) if n else 0
+            d.p, d.g, d.m = _vec(p, n, "p"), _vec(e["g"], n, "g"), _vec(e["m"], n, "m", torch.float32)
+            d.master = _vec(e.get("master"), n, "master", torch.float32)
+            d.p_dtype, d.g_dtype = _dtype(p, "p"), _dtype(e["g"], "g")
+            d.lr, d.weight_decay = e.get("lr", 1e-3), e.get("weight_decay", 0.0)
+            scale = e.get("scale")
+            d.scale = max(1.0, d.rows / max(1, d.cols)) ** 0.5 if scale is None else scale
+        b = int(lib().moe_lora_muon_scratch_bytes(self.table, len(self.entries)))
+        if b == 0:
+            raise MoeLoraError(-5, "moe_lora_muon_scratch_bytes")
+        device = self.entries[0]["p"].device if self.entries else "cuda"
+        self.scratch = torch.empty(b, dtype=torch.uint8, device=device)
+        self.scratch[:16].zero_()  # the error word
+
+    def set_lr(self, lr: float) -> None:
+        for d in self.table:
+            d.lr = lr
+
+
+def moe_lora_muon_step(tensors: MuonTensors, momentum: float = 0.95, nesterov: bool = True, steps: int = 5,
+                       coefs: Sequence[float] = (3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                       grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One Muon step over all tensors: momentum, `steps` Newton-Schulz steps with the coefficients (a, b, c)
+    on every matrix, weights.  grad_scale: a device fp32 scalar that multiplies every gradient."""
+    a, b, c = coefs
+    opt = Muon(momentum, eps, a, b, c, int(nesterov), steps, _vec(grad_scale, 1, "grad_scale", torch.float32))
+    rc = lib().moe_lora_muon_step(opt, tensors.table, len(tensors.entries), tensors.scratch.data_ptr(),
+                                  tensors.scratch.numel(), _stream(stream))
+    _check(rc, "moe_lora_muon_step")
+
+
+def moe_lora_muon_get_error(tensors: MuonTensors, stream=None) -> int:
+    rc = lib().moe_lora_muon_get_error(tensors.scratch.data_ptr(), _stream(stream))
+    if rc < 0:
+        raise MoeLoraError(rc, "moe_lora_muon_get_error")
+    return rc
 
 
 # ------------------------------------------------------------------ convenience

@@ -14,6 +14,8 @@ enum ProfSlot {
   K_ROUTER_FWD, K_ROUTER_DL, K_ROUTER_DX, K_ROUTER_DW,
   K_W13_NV, K_W2_NV, K_DW_NV,  // native FP4 forward
   K_NORM_FWD, K_NORM_BWD, K_NORM_WGRAD, K_BAL_COUNT, K_BAL_LOSS, K_BAL_SUM, K_ADAMW,  // training step
+  K_TOKEN_FWD, K_TOKEN_BWD, K_TOKEN_COUNT, K_POLICY, K_TERM_SUM, K_PREF,  // post-training
+  K_MUON_GRAM, K_MUON_POLY, K_MUON_APPLY, K_MUON_UPDATE,
   K_NUM_SLOTS
 };
 
