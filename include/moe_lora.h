@@ -434,7 +434,7 @@ MOE_LORA_API int moe_lora_adamw_step(const moe_lora_adamw* opt, const moe_lora_a
  * are the row strides of the logits and of their gradient in elements (0 = n, else >= n), and
  * rows need not start on 16 bytes.  0 <= rows <= 2^26, 1 <= n <= 2^19 (else
  * MOE_LORA_ERR_UNSUPPORTED); rows = 0 is a no-op.  inv_temp multiplies the logits (the inverse
- * of the sampling temperature), 1e-30 <= inv_temp <= 1e30. */
+ * of the sampling temperature), 1e-6 <= inv_temp <= 1e6. */
 typedef struct moe_lora_rows {
   int64_t rows;
   int64_t ld;
@@ -480,7 +480,8 @@ MOE_LORA_API int moe_lora_token_logp_backward(const moe_lora_rows* r, const void
  * Logits are read once, for the loss and the gradient together.  Equal calls give equal bits, and an
  * adapter's tokens are added in an order of their own; calls with other numbers of rows may cut rows
  * differently, and differ in the last bits of a token's values.  scratch: moe_lora_policy_scratch_bytes(rows, adapters) bytes (0 for
- * bad sizes); calls that may run at the same time need one each. */
+ * bad sizes), whose first 16 bytes the caller clears once; calls that may run at the same time need one
+ * each. */
 typedef struct moe_lora_policy {
   float clip_low;   /* in [0, 1] */
   float clip_high;  /* >= 0 */
@@ -512,8 +513,8 @@ MOE_LORA_API int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_pol
  *   seq_logp [2 pairs] fp32 (s_j) or NULL
  *   dlogp [tokens] fp32 or NULL: 0 at the sequences' tokens that are not live; tokens of no sequence
  *            are left as they were
- * scratch: moe_lora_preference_scratch_bytes(pairs) bytes; calls that may run at the same time need
- * one each. */
+ * scratch: moe_lora_preference_scratch_bytes(pairs) bytes, whose first 16 bytes the caller clears
+ * once; calls that may run at the same time need one each. */
 #define MOE_LORA_PREF_SIGMOID 0
 #define MOE_LORA_PREF_SQUARED 1
 #define MOE_LORA_PREF_HINGE 2

@@ -708,12 +708,19 @@ def moe_lora_token_logp_backward(logits: torch.Tensor, targets: torch.Tensor, ls
     _check(rc, "moe_lora_token_logp_backward")
 
 
+def _ticket_scratch(nbytes: int, device) -> torch.Tensor:
+    """A workspace whose first 16 bytes are cleared, once."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    t[:16].zero_()
+    return t
+
+
 def policy_scratch(rows: int, adapters: int = 1, device="cuda") -> torch.Tensor:
     """Workspace of moe_lora_policy_loss."""
     b = int(lib().moe_lora_policy_scratch_bytes(rows, adapters))
     if b == 0:
         raise MoeLoraError(-2, "moe_lora_policy_scratch_bytes")
-    return torch.empty(b, dtype=torch.uint8, device=device)
+    return _ticket_scratch(b, device)
 
 
 def _host_offsets(offsets: Optional[Sequence[int]], adapters: int, name: str):
@@ -759,7 +766,7 @@ def preference_scratch(pairs: int, adapters: int = 1, device="cuda") -> torch.Te
     b = int(lib().moe_lora_preference_scratch_bytes(pairs))
     if b == 0 or not 1 <= adapters <= 64:
         raise MoeLoraError(-2, "moe_lora_preference_scratch_bytes")
-    return torch.empty(b, dtype=torch.uint8, device=device)
+    return _ticket_scratch(b, device)
 
 
 def moe_lora_preference_loss(logp: torch.Tensor, targets: torch.Tensor, seq_offsets: torch.Tensor,
@@ -821,8 +828,7 @@ class MuonTensors:
         if b == 0:
             raise MoeLoraError(-5, "moe_lora_muon_scratch_bytes")
         device = self.entries[0]["p"].device if self.entries else "cuda"
-        self.scratch = torch.empty(b, dtype=torch.uint8, device=device)
-        self.scratch[:16].zero_()  # the error word
+        self.scratch = _ticket_scratch(b, device)  # starts with the error word
 
     def set_lr(self, lr: float) -> None:
         for d in self.table:

@@ -58,6 +58,9 @@ struct PolicyArgs {
   float low, high, kl;  // borders of the ratio, weight of the KL term
   const int* count;     // [A][kCountParts] live tokens, where there are no weights
   float* terms;         // [kTerms][rows]
+  bool few;             // so few rows that the last one done adds the terms
+  unsigned* ticket;     // of those
+  float *loss, *stats;
 };
 struct GradArgs {
   void* dx;
@@ -80,10 +83,11 @@ struct Slice {
   int lead, count; // elements ahead of the first vector; vectors of this slice
   int first;       // column of the slice's first vector
   int edge;        // this thread's single element, -1 = none
-  __device__ __forceinline__ Slice(const T* row, int n, int rank, int slices, int tid) : p(row) {
+  // `per` vectors to a slice; enough for the row
+  __device__ __forceinline__ Slice(const T* row, int n, int rank, int slices, int per, int tid) : p(row) {
     const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
     lead = min(n, off ? VL - off : 0);
-    const int all = (n - lead) / VL, per = (all + slices - 1) / slices;
+    const int all = (n - lead) / VL;
     const int v0 = min(all, rank * per);
     count = min(per, all - v0);
     first = lead + v0 * VL;
@@ -151,31 +155,156 @@ __device__ __forceinline__ Vec<T, 16 / sizeof(T)> grad_vec(const float2 (&e)[8 /
   return v;
 }
 
+// The largest value of a warp's lanes (NaN is passed over).
+__device__ __forceinline__ float warp_top(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// A maximum, the sum of 2^((x - m) c) and of that times x - m.
+struct Softmax {
+  float m, s, w;
+  // the same sums relative to another maximum
+  template <bool kEntropy>
+  __device__ __forceinline__ void move(float to, float c) {
+    const float ref = to == -INFINITY ? 0.f : to, d = fmaxf(m - ref, -3e38f), f = ex2_fast(d * c);
+    if (kEntropy) w = f > 0.f ? f * (w + s * d) : 0.f;
+    s *= f;
+    m = to;
+  }
+  // of all lanes: the maximum first, then symmetric sums, so that every lane has the same bits
+  template <bool kEntropy>
+  __device__ __forceinline__ void over_warp(float c) {
+    move<kEntropy>(warp_top(m), c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (kEntropy) w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
+  }
+};
+
+// Two elements (one of fp32) in a word: the larger ones, NaN passed over; and -inf made the type's
+// lowest number, NaN kept.
+template <class T>
+__device__ __forceinline__ uint32_t top_words(uint32_t a, uint32_t b);
+template <class T>
+__device__ __forceinline__ uint32_t lift_word(uint32_t a);
+template <class T>
+constexpr float kLowest = -3.4028234663852886e38f;
+template <>
+constexpr float kLowest<__nv_bfloat16> = -3.3895313892515355e38f;
+template <>
+constexpr float kLowest<__half> = -65504.f;
+template <>
+__device__ __forceinline__ uint32_t top_words<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+__device__ __forceinline__ uint32_t top_words<__half>(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+__device__ __forceinline__ uint32_t top_words<float>(uint32_t a, uint32_t b) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+template <>
+__device__ __forceinline__ uint32_t lift_word<__nv_bfloat16>(uint32_t a) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0xFF7FFF7Fu));
+  return d;
+}
+template <>
+__device__ __forceinline__ uint32_t lift_word<__half>(uint32_t a) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0xFBFFFBFFu));
+  return d;
+}
+template <>
+__device__ __forceinline__ uint32_t lift_word<float>(uint32_t a) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(kLowest<float>));
+  return __float_as_uint(d);
+}
+
+// The sums of few rows (pairs) by the warp that came last, an adapter after the other: lanes add
+// their elements in order, then a butterfly.
+template <class F>
+__device__ __forceinline__ void sum_terms_here(const float* terms, int64_t stride, const Ranges& ad, F by, float* loss, float* stats) {
+  const int lane = threadIdx.x & 31;
+  for (int a = 0; a < ad.n; ++a) {
+    float v[kTerms] = {};
+#pragma unroll 4
+    for (int64_t i = ad.off[a] + lane; i < ad.off[a + 1]; i += 32)
+#pragma unroll
+      for (int k = 0; k < kTerms; ++k) v[k] += __ldcg(terms + k * stride + i);
+    const float f = by(a);
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      if (lane == 0) (k ? stats[a * (kTerms - 1) + k - 1] : loss[a]) = v[k] * f;
+    }
+  }
+}
+// Notes that this warp's terms are written; true for all lanes of the warp that came last of `all`.
+__device__ __forceinline__ bool came_last(unsigned* ticket, unsigned all) {
+  unsigned at = 0;
+  if ((threadIdx.x & 31) == 0) {
+    __threadfence();
+    at = atomicInc(ticket, all - 1);  // back to 0 after the last
+    __threadfence();
+  }
+  return __shfl_sync(0xffffffffu, at, 0) == all - 1;
+}
+__device__ __forceinline__ int live_in(const int32_t* targets, int n, int64_t lo, int64_t hi) {
+  int c = 0;
+#pragma unroll 4
+  for (int64_t t = lo + (threadIdx.x & 31); t < hi; t += 32) c += (unsigned)targets[t] < (unsigned)n;
+  return __reduce_add_sync(0xffffffffu, c);
+}
+
 // Log probabilities (kPolicy false), or the policy loss's terms and, with kGrad, its
-// gradient.  kTeam threads work on a slice: a block's 256, or a warp whose slice is the row.
-//
-// Both reductions (the maximum, then the sums relative to it) are symmetric, so that every
-// thread of the cluster has the same bits.
+// gradient.  kTeam threads work on a slice: a block's, or a warp whose slice is the row.
+// What happens once per row is left to one warp: with a slice of 64 KB a warp has 16 vectors
+// a lane, and a few hundred instructions around them cost as much as the vectors.
 template <class T, int kTeam, int kGroups, bool kEntropy, bool kPolicy, bool kGrad>
 __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     token_row_kernel(const __grid_constant__ RowArgs g, const __grid_constant__ PolicyArgs pg,
-                     const __grid_constant__ GradArgs dg, const __grid_constant__ Ranges ad, int slices) {
+                     const __grid_constant__ GradArgs dg, const __grid_constant__ Ranges ad, int slices, int per) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2, kWarps = kTeam / 32;
   extern __shared__ __align__(16) uint8_t row_smem[];
-  __shared__ float3 part[kMaxCluster * kWarps];
+  __shared__ Softmax part[kMaxCluster + kWarps];
+  __shared__ float3 result;  // the maximum, the factor of all exponentials and of the target's one
   __shared__ float at_target;
   const Ring<1, kGroups * kGroup> ring(row_smem);
-  const int tid = threadIdx.x % kTeam, lane = threadIdx.x & 31, rank = kTeam == 32 ? 0 : blockIdx.x % slices;
-  const int64_t t = kTeam == 32 ? (int64_t)blockIdx.x * (kShortThreads / 32) + (threadIdx.x >> 5) : blockIdx.x / slices;
+  const int tid = threadIdx.x % kTeam, lane = threadIdx.x & 31, warp = tid >> 5;
+  const int rank = kTeam > 32 && slices > 1 ? (int)cluster_rank() : 0;
+  int64_t t = blockIdx.x;
+  if (kTeam == 32)
+    t = t * (kShortThreads / 32) + (threadIdx.x >> 5);
+  else if (slices > 1)
+    asm("{ .reg .u32 c; mov.u32 c, %%clusterid.x; cvt.u64.u32 %0, c; }" : "=l"(t));
   if (kPolicy) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (t >= g.rows) return;  // (a warp's own row)
   const T* row = static_cast<const T*>(g.x) + t * g.ld;
   const int y = checked_target(g.targets[t], g.n, g.err, rank == 0 && tid == 0);
-  const Slice<T> sl(row, g.n, rank, slices, tid);
+  const Slice<T> sl(row, g.n, rank, slices, per, tid);
   T* out = kGrad ? static_cast<T*>(dg.dx) + t * dg.ldd : nullptr;
   const bool aligned = kGrad && same_phase(row, out);
+  const bool clerk = rank == 0 && warp == 0;  // the warp that works for the row
+  const auto finish = [&] {  // few rows: the last one adds them all
+    if (kPolicy && pg.few && clerk && came_last(pg.ticket, (unsigned)g.rows))
+      sum_terms_here(pg.terms, g.rows, ad, [&](int a) {
+        return pg.weight ? 1.f : 1.f / (float)max(live_in(g.targets, g.n, ad.off[a], ad.off[a + 1]), 1);
+      }, pg.loss, pg.stats);
+  };
   if (y < 0) {  // the same for the whole cluster, which has not met yet
-    if (rank == 0 && tid == 0) {
+    if (clerk && lane == 0) {
       if (g.logp) g.logp[t] = 0.f;
       if (g.lse) g.lse[t] = 0.f;
       if (g.entropy) g.entropy[t] = 0.f;
@@ -185,14 +314,17 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     }
     if (kGrad) zero_slice<T, kTeam>(sl, out, aligned, tid);
     if (kPolicy) asm volatile("griddepcontrol.wait;" ::: "memory");
+    finish();
     return;
   }
   // a thread's vectors: tid, tid + kTeam, ... of the slice
+  {
+    const T* src = row + sl.first + tid * VL;
 #pragma unroll
-  for (int i = 0; i < kGroups * kGroup; ++i) {
-    const int v = tid + i * kTeam;
-    if (v < sl.count) async_copy16(ring.slot(0, i), row + sl.first + v * VL);
-    if (i % kGroup == kGroup - 1) async_commit();
+    for (int i = 0; i < kGroups * kGroup; ++i) {
+      if (tid + i * kTeam < sl.count) async_copy16(ring.slot(0, i), src + i * kTeam * VL);
+      if (i % kGroup == kGroup - 1) async_commit();
+    }
   }
   if (kTeam > 32 && slices > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const float xe = sl.edge >= 0 ? to_f32(row[sl.edge]) : -INFINITY;
@@ -202,26 +334,27 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
   if (kTeam > 32 && tid == 0) at_target = xy;
   float adv = 0.f, old = 0.f, ref = 0.f, wt = 1.f, up = 1.f;
   int a = 0;
-  if (kPolicy) {
+  if (kPolicy && warp == 0) {
     a = range_of(ad, t);
     adv = pg.adv[t];
     old = pg.old[t];
     if (pg.ref) ref = pg.ref[t];
     if (pg.weight) wt = pg.weight[t];
     if (pg.dloss) up = pg.dloss[a];
+    if (kGrad && pg.few && !pg.weight) up /= (float)max(live_in(g.targets, g.n, ad.off[a], ad.off[a + 1]), 1);
   }
 
   const float c = g.inv_temp * kLog2e;
   // An empty place reads as -inf.
   const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
-  float m = -INFINITY;
+  Softmax sm{-INFINITY, 0.f, 0.f};
   float2 s2 = both(0.f), w2 = both(0.f);
   const auto shift = [&](float top) {  // sums relative to the maximum so far, or 0 while there is none
-    const float from = m, to = fmaxf(m, top), ref0 = to == -INFINITY ? 0.f : to;
-    const float d = fmaxf((from - ref0) * c, -127.f), f = ex2_fast(d);
-    if (kEntropy) w2 = mul2(fma2(s2, both(d), w2), both(f));
+    const float to = fmaxf(sm.m, top), ref0 = to == -INFINITY ? 0.f : to;
+    const float d = fmaxf(sm.m - ref0, -3e38f), f = ex2_fast(d * c);
+    if (kEntropy) w2 = f > 0.f ? mul2(fma2(s2, both(d), w2), both(f)) : both(0.f);
     s2 = mul2(s2, both(f));
-    m = to;
+    sm.m = to;
     return ref0;
   };
 #pragma unroll
@@ -239,7 +372,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     else
       async_wait<4>();
     Vec<T, VL> u[kGroup];
-    float top = -INFINITY;
+    uint32_t tw = none;
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) {
       const int i = gr * kGroup + j;
@@ -248,133 +381,138 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
       else
         u[j].w[0] = u[j].w[1] = u[j].w[2] = u[j].w[3] = none;
 #pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        const float2 f = u[j].get(p);
-        top = fmaxf(top, fmaxf(f.x, f.y));
+      for (int k = 0; k < 4; ++k) {
+        tw = top_words<T>(tw, u[j].w[k]);
       }
+    }
+    float top;
+    if constexpr (sizeof(T) == 4) {
+      top = __uint_as_float(tw);
+    } else {
+      const float2 t2 = Two<T>::get(&tw);
+      top = fmaxf(t2.x, t2.y);
     }
     const float r = shift(top);
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j)
+    for (int j = 0; j < kGroup; ++j) {
+      if (kEntropy)  // 0 * -inf: the type's lowest number takes the place of -inf, two at a time
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[j].w[k] = lift_word<T>(u[j].w[k]);
 #pragma unroll
       for (int p = 0; p < kP; ++p) {
-        float2 x = mul2(add2(u[j].get(p), both(-r)), both(c));
+        const float2 d = add2(u[j].get(p), both(-r)), x = mul2(d, both(c));
         const float2 e = make_float2(ex2_fast(x.x), ex2_fast(x.y));
         s2 = add2(s2, e);
-        // 0 * -inf is 0 here, and a NaN stays one in e
-        if (kEntropy) w2 = fma2(e, make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f)), w2);
+        if (kEntropy) w2 = fma2(e, d, w2);
       }
+    }
+  }
+  // Where the maximum is so near the type's lowest number that its probability is not 0, the sums
+  // are formed again with -inf as it is.
+  if (kEntropy && sm.m != -INFINITY && !((kLowest<T> - sm.m) * c <= -150.f)) {
+    s2 = w2 = both(0.f);
+#pragma unroll 1
+    for (int v = tid, i = 0; v < sl.count; v += kTeam, ++i) {
+      Vec<T, VL> u;
+      u.from_smem(ring.slot(0, i));
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        const float2 d = add2(u.get(p), both(-sm.m)), x = mul2(d, both(c));
+        const float2 e = make_float2(ex2_fast(x.x), ex2_fast(x.y));
+        s2 = add2(s2, e);
+        w2 = fma2(e, make_float2(fmaxf(d.x, -3e38f), fmaxf(d.y, -3e38f)), w2);
+      }
+    }
   }
   async_wait<0>();
   if (sl.edge >= 0) {
-    const float r = shift(xe);
-    const float x = (xe - r) * c, e = ex2_fast(x);
+    const float r = shift(xe), e = ex2_fast((xe - r) * c);
     s2.x += e;
-    if (kEntropy) w2.x += e * fmaxf(x, -127.f);
+    if (kEntropy) w2.x += e * fmaxf(xe - r, -3e38f);
   }
-  // the warp's, then the cluster's maximum and sums
-  float s = s2.x + s2.y, w = w2.x + w2.y;
-  const auto meet = [&](float top, float mine, float& sum, float& wsum) {  // sum relative to `mine` -> to `top`
-    const float d = fmaxf((mine - (top == -INFINITY ? 0.f : top)) * c, -127.f), f = ex2_fast(d);
-    if (kEntropy) wsum = f * (wsum + sum * d);
-    sum *= f;
-  };
-  float top = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  meet(top, m, s, w);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (kEntropy) w += __shfl_xor_sync(0xffffffffu, w, o);
-  }
-  m = top;
+  sm.s = s2.x + s2.y;
+  sm.w = w2.x + w2.y;
+  sm.over_warp<kEntropy>(c);
+  float q = 0.f, coef = 0.f;
   if (kTeam > 32) {
-    const int warp = threadIdx.x >> 5;
-    if (slices > 1) {
+    if (lane == 0) part[kMaxCluster + warp] = sm;
+    __syncthreads();
+    if (warp == 0) {  // the block's sums
+      sm = lane < kWarps ? part[kMaxCluster + lane] : Softmax{-INFINITY, 0.f, 0.f};
+      sm.over_warp<kEntropy>(c);
+    }
+    if (slices > 1) {  // and the cluster's
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks have started
-      if (lane < slices) {
-        const uint32_t at = mapa_shared(smem_u32(&part[rank * kWarps + warp]), lane);
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(m) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(s) : "memory");
-        if (kEntropy) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(w) : "memory");
+      if (warp == 0 && lane < slices) {
+        const uint32_t at = mapa_shared(smem_u32(&part[rank]), lane);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(sm.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(sm.s) : "memory");
+        if (kEntropy) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(sm.w) : "memory");
       }
       cluster_sync_all();
-    } else {
-      if (lane == 0) part[warp] = make_float3(m, s, w);
-      __syncthreads();
+      if (warp == 0) {
+        sm = lane < slices ? part[lane] : Softmax{-INFINITY, 0.f, 0.f};
+        sm.over_warp<kEntropy>(c);
+      }
     }
     xy = at_target;
-    const int all = slices * kWarps;
-    constexpr int kParts = (kMaxCluster * kWarps + 31) / 32;
-    float mi[kParts];
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-      mi[i] = lane + 32 * i < all ? part[lane + 32 * i].x : -INFINITY;
-      top = fmaxf(top, mi[i]);
+  }
+  if (warp == 0) {
+    const float ls = logf(sm.s);
+    // target minus maximum first: their difference is what counts, not their size
+    const float logp = (xy - sm.m) * g.inv_temp - ls;
+    const float inv_s = 1.0f / sm.s, entropy = kEntropy ? ls - sm.w * inv_s * g.inv_temp : 0.f;
+    if (clerk && lane == 0) {
+      if (g.logp) g.logp[t] = logp;
+      if (g.lse) g.lse[t] = sm.m * g.inv_temp + ls;
+      if (g.entropy) g.entropy[t] = entropy;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    s = w = 0.f;
-#pragma unroll
-    for (int i = 0; i < kParts; ++i)
-      if (lane + 32 * i < all) {
-        float si = part[lane + 32 * i].y, wi = kEntropy ? part[lane + 32 * i].z : 0.f;
-        meet(top, mi[i], si, wi);
-        s += si;
-        w += wi;
+    if (kPolicy) {
+      const float rho = expf(logp - old), clip = fminf(fmaxf(rho, pg.low), pg.high);
+      const bool cut = (adv > 0.f && rho > pg.high) || (adv < 0.f && rho < pg.low);
+      float loss = -(cut ? clip : rho) * adv, kl = 0.f, dl = cut ? 0.f : -rho * adv;
+      if (pg.ref) {
+        const float d = ref - logp, em = expm1f(d);
+        kl = em - d;
+        loss += pg.kl * kl;
+        dl -= pg.kl * em;
       }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (kEntropy) w += __shfl_xor_sync(0xffffffffu, w, o);
+      if (clerk && lane == 0) {  // a token of weight 0 has no part in the loss, whatever its values
+        float* to = pg.terms + t;
+        to[0] = wt == 0.f ? 0.f : wt * loss;
+        to[g.rows] = wt == 0.f ? 0.f : wt * kl;
+        to[2 * g.rows] = cut ? wt : 0.f;
+        to[3 * g.rows] = wt == 0.f ? 0.f : wt * rho;
+        to[4 * g.rows] = wt == 0.f ? 0.f : wt * entropy;
+      }
+      if (!pg.weight && !pg.few) {
+        // the counts, and with them every launch that the sums behind this one rely on
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int k = lane < kCountParts ? pg.count[a * kCountParts + lane] : 0;
+        k = __reduce_add_sync(0xffffffffu, k);
+        up /= (float)max(k, 1);
+      }
+      coef = wt == 0.f ? 0.f : up * wt * dl * g.inv_temp;
+      q = -coef * inv_s;
+      if (kTeam > 32 && kGrad && lane == 0) result = make_float3(sm.m, q, coef);
     }
-    m = top;
   }
-  const float r = m == -INFINITY ? 0.f : m, ls = logf(s);
-  // target minus maximum first: their difference is what counts, not their size
-  const float logp = (xy - m) * g.inv_temp - ls;
-  const float inv_s = 1.0f / s, entropy = kEntropy ? ls - w * inv_s * 0.6931471805599453f : 0.f;
-  const bool scribe = rank == 0 && tid == 0;
-  if (kPolicy && !pg.weight) {
-    // the counts, and with them every launch that the sums behind this one rely on
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int k = 0;
-    if (kGrad)
-#pragma unroll
-      for (int i = 0; i < kCountParts; ++i) k += pg.count[a * kCountParts + i];
-    up /= (float)max(k, 1);
-  }
-  if (scribe) {
-    if (g.logp) g.logp[t] = logp;
-    if (g.lse) g.lse[t] = m * g.inv_temp + ls;
-    if (g.entropy) g.entropy[t] = entropy;
-  }
-  if (!kPolicy) return;
-  const float rho = expf(logp - old), clip = fminf(fmaxf(rho, pg.low), pg.high);
-  const bool cut = (adv > 0.f && rho > pg.high) || (adv < 0.f && rho < pg.low);
-  float loss = -(cut ? clip : rho) * adv, kl = 0.f, dl = cut ? 0.f : -rho * adv;
-  if (pg.ref) {
-    const float d = ref - logp, em = expm1f(d);
-    kl = em - d;
-    loss += pg.kl * kl;
-    dl -= pg.kl * em;
-  }
-  if (scribe) {  // a token of weight 0 has no part in the loss, whatever its values
-    float* to = pg.terms + t;
-    to[0] = wt == 0.f ? 0.f : wt * loss;
-    to[g.rows] = wt == 0.f ? 0.f : wt * kl;
-    to[2 * g.rows] = cut ? wt : 0.f;
-    to[3 * g.rows] = wt == 0.f ? 0.f : wt * rho;
-    to[4 * g.rows] = wt == 0.f ? 0.f : wt * entropy;
-  }
-  if (!kGrad) return;
-  if (wt == 0.f) {
-    zero_slice<T, kTeam>(sl, out, aligned, tid);
+  if (!kGrad) {
+    finish();
     return;
   }
-  const float coef = up * wt * dl * g.inv_temp, q = -coef * inv_s;
+  if (kTeam > 32) {
+    __syncthreads();
+    sm.m = result.x;
+    q = result.y;
+    coef = result.z;
+  }
+  if (coef == 0.f) {  // clipped, without a KL term
+    zero_slice<T, kTeam>(sl, out, aligned, tid);
+    finish();
+    return;
+  }
+  const float r = sm.m == -INFINITY ? 0.f : sm.m;
 #pragma unroll
   for (int i = 0; i < kGroups * kGroup; ++i) {
     const int v = tid + i * kTeam;
@@ -390,6 +528,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     store_vec<T>(out, sl.first + v * VL, aligned, grad_vec<T>(e, q, coef, sl.first + v * VL, y));
   }
   if (sl.edge >= 0) out[sl.edge] = from_f32<T>(q * ex2_fast((xe - r) * c) + (sl.edge == y ? coef : 0.f));
+  finish();
 }
 
 // dlogits from a saved lse: no reduction, every element on its own.  A block takes up to
@@ -397,7 +536,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
 constexpr int kBwdThreads = 256, kBwdVecs = 4;
 template <class T, int kTeam>
 __global__ void __launch_bounds__(kBwdThreads)
-    token_bwd_kernel(const __grid_constant__ RowArgs g, const __grid_constant__ GradArgs dg, const float* dlogp, int slices) {
+    token_bwd_kernel(const __grid_constant__ RowArgs g, const __grid_constant__ GradArgs dg, const float* dlogp, int slices, int per) {
   constexpr int VL = 16 / sizeof(T), kP = VL / 2;
   const int tid = threadIdx.x % kTeam;
   const int rank = kTeam == 32 ? 0 : blockIdx.x % slices;
@@ -406,7 +545,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   const T* row = static_cast<const T*>(g.x) + t * g.ld;
   T* out = static_cast<T*>(dg.dx) + t * dg.ldd;
   const int y = checked_target(g.targets[t], g.n, g.err, rank == 0 && tid == 0);
-  const Slice<T> sl(row, g.n, rank, slices, tid);
+  const Slice<T> sl(row, g.n, rank, slices, per, tid);
   const bool aligned = same_phase(row, out);
   const float up = y < 0 ? 0.f : dlogp[t];
   if (up == 0.f) {
@@ -522,6 +661,31 @@ __global__ void __launch_bounds__(kSumThreads) term_sum_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ preference loss
+// A sum as an fp32 number and what its rounding left: a loss lives on the difference of two large
+// sums, and fp64 additions are slow here.
+struct Long {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {  // exactly
+    const float t = hi + v, b = t - hi;
+    lo += (hi - (t - b)) + (v - b);
+    hi = t;
+  }
+  __device__ __forceinline__ void add(const Long& v) {
+    add(v.hi);
+    lo += v.lo;
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
+  __device__ __forceinline__ Long over(float n) const {
+    const float q = hi / n;
+    return Long{q, (fmaf(-q, n, hi) + lo) / n};
+  }
+};
+__device__ __forceinline__ Long long_over_warp(Long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.add(Long{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
 struct PrefArgs {
   const float* logp;
   const int32_t* targets;
@@ -535,91 +699,157 @@ struct PrefArgs {
   float* terms;  // [kTerms][pairs]
   int64_t pairs;
   int* err;
+  Long target;   // squared: 1 / (2 beta)
+  bool few;      // so few pairs that the last one done adds the terms
+  unsigned* ticket;
+  float *loss, *stats;
 };
-// A block per pair: sums of both sequences (64 bits from the threads' own sums on, since
-// the loss lives on the difference of two large sums), the pair's terms, then the gradient.
+// A block per pair, whose two sequences lie one behind the other: their sums, the pair's
+// terms, then the gradient.  Latency bounds it: a thread has four vectors of four tokens
+// under way, and what it learnt of the first four (which tokens are live) stays with it.
+constexpr int kPrefAhead = 4;
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ PrefArgs g, const __grid_constant__ Ranges ad) {
-  __shared__ double sums[2][kThreads / 32];
+  __shared__ Long sums[2][kThreads / 32];
   __shared__ int counts[2][kThreads / 32];
+  __shared__ float per_token[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t i = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t off[3];
   bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) off[j] = g.seq[2 * i + j];
+#pragma unroll
   for (int j = 0; j < 3; ++j) {  // offsets that go back or past the end are noted; what is left of them is inside
-    const int64_t o = g.seq[2 * i + j], at = max(j ? off[j - 1] : (int64_t)0, min(o, g.T));
-    bad |= at != o;
+    const int64_t at = max(j ? off[j - 1] : (int64_t)0, min(off[j], g.T));
+    bad |= at != off[j];
     off[j] = at;
   }
   if (bad && g.err && threadIdx.x == 0) atomicOr(g.err, MOE_LORA_DEV_BAD_ID);
-  // everything below is of the sequence whose half of the block this is
-  constexpr int kHalf = kThreads / 2;
-  const int j = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, lane = threadIdx.x & 31, warp = tid >> 5;
-  float s = 0.f;
-  int n = 0;
-#pragma unroll 4
-  for (int64_t t = off[j] + tid; t < off[j + 1]; t += kHalf) {
-    const bool live = g.targets[t] >= 0;
-    s += live ? g.logp[t] : 0.f;
-    n += live;
-  }
-  double d = s;
+  const int64_t base = off[0] & ~(int64_t)3;
+  const int64_t vecs = (off[2] - base + 3) / 4;  // of four tokens, on 16 bytes; the first and last may be partly outside
+  const auto load_mask = [&](int64_t v, float (&x)[4]) {  // live tokens of a vector that belong to the pair, and their values
+    const int64_t t = base + 4 * v;
+    int y[4];
+    if (t + 4 <= g.T) {
+      const int4 u = *reinterpret_cast<const int4*>(g.targets + t);
+      const float4 f = *reinterpret_cast<const float4*>(g.logp + t);
+      y[0] = u.x, y[1] = u.y, y[2] = u.z, y[3] = u.w;
+      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (lane == 0) {
-    sums[j][warp] = d;
-    counts[j][warp] = n;
+      for (int e = 0; e < 4; ++e) {
+        y[e] = t + e < g.T ? g.targets[t + e] : -1;
+        x[e] = t + e < g.T ? g.logp[t + e] : 0.f;
+      }
+    }
+    uint32_t live = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) live |= (y[e] >= 0 && t + e >= off[0] && t + e < off[2]) << e;
+    return live;
+  };
+  Long s[2] = {};
+  int n[2] = {0, 0};
+  uint32_t known = 0;  // live tokens of this thread's first vectors
+  for (int64_t v0 = threadIdx.x; v0 < vecs; v0 += kPrefAhead * kThreads) {
+    float x[kPrefAhead][4];
+    uint32_t live[kPrefAhead];
+#pragma unroll
+    for (int j = 0; j < kPrefAhead; ++j) live[j] = v0 + j * kThreads < vecs ? load_mask(v0 + j * kThreads, x[j]) : 0;
+#pragma unroll
+    for (int j = 0; j < kPrefAhead; ++j) {
+      if (v0 < kThreads) known |= live[j] << (4 * j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (live[j] >> e & 1) {
+          const int q = base + 4 * (v0 + j * kThreads) + e >= off[1];
+          const float f = x[j][e];
+          s[0].add(q ? 0.f : f);
+          s[1].add(q ? f : 0.f);
+          n[q] += 1;
+        }
+    }
   }
-  __syncthreads();
-  double tot[2];
-  int cnt[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    tot[q] = 0;
-    cnt[q] = 0;
-    for (int w = 0; w < kHalf / 32; ++w) {
-      tot[q] += sums[q][w];
-      cnt[q] += counts[q][w];
+    s[q] = long_over_warp(s[q]);
+    n[q] = __reduce_add_sync(0xffffffffu, n[q]);
+    if (lane == 0) {
+      sums[q][warp] = s[q];
+      counts[q][warp] = n[q];
     }
-    if (g.average) tot[q] /= max(cnt[q], 1);
   }
-  const double rc = tot[0] - (g.ref ? (double)g.ref[2 * i] : 0.0), rr = tot[1] - (g.ref ? (double)g.ref[2 * i + 1] : 0.0);
-  const double hd = rc - rr;
-  const float h = (float)hd, x = (float)(g.beta * hd - g.margin);
-  float loss, dh;
-  if (g.kind == MOE_LORA_PREF_SIGMOID) {
-    const float e = expf(-fabsf(x)), soft = log1pf(e), near = e / (1.f + e);  // 1 - sigmoid(|x|)
-    loss = (1.f - g.smooth) * (soft + fmaxf(-x, 0.f)) + g.smooth * (soft + fmaxf(x, 0.f));
-    // sigmoid(x) - (1 - smooth) without the difference of two numbers near 1
-    dh = g.beta * (x >= 0.f ? g.smooth - near : near - (1.f - g.smooth));
-  } else if (g.kind == MOE_LORA_PREF_SQUARED) {
-    const float o = (float)(hd - 0.5 / (double)g.beta);
-    loss = o * o;
-    dh = 2.f * o;
-  } else {
-    loss = fmaxf(1.f - x, 0.f);
-    dh = x < 1.f ? -g.beta : 0.f;
+  __syncthreads();
+  if (warp == 0) {
+    Long r[2];
+    float cnt[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      r[q] = long_over_warp(lane < kThreads / 32 ? sums[q][lane] : Long{0.f, 0.f});
+      const int k = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? counts[q][lane] : 0);
+      cnt[q] = g.average ? (float)max(k, 1) : 1.f;
+      if (g.average) r[q] = r[q].over(cnt[q]);
+      if (g.seq_logp && lane == 0) g.seq_logp[2 * i + q] = r[q].value();
+      if (g.ref) r[q].add(-g.ref[2 * i + q]);
+    }
+    Long d = r[0];
+    d.add(Long{-r[1].hi, -r[1].lo});
+    const float h = d.value(), x = g.beta * h - g.margin;
+    float loss, dh;
+    if (g.kind == MOE_LORA_PREF_SIGMOID) {
+      const float e = expf(-fabsf(x)), soft = log1pf(e), near = e / (1.f + e);  // 1 - sigmoid(|x|)
+      loss = (1.f - g.smooth) * (soft + fmaxf(-x, 0.f)) + g.smooth * (soft + fmaxf(x, 0.f));
+      // sigmoid(x) - (1 - smooth) without the difference of two numbers near 1
+      dh = g.beta * (x >= 0.f ? g.smooth - near : near - (1.f - g.smooth));
+    } else if (g.kind == MOE_LORA_PREF_SQUARED) {
+      d.add(-g.target.hi);
+      d.lo -= g.target.lo;
+      const float o = d.value();
+      loss = o * o;
+      dh = 2.f * o;
+    } else {
+      loss = fmaxf(1.f - x, 0.f);
+      dh = x < 1.f ? -g.beta : 0.f;
+    }
     if (isnan(x)) loss = dh = x;
-  }
-  const int a = range_of(ad, i);
-  if (threadIdx.x == 0) {
-    float* to = g.terms + i;
-    to[0] = loss;
-    to[g.pairs] = x > 0.f ? 1.f : 0.f;
-    to[2 * g.pairs] = (float)(g.beta * rc);
-    to[3 * g.pairs] = (float)(g.beta * rr);
-    to[4 * g.pairs] = h;
-    if (g.seq_logp) {
-      g.seq_logp[2 * i] = (float)tot[0];
-      g.seq_logp[2 * i + 1] = (float)tot[1];
+    const int a = range_of(ad, i);
+    if (lane == 0) {
+      float* to = g.terms + i;
+      to[0] = loss;
+      to[g.pairs] = x > 0.f ? 1.f : 0.f;
+      to[2 * g.pairs] = g.beta * r[0].value();
+      to[3 * g.pairs] = g.beta * r[1].value();
+      to[4 * g.pairs] = h;
+      const float up = (g.dloss ? g.dloss[a] : 1.f) / (float)(ad.off[a + 1] - ad.off[a]);
+      per_token[0] = up * dh / cnt[0];
+      per_token[1] = -up * dh / cnt[1];
     }
   }
-  if (!g.dlogp) return;
-  const float up = (g.dloss ? g.dloss[a] : 1.f) / (float)(ad.off[a + 1] - ad.off[a]);
-  const float v = up * dh * (j ? -1.f : 1.f) / (g.average ? (float)max(cnt[j], 1) : 1.f);
-#pragma unroll 4
-  for (int64_t t = off[j] + tid; t < off[j + 1]; t += kHalf) g.dlogp[t] = g.targets[t] >= 0 ? v : 0.f;
+  if (g.dlogp) {
+    __syncthreads();
+    const float p0 = per_token[0], p1 = per_token[1];
+    for (int64_t v = threadIdx.x, j = 0; v < vecs; v += kThreads, ++j) {
+      const int64_t t = base + 4 * v;
+      uint32_t live = known >> (4 * j) & 15;
+      if (j >= kPrefAhead) {
+        float unused[4];
+        live = load_mask(v, unused);
+      }
+      float o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = live >> e & 1 ? (t + e < off[1] ? p0 : p1) : 0.f;
+      if (t >= off[0] && t + 4 <= off[2]) {
+        *reinterpret_cast<float4*>(g.dlogp + t) = make_float4(o[0], o[1], o[2], o[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t + e >= off[0] && t + e < off[2]) g.dlogp[t + e] = o[e];
+      }
+    }
+  }
+  if (g.few && warp == 0 && came_last(g.ticket, (unsigned)g.pairs))
+    sum_terms_here(g.terms, g.pairs, ad, [&](int a) { return 1.f / (float)max(ad.off[a + 1] - ad.off[a], (int64_t)1); }, g.loss, g.stats);
 }
 
 // ------------------------------------------------------------------ host
@@ -652,8 +882,7 @@ int check_rows(const moe_lora_rows* r) {
   if (r->n > kMaxVocab) return MOE_LORA_ERR_UNSUPPORTED;
   if ((r->ld && r->ld < r->n) || (r->ldd && r->ldd < r->n) || r->ld > (int64_t)1 << 32 || r->ldd > (int64_t)1 << 32)
     return MOE_LORA_ERR_DIMS;
-  // the base-2 scale has to be a normal number
-  if (!(r->inv_temp >= 1e-30f) || !(r->inv_temp <= 1e30f)) return MOE_LORA_ERR_DIMS;
+  if (!(r->inv_temp >= 1e-6f) || !(r->inv_temp <= 1e6f)) return MOE_LORA_ERR_DIMS;
   return MOE_LORA_OK;
 }
 RowArgs row_args(const moe_lora_rows* r, const void* x, const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* err) {
@@ -662,12 +891,13 @@ RowArgs row_args(const moe_lora_rows* r, const void* x, const int32_t* targets, 
 
 template <class T, int kTeam, int kGroups, bool kEntropy, bool kPolicy, bool kGrad>
 int launch_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, const Ranges& ad, int slices, bool overlap, cudaStream_t s) {
+  const int vecs = g.n / (int)(16 / sizeof(T)), per = (vecs + slices - 1) / slices;
   const int64_t grid = kTeam == 32 ? (g.rows + kShortThreads / 32 - 1) / (kShortThreads / 32) : g.rows * slices;
   const int threads = kTeam == 32 ? kShortThreads : kTeam;
   const RowLaunch l(grid, threads, ring_bytes<1, kGroups * kGroup>(threads), slices, overlap, s);
   const int slot = kPolicy ? K_POLICY : K_TOKEN_FWD;
   prof_begin(slot, s);
-  const cudaError_t e = launch_allowed(l.cfg, slices > 8, token_row_kernel<T, kTeam, kGroups, kEntropy, kPolicy, kGrad>, g, pg, dg, ad, slices);
+  const cudaError_t e = launch_allowed(l.cfg, slices > 8, token_row_kernel<T, kTeam, kGroups, kEntropy, kPolicy, kGrad>, g, pg, dg, ad, slices, per);
   prof_end(slot, s);
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
@@ -708,9 +938,9 @@ int run_bwd(const RowArgs& g, const GradArgs& dg, const float* dlogp, cudaStream
   const int vecs = g.n / VL, slices = std::max(1, (vecs + kBwdThreads * kBwdVecs - 1) / (kBwdThreads * kBwdVecs));
   prof_begin(K_TOKEN_BWD, s);
   if (vecs <= 32 * kBwdVecs)
-    token_bwd_kernel<T, 32><<<(unsigned)((g.rows + kBwdThreads / 32 - 1) / (kBwdThreads / 32)), kBwdThreads, 0, s>>>(g, dg, dlogp, 1);
+    token_bwd_kernel<T, 32><<<(unsigned)((g.rows + kBwdThreads / 32 - 1) / (kBwdThreads / 32)), kBwdThreads, 0, s>>>(g, dg, dlogp, 1, vecs);
   else
-    token_bwd_kernel<T, kBwdThreads><<<(unsigned)(g.rows * slices), kBwdThreads, 0, s>>>(g, dg, dlogp, slices);
+    token_bwd_kernel<T, kBwdThreads><<<(unsigned)(g.rows * slices), kBwdThreads, 0, s>>>(g, dg, dlogp, slices, (vecs + slices - 1) / slices);
   prof_end(K_TOKEN_BWD, s);
   return cudaGetLastError() == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
@@ -738,8 +968,11 @@ int launch_sums(const SumArgs& g, const Ranges& ad, cudaStream_t s) {
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-// Scratch of the losses: the items' terms, then the adapters' partial counts.
+// Scratch of the losses: a ticket, the items' terms, then the adapters' partial counts.
+constexpr size_t kTicketBytes = 256;
 size_t terms_bytes(int64_t items) { return align_up(sizeof(float) * kTerms * (size_t)std::max<int64_t>(items, 1), 256); }
+// Few items: counted, and their terms added, where the items are worked on, in one launch.
+constexpr int kFew = 256;
 
 }  // namespace
 
@@ -787,7 +1020,7 @@ extern "C" int moe_lora_token_logp_backward(const moe_lora_rows* r, const void* 
 
 extern "C" size_t moe_lora_policy_scratch_bytes(int64_t rows, int32_t adapters) {
   if (rows < 0 || rows > (int64_t)1 << 26 || adapters < 1 || adapters > kMaxAdapters) return 0;
-  return terms_bytes(rows) + align_up(sizeof(int) * kCountParts * adapters, 256);
+  return kTicketBytes + terms_bytes(rows) + align_up(sizeof(int) * kCountParts * adapters, 256);
 }
 
 extern "C" int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_policy* o, const void* logits, const int32_t* targets,
@@ -814,26 +1047,29 @@ extern "C" int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_polic
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int* count = reinterpret_cast<int*>(static_cast<char*>(scratch) + terms_bytes(r->rows));
-  PolicyArgs pg{advantages, old_logp, ref_logp, weight, dloss, 1.f - o->clip_low, 1.f + o->clip_high, o->kl_coef, count,
-                static_cast<float*>(scratch)};
-  if (!weight) {
+  char* at = static_cast<char*>(scratch);
+  float* terms = reinterpret_cast<float*>(at + kTicketBytes);
+  int* count = reinterpret_cast<int*>(at + kTicketBytes + terms_bytes(r->rows));
+  const bool few = r->rows > 0 && r->rows <= kFew;
+  const PolicyArgs pg{advantages, old_logp, ref_logp, weight, dloss, 1.f - o->clip_low, 1.f + o->clip_high, o->kl_coef, count, terms,
+                      few, reinterpret_cast<unsigned*>(at), loss, stats};
+  if (!weight && !few) {
     prof_begin(K_TOKEN_COUNT, s);
     token_count_kernel<<<ad.n * kCountParts, 256, 0, s>>>(targets, r->n, ad, count);
     prof_end(K_TOKEN_COUNT, s);
     if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
   }
   if (r->rows > 0) {
-    rc = r->dtype == MOE_LORA_F32    ? run_policy<float>(g, pg, dg, ad, sms, !weight, s)
-         : r->dtype == MOE_LORA_BF16 ? run_policy<__nv_bfloat16>(g, pg, dg, ad, sms, !weight, s)
-                                     : run_policy<__half>(g, pg, dg, ad, sms, !weight, s);
-    if (rc) return rc;
+    rc = r->dtype == MOE_LORA_F32    ? run_policy<float>(g, pg, dg, ad, sms, !weight && !few, s)
+         : r->dtype == MOE_LORA_BF16 ? run_policy<__nv_bfloat16>(g, pg, dg, ad, sms, !weight && !few, s)
+                                     : run_policy<__half>(g, pg, dg, ad, sms, !weight && !few, s);
+    if (rc || few) return rc;
   }
-  return launch_sums(SumArgs{static_cast<float*>(scratch), r->rows, weight ? nullptr : count, false, loss, stats}, ad, s);
+  return launch_sums(SumArgs{terms, r->rows, weight ? nullptr : count, false, loss, stats}, ad, s);
 }
 
 extern "C" size_t moe_lora_preference_scratch_bytes(int64_t pairs) {
-  return pairs < 0 || pairs > (int64_t)1 << 26 ? 0 : terms_bytes(pairs);
+  return pairs < 0 || pairs > (int64_t)1 << 26 ? 0 : kTicketBytes + terms_bytes(pairs);
 }
 
 extern "C" int moe_lora_preference_loss(const moe_lora_preference* o, const float* logp, const int32_t* targets,
@@ -858,12 +1094,15 @@ extern "C" int moe_lora_preference_loss(const moe_lora_preference* o, const floa
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* terms = static_cast<float*>(scratch);
+  float* terms = reinterpret_cast<float*>(static_cast<char*>(scratch) + kTicketBytes);
   if (o->pairs > 0) {
+    const bool few = o->pairs <= kFew;
+    const double target = 0.5 / (double)o->beta;
     const PrefArgs g{logp, targets, o->tokens, seq_offsets, ref, o->beta, o->margin, o->label_smoothing, o->kind, o->average,
-                     dloss, seq_logp, dlogp, terms, o->pairs, err};
-    // sequences of a thousand tokens and more get a large block
-    const bool wide = o->tokens / (2 * o->pairs) >= 1024;
+                     dloss, seq_logp, dlogp, terms, o->pairs, err, Long{(float)target, (float)(target - (float)target)},
+                     few, static_cast<unsigned*>(scratch), loss, stats};
+    // pairs of more tokens than a small block has under way get a large one
+    const bool wide = o->tokens / o->pairs >= 256 * 4 * kPrefAhead;
     prof_begin(K_PREF, s);
     if (wide)
       pref_kernel<1024><<<(unsigned)o->pairs, 1024, 0, s>>>(g, ad);
@@ -871,6 +1110,7 @@ extern "C" int moe_lora_preference_loss(const moe_lora_preference* o, const floa
       pref_kernel<256><<<(unsigned)o->pairs, 256, 0, s>>>(g, ad);
     prof_end(K_PREF, s);
     if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
+    if (few) return MOE_LORA_OK;
   }
   return launch_sums(SumArgs{terms, o->pairs, nullptr, true, loss, stats}, ad, s);
 }

@@ -38,6 +38,12 @@ def _within(name, got, want, tol):
     assert (off <= tol).all(), (name, float((off / tol).max()))
 
 
+def _poisoned(scratch):
+    """A workspace whose contents do not matter, but for the 16 bytes that are cleared once."""
+    scratch[16:].fill_(0xFF)
+    return scratch
+
+
 def _inputs(rows, n, dt, pad, masked, seed, spread=3.0):
     g = _gen(seed)
     buf = torch.full((rows, n + pad), float("nan"), dtype=dt, device="cuda")
@@ -111,7 +117,7 @@ def test_policy_loss(rows, n, dt, pad, masked, it, with_ref, weighted, adapters)
     dloss = torch.rand(adapters, generator=g, device="cuda") + 0.5
     loss, stats = torch.full((adapters,), float("nan"), device="cuda"), torch.full((adapters, 4), float("nan"), device="cuda")
     logp = torch.full((rows,), float("nan"), device="cuda")
-    sc = m.policy_scratch(rows, adapters).fill_(0xFF)
+    sc = _poisoned(m.policy_scratch(rows, adapters))
     db = torch.full((rows, n + pad), 5.0, dtype=dt, device="cuda")
     kw = dict(clip_low=low, clip_high=high, kl_coef=beta, weight=w, adapter_offsets=offs, inv_temp=it)
     m.moe_lora_policy_loss(x, y, adv, old, rlp, loss, stats, sc, logp=logp, dlogits=db[:, :n], dloss=dloss, **kw)
@@ -268,7 +274,7 @@ def test_preference_loss(lens, offs, kind, average, with_ref, smooth):
     sl, dl = torch.full((2 * P,), float("nan"), device="cuda"), torch.full((T,), 5.0, device="cuda")
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     kw = dict(beta=0.2, kind=kind, label_smoothing=smooth, margin=0.1, average=average, pair_offsets=offs, err=err)
-    m.moe_lora_preference_loss(lp, y, seq, rf, loss, stats, m.preference_scratch(P, A).fill_(0xFF), seq_logp=sl, dlogp=dl, dloss=dloss, **kw)
+    m.moe_lora_preference_loss(lp, y, seq, rf, loss, stats, _poisoned(m.preference_scratch(P, A)), seq_logp=sl, dlogp=dl, dloss=dloss, **kw)
     b32 = torch.tensor(0.2, dtype=F32).item()
     s32, m32 = torch.tensor(smooth, dtype=F32).item(), torch.tensor(0.1, dtype=F32).item()
     wl, ws, wt, wd = ref.preference(clean, y, seq, None if rf is None else rf.cpu(), offs or [0, P], dloss, b32, kind, s32, m32, average)
