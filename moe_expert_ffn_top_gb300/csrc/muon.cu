@@ -25,10 +25,12 @@
 //
 // A tile is 128 rows of the short sides: 128 / s matrices of a tensor, one below the other,
 // whose products with each other are set to 0 wherever a tile of G is read.  A chunk is 64
-// places of the long side, a piece a few chunks of a tile: the work of a block.
+// places of the long side.  Blocks share all chunks evenly; what a block has of one tile is a
+// stretch, and leaves one partial G.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "element.cuh"
@@ -56,205 +58,213 @@ struct MuonTensor {
   float* master;
   const void* g;
   float* m;
-  int64_t batch, tile0, piece0;  // matrices; first tile and piece of the launch
+  int64_t batch;                 // matrices
+  int32_t tile0, chunk0;         // first tile and chunk of the launch
   int32_t s, L, tall;            // tall: [L, s] in memory
-  int32_t per, pieces;           // matrices of a tile, pieces of a tile
+  int32_t per, chunks;           // matrices, and chunks, of a tile
   int32_t p_dtype, g_dtype;
   float decay, step;             // 1 - lr * weight_decay, lr * scale
 };
 struct MuonTable {
-  int n, piece;                  // tensors; chunks of a piece
-  int64_t tiles, pieces;
+  int n, blocks, chunks;         // tensors; blocks, which share the chunks evenly
   float mu, nu, eps, a, b, c;    // nu = 1 - mu
   int nesterov;
   const float* gs;
   int* err;
-  float *gram, *norm;            // [pieces][128][128], [tiles][128]: norm, factor of a row's matrix
+  float *gram, *norm;            // [tiles + blocks][128][128], [tiles][2][128]: scale and factor of a row's matrix
   uint8_t *poly, *x;             // [tiles][kPoly], [chunks][kImage]
   MuonTensor t[kMaxTensors];
 };
 static_assert(sizeof(MuonTable) <= 32764, "kernel parameter limit");
 
-struct Place {  // of a piece
+// Block b's chunks begin at b * chunks / blocks: all blocks have the same number, give or take
+// one, wherever tiles begin.
+__device__ __forceinline__ int first_chunk(const MuonTable& tab, int b) { return (int)((int64_t)b * tab.chunks / tab.blocks); }
+// Where the sums of a stretch of a tile that begins at chunk x lie: stretches begin with tiles and
+// with blocks, so that the tile and the blocks begun by then number them without gaps within a tile.
+__device__ __forceinline__ int64_t stretch_slot(const MuonTable& tab, int tile, int x) {
+  return tile + ((int64_t)(x + 1) * tab.blocks - 1) / tab.chunks;
+}
+struct Place {  // a stretch of one tile's chunks
   const MuonTensor* t;
-  int64_t tile, image;  // of the launch; first chunk's image in the scratch
+  int tile, x;          // of the launch; its first chunk, whose image in the scratch has that place
   int64_t first;        // first matrix
   int rows;             // short sides in use
-  int c0, c1;           // chunks
+  int c0, c1;           // chunks of the tile
 };
-__device__ __forceinline__ int64_t chunks_of(const MuonTensor& t) { return (t.L + kChunk - 1) / kChunk; }
-__device__ __forceinline__ Place place_of(const MuonTable& tab, int64_t piece) {
+// The stretch from chunk x on that ends with its tile or at chunk `end`.
+__device__ __forceinline__ Place place_of(const MuonTable& tab, int x, int end) {
   int lo = 0, hi = tab.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (piece >= tab.t[mid].piece0)
+    if (x >= tab.t[mid].chunk0)
       lo = mid;
     else
       hi = mid - 1;
   }
   const MuonTensor& t = tab.t[lo];
-  const int64_t tile = (piece - t.piece0) / t.pieces, part = (piece - t.piece0) % t.pieces;
+  const int tile = (x - t.chunk0) / t.chunks;
   Place p;
   p.t = &t;
   p.tile = t.tile0 + tile;
-  p.first = tile * t.per;
+  p.x = x;
+  p.first = (int64_t)tile * t.per;
   p.rows = (int)min((int64_t)t.per, t.batch - p.first) * t.s;
-  p.c0 = (int)part * tab.piece;
-  p.c1 = min(p.c0 + tab.piece, (int)chunks_of(t));
-  // images lie piece by piece, tab.piece to each
-  p.image = piece * tab.piece;
+  p.c0 = x - t.chunk0 - tile * t.chunks;
+  p.c1 = min(t.chunks, p.c0 + (end - x));
   return p;
 }
 
 // ------------------------------------------------------------------ a thread's share of a chunk
-// Quad i of a thread: four neighbouring elements in memory.  Rows of the short side [s, L]:
-// along the long side; tall matrices [L, s]: along the short one.
-struct Quad {
-  int row, col;  // short side within the tile, long side within the chunk, of its first element
-  __device__ __forceinline__ Quad(bool tall, int i) {
-    if (tall) {
+// A thread's quads of a chunk, four neighbouring elements in memory each.  Of [s, L]: along the
+// long side, 16 to a row.  Of tall matrices [L, s]: along the short side, 32 to a long place.
+// Everything is linear in the quad and the chunk, divisions are done once.
+struct Walk {
+  int64_t at, hop, chunk;     // element of quad 0 in chunk 0 of the tile; to the next quad, chunk
+  int row, col;               // of quad 0: short side within the tile, long side within the chunk
+  int hop_row, hop_col;
+  uint32_t smem, hop_smem;    // bytes in a part of an operand tile
+  int rows, L;
+  // Operand tiles have rows of 128 bytes whose 16-byte units are exchanged by row (unit ^ row % 8).
+  // A chunk of [s, L]: 128 rows of 64 long places.  Of [L, s]: two halves of 64 short places, a
+  // row per long place.  Neither the quads' steps nor the chunks' change row % 8.
+  __device__ __forceinline__ Walk(const MuonTensor& t, int64_t first, int rows_) : rows(rows_), L(t.L) {
+    const int64_t base = first * t.s * t.L;
+    int r, k, half;
+    if (t.tall) {
       row = (threadIdx.x & 31) * 4;
-      col = i * (kThreads / 32) + (threadIdx.x >> 5);
+      col = threadIdx.x >> 5;
+      hop_row = 0;
+      hop_col = kThreads / 32;
+      const int j = row / t.s;
+      at = base + ((int64_t)j * t.L + col) * t.s + (row - j * t.s);
+      hop = (int64_t)hop_col * t.s;
+      chunk = (int64_t)kChunk * t.s;
+      r = col, k = row % 64, half = row / 64 * (kPart / 2);
+      hop_smem = hop_col * 128;
     } else {
-      row = i * (kThreads / 16) + (threadIdx.x >> 4);
+      row = threadIdx.x >> 4;
       col = (threadIdx.x & 15) * 4;
+      hop_row = kThreads / 16;
+      hop_col = 0;
+      at = base + (int64_t)row * t.L + col;
+      hop = (int64_t)hop_row * t.L;
+      chunk = kChunk;
+      r = row, k = col, half = 0;
+      hop_smem = hop_row * 128;
     }
+    smem = half + r * 128 + ((((k >> 3) ^ (r & 7)) << 4) | ((k & 4) << 1));
+  }
+  // How many of the quads of chunk c lie inside, where quads lie inside or outside as a whole.
+  __device__ __forceinline__ int inside(int c) const {
+    const int l = L - c * kChunk - col, r = rows - row;
+    if (hop_row) return l <= 0 || r <= 0 ? 0 : min(kQuads, (r + hop_row - 1) / hop_row);
+    return l <= 0 || r <= 0 ? 0 : min(kQuads, (l + hop_col - 1) / hop_col);
   }
 };
-// Element offset of (row, long index) from the tile's first matrix.
-__device__ __forceinline__ int64_t offset_of(const MuonTensor& t, int row, int l) {
-  if (!t.tall) return (int64_t)row * t.L + l;
-  const int j = row / t.s;
-  return ((int64_t)j * t.L + l) * t.s + (row - j * t.s);
-}
-// Whether all quads lie inside one matrix's run of memory and on 16 bytes (8 of 16-bit types).
+// Whether quads lie inside one matrix's run of memory, and on 16 bytes (8 of 16-bit types).
 __device__ __forceinline__ bool quads_aligned(const MuonTensor& t) { return t.tall ? t.s % 4 == 0 : t.L % 4 == 0; }
+// Element e of quad i elsewhere: its offset, or -1 outside.
+__device__ __forceinline__ int64_t element_at(const MuonTensor& t, const Walk& w, int64_t first, int c, int i, int e) {
+  const int row = w.row + i * w.hop_row + (t.tall ? e : 0), l = c * kChunk + w.col + i * w.hop_col + (t.tall ? 0 : e);
+  if (row >= w.rows || l >= t.L) return -1;
+  const int j = row / t.s, r = row - j * t.s;
+  return (first + j) * t.s * t.L + (t.tall ? (int64_t)l * t.s + r : (int64_t)r * t.L + l);
+}
 
-__device__ __forceinline__ float ld_one(const void* p, int dtype, int64_t i) {
-  return dtype == MOE_LORA_F32    ? static_cast<const float*>(p)[i]
-         : dtype == MOE_LORA_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[i])
-                                  : to_f32(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void st_one(void* p, int dtype, int64_t i, float v) {
-  if (dtype == MOE_LORA_F32)
-    static_cast<float*>(p)[i] = v;
-  else if (dtype == MOE_LORA_BF16)
-    static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v);
-  else
-    static_cast<__half*>(p)[i] = from_f32<__half>(v);
-}
-// Four elements as loaded, and widened.
-__device__ __forceinline__ uint4 ld_quad(const void* p, int dtype, int64_t i) {
-  if (dtype == MOE_LORA_F32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+template <int kType>
+__device__ __forceinline__ uint4 ld_quad(const void* p, int64_t i) {
+  if (kType == MOE_LORA_F32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
   const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
   return make_uint4(u.x, u.y, 0, 0);
 }
-__device__ __forceinline__ float4 widen(const uint4& u, int dtype) {
-  if (dtype == MOE_LORA_F32)
-    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
-  const float2 a = dtype == MOE_LORA_BF16 ? Two<__nv_bfloat16>::get(&u.x) : Two<__half>::get(&u.x);
-  const float2 b = dtype == MOE_LORA_BF16 ? Two<__nv_bfloat16>::get(&u.y) : Two<__half>::get(&u.y);
-  return make_float4(a.x, a.y, b.x, b.y);
+struct Four {
+  float2 a, b;
+};
+template <int kType>
+__device__ __forceinline__ Four widen(const uint4& u) {
+  if constexpr (kType == MOE_LORA_F32) return Four{Two<float>::get(&u.x), Two<float>::get(&u.z)};
+  using E = typename std::conditional<kType == MOE_LORA_F16, __half, __nv_bfloat16>::type;
+  return Four{Two<E>::get(&u.x), Two<E>::get(&u.y)};
 }
-__device__ __forceinline__ void st_quad(void* p, int dtype, int64_t i, const float4& v) {
-  if (dtype == MOE_LORA_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
-    return;
-  }
-  uint2 u;
-  if (dtype == MOE_LORA_BF16) {
-    Two<__nv_bfloat16>::put(&u.x, make_float2(v.x, v.y));
-    Two<__nv_bfloat16>::put(&u.y, make_float2(v.z, v.w));
+template <int kType>
+__device__ __forceinline__ void st_quad(void* p, int64_t i, const Four& v) {
+  if constexpr (kType == MOE_LORA_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
   } else {
-    Two<__half>::put(&u.x, make_float2(v.x, v.y));
-    Two<__half>::put(&u.y, make_float2(v.z, v.w));
+    using E = typename std::conditional<kType == MOE_LORA_F16, __half, __nv_bfloat16>::type;
+    uint2 u;
+    Two<E>::put(&u.x, v.a);
+    Two<E>::put(&u.y, v.b);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = u;
   }
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = u;
+}
+template <int kType>
+__device__ __forceinline__ float ld_one(const void* p, int64_t i) {
+  using E = typename std::conditional<kType == MOE_LORA_F32, float, typename std::conditional<kType == MOE_LORA_F16, __half, __nv_bfloat16>::type>::type;
+  return to_f32(static_cast<const E*>(p)[i]);
+}
+template <int kType>
+__device__ __forceinline__ void st_one(void* p, int64_t i, float v) {
+  using E = typename std::conditional<kType == MOE_LORA_F32, float, typename std::conditional<kType == MOE_LORA_F16, __half, __nv_bfloat16>::type>::type;
+  static_cast<E*>(p)[i] = from_f32<E>(v);
 }
 
-// The gradient and momentum of a thread's quads of a chunk, on their way.
+// The gradient and momentum of a thread's quads of a chunk, on their way: the next chunk's take a
+// quad's place as soon as it is used.
 struct Loads {
   uint4 g[kQuads], m[kQuads];
 };
-__device__ __forceinline__ void load_chunk(const Place& pl, int c, bool aligned, bool with_g, Loads& ld) {
+template <int kType>
+__device__ __forceinline__ void load_quad(const Place& pl, const Walk& w, int c, int i, int n, bool aligned, bool with_g, Loads& ld) {
   const MuonTensor& t = *pl.t;
-  const int64_t base = pl.first * t.s * t.L;
-#pragma unroll
-  for (int i = 0; i < kQuads; ++i) {
-    const Quad q(t.tall, i);
-    const int l = c * kChunk + q.col;
-    ld.g[i] = ld.m[i] = make_uint4(0, 0, 0, 0);
-    if (aligned) {
-      if (q.row < pl.rows && l < t.L) {
-        const int64_t at = base + offset_of(t, q.row, l);
-        if (with_g) ld.g[i] = ld_quad(t.g, t.g_dtype, at);
-        ld.m[i] = *reinterpret_cast<const uint4*>(t.m + at);
-      }
-    } else {  // widened at once
-      float gv[4] = {}, mv[4] = {};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = q.row + (t.tall ? e : 0), k = l + (t.tall ? 0 : e);
-        if (r < pl.rows && k < t.L) {
-          const int64_t at = base + offset_of(t, r, k);
-          if (with_g) gv[e] = ld_one(t.g, t.g_dtype, at);
-          mv[e] = t.m[at];
-        }
-      }
-      ld.g[i] = make_uint4(__float_as_uint(gv[0]), __float_as_uint(gv[1]), __float_as_uint(gv[2]), __float_as_uint(gv[3]));
-      ld.m[i] = make_uint4(__float_as_uint(mv[0]), __float_as_uint(mv[1]), __float_as_uint(mv[2]), __float_as_uint(mv[3]));
-    }
-  }
-}
-__device__ __forceinline__ void store_m(const Place& pl, int c, bool aligned, int i, const float4& v) {
-  const MuonTensor& t = *pl.t;
-  const int64_t base = pl.first * t.s * t.L;
-  const Quad q(t.tall, i);
-  const int l = c * kChunk + q.col;
+  ld.g[i] = ld.m[i] = make_uint4(0, 0, 0, 0);
   if (aligned) {
-    if (q.row < pl.rows && l < t.L) *reinterpret_cast<float4*>(t.m + base + offset_of(t, q.row, l)) = v;
+    if (i < n) {
+      const int64_t at = w.at + c * w.chunk + i * w.hop;
+      if (with_g) ld.g[i] = ld_quad<kType>(t.g, at);
+      ld.m[i] = ld_quad<MOE_LORA_F32>(t.m, at);
+    }
     return;
   }
-  const float x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t g[4] = {}, m[4] = {};  // element by element, 16-bit ones packed again
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int r = q.row + (t.tall ? e : 0), k = l + (t.tall ? 0 : e);
-    if (r < pl.rows && k < t.L) t.m[base + offset_of(t, r, k)] = x[e];
+    const int64_t at = element_at(t, w, pl.first, c, i, e);
+    if (at < 0) continue;
+    m[e] = __float_as_uint(t.m[at]);
+    if (with_g) g[e] = kType == MOE_LORA_F32 ? static_cast<const uint32_t*>(t.g)[at] : static_cast<const uint16_t*>(t.g)[at];
   }
+  ld.m[i] = make_uint4(m[0], m[1], m[2], m[3]);
+  ld.g[i] = kType == MOE_LORA_F32 ? make_uint4(g[0], g[1], g[2], g[3]) : make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, 0, 0);
 }
-// mu m + nu g, products and sum rounded one by one as the definition's are.
-__device__ __forceinline__ float mix(float mu, float m, float nu, float g) { return __fadd_rn(__fmul_rn(mu, m), __fmul_rn(nu, g)); }
-__device__ __forceinline__ float4 mix4(float mu, const float4& m, float nu, const float4& g) {
-  return make_float4(mix(mu, m.x, nu, g.x), mix(mu, m.y, nu, g.y), mix(mu, m.z, nu, g.z), mix(mu, m.w, nu, g.w));
+template <int kType>
+__device__ __forceinline__ void load_chunk(const Place& pl, const Walk& w, int c, bool aligned, bool with_g, Loads& ld) {
+  const int n = w.inside(c);
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) load_quad<kType>(pl, w, c, i, n, aligned, with_g, ld);
 }
-__device__ __forceinline__ float4 scale4(const float4& v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
+// mu m + nu g
+__device__ __forceinline__ Four mix(float mu, const Four& m, float nu, const Four& g) {
+  return Four{fma2(both(mu), m.a, mul2(both(nu), g.a)), fma2(both(mu), m.b, mul2(both(nu), g.b))};
+}
 
 // ------------------------------------------------------------------ operands in shared memory
-// All tiles have rows of 128 bytes whose 16-byte units are exchanged by row (unit ^ row % 8).
-// A chunk of [s, L]: 128 rows of 64 long places.  Of [L, s]: two halves of 64 short places, a
-// row per long place.
-__device__ __forceinline__ uint32_t quad_at(bool tall, const Quad& q) {
-  const uint32_t r = tall ? q.col : q.row, k = tall ? q.row % 64 : q.col, half = tall ? q.row / 64 * (kPart / 2) : 0;
-  return half + r * 128 + ((((k >> 3) ^ (r & 7)) << 4) | ((k & 4) << 1));
-}
 __device__ __forceinline__ uint32_t hf2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return reinterpret_cast<const uint32_t&>(h);
 }
-// v -> its bf16 parts, each stored as eight bytes
-__device__ __forceinline__ void put_bf16_parts(uint8_t* at, float4 v) {
-#pragma unroll
-  for (int p = 0; p < 3; ++p) {
-    const uint2 u = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    *reinterpret_cast<uint2*>(at + p * kPart) = u;
-    if (p < 2) v = make_float4(v.x - bf16_lo(u.x), v.y - bf16_hi(u.x), v.z - bf16_lo(u.y), v.w - bf16_hi(u.y));
-  }
+// Two values to a bf16 pair; `v` keeps what the rounding left.
+__device__ __forceinline__ uint32_t take_bf16(float2& v) {
+  const uint32_t h = pack_bf16x2(v.x, v.y);
+  v = fma2(make_float2(bf16_lo(h), bf16_hi(h)), both(-1.f), v);
+  return h;
 }
-// Two values to their fp16 parts.
-__device__ __forceinline__ void fp16_parts(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = hf2(a, b);
-  const float2 h = __half22float2(reinterpret_cast<const __half2&>(hi));
-  lo = hf2(a - h.x, b - h.y);
+// ... to their two fp16 parts.
+__device__ __forceinline__ void fp16_parts(float2 v, uint32_t& hi, uint32_t& lo) {
+  hi = hf2(v.x, v.y);
+  v = fma2(__half22float2(reinterpret_cast<const __half2&>(hi)), both(-1.f), v);
+  lo = hf2(v.x, v.y);
 }
 
 // Instruction descriptor of kind::f16 with fp32 accumulation: fp16 operands (type code 0)
@@ -263,6 +273,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bo
   return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
+__device__ __forceinline__ void bulk_store(void* dst, const void* src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src_smem)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) { return p + ((1024 - (smem_u32(p) & 1023)) & 1023); }
 // Tensor memory of a block, opened and closed by all its threads.
 __device__ __forceinline__ uint32_t tmem_open(uint32_t* slot, int columns) {
   if (threadIdx.x < 32) {
@@ -280,116 +295,156 @@ __device__ __forceinline__ void tmem_close(uint32_t base, int columns) {
   tc_fence_after();
   if (threadIdx.x < 32) tmem_dealloc(base, columns);
 }
-// All threads wait for the products committed to `bar`; false where they did not end in time.
-__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, int* err) {
-  const int ok = threadIdx.x == 0 ? mbar_wait(bar, parity, err) : 1;
-  const bool all = __syncthreads_and(ok);
-  tc_fence_after();
-  return all;
-}
-// This thread's 32 columns from `col` on of its row: warps w and w + 4 have rows 32 (w % 4) + lane.
+// Every thread's wait for products; one that did not end in time is noted, and the thread's later
+// waits are left out, so that the block ends with its barriers in step.
+struct Waits {
+  int* err;
+  bool late = false;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!late) late = !mbar_wait(bar, parity, err);
+    tc_fence_after();
+  }
+};
+// This thread's 32 columns from `col` on of its row: warp w has rows 32 (w % 4) + lane.
 __device__ __forceinline__ void tmem_row32(uint32_t base, int col, float (&v)[32]) {
   const uint32_t lanes = ((threadIdx.x >> 5) & 3) * 32;
   tmem_ld32(base + (lanes << 16) + col, v);
 }
 __device__ __forceinline__ int my_row() { return ((threadIdx.x >> 5) & 3) * 32 + (threadIdx.x & 31); }
-__device__ __forceinline__ int my_half() { return threadIdx.x >> 7; }
+__device__ __forceinline__ int my_part() { return threadIdx.x >> 7; }  // of the columns
+
+// Each launch starts while the one before it runs out, and waits for it before it touches what
+// that one, or any before, has written.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// f(integral constant of the tensor's type)
+template <class F>
+__device__ __forceinline__ void with_type(int dtype, F f) {
+  if (dtype == MOE_LORA_F32)
+    f(std::integral_constant<int, MOE_LORA_F32>{});
+  else if (dtype == MOE_LORA_BF16)
+    f(std::integral_constant<int, MOE_LORA_BF16>{});
+  else
+    f(std::integral_constant<int, MOE_LORA_F16>{});
+}
 
 // ------------------------------------------------------------------ gram
 constexpr int kGramStages = 2, kGramSmem = kGramStages * 3 * kPart + 1024;
 constexpr int kGramCols = 256;
-
-__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
-  return p + ((1024 - (smem_u32(p) & 1023)) & 1023);
-}
 
 __global__ void __launch_bounds__(kThreads, 2) muon_gram_kernel(const __grid_constant__ MuonTable tab) {
   extern __shared__ uint8_t muon_smem[];
   __shared__ uint64_t done[kGramStages];
   __shared__ uint32_t slot;
   uint8_t* sm = aligned_smem(muon_smem);
-  const Place pl = place_of(tab, blockIdx.x);
-  const MuonTensor& t = *pl.t;
-  const bool aligned = quads_aligned(t), tall = t.tall;
-  Loads ld;
-  load_chunk(pl, pl.c0, aligned, true, ld);
+  launch_next();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kGramStages; ++i) mbar_init(&done[i], 1);
     fence_mbar_init();
   }
   const uint32_t acc = tmem_open(&slot, kGramCols);
-  const float gs = tab.gs ? *tab.gs : 1.f;
-  bool ok = true;
-  for (int c = pl.c0; c < pl.c1; ++c) {
-    const int k = c - pl.c0, st = k % kGramStages;
-    uint8_t* part = sm + st * 3 * kPart;
-    if (k >= kGramStages && !(ok = all_wait(&done[st], (k / kGramStages - 1) & 1, tab.err))) break;
+  Waits wait{tab.err};
+  int used = 0;  // chunks so far
+  const float nu = tab.nu * (tab.gs ? *tab.gs : 1.f);
+  const int end = first_chunk(tab, blockIdx.x + 1);
+  for (int x = first_chunk(tab, blockIdx.x); x < end;) {
+    const Place pl = place_of(tab, x, end);
+    const MuonTensor& t = *pl.t;
+    const bool aligned = quads_aligned(t), tall = t.tall;
+    const Walk w(t, pl.first, pl.rows);
+    with_type(t.g_dtype, [&](auto type) {
+      constexpr int kType = decltype(type)::value;
+      Loads ld;
+      load_chunk<kType>(pl, w, pl.c0, aligned, true, ld);
+      for (int c = pl.c0; c < pl.c1; ++c, ++used) {
+        const int st = used % kGramStages;
+        uint8_t* part = sm + st * 3 * kPart;
+        if (used >= kGramStages) wait(&done[st], (used / kGramStages - 1) & 1);
+        const int n = w.inside(c), next = c + 1 < pl.c1 ? w.inside(c + 1) : 0;
+        const int64_t at = w.at + c * w.chunk;
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i) {
-      const Quad q(tall, i);
-      const float4 g = scale4(widen(ld.g[i], aligned ? t.g_dtype : MOE_LORA_F32), gs);
-      const float4 m = mix4(tab.mu, widen(ld.m[i], MOE_LORA_F32), tab.nu, g);
-      store_m(pl, c, aligned, i, m);
-      put_bf16_parts(part + quad_at(tall, q), tab.nesterov ? mix4(tab.mu, m, tab.nu, g) : m);
-    }
-    if (c + 1 < pl.c1) load_chunk(pl, c + 1, aligned, true, ld);
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-      const uint32_t h = smem_u32(part), m = h + kPart, l = m + kPart;
-      const uint32_t id = idesc_bf16_f32(kTile, kTile, tall, tall);
+        for (int i = 0; i < kQuads; ++i) {
+          const Four g = widen<kType>(ld.g[i]);
+          const Four m = mix(tab.mu, widen<MOE_LORA_F32>(ld.m[i]), nu, g);
+          if (c + 1 < pl.c1) load_quad<kType>(pl, w, c + 1, i, next, aligned, true, ld);
+          if (aligned) {
+            if (i < n) st_quad<MOE_LORA_F32>(t.m, at + i * w.hop, m);
+          } else {
+            const float y[4] = {m.a.x, m.a.y, m.b.x, m.b.y};
 #pragma unroll
-      for (int kk = 0; kk < kChunk / 16; ++kk) {
-        const uint32_t at = tall ? kk * 2048 : kk * 32, lbo = tall ? kPart / 2 : 16;
-        const uint64_t dh = sw128_desc(h + at, lbo, 1024), dm = sw128_desc(m + at, lbo, 1024), dl = sw128_desc(l + at, lbo, 1024);
-        const uint32_t more = k > 0 || kk > 0;
-        mma_bf16(acc, dh, dh, id, more);
-        mma_bf16(acc, dm, dm, id, 1);
-        mma_bf16(acc + kTile, dh, dm, id, more);
-        mma_bf16(acc + kTile, dh, dl, id, 1);
+            for (int e = 0; e < 4; ++e) {
+              const int64_t to = element_at(t, w, pl.first, c, i, e);
+              if (to >= 0) t.m[to] = y[e];
+            }
+          }
+          Four u = tab.nesterov ? mix(tab.mu, m, nu, g) : m;
+          uint8_t* to = part + w.smem + i * w.hop_smem;
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const uint32_t a = take_bf16(u.a), b = take_bf16(u.b);
+            *reinterpret_cast<uint2*>(to + q * kPart) = make_uint2(a, b);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          tc_fence_after();
+          const uint32_t h = smem_u32(part), m = h + kPart, l = m + kPart;
+          const uint32_t id = idesc_bf16_f32(kTile, kTile, tall, tall);
+          const uint32_t step = tall ? 2048 : 32, lbo = tall ? kPart / 2 : 16;
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk) {
+            const uint64_t dh = sw128_desc(h + kk * step, lbo, 1024), dm = sw128_desc(m + kk * step, lbo, 1024),
+                           dl = sw128_desc(l + kk * step, lbo, 1024);
+            const uint32_t more = c > pl.c0 || kk > 0;
+            mma_bf16(acc, dh, dh, id, more);
+            mma_bf16(acc, dm, dm, id, 1);
+            mma_bf16(acc + kTile, dh, dm, id, more);
+            mma_bf16(acc + kTile, dh, dl, id, 1);
+          }
+          mma_commit(&done[st]);
+        }
       }
-      mma_commit(&done[st]);
+    });
+    wait(&done[(used - 1) % kGramStages], ((used - 1) / kGramStages) & 1);
+    // (hh + mm) / 2 + h(m + l): this and its transpose are added where it is read, so that its rows may
+    // be stored as columns, a warp's side by side
+    float* out = tab.gram + stretch_slot(tab, pl.tile, x) * kTile * kTile + my_row();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int col = my_part() * 64 + b * 32;
+      float v[32], y[32];
+      tmem_row32(acc, col, v);
+      tmem_row32(acc + kTile, col, y);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) out[(col + i) * kTile] = 0.5f * v[i] + y[i];
     }
-  }
-  const int last = pl.c1 - pl.c0 - 1;
-  if (ok) ok = all_wait(&done[last % kGramStages], (last / kGramStages) & 1, tab.err);
-  // (hh + mm) / 2 + h(m + l): this and its transpose are added where it is read
-  float* out = tab.gram + (int64_t)blockIdx.x * kTile * kTile + my_row() * kTile;
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int col = my_half() * 64 + b * 32;
-    float v[32], w[32];
-    tmem_row32(acc, col, v);
-    tmem_row32(acc + kTile, col, w);
-#pragma unroll
-    for (int i = 0; i < 32; i += 4)
-      *reinterpret_cast<float4*>(out + col + i) = make_float4(0.5f * v[i] + w[i], 0.5f * v[i + 1] + w[i + 1], 0.5f * v[i + 2] + w[i + 2], 0.5f * v[i + 3] + w[i + 3]);
+    x += pl.c1 - pl.c0;
   }
   tmem_close(acc, kGramCols);
 }
 
 // ------------------------------------------------------------------ poly
-// A block per tile.  A thread has half a row of each square matrix; they pass through
-// shared memory as operands (fp16 parts of scaled values, zero outside the matrices' own
-// blocks).
-constexpr int kPolySmem = 3 * kPoly + 1024, kPolyCols = 256;
+// A block per tile, a thread per row and quarter of the columns.  The square matrices pass
+// through shared memory as operands (fp16 parts of scaled values, zero outside the matrices'
+// own blocks); G stays in tensor memory beside the products.  A product is a chain of
+// latencies (operands written, 24 instructions on the tensor cores, 32 columns read back), of
+// which five or eight follow each other.
+constexpr int kPolyThreads = 512, kPolySmem = 3 * kPoly + 1024, kPolyCols = 512;
 
-struct Block {  // columns [lo, hi) of this thread's row that belong to its matrix
-  int lo, hi;
-  __device__ __forceinline__ bool has(int col) const { return col >= lo && col < hi; }
-};
-// Writes this thread's half row, times `scale`, as fp16 parts of a square tile: two halves of 64
-// columns, then the lower parts.
-__device__ __forceinline__ void put_half_row(uint8_t* tile, const float (&v)[64], float scale) {
-  const int r = my_row();
-  uint8_t* at = tile + my_half() * kPart + r * 128;
+// Writes this thread's 32 columns as fp16 parts of a square tile: two halves of 64 columns, then the
+// lower parts.
+__device__ __forceinline__ void put_row32(uint8_t* tile, const float (&v)[32]) {
+  const int r = my_row(), q = my_part();
+  uint8_t* at = tile + (q >> 1) * kPart + r * 128;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
+  for (int u = 0; u < 4; ++u) {
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fp16_parts(v[8 * u + 2 * i] * scale, v[8 * u + 2 * i + 1] * scale, hi[i], lo[i]);
-    const int sw = (u ^ (r & 7)) << 4;
+    for (int i = 0; i < 4; ++i) fp16_parts(make_float2(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]), hi[i], lo[i]);
+    const int sw = (((q & 1) * 4 + u) ^ (r & 7)) << 4;
     *reinterpret_cast<uint4*>(at + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + kTileBytes + sw) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
@@ -397,7 +452,7 @@ __device__ __forceinline__ void put_half_row(uint8_t* tile, const float (&v)[64]
 // D = A B^T of square tiles (both fp16 parts; the product of the lower parts is below fp32's rounding).
 __device__ __forceinline__ void square_product(uint32_t d, uint32_t a, uint32_t b) {
   const uint32_t id = idesc_f16_f32(kTile, kTile, false, false);
-#pragma unroll
+#pragma unroll 1
   for (int p = 0; p < 3; ++p) {
     const uint32_t pa = a + (p == 2 ? kTileBytes : 0), pb = b + (p == 1 ? kTileBytes : 0);
 #pragma unroll
@@ -407,85 +462,113 @@ __device__ __forceinline__ void square_product(uint32_t d, uint32_t a, uint32_t 
     }
   }
 }
-// This thread's half row of a product, times f, zero outside its block.
-__device__ __forceinline__ void get_half_row(uint32_t d, const Block& blk, float f, float (&v)[64]) {
+__device__ __forceinline__ void tmem_put_row32(uint32_t base, int col, const float (&v)[32]) {
+  const uint32_t at = base + ((((threadIdx.x >> 5) & 3) * 32) << 16) + col;
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    float w[32];
-    tmem_row32(d, my_half() * 64 + b * 32, w);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[b * 32 + i] = blk.has(my_half() * 64 + b * 32 + i) ? w[i] * f : 0.f;
-  }
+  for (int i = 0; i < 32; i += 4)
+    tmem_st4(at + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+  tmem_wait_st();
 }
 
 // `first`: G is of the update itself, whose norm is taken here.  Otherwise G is of X in the
 // scratch, times kXScale^2.
-__global__ void __launch_bounds__(kThreads, 1) muon_poly_kernel(const __grid_constant__ MuonTable tab, int steps, bool first) {
+__global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid_constant__ MuonTable tab, int steps, bool first) {
   extern __shared__ uint8_t muon_smem[];
   __shared__ uint64_t done;
   __shared__ uint32_t slot;
   __shared__ float diag[kTile];
   uint8_t* sm = aligned_smem(muon_smem);
   uint8_t *qt = sm, *gt = sm + kPoly, *pt = sm + 2 * kPoly;
-  const int64_t tile = blockIdx.x;
+  const int tile = blockIdx.x;
   int ti = 0;
   while (ti + 1 < tab.n && tile >= tab.t[ti + 1].tile0) ++ti;
   const MuonTensor& t = tab.t[ti];
-  const int rows = (int)min((int64_t)t.per, t.batch - (tile - t.tile0) * t.per) * t.s;
-  const int row = my_row(), half = my_half();
-  const Block blk{row < rows ? row / t.s * t.s : 0, row < rows ? row / t.s * t.s + t.s : 0};
+  const int rows = (int)min((int64_t)t.per, t.batch - (int64_t)(tile - t.tile0) * t.per) * t.s;
+  const int row = my_row(), col = my_part() * 32;
+  // the columns [lo, hi) of this thread's 32 that belong to its row's matrix
+  const int block = row < rows ? row / t.s * t.s : kTile;
+  const int lo = block - col, hi = min(block + t.s, rows) - col;
+  const bool whole = t.s == kTile;
+  const auto scaled = [&](float (&v)[32], float f) {  // times f, and 0 outside the matrix
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 x = mul2(make_float2(v[i], v[i + 1]), both(f));
+      v[i] = x.x;
+      v[i + 1] = x.y;
+    }
+    if (!whole)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = i >= lo && i < hi ? v[i] : 0.f;
+  };
   if (threadIdx.x == 0) {
     mbar_init(&done, 1);
     fence_mbar_init();
   }
-  const uint32_t acc = tmem_open(&slot, kPolyCols);
-  // G: the pieces' partial sums in order, each with its transpose
-  float g[64];
+  launch_next();
+  const uint32_t tmem = tmem_open(&slot, kPolyCols);
+  const uint32_t g_at = tmem, x_at = tmem + kTile, p_at = tmem + 2 * kTile;  // G, another product, P
+  Waits wait{tab.err};
+  wait_for_last();
+  // G: the stretches' sums in order, then with the transpose, through shared memory
+  float v[32];
+  {
+    constexpr int kEach = kTile * kTile / 4 / kPolyThreads;
+    const int x = t.chunk0 + (tile - t.tile0) * t.chunks;
+    const int64_t s0 = stretch_slot(tab, tile, x);
+    const int stretches = (int)(stretch_slot(tab, tile, x + t.chunks - 1) - s0) + 1;
+    const float4* in = reinterpret_cast<const float4*>(tab.gram + s0 * kTile * kTile) + threadIdx.x;
+    float4 sum[kEach];
 #pragma unroll
-  for (int i = 0; i < 64; ++i) g[i] = 0.f;
-  const float* in = tab.gram + (t.piece0 + (tile - t.tile0) * t.pieces) * kTile * kTile;
-  for (int p = 0; p < t.pieces; ++p, in += kTile * kTile) {
-    const float* r = in + row * kTile + half * 64;
-    const float* c = in + (int64_t)half * 64 * kTile + row;
+    for (int i = 0; i < kEach; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int p = 0; p < stretches; ++p)
 #pragma unroll
-    for (int i = 0; i < 64; i += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(r + i);
-      g[i] += u.x + c[i * kTile];
-      g[i + 1] += u.y + c[(i + 1) * kTile];
-      g[i + 2] += u.z + c[(i + 2) * kTile];
-      g[i + 3] += u.w + c[(i + 3) * kTile];
+      for (int i = 0; i < kEach; ++i) {
+        const float4 u = in[p * (kTile * kTile / 4) + i * kPolyThreads];
+        sum[i] = make_float4(sum[i].x + u.x, sum[i].y + u.y, sum[i].z + u.z, sum[i].w + u.w);
+      }
+    float* e = reinterpret_cast<float*>(qt);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int at = (threadIdx.x + i * kPolyThreads) * 4;
+      float* to = e + at / kTile * (kTile + 1) + at % kTile;
+      to[0] = sum[i].x;
+      to[1] = sum[i].y;
+      to[2] = sum[i].z;
+      to[3] = sum[i].w;
     }
-  }
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 64; ++i)
-    if (!blk.has(half * 64 + i)) g[i] = 0.f;
+    for (int i = 0; i < 32; ++i) v[i] = e[row * (kTile + 1) + col + i] + e[(col + i) * (kTile + 1) + row];
+    __syncthreads();
+  }
   float unit = 1.f / (kXScale * kXScale);  // X in the scratch is scaled
+  bool fine = true;
   if (first) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-      if (half * 64 + i == row) diag[row] = g[i];
+    for (int i = 0; i < 32; ++i)
+      if (col + i == row) diag[row] = v[i];
     __syncthreads();
     float n2 = 0.f;
-    for (int i = blk.lo; i < blk.hi; ++i) n2 += diag[i];
+    for (int i = max(lo, -col); i < hi; ++i) n2 += diag[col + i];
     // a norm whose square fp32 does not hold: 0, or not finite, which is passed on as NaN
-    const bool fine = n2 < INFINITY;
+    fine = n2 < INFINITY;
     const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
     // X = u / (norm + eps) = (u * up) * down, up a power of two that makes the matrix's norm 2^9 to 2^10
-    float up = 0.f;
-    if (norm > 0.f) up = ldexpf(1.f, 10 - (ilogbf(norm) + 1));
+    const float up = norm > 0.f ? ldexpf(1.f, 9 - ilogbf(norm)) : 0.f;
     unit = norm > 0.f ? inv * inv : 0.f;
-    if (half == 0) {
-      tab.norm[tile * 2 * kTile + row] = up;
-      tab.norm[tile * 2 * kTile + kTile + row] = !fine ? NAN : norm > 0.f ? inv / up : 0.f;
+    if (my_part() == 0) {
+      tab.norm[(int64_t)tile * 2 * kTile + row] = up;
+      tab.norm[(int64_t)tile * 2 * kTile + kTile + row] = !fine ? NAN : norm > 0.f ? inv / up : 0.f;
     }
-    if (!fine)
-#pragma unroll
-      for (int i = 0; i < 64; ++i) g[i] = 0.f;
   }
+  if (!fine)
 #pragma unroll
-  for (int i = 0; i < 64; ++i) g[i] *= unit;
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+  // all matrices are held times their scales from here on
+  scaled(v, unit * kGScale);
+  tmem_put_row32(g_at, col, v);
   uint32_t phase = 0;
-  bool ok = true;
   // Runs products issued by one thread; operands are in shared memory.
   const auto products = [&](auto issue) {
     fence_proxy_async_smem();
@@ -496,45 +579,64 @@ __global__ void __launch_bounds__(kThreads, 1) muon_poly_kernel(const __grid_con
       issue();
       mma_commit(&done);
     }
-    ok = all_wait(&done, phase, tab.err) && ok;
+    wait(&done, phase);
     phase ^= 1;
   };
   const uint32_t qa = smem_u32(qt), ga = smem_u32(gt), pa = smem_u32(pt);
-  float v[64];
+  put_row32(gt, v);
+  if (steps == 0) {
 #pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = blk.has(half * 64 + i) && half * 64 + i == row ? 1.f : 0.f;
-  if (steps == 0) put_half_row(pt, v, kQScale);
-  for (int k = 0; k < steps && ok; ++k) {
-    put_half_row(gt, g, kGScale);
-    products([&] { square_product(acc, ga, ga); });
-    get_half_row(acc, blk, tab.c / (kGScale * kGScale), v);
+    for (int i = 0; i < 32; ++i) v[i] = col + i == row ? kQScale : 0.f;
+    scaled(v, 1.f);
+    put_row32(pt, v);
+  }
+  const float ka = tab.a * kQScale, kb = tab.b * (kQScale / kGScale), kc = tab.c * (kQScale / (kGScale * kGScale));
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    products([&] { square_product(x_at, ga, ga); });
+    {
+      float g[32];
+      tmem_row32(g_at, col, g);
+      tmem_row32(x_at, col, v);
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      v[i] += tab.b * g[i];
-      if (half * 64 + i == row && blk.has(row)) v[i] += tab.a;
+      for (int i = 0; i < 32; i += 2) {
+        const float2 x = fma2(both(kc), make_float2(v[i], v[i + 1]), mul2(both(kb), make_float2(g[i], g[i + 1])));
+        v[i] = x.x + (col + i == row ? ka : 0.f);
+        v[i + 1] = x.y + (col + i + 1 == row ? ka : 0.f);
+      }
+      if (!whole) scaled(v, 1.f);
     }
-    put_half_row(qt, v, kQScale);
-    if (k == 0) put_half_row(pt, v, kQScale);
+    put_row32(qt, v);
+    if (k == 0) put_row32(pt, v);
     const bool last = k == steps - 1;
     if (last && k == 0) break;
     products([&] {
-      if (!last) square_product(acc, qa, ga);
-      if (k > 0) square_product(acc + kTile, qa, pa);
+      if (!last) square_product(x_at, qa, ga);
+      if (k > 0) square_product(p_at, qa, pa);
     });
     if (k > 0) {
-      get_half_row(acc + kTile, blk, 1.f / (kQScale * kQScale), v);
-      put_half_row(pt, v, kQScale);
+      tmem_row32(p_at, col, v);
+      scaled(v, 1.f / kQScale);
+      put_row32(pt, v);
     }
     if (last) break;
-    get_half_row(acc, blk, 1.f / (kQScale * kGScale), v);
-    put_half_row(gt, v, kGScale);
-    products([&] { square_product(acc, qa, ga); });
-    get_half_row(acc, blk, 1.f / (kQScale * kGScale), g);
+    tmem_row32(x_at, col, v);
+    scaled(v, 1.f / kQScale);
+    put_row32(gt, v);
+    products([&] { square_product(x_at, qa, ga); });
+    tmem_row32(x_at, col, v);
+    scaled(v, 1.f / kQScale);
+    tmem_put_row32(g_at, col, v);
+    put_row32(gt, v);
   }
+  fence_proxy_async_smem();
   __syncthreads();
-  uint4* out = reinterpret_cast<uint4*>(tab.poly + tile * kPoly);
-  for (int i = threadIdx.x; i < kPoly / 16; i += kThreads) out[i] = reinterpret_cast<const uint4*>(pt)[i];
-  tmem_close(acc, kPolyCols);
+  if (threadIdx.x == 0) {
+    bulk_store(tab.poly + (int64_t)tile * kPoly, pt, kPoly);
+    bulk_commit_group();
+    bulk_wait_group<0>();
+  }
+  tmem_close(tmem, kPolyCols);
 }
 
 // ------------------------------------------------------------------ apply and update
@@ -542,19 +644,21 @@ __global__ void __launch_bounds__(kThreads, 1) muon_poly_kernel(const __grid_con
 // each), or two halves of 64 short places (a row per long place).
 __device__ __forceinline__ void poly_product(uint32_t d, uint32_t p, uint32_t x, bool tall) {
   const uint32_t id = idesc_f16_f32(kTile, kChunk, false, !tall);
-#pragma unroll
+  const uint32_t lbo = tall ? 16 : 8192;
+#pragma unroll 1
   for (int q = 0; q < 3; ++q) {
     const uint32_t a = p + (q == 2 ? kTileBytes : 0), b = x + (q == 1 ? kPart : 0);
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk) {
-      const uint64_t ad = sw128_desc(a + kk / 4 * kPart + kk % 4 * 32, 16, 1024);
-      const uint64_t bd = tall ? sw128_desc(b + kk / 4 * (kPart / 2) + kk % 4 * 32, 16, 1024) : sw128_desc(b + kk * 2048, 8192, 1024);
-      mma_bf16(d, ad, bd, id, q > 0 || kk > 0);
+      const uint32_t at = tall ? kk / 4 * (kPart / 2) + kk % 4 * 32 : kk * 2048;
+      mma_bf16(d, sw128_desc(a + kk / 4 * kPart + kk % 4 * 32, 16, 1024), sw128_desc(b + at, lbo, 1024), id, q > 0 || kk > 0);
     }
   }
 }
-__device__ __forceinline__ void copy_async(uint8_t* dst, const uint8_t* src, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) async_copy16(dst + i, src + i);
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint8_t* dst, const uint8_t* src) {
+#pragma unroll
+  for (int i = 0; i < kBytes / 16 / kThreads; ++i) async_copy16(dst + (threadIdx.x + i * kThreads) * 16, src + (threadIdx.x + i * kThreads) * 16);
   async_commit();
 }
 
@@ -568,196 +672,235 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
   __shared__ float row_up[kTile];
   uint8_t* sm = aligned_smem(muon_smem);
   uint8_t *pt = sm, *xt = sm + kPoly;
-  const int64_t piece = tab.pieces - 1 - blockIdx.x;  // what the launch before it wrote last may still be in L2
-  const Place pl = place_of(tab, piece);
-  const MuonTensor& t = *pl.t;
-  const bool aligned = quads_aligned(t), tall = t.tall, with_g = tab.nesterov;
-  copy_async(pt, tab.poly + pl.tile * kPoly, kPoly);
-  Loads ld;
-  load_chunk(pl, pl.c0, aligned, with_g, ld);
   if (threadIdx.x == 0) {
     mbar_init(&done[0], 1);
     mbar_init(&done[1], 1);
     fence_mbar_init();
   }
-  const float* norm = tab.norm + pl.tile * 2 * kTile;
-  if (threadIdx.x < kTile) row_up[threadIdx.x] = norm[threadIdx.x];
-  // P's scale, and the factor that makes the products X
-  const float down = norm[kTile + my_row()] == norm[kTile + my_row()] ? norm[kTile + my_row()] * (kXScale / kQScale) : 0.f;
-  const uint32_t acc = tmem_open(&slot, kApplyCols);
-  const uint32_t gram = acc + 64;
-  const float gs = tab.gs ? *tab.gs : 1.f;
-  async_wait<0>();
-  bool ok = true;
-  for (int c = pl.c0; c < pl.c1; ++c) {
-    const int k = c - pl.c0;
-    if (k > 0 && !(ok = all_wait(&done[1], (k - 1) & 1, tab.err))) break;
+  launch_next();
+  const uint32_t acc = tmem_open(&slot, kApplyCols), gram = acc + 64;
+  wait_for_last();
+  Waits wait{tab.err};
+  int used = 0;  // chunks so far
+  const int r = my_row();
+  const bool with_g = tab.nesterov;
+  const float nu = tab.nu * (tab.gs ? *tab.gs : 1.f);
+  const int end = first_chunk(tab, blockIdx.x + 1);
+  for (int x = first_chunk(tab, blockIdx.x); x < end;) {
+    const Place pl = place_of(tab, x, end);
+    const MuonTensor& t = *pl.t;
+    const bool aligned = quads_aligned(t), tall = t.tall;
+    const Walk w(t, pl.first, pl.rows);
+    copy_async<kPoly>(pt, tab.poly + (int64_t)pl.tile * kPoly);  // no product is under way here
+    const float* norm = tab.norm + (int64_t)pl.tile * 2 * kTile;
+    __syncthreads();  // the last stretch's scales have been read
+    if (threadIdx.x < kTile) row_up[threadIdx.x] = norm[threadIdx.x];
+    // P's scale, and the factor that makes the products X
+    const float factor = norm[kTile + r], down = factor == factor ? factor * (kXScale / kQScale) : 0.f;
+    with_type(t.g_dtype, [&](auto type) {
+      constexpr int kType = decltype(type)::value;
+      Loads ld;
+      load_chunk<kType>(pl, w, pl.c0, aligned, with_g, ld);
+      async_wait<0>();
+      __syncthreads();
+      for (int c = pl.c0; c < pl.c1; ++c, ++used) {
+        if (used > 0) {  // the products and the copy that read the tile
+          wait(&done[1], (used - 1) & 1);
+          if (threadIdx.x == 0) bulk_wait_group_read<0>();
+          __syncthreads();
+        }
+        const int next = c + 1 < pl.c1 ? w.inside(c + 1) : 0;
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i) {
-      const Quad q(tall, i);
-      float4 u = widen(ld.m[i], MOE_LORA_F32);
-      if (with_g) u = mix4(tab.mu, u, tab.nu, scale4(widen(ld.g[i], aligned ? t.g_dtype : MOE_LORA_F32), gs));
-      float f[4];
+        for (int i = 0; i < kQuads; ++i) {
+          Four u = widen<MOE_LORA_F32>(ld.m[i]);
+          if (with_g) u = mix(tab.mu, u, nu, widen<kType>(ld.g[i]));
+          if (c + 1 < pl.c1) load_quad<kType>(pl, w, c + 1, i, next, aligned, with_g, ld);
+          const float* f = row_up + w.row + i * w.hop_row;
+          const float2 fa = tall ? make_float2(f[0], f[1]) : both(f[0]), fb = tall ? make_float2(f[2], f[3]) : both(f[0]);
+          u = Four{mul2(u.a, fa), mul2(u.b, fb)};
+          // matrices without a norm (0, or not finite) take no part
+          u.a = make_float2(fa.x > 0.f ? u.a.x : 0.f, fa.y > 0.f ? u.a.y : 0.f);
+          u.b = make_float2(fb.x > 0.f ? u.b.x : 0.f, fb.y > 0.f ? u.b.y : 0.f);
+          uint2 hi, lo;
+          fp16_parts(u.a, hi.x, lo.x);
+          fp16_parts(u.b, hi.y, lo.y);
+          uint8_t* to = xt + w.smem + i * w.hop_smem;
+          *reinterpret_cast<uint2*>(to) = hi;
+          *reinterpret_cast<uint2*>(to + kPart) = lo;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          tc_fence_after();
+          poly_product(acc, smem_u32(pt), smem_u32(xt), tall);
+          mma_commit(&done[0]);
+        }
+        wait(&done[0], used & 1);
+        // rows of 64 long places from here on: half a row each
+        {
+          float v[32];
+          tmem_row32(acc, my_part() * 32, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = row_up[q.row + (tall ? e : 0)];
-      // matrices without a norm (0, or not finite) take no part
-      u = make_float4(f[0] > 0.f ? u.x * f[0] : 0.f, f[1] > 0.f ? u.y * f[1] : 0.f, f[2] > 0.f ? u.z * f[2] : 0.f, f[3] > 0.f ? u.w * f[3] : 0.f);
-      uint2 hi, lo;
-      fp16_parts(u.x, u.y, hi.x, lo.x);
-      fp16_parts(u.z, u.w, hi.y, lo.y);
-      uint8_t* at = xt + quad_at(tall, q);
-      *reinterpret_cast<uint2*>(at) = hi;
-      *reinterpret_cast<uint2*>(at + kPart) = lo;
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-      poly_product(acc, smem_u32(pt), smem_u32(xt), tall);
-      mma_commit(&done[0]);
-    }
-    if (c + 1 < pl.c1) load_chunk(pl, c + 1, aligned, with_g, ld);
-    if (!(ok = all_wait(&done[0], k & 1, tab.err))) break;
-    // rows of 64 long places from here on: half a row each, to shared memory and to the scratch
-    {
+          for (int u = 0; u < 4; ++u) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fp16_parts(mul2(make_float2(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]), both(down)), hi[i], lo[i]);
+            const int at = r * 128 + (((my_part() * 4 + u) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(xt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(xt + kPart + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          tc_fence_after();
+          const uint32_t h = smem_u32(xt), l = h + kPart, id = idesc_f16_f32(kTile, kTile, false, false);
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk) {
+            const uint64_t dh = sw128_desc(h + kk * 32, 16, 1024), dl = sw128_desc(l + kk * 32, 16, 1024);
+            mma_bf16(gram, dh, dh, id, c > pl.c0 || kk > 0);
+            mma_bf16(gram, dh, dl, id, 1);
+            mma_bf16(gram, dl, dh, id, 1);
+          }
+          mma_commit(&done[1]);
+          // the tile as it lies, 32 KB in one copy (16-byte stores by the threads that formed it: 789 us
+          // instead of 5xx for 203 M elements)
+          bulk_store(tab.x + (x + c - pl.c0) * (int64_t)kImage, xt, kImage);
+          bulk_commit_group();
+        }
+      }
+    });
+    wait(&done[1], (used - 1) & 1);
+    float* out = tab.gram + stretch_slot(tab, pl.tile, x) * kTile * kTile + r;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int col = my_part() * 64 + b * 32;
       float v[32];
-      tmem_row32(acc, my_half() * 32, v);
-      const int r = my_row();
-      uint8_t* img = tab.x + (pl.image + k) * (int64_t)kImage;
+      tmem_row32(gram, col, v);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint4 hi, lo;
-        fp16_parts(v[8 * u] * down, v[8 * u + 1] * down, hi.x, lo.x);
-        fp16_parts(v[8 * u + 2] * down, v[8 * u + 3] * down, hi.y, lo.y);
-        fp16_parts(v[8 * u + 4] * down, v[8 * u + 5] * down, hi.z, lo.z);
-        fp16_parts(v[8 * u + 6] * down, v[8 * u + 7] * down, hi.w, lo.w);
-        const int at = r * 128 + (((my_half() * 4 + u) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(xt + at) = hi;
-        *reinterpret_cast<uint4*>(xt + kPart + at) = lo;
-        *reinterpret_cast<uint4*>(img + at) = hi;
-        *reinterpret_cast<uint4*>(img + kPart + at) = lo;
-      }
+      for (int i = 0; i < 32; ++i) out[(col + i) * kTile] = 0.5f * v[i];
     }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-      const uint32_t h = smem_u32(xt), l = h + kPart, id = idesc_f16_f32(kTile, kTile, false, false);
-#pragma unroll
-      for (int kk = 0; kk < kChunk / 16; ++kk) {
-        const uint64_t dh = sw128_desc(h + kk * 32, 16, 1024), dl = sw128_desc(l + kk * 32, 16, 1024);
-        mma_bf16(gram, dh, dh, id, k > 0 || kk > 0);
-        mma_bf16(gram, dh, dl, id, 1);
-        mma_bf16(gram, dl, dh, id, 1);
-      }
-      mma_commit(&done[1]);
-    }
+    x += pl.c1 - pl.c0;
   }
-  const int last = pl.c1 - pl.c0 - 1;
-  if (ok) all_wait(&done[1], last & 1, tab.err);
-  float* out = tab.gram + piece * kTile * kTile + my_row() * kTile;
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int col = my_half() * 64 + b * 32;
-    float v[32];
-    tmem_row32(gram, col, v);
-#pragma unroll
-    for (int i = 0; i < 32; i += 4)
-      *reinterpret_cast<float4*>(out + col + i) = make_float4(0.5f * v[i], 0.5f * v[i + 1], 0.5f * v[i + 2], 0.5f * v[i + 3]);
-  }
+  if (threadIdx.x == 0) bulk_wait_group<0>();
   tmem_close(acc, kApplyCols);
 }
 
-constexpr int kUpdateSmem = kPoly + kImage + 1024, kUpdateCols = 64;
-constexpr int kPitch = 65;  // of the products in shared memory, fp32: rows and columns of a warp on different banks
+// The products change threads through shared memory, where X was, so that quads can be read:
+// rows of the short side, or of long places where the weights are tall.
+constexpr int kPitch = 68, kTallPitch = 132;
+constexpr int kOutBytes = kTile * kPitch * 4;
+static_assert(kOutBytes >= kImage && kOutBytes >= kChunk * kTallPitch * 4, "one place for both");
+constexpr int kUpdateSmem = kPoly + kOutBytes + 1024, kUpdateCols = 64;
 
-// O = P X and the weights.
+// O = P X and the weights of the tensors of one kind (kW: type of the weights that are read, master
+// or p; kP: of p).  A launch for each kind that there is; its blocks pass over the others' stretches.
+template <int kW, int kP>
 __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_constant__ MuonTable tab) {
+  constexpr bool kMaster = kW != kP;
   extern __shared__ uint8_t muon_smem[];
   __shared__ uint64_t done;
   __shared__ uint32_t slot;
   uint8_t* sm = aligned_smem(muon_smem);
   uint8_t *pt = sm, *xt = sm + kPoly;
-  const Place pl = place_of(tab, blockIdx.x);
-  const MuonTensor& t = *pl.t;
-  const bool aligned = quads_aligned(t), tall = t.tall;
-  copy_async(pt, tab.poly + pl.tile * kPoly, kPoly);
-  copy_async(xt, tab.x + pl.image * (int64_t)kImage, kImage);
   if (threadIdx.x == 0) {
     mbar_init(&done, 1);
     fence_mbar_init();
   }
-  const float factor = tab.norm[pl.tile * 2 * kTile + kTile + my_row()];
-  // NaN for a matrix whose norm is not finite
-  const float f = (factor == factor ? 1.f : factor) * (1.f / (kXScale * kQScale));
+  launch_next();
   const uint32_t acc = tmem_open(&slot, kUpdateCols);
-  const int64_t base = pl.first * t.s * t.L;
-  const int wd = t.master ? MOE_LORA_F32 : t.p_dtype;
-  const void* wp = t.master ? static_cast<const void*>(t.master) : t.p;
-  for (int c = pl.c0; c < pl.c1; ++c) {
-    async_wait<0>();
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-      poly_product(acc, smem_u32(pt), smem_u32(xt), false);
-      mma_commit(&done);
-    }
-    uint4 w[kQuads];
-    if (aligned)
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const Quad q(tall, i);
-        const int l = c * kChunk + q.col;
-        if (q.row < pl.rows && l < t.L) w[i] = ld_quad(wp, wd, base + offset_of(t, q.row, l));
-      }
-    if (!all_wait(&done, (c - pl.c0) & 1, tab.err)) break;
-    // the products change threads through shared memory, where X was
-    float v[32];
-    tmem_row32(acc, my_half() * 32, v);
+  wait_for_last();
+  Waits wait{tab.err};
+  uint32_t used = 0;  // chunks so far
+  const int end = first_chunk(tab, blockIdx.x + 1);
+  for (int x = first_chunk(tab, blockIdx.x); x < end;) {
+    const Place pl = place_of(tab, x, end);
+    const MuonTensor& t = *pl.t;
+    const uint8_t* image = tab.x + x * (int64_t)kImage;
+    x += pl.c1 - pl.c0;
+    if ((t.master != nullptr) != kMaster || t.p_dtype != kP) continue;
+    copy_async<kPoly>(pt, tab.poly + (int64_t)pl.tile * kPoly);  // no product is under way, and all have read the last ones
+    copy_async<kImage>(xt, image);
+    const float factor = tab.norm[(int64_t)pl.tile * 2 * kTile + kTile + my_row()];
+    // NaN for a matrix whose norm is not finite
+    const float f = (factor == factor ? 1.f : factor) * (1.f / (kXScale * kQScale));
+    const bool aligned = quads_aligned(t), tall = t.tall;
+    const void* wp = kMaster ? static_cast<const void*>(t.master) : t.p;
+    const Walk w(t, pl.first, pl.rows);
     float* o = reinterpret_cast<float*>(xt);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {  // 64 rows at a time: kPitch * 128 floats are more than X's place
-      if (my_row() / 64 == half)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[(my_row() % 64) * kPitch + my_half() * 32 + i] = v[i] * f;
+    // a thread's quads among the products
+    const float* mine = tall ? o + w.col * kTallPitch + w.row : o + w.row * kPitch + w.col;
+    const int hop = tall ? w.hop_col * kTallPitch : w.hop_row * kPitch;
+    for (int c = pl.c0; c < pl.c1; ++c, ++used) {
+      const int n = w.inside(c);
+      const int64_t at = w.at + c * w.chunk;
+      async_wait<0>();
+      fence_proxy_async_smem();
+      tc_fence_before();
       __syncthreads();
+      if (threadIdx.x == 0) {
+        tc_fence_after();
+        poly_product(acc, smem_u32(pt), smem_u32(xt), false);
+        mma_commit(&done);
+      }
+      uint4 old[kQuads];
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const Quad q(tall, i);
-        const int l = c * kChunk + q.col;
-        if (q.row / 64 != half) continue;
-        float x[4];
+      for (int i = 0; i < kQuads; ++i) old[i] = aligned && i < n ? ld_quad<kW>(wp, at + i * w.hop) : make_uint4(0, 0, 0, 0);
+      wait(&done, used & 1);
+      {
+        float v[32];
+        tmem_row32(acc, my_part() * 32, v);
+        if (tall) {
+          float* to = o + my_part() * 32 * kTallPitch + my_row();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = o[(q.row % 64 + (tall ? e : 0)) * kPitch + q.col + (tall ? 0 : e)];
-        if (aligned) {
-          if (q.row < pl.rows && l < t.L) {
-            const int64_t at = base + offset_of(t, q.row, l);
-            float4 u = widen(w[i], wd);
-            u = make_float4(u.x * t.decay - t.step * x[0], u.y * t.decay - t.step * x[1], u.z * t.decay - t.step * x[2], u.w * t.decay - t.step * x[3]);
-            if (t.master) *reinterpret_cast<float4*>(t.master + at) = u;
-            st_quad(t.p, t.p_dtype, at, u);
-          }
+          for (int i = 0; i < 32; ++i) to[i * kTallPitch] = v[i] * f;
         } else {
+          float* to = o + my_row() * kPitch + my_part() * 32;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = q.row + (tall ? e : 0), k = l + (tall ? 0 : e);
-            if (r < pl.rows && k < t.L) {
-              const int64_t at = base + offset_of(t, r, k);
-              const float u = ld_one(wp, wd, at) * t.decay - t.step * x[e];
-              if (t.master) t.master[at] = u;
-              st_one(t.p, t.p_dtype, at, u);
-            }
-          }
+          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
         }
       }
       __syncthreads();
+      float4 y[kQuads];  // the products, then the weights
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        y[i] = *reinterpret_cast<const float4*>(mine + i * hop);
+        if (aligned) {
+          const Four u = widen<kW>(old[i]);
+          const float2 a = fma2(both(-t.step), make_float2(y[i].x, y[i].y), mul2(u.a, both(t.decay)));
+          const float2 b = fma2(both(-t.step), make_float2(y[i].z, y[i].w), mul2(u.b, both(t.decay)));
+          y[i] = make_float4(a.x, a.y, b.x, b.y);
+        }
+      }
+      __syncthreads();
+      image += kImage;
+      if (c + 1 < pl.c1) copy_async<kImage>(xt, image);
+      if (aligned) {
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+          if (i < n) {
+            const Four u{make_float2(y[i].x, y[i].y), make_float2(y[i].z, y[i].w)};
+            if (kMaster) st_quad<MOE_LORA_F32>(t.master, at + i * w.hop, u);
+            st_quad<kP>(t.p, at + i * w.hop, u);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const float z[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t to = element_at(t, w, pl.first, c, i, e);
+            if (to < 0) continue;
+            const float u = fmaf(-t.step, z[e], ld_one<kW>(wp, to) * t.decay);
+            if (kMaster) t.master[to] = u;
+            st_one<kP>(t.p, to, u);
+          }
+        }
+      }
     }
-    if (c + 1 < pl.c1) copy_async(xt, tab.x + (pl.image + c + 1 - pl.c0) * (int64_t)kImage, kImage);
   }
-  async_wait<0>();
   tmem_close(acc, kUpdateCols);
 }
 
@@ -791,45 +934,44 @@ Shape shape_of(const moe_lora_muon_tensor& t) {
   h.chunks = (h.L + kChunk - 1) / kChunk;
   return h;
 }
-// Chunks of a piece, from all tensors of a launch: enough pieces for two blocks on each of
-// 152 SMs, and at most sixteen chunks (more than that adds up over a hundred products into one
-// accumulator, whose additions the tensor cores cut off rather than round).
-int piece_of(const moe_lora_muon_tensor* t, int n) {
-  int64_t all = 0;
-  for (int i = 0; i < n; ++i) all += shape_of(t[i]).tiles * shape_of(t[i]).chunks;
-  return (int)std::min<int64_t>(16, std::max<int64_t>(1, (all + 303) / 304));
-}
+// Two blocks on each of 152 SMs share the chunks of a launch.
+constexpr int kBlocks = 304;
 struct Layout {
   size_t err, norm, poly, gram, x, total;
-  int piece;
-  int64_t tiles, pieces;
+  int blocks;
+  int64_t tiles, chunks;
 };
 Layout layout_of(const moe_lora_muon_tensor* t, int n) {
   Layout l = {};
-  l.piece = piece_of(t, n);
   for (int i = 0; i < n; ++i) {
     const Shape h = shape_of(t[i]);
     l.tiles += h.tiles;
-    l.pieces += h.tiles * ((h.chunks + l.piece - 1) / l.piece);
+    l.chunks += h.tiles * h.chunks;
   }
+  l.blocks = (int)std::min<int64_t>(kBlocks, l.chunks);
   size_t o = 0;
   const auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   l.err = take(16);
   l.norm = take(sizeof(float) * 2 * kTile * l.tiles);
   l.poly = take((size_t)kPoly * l.tiles);
-  l.gram = take(sizeof(float) * kTile * kTile * l.pieces);
-  l.x = take((size_t)kImage * l.pieces * l.piece);
+  l.gram = take(sizeof(float) * kTile * kTile * (l.tiles + l.blocks));
+  l.x = take((size_t)kImage * l.chunks);
   l.total = o;
   return l;
 }
 
 template <class K, class... A>
-int launch_muon(int slot, K kernel, int64_t grid, size_t smem, cudaStream_t s, A... args) {
+int launch_muon(int slot, K kernel, int64_t grid, int threads, size_t smem, bool overlap, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = overlap ? 1 : 0;
   prof_begin(slot, s);
   const cudaError_t e = launch_allowed(cfg, false, kernel, args...);
   prof_end(slot, s);
@@ -842,9 +984,8 @@ int run_muon(const moe_lora_muon* o, const moe_lora_muon_tensor* in, int n, uint
   if (l.tiles == 0) return MOE_LORA_OK;
   MuonTable tab;
   tab.n = 0;
-  tab.piece = l.piece;
-  tab.tiles = l.tiles;
-  tab.pieces = l.pieces;
+  tab.blocks = l.blocks;
+  tab.chunks = (int)l.chunks;
   tab.mu = (float)o->momentum;
   tab.nu = (float)(1 - o->momentum);
   tab.eps = (float)o->eps;
@@ -858,24 +999,39 @@ int run_muon(const moe_lora_muon* o, const moe_lora_muon_tensor* in, int n, uint
   tab.poly = ws + l.poly;
   tab.gram = reinterpret_cast<float*>(ws + l.gram);
   tab.x = ws + l.x;
-  int64_t tile = 0, piece = 0;
+  int64_t tile = 0, chunk = 0;
   for (int i = 0; i < n; ++i) {
     const Shape h = shape_of(in[i]);
     if (h.tiles == 0) continue;
     MuonTensor& t = tab.t[tab.n++];
-    t = MuonTensor{in[i].p, in[i].master, in[i].g, in[i].m, in[i].batch, tile, piece, h.s, h.L, in[i].rows > in[i].cols, h.per,
-                   (int)((h.chunks + l.piece - 1) / l.piece), in[i].p_dtype, in[i].g_dtype,
+    t = MuonTensor{in[i].p, in[i].master, in[i].g, in[i].m, in[i].batch, (int)tile, (int)chunk, h.s, h.L, in[i].rows > in[i].cols, h.per,
+                   (int)h.chunks, in[i].p_dtype, in[i].g_dtype,
                    (float)(1 - in[i].lr * in[i].weight_decay), (float)(in[i].lr * in[i].scale)};
     tile += h.tiles;
-    piece += h.tiles * t.pieces;
+    chunk += h.tiles * h.chunks;
   }
   const int first = std::min(kFirstSteps, o->steps > 3 ? 2 : 1);
   int rc;
-  if ((rc = launch_muon(K_MUON_GRAM, muon_gram_kernel, l.pieces, kGramSmem, s, tab)) ||
-      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, l.tiles, kPolySmem, s, tab, first, true)) ||
-      (rc = launch_muon(K_MUON_APPLY, muon_apply_kernel, l.pieces, kApplySmem, s, tab)) ||
-      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, l.tiles, kPolySmem, s, tab, o->steps - first, false)) ||
-      (rc = launch_muon(K_MUON_UPDATE, muon_update_kernel, l.pieces, kUpdateSmem, s, tab)))
+  if ((rc = launch_muon(K_MUON_GRAM, muon_gram_kernel, l.blocks, kThreads, kGramSmem, false, s, tab)) ||
+      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, l.tiles, kPolyThreads, kPolySmem, true, s, tab, first, true)) ||
+      (rc = launch_muon(K_MUON_APPLY, muon_apply_kernel, l.blocks, kThreads, kApplySmem, true, s, tab)) ||
+      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, l.tiles, kPolyThreads, kPolySmem, true, s, tab, o->steps - first, false)))
+    return rc;
+  bool overlap = true;  // the first kind's launch with what is before it; the others follow it as any launch does
+  const auto update = [&](auto kernel, int dtype, bool master) {
+    for (int i = 0; i < tab.n; ++i)
+      if (tab.t[i].p_dtype == dtype && (tab.t[i].master != nullptr) == master) {
+        const int e = launch_muon(K_MUON_UPDATE, kernel, l.blocks, kThreads, kUpdateSmem, overlap, s, tab);
+        overlap = false;
+        return e;
+      }
+    return MOE_LORA_OK;
+  };
+  if ((rc = update(muon_update_kernel<MOE_LORA_F32, MOE_LORA_BF16>, MOE_LORA_BF16, true)) ||
+      (rc = update(muon_update_kernel<MOE_LORA_F32, MOE_LORA_F16>, MOE_LORA_F16, true)) ||
+      (rc = update(muon_update_kernel<MOE_LORA_F32, MOE_LORA_F32>, MOE_LORA_F32, false)) ||
+      (rc = update(muon_update_kernel<MOE_LORA_BF16, MOE_LORA_BF16>, MOE_LORA_BF16, false)) ||
+      (rc = update(muon_update_kernel<MOE_LORA_F16, MOE_LORA_F16>, MOE_LORA_F16, false)))
     return rc;
   return MOE_LORA_OK;
 }
@@ -908,10 +1064,8 @@ extern "C" int moe_lora_muon_step(const moe_lora_muon* o, const moe_lora_muon_te
     if ((rc = check_muon(tensors[i]))) return rc;
   if ((rc = check_ptr(scratch))) return rc;
   if (scratch_bytes < moe_lora_muon_scratch_bytes(tensors, n)) return MOE_LORA_ERR_WORKSPACE;
-  for (int i = 0; i < n; i += kMaxTensors) {
-    const int64_t pieces = layout_of(tensors + i, std::min(kMaxTensors, n - i)).pieces;
-    if (pieces > ((int64_t)1 << 31) - 1) return MOE_LORA_ERR_DIMS;
-  }
+  for (int i = 0; i < n; i += kMaxTensors)
+    if (layout_of(tensors + i, std::min(kMaxTensors, n - i)).chunks > (int64_t)1 << 30) return MOE_LORA_ERR_DIMS;
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
