@@ -117,43 +117,61 @@ __device__ __forceinline__ Place place_of(const MuonTable& tab, int x, int end) 
 
 // ------------------------------------------------------------------ a thread's share of a chunk
 // A thread's quads of a chunk, four neighbouring elements in memory each.  Of [s, L]: along the
-// long side, 16 to a row.  Of tall matrices [L, s]: along the short side, 32 to a long place.
-// Everything is linear in the quad and the chunk, divisions are done once.
+// long side, 16 to a row.  Of tall matrices [L, s]: along the short side; a warp's 32 are one run of
+// memory where s is a power of two (128 / s long places of one matrix), and otherwise a long place of
+// all matrices of the tile.  With the latter for s = 8 too, whose runs are then 16 or 32 bytes, 38.6 M
+// elements took 488 us instead of XXX.  Steps from quad to quad and from chunk to chunk are the same
+// throughout, divisions are done once.
 struct Walk {
   int64_t at, hop, chunk;     // element of quad 0 in chunk 0 of the tile; to the next quad, chunk
   int row, col;               // of quad 0: short side within the tile, long side within the chunk
-  int hop_row, hop_col;
-  uint32_t smem, hop_smem;    // bytes in a part of an operand tile
+  int hop_row, hop_col;       // one of them is 0
   int rows, L;
-  // Operand tiles have rows of 128 bytes whose 16-byte units are exchanged by row (unit ^ row % 8).
-  // A chunk of [s, L]: 128 rows of 64 long places.  Of [L, s]: two halves of 64 short places, a
-  // row per long place.  Neither the quads' steps nor the chunks' change row % 8.
-  __device__ __forceinline__ Walk(const MuonTensor& t, int64_t first, int rows_) : rows(rows_), L(t.L) {
+  bool tall;
+  __device__ __forceinline__ Walk(const MuonTensor& t, int64_t first, int rows_) : rows(rows_), L(t.L), tall(t.tall) {
+    constexpr int kWarps = kThreads / 32;
     const int64_t base = first * t.s * t.L;
-    int r, k, half;
-    if (t.tall) {
-      row = (threadIdx.x & 31) * 4;
-      col = threadIdx.x >> 5;
-      hop_row = 0;
-      hop_col = kThreads / 32;
-      const int j = row / t.s;
-      at = base + ((int64_t)j * t.L + col) * t.s + (row - j * t.s);
-      hop = (int64_t)hop_col * t.s;
-      chunk = (int64_t)kChunk * t.s;
-      r = col, k = row % 64, half = row / 64 * (kPart / 2);
-      hop_smem = hop_col * 128;
-    } else {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    hop_row = hop_col = 0;
+    if (!tall) {
       row = threadIdx.x >> 4;
       col = (threadIdx.x & 15) * 4;
       hop_row = kThreads / 16;
-      hop_col = 0;
-      at = base + (int64_t)row * t.L + col;
-      hop = (int64_t)hop_row * t.L;
-      chunk = kChunk;
-      r = row, k = col, half = 0;
-      hop_smem = hop_row * 128;
+      at = base + (int64_t)row * L + col;
+    } else {
+      int j, r;  // matrix, and place on its short side
+      if (t.s >= 4 && (t.s & (t.s - 1)) == 0) {
+        const int places = kTile / t.s, runs = kChunk / places, mats = kTile / t.s;  // of a run; of a matrix; of the tile
+        r = lane * 4 % t.s;
+        col = lane * 4 / t.s;
+        if (mats <= kWarps) {
+          j = warp % mats;
+          col += warp / mats * places;
+          hop_col = kWarps / mats * places;
+        } else {
+          j = warp / runs;
+          col += warp % runs * places;
+          hop_row = kWarps / runs * t.s;
+        }
+      } else {
+        j = lane * 4 / t.s;
+        r = lane * 4 - j * t.s;
+        col = warp;
+        hop_col = kWarps;
+      }
+      row = j * t.s + r;
+      at = base + ((int64_t)j * L + col) * t.s + r;
     }
-    smem = half + r * 128 + ((((k >> 3) ^ (r & 7)) << 4) | ((k & 4) << 1));
+    hop = hop_row ? (int64_t)hop_row * L : (int64_t)hop_col * t.s;
+    chunk = tall ? (int64_t)kChunk * t.s : kChunk;
+  }
+  // Bytes of quad i in a part of an operand tile.  These have rows of 128 bytes whose 16-byte units are
+  // exchanged by row (unit ^ row % 8).  A chunk of [s, L]: 128 rows of 64 long places.  Of [L, s]: two
+  // halves of 64 short places, a row per long place.
+  __device__ __forceinline__ uint32_t operand(int i) const {
+    const int r = row + i * hop_row, c = col + i * hop_col;
+    const uint32_t line = tall ? c : r, k = tall ? r % 64 : c, half = tall ? r / 64 * (kPart / 2) : 0;
+    return half + line * 128 + ((((k >> 3) ^ (line & 7)) << 4) | ((k & 4) << 1));
   }
   // How many of the quads of chunk c lie inside, where quads lie inside or outside as a whole.
   __device__ __forceinline__ int inside(int c) const {
@@ -379,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_gram_kernel(const __grid_con
             }
           }
           Four u = tab.nesterov ? mix(tab.mu, m, nu, g) : m;
-          uint8_t* to = part + w.smem + i * w.hop_smem;
+          uint8_t* to = part + w.operand(i);
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
             const uint32_t a = take_bf16(u.a), b = take_bf16(u.b);
@@ -724,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
           uint2 hi, lo;
           fp16_parts(u.a, hi.x, lo.x);
           fp16_parts(u.b, hi.y, lo.y);
-          uint8_t* to = xt + w.smem + i * w.hop_smem;
+          uint8_t* to = xt + w.operand(i);
           *reinterpret_cast<uint2*>(to) = hi;
           *reinterpret_cast<uint2*>(to + kPart) = lo;
         }
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_c
     float* o = reinterpret_cast<float*>(xt);
     // a thread's quads among the products
     const float* mine = tall ? o + w.col * kTallPitch + w.row : o + w.row * kPitch + w.col;
-    const int hop = tall ? w.hop_col * kTallPitch : w.hop_row * kPitch;
+    const int hop = tall ? w.hop_col * kTallPitch + w.hop_row : w.hop_row * kPitch;
     for (int c = pl.c0; c < pl.c1; ++c, ++used) {
       const int n = w.inside(c);
       const int64_t at = w.at + c * w.chunk;

@@ -9,6 +9,7 @@
 // its own elements; the threads' pairs meet once, in distributed shared memory, and where a
 // gradient is wanted it is formed from the slice in shared memory: one read and one write.
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -25,6 +26,7 @@ namespace {
 
 constexpr int kGroup = 4;            // vectors of a thread that are waited for together
 constexpr int kRowThreads = 256;     // of a block that works on a slice of a row
+constexpr int kReadThreads = 128;    // of one for log probabilities alone
 constexpr int kShortThreads = 128;   // of a block whose warps have a row each
 constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 1 << 19;
@@ -48,7 +50,7 @@ struct RowArgs {
   const void* x;
   int64_t ld, rows;
   int n;
-  float inv_temp;
+  float inv_temp, c, floor;  // see Temper
   const int32_t* targets;
   float *logp, *lse, *entropy;
   int* err;
@@ -161,21 +163,23 @@ __device__ __forceinline__ float warp_top(float v) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// A maximum, the sum of 2^((x - m) c) and of that times x - m.
+// A reference M, the sum of 2^(x c - M) and of that times x c - M.  M is the maximum of x c rounded
+// up to a whole number, so that x c - M is rounded once and moving to another M scales exactly;
+// -inf where there is no element.
 struct Softmax {
   float m, s, w;
-  // the same sums relative to another maximum
+  // the same sums relative to another reference
   template <bool kEntropy>
-  __device__ __forceinline__ void move(float to, float c) {
-    const float ref = to == -INFINITY ? 0.f : to, d = fmaxf(m - ref, -3e38f), f = ex2_fast(d * c);
+  __device__ __forceinline__ void move(float to) {
+    const float d = m - (to == -INFINITY ? 0.f : to), f = ex2_fast(d);
     if (kEntropy) w = f > 0.f ? f * (w + s * d) : 0.f;
     s *= f;
     m = to;
   }
   // of all lanes: the maximum first, then symmetric sums, so that every lane has the same bits
   template <bool kEntropy>
-  __device__ __forceinline__ void over_warp(float c) {
-    move<kEntropy>(warp_top(m), c);
+  __device__ __forceinline__ void over_warp() {
+    move<kEntropy>(warp_top(m));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -184,51 +188,130 @@ struct Softmax {
   }
 };
 
-// Two elements (one of fp32) in a word: the larger ones, NaN passed over; and -inf made the type's
-// lowest number, NaN kept.
+// z in base 2 is x c.  Logits below `floor` count as `floor`: -inf, the types' lowest numbers, and
+// whatever else masks them.  Next to any other logit their probability is 0, and 0 times their
+// distance is 0, not NaN.  floor c is about -2^20, which leaves room for the fraction of x c - M; floor
+// is a bf16 number.
+struct Temper {
+  float c, floor;
+  __device__ __forceinline__ float lift(float x) const {  // NaN kept
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(floor));
+    return d;
+  }
+  // The same of a vector's words, two elements at a time, where the type reaches that far;
+  template <class T>
+  __device__ __forceinline__ void lift_words(uint32_t (&w)[4]) const {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      const uint32_t both_floors = __float_as_uint(floor) | __float_as_uint(floor) >> 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[k]) : "r"(both_floors));
+    }
+  }
+  // elsewhere in fp32, as pairs are taken.
+  template <class T>
+  __device__ __forceinline__ float2 lifted(const Vec<T, 16 / sizeof(T)>& u, int p) const {
+    const float2 f = u.get(p);
+    return std::is_same<T, __nv_bfloat16>::value ? f : make_float2(lift(f.x), lift(f.y));
+  }
+  // 2^(x c - m) of a pair, and the exponents
+  __device__ __forceinline__ float2 exp(float2 x, float m, float2& t) const {
+    t = fma2(x, both(c), both(-m));
+    return make_float2(ex2_fast(t.x), ex2_fast(t.y));
+  }
+};
+// The largest of a vector's elements (NaN is passed over) and `top`, in words.
 template <class T>
-__device__ __forceinline__ uint32_t top_words(uint32_t a, uint32_t b);
+__device__ __forceinline__ uint32_t top_word(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (sizeof(T) == 4)
+    d = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  else if constexpr (std::is_same<T, __half>::value)
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A thread's maximum and sums over its own elements, so far.
+template <class T, bool kEntropy>
+struct Running {
+  static constexpr int VL = 16 / sizeof(T), kP = VL / 2;
+  // an empty place reads as -inf
+  static constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+  Temper z;
+  float m;
+  float2 s2, w2;
+  __device__ __forceinline__ explicit Running(const Temper& z_) : z(z_), m(-INFINITY), s2(both(0.f)), w2(both(0.f)) {}
+  __device__ __forceinline__ Softmax sums() const { return Softmax{m, s2.x + s2.y, w2.x + w2.y}; }
+  // sums relative to a reference that `top` does not pass
+  __device__ __forceinline__ void shift(float top) {
+    const float to = fmaxf(m, ceilf(fmaxf(top, z.floor) * z.c)), d = m - to, f = ex2_fast(d);
+    if (kEntropy) w2 = f > 0.f ? mul2(fma2(s2, both(d), w2), both(f)) : both(0.f);
+    s2 = mul2(s2, both(f));
+    m = to;
+  }
+  // up to kGroup vectors, v, v + kTeam, ... of `count`, from a row of the ring
+  template <int kTeam, class R>
+  __device__ __forceinline__ void add(const R& ring, int stage, int first, int v, int count) {
+    Vec<T, VL> u[kGroup];
+    uint32_t tw = kNone;
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j)
+      if (v + j * kTeam < count) {
+        u[j].from_smem(ring.slot(stage, first + j));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tw = top_word<T>(tw, u[j].w[k]);
+      }
+    if (v >= count) return;
+    if constexpr (sizeof(T) == 4) {
+      shift(__uint_as_float(tw));
+    } else {
+      const float2 t2 = Two<T>::get(&tw);
+      shift(fmaxf(t2.x, t2.y));
+    }
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j)
+      if (v + j * kTeam < count) {
+        z.template lift_words<T>(u[j].w);
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          float2 t;
+          const float2 e = z.exp(z.template lifted<T>(u[j], p), m, t);
+          s2 = add2(s2, e);
+          if (kEntropy) w2 = fma2(e, t, w2);
+        }
+      }
+  }
+  __device__ __forceinline__ void add_one(float x) {
+    shift(x);
+    const float t = fmaf(z.lift(x), z.c, -m), e = ex2_fast(t);
+    s2.x += e;
+    if (kEntropy) w2.x += e * t;
+  }
+};
+// What a row's sums say of the element with logit x.
+struct Outcome {
+  float logp, lse, entropy, inv_s;
+  __device__ __forceinline__ Outcome(const Softmax& sm, float x, const Temper& z) {
+    constexpr float kLn2 = 0.6931471805599453f;
+    const float ls = log2f(sm.s);
+    // element minus reference first: their difference is what counts, not their size
+    logp = kLn2 * (fmaf(x == -INFINITY ? x : z.lift(x), z.c, -sm.m) - ls);
+    lse = kLn2 * (sm.m + ls);
+    inv_s = 1.0f / sm.s;
+    entropy = kLn2 * (ls - sm.w * inv_s);
+  }
+};
+// The gradient of a vector whose first element is column `col`: q 2^(x c - m), and coef more at the target.
 template <class T>
-__device__ __forceinline__ uint32_t lift_word(uint32_t a);
-template <class T>
-constexpr float kLowest = -3.4028234663852886e38f;
-template <>
-constexpr float kLowest<__nv_bfloat16> = -3.3895313892515355e38f;
-template <>
-constexpr float kLowest<__half> = -65504.f;
-template <>
-__device__ __forceinline__ uint32_t top_words<__nv_bfloat16>(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-template <>
-__device__ __forceinline__ uint32_t top_words<__half>(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-template <>
-__device__ __forceinline__ uint32_t top_words<float>(uint32_t a, uint32_t b) {
-  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-}
-template <>
-__device__ __forceinline__ uint32_t lift_word<__nv_bfloat16>(uint32_t a) {
-  uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0xFF7FFF7Fu));
-  return d;
-}
-template <>
-__device__ __forceinline__ uint32_t lift_word<__half>(uint32_t a) {
-  uint32_t d;
-  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0xFBFFFBFFu));
-  return d;
-}
-template <>
-__device__ __forceinline__ uint32_t lift_word<float>(uint32_t a) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(kLowest<float>));
-  return __float_as_uint(d);
+__device__ __forceinline__ Vec<T, 16 / sizeof(T)> grad_of(Vec<T, 16 / sizeof(T)> u, const Temper& z, float m, float q, float coef, int col, int y) {
+  constexpr int kP = 8 / sizeof(T);
+  float2 e[kP], t;
+  z.template lift_words<T>(u.w);
+#pragma unroll
+  for (int p = 0; p < kP; ++p) e[p] = z.exp(z.template lifted<T>(u, p), m, t);
+  return grad_vec<T>(e, q, coef, col, y);
 }
 
 // The sums of few rows (pairs) by the warp that came last, an adapter after the other: lanes add
@@ -268,6 +351,48 @@ __device__ __forceinline__ int live_in(const int32_t* targets, int n, int64_t lo
   return __reduce_add_sync(0xffffffffu, c);
 }
 
+// 1 / (live tokens of adapter a), from the counts of a launch before.
+__device__ __forceinline__ float count_factor(const PolicyArgs& pg, int a) {
+  const int lane = threadIdx.x & 31;
+  const int k = __reduce_add_sync(0xffffffffu, lane < kCountParts ? pg.count[a * kCountParts + lane] : 0);
+  return 1.0f / (float)max(k, 1);
+}
+// What a token's own values make of the softmax of its row.
+struct Token {
+  float adv, old, ref, wt, up;
+  int a;  // adapter
+  __device__ __forceinline__ Token() {}
+  __device__ __forceinline__ Token(const PolicyArgs& pg, const Ranges& ad, int64_t t) : ref(0.f), wt(1.f), up(1.f) {
+    a = range_of(ad, t);
+    adv = pg.adv[t];
+    old = pg.old[t];
+    if (pg.ref) ref = pg.ref[t];
+    if (pg.weight) wt = pg.weight[t];
+    if (pg.dloss) up = pg.dloss[a];
+  }
+  // The loss's terms (stored where `writes`), and the factor of the gradient to the log probability.
+  __device__ __forceinline__ float terms(const PolicyArgs& pg, int64_t rows, int64_t t, float logp, float entropy, bool writes) const {
+    const float rho = expf(logp - old), clip = fminf(fmaxf(rho, pg.low), pg.high);
+    const bool cut = (adv > 0.f && rho > pg.high) || (adv < 0.f && rho < pg.low);
+    float loss = -(cut ? clip : rho) * adv, kl = 0.f, dl = cut ? 0.f : -rho * adv;
+    if (pg.ref) {
+      const float d = ref - logp, em = expm1f(d);
+      kl = em - d;
+      loss += pg.kl * kl;
+      dl -= pg.kl * em;
+    }
+    if (writes) {  // a token of weight 0 has no part in the loss, whatever its values
+      float* to = pg.terms + t;
+      to[0] = wt == 0.f ? 0.f : wt * loss;
+      to[rows] = wt == 0.f ? 0.f : wt * kl;
+      to[2 * rows] = cut ? wt : 0.f;
+      to[3 * rows] = wt == 0.f ? 0.f : wt * rho;
+      to[4 * rows] = wt == 0.f ? 0.f : wt * entropy;
+    }
+    return wt == 0.f ? 0.f : up * wt * dl;
+  }
+};
+
 // Log probabilities (kPolicy false), or the policy loss's terms and, with kGrad, its
 // gradient.  kTeam threads work on a slice: a block's, or a warp whose slice is the row.
 // What happens once per row is left to one warp: with a slice of 64 KB a warp has 16 vectors
@@ -276,10 +401,10 @@ template <class T, int kTeam, int kGroups, bool kEntropy, bool kPolicy, bool kGr
 __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     token_row_kernel(const __grid_constant__ RowArgs g, const __grid_constant__ PolicyArgs pg,
                      const __grid_constant__ GradArgs dg, const __grid_constant__ Ranges ad, int slices, int per) {
-  constexpr int VL = 16 / sizeof(T), kP = VL / 2, kWarps = kTeam / 32;
+  constexpr int VL = 16 / sizeof(T), kWarps = kTeam / 32;
   extern __shared__ __align__(16) uint8_t row_smem[];
   __shared__ Softmax part[kMaxCluster + kWarps];
-  __shared__ float3 result;  // the maximum, the factor of all exponentials and of the target's one
+  __shared__ float3 result;  // the reference, the factor of all exponentials and of the target's one
   __shared__ float at_target;
   const Ring<1, kGroups * kGroup> ring(row_smem);
   const int tid = threadIdx.x % kTeam, lane = threadIdx.x & 31, warp = tid >> 5;
@@ -332,31 +457,12 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
   float xy = 0.f;
   if (kTeam == 32 || tid == 0) xy = to_f32(row[y]);
   if (kTeam > 32 && tid == 0) at_target = xy;
-  float adv = 0.f, old = 0.f, ref = 0.f, wt = 1.f, up = 1.f;
-  int a = 0;
-  if (kPolicy && warp == 0) {
-    a = range_of(ad, t);
-    adv = pg.adv[t];
-    old = pg.old[t];
-    if (pg.ref) ref = pg.ref[t];
-    if (pg.weight) wt = pg.weight[t];
-    if (pg.dloss) up = pg.dloss[a];
-    if (kGrad && pg.few && !pg.weight) up /= (float)max(live_in(g.targets, g.n, ad.off[a], ad.off[a + 1]), 1);
-  }
+  Token tok = kPolicy && warp == 0 ? Token(pg, ad, t) : Token();
+  if (kPolicy && kGrad && warp == 0 && pg.few && !pg.weight)
+    tok.up /= (float)max(live_in(g.targets, g.n, ad.off[tok.a], ad.off[tok.a + 1]), 1);
 
-  const float c = g.inv_temp * kLog2e;
-  // An empty place reads as -inf.
-  const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
-  Softmax sm{-INFINITY, 0.f, 0.f};
-  float2 s2 = both(0.f), w2 = both(0.f);
-  const auto shift = [&](float top) {  // sums relative to the maximum so far, or 0 while there is none
-    const float to = fmaxf(sm.m, top), ref0 = to == -INFINITY ? 0.f : to;
-    const float d = fmaxf(sm.m - ref0, -3e38f), f = ex2_fast(d * c);
-    if (kEntropy) w2 = f > 0.f ? mul2(fma2(s2, both(d), w2), both(f)) : both(0.f);
-    s2 = mul2(s2, both(f));
-    sm.m = to;
-    return ref0;
-  };
+  const Temper z{g.c, g.floor};
+  Running<T, kEntropy> run(z);
 #pragma unroll
   for (int gr = 0; gr < kGroups; ++gr) {
     if (gr * kGroup * kTeam >= sl.count) break;
@@ -371,75 +477,19 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
       async_wait<3>();
     else
       async_wait<4>();
-    Vec<T, VL> u[kGroup];
-    uint32_t tw = none;
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      const int i = gr * kGroup + j;
-      if (tid + i * kTeam < sl.count)
-        u[j].from_smem(ring.slot(0, i));
-      else
-        u[j].w[0] = u[j].w[1] = u[j].w[2] = u[j].w[3] = none;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        tw = top_words<T>(tw, u[j].w[k]);
-      }
-    }
-    float top;
-    if constexpr (sizeof(T) == 4) {
-      top = __uint_as_float(tw);
-    } else {
-      const float2 t2 = Two<T>::get(&tw);
-      top = fmaxf(t2.x, t2.y);
-    }
-    const float r = shift(top);
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      if (kEntropy)  // 0 * -inf: the type's lowest number takes the place of -inf, two at a time
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[j].w[k] = lift_word<T>(u[j].w[k]);
-#pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        const float2 d = add2(u[j].get(p), both(-r)), x = mul2(d, both(c));
-        const float2 e = make_float2(ex2_fast(x.x), ex2_fast(x.y));
-        s2 = add2(s2, e);
-        if (kEntropy) w2 = fma2(e, d, w2);
-      }
-    }
-  }
-  // Where the maximum is so near the type's lowest number that its probability is not 0, the sums
-  // are formed again with -inf as it is.
-  if (kEntropy && sm.m != -INFINITY && !((kLowest<T> - sm.m) * c <= -150.f)) {
-    s2 = w2 = both(0.f);
-#pragma unroll 1
-    for (int v = tid, i = 0; v < sl.count; v += kTeam, ++i) {
-      Vec<T, VL> u;
-      u.from_smem(ring.slot(0, i));
-#pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        const float2 d = add2(u.get(p), both(-sm.m)), x = mul2(d, both(c));
-        const float2 e = make_float2(ex2_fast(x.x), ex2_fast(x.y));
-        s2 = add2(s2, e);
-        w2 = fma2(e, make_float2(fmaxf(d.x, -3e38f), fmaxf(d.y, -3e38f)), w2);
-      }
-    }
+    run.template add<kTeam>(ring, 0, gr * kGroup, tid + gr * kGroup * kTeam, sl.count);
   }
   async_wait<0>();
-  if (sl.edge >= 0) {
-    const float r = shift(xe), e = ex2_fast((xe - r) * c);
-    s2.x += e;
-    if (kEntropy) w2.x += e * fmaxf(xe - r, -3e38f);
-  }
-  sm.s = s2.x + s2.y;
-  sm.w = w2.x + w2.y;
-  sm.over_warp<kEntropy>(c);
+  if (sl.edge >= 0) run.add_one(xe);
+  Softmax sm = run.sums();
+  sm.over_warp<kEntropy>();
   float q = 0.f, coef = 0.f;
   if (kTeam > 32) {
     if (lane == 0) part[kMaxCluster + warp] = sm;
     __syncthreads();
     if (warp == 0) {  // the block's sums
       sm = lane < kWarps ? part[kMaxCluster + lane] : Softmax{-INFINITY, 0.f, 0.f};
-      sm.over_warp<kEntropy>(c);
+      sm.over_warp<kEntropy>();
     }
     if (slices > 1) {  // and the cluster's
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks have started
@@ -452,48 +502,26 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
       cluster_sync_all();
       if (warp == 0) {
         sm = lane < slices ? part[lane] : Softmax{-INFINITY, 0.f, 0.f};
-        sm.over_warp<kEntropy>(c);
+        sm.over_warp<kEntropy>();
       }
     }
     xy = at_target;
   }
   if (warp == 0) {
-    const float ls = logf(sm.s);
-    // target minus maximum first: their difference is what counts, not their size
-    const float logp = (xy - sm.m) * g.inv_temp - ls;
-    const float inv_s = 1.0f / sm.s, entropy = kEntropy ? ls - sm.w * inv_s * g.inv_temp : 0.f;
+    const Outcome o(sm, xy, z);
     if (clerk && lane == 0) {
-      if (g.logp) g.logp[t] = logp;
-      if (g.lse) g.lse[t] = sm.m * g.inv_temp + ls;
-      if (g.entropy) g.entropy[t] = entropy;
+      if (g.logp) g.logp[t] = o.logp;
+      if (g.lse) g.lse[t] = o.lse;
+      if (g.entropy) g.entropy[t] = o.entropy;
     }
     if (kPolicy) {
-      const float rho = expf(logp - old), clip = fminf(fmaxf(rho, pg.low), pg.high);
-      const bool cut = (adv > 0.f && rho > pg.high) || (adv < 0.f && rho < pg.low);
-      float loss = -(cut ? clip : rho) * adv, kl = 0.f, dl = cut ? 0.f : -rho * adv;
-      if (pg.ref) {
-        const float d = ref - logp, em = expm1f(d);
-        kl = em - d;
-        loss += pg.kl * kl;
-        dl -= pg.kl * em;
-      }
-      if (clerk && lane == 0) {  // a token of weight 0 has no part in the loss, whatever its values
-        float* to = pg.terms + t;
-        to[0] = wt == 0.f ? 0.f : wt * loss;
-        to[g.rows] = wt == 0.f ? 0.f : wt * kl;
-        to[2 * g.rows] = cut ? wt : 0.f;
-        to[3 * g.rows] = wt == 0.f ? 0.f : wt * rho;
-        to[4 * g.rows] = wt == 0.f ? 0.f : wt * entropy;
-      }
       if (!pg.weight && !pg.few) {
         // the counts, and with them every launch that the sums behind this one rely on
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        int k = lane < kCountParts ? pg.count[a * kCountParts + lane] : 0;
-        k = __reduce_add_sync(0xffffffffu, k);
-        up /= (float)max(k, 1);
+        tok.up *= count_factor(pg, tok.a);
       }
-      coef = wt == 0.f ? 0.f : up * wt * dl * g.inv_temp;
-      q = -coef * inv_s;
+      coef = tok.terms(pg, g.rows, t, o.logp, o.entropy, clerk && lane == 0) * g.inv_temp;
+      q = -coef * o.inv_s;
       if (kTeam > 32 && kGrad && lane == 0) result = make_float3(sm.m, q, coef);
     }
   }
@@ -512,22 +540,15 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     finish();
     return;
   }
-  const float r = sm.m == -INFINITY ? 0.f : sm.m;
 #pragma unroll
   for (int i = 0; i < kGroups * kGroup; ++i) {
     const int v = tid + i * kTeam;
     if (v >= sl.count) break;
     Vec<T, VL> u;
     u.from_smem(ring.slot(0, i));
-    float2 e[kP];
-#pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      const float2 x = mul2(add2(u.get(p), both(-r)), both(c));
-      e[p] = make_float2(ex2_fast(x.x), ex2_fast(x.y));
-    }
-    store_vec<T>(out, sl.first + v * VL, aligned, grad_vec<T>(e, q, coef, sl.first + v * VL, y));
+    store_vec<T>(out, sl.first + v * VL, aligned, grad_of<T>(u, z, sm.m, q, coef, sl.first + v * VL, y));
   }
-  if (sl.edge >= 0) out[sl.edge] = from_f32<T>(q * ex2_fast((xe - r) * c) + (sl.edge == y ? coef : 0.f));
+  if (sl.edge >= 0) out[sl.edge] = from_f32<T>(q * ex2_fast(fmaf(z.lift(xe), z.c, -sm.m)) + (sl.edge == y ? coef : 0.f));
   finish();
 }
 
@@ -886,7 +907,13 @@ int check_rows(const moe_lora_rows* r) {
   return MOE_LORA_OK;
 }
 RowArgs row_args(const moe_lora_rows* r, const void* x, const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* err) {
-  return RowArgs{x, r->ld ? r->ld : r->n, r->rows, r->n, r->inv_temp, targets, logp, lse, entropy, err};
+  const float c = r->inv_temp * kLog2e, floor = -1048576.f / c;
+  uint32_t bits;
+  memcpy(&bits, &floor, 4);
+  bits &= 0xFFFF0000u;  // a bf16 number
+  float cut;
+  memcpy(&cut, &bits, 4);
+  return RowArgs{x, r->ld ? r->ld : r->n, r->rows, r->n, r->inv_temp, c, cut, targets, logp, lse, entropy, err};
 }
 
 template <class T, int kTeam, int kGroups, bool kEntropy, bool kPolicy, bool kGrad>
@@ -911,16 +938,16 @@ int pick_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, const 
   const int vecs = g.n / VL;
   if (vecs <= 32 * kGroup) return launch_rows<T, 32, 1, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
   if (vecs <= 32 * 4 * kGroup && g.rows >= sms) return launch_rows<T, 32, 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
-  constexpr int one = kRowThreads * kGroup;  // vectors of a group of a block
+  constexpr int kTeam = kPolicy ? kRowThreads : kReadThreads, one = kTeam * kGroup, kFull = 4 * kRowThreads / kTeam;
   const auto need = [&](int per) { return (vecs + per - 1) / per; };
-  int slices = need(4 * one);
-  if (slices > 8) slices = std::max(8, need(8 * one));
+  int slices = need(kFull * one);
+  if (slices > 8) slices = std::max(8, need(2 * kFull * one));
   while (slices < 8 && g.rows * (slices + 1) <= sms && vecs / (slices + 1) >= kRowThreads) ++slices;
   const int per = (vecs + slices - 1) / slices;
-  return per <= one       ? launch_rows<T, kRowThreads, 1, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
-         : per <= 2 * one ? launch_rows<T, kRowThreads, 2, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
-         : per <= 4 * one ? launch_rows<T, kRowThreads, 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
-                          : launch_rows<T, kRowThreads, 8, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s);
+  return per <= kFull / 4 * one   ? launch_rows<T, kTeam, kFull / 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
+         : per <= kFull / 2 * one ? launch_rows<T, kTeam, kFull / 2, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
+         : per <= kFull * one     ? launch_rows<T, kTeam, kFull, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
+                                  : launch_rows<T, kTeam, 2 * kFull, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s);
 }
 template <class T>
 int run_logp(const RowArgs& g, int sms, cudaStream_t s) {
