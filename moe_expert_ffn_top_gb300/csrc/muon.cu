@@ -467,16 +467,19 @@ __device__ __forceinline__ void put_row32(uint8_t* tile, const float (&v)[32]) {
     *reinterpret_cast<uint4*>(at + kTileBytes + sw) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
-// D = A B^T of square tiles (both fp16 parts; the product of the lower parts is below fp32's rounding).
-__device__ __forceinline__ void square_product(uint32_t d, uint32_t a, uint32_t b) {
-  const uint32_t id = idesc_f16_f32(kTile, kTile, false, false);
+// D = A B^T of square tiles (both fp16 parts; the product of the lower parts is below fp32's
+// rounding).  The tiles are zero outside blocks of `width` (16, 32, 64 or 128) rows and columns: a step
+// along 16 columns of both has to fill its own block's columns of D alone, and nobody reads the others.
+__device__ __forceinline__ void square_product(uint32_t d, uint32_t a, uint32_t b, int width) {
+  const uint32_t id = idesc_f16_f32(kTile, width, false, false);
 #pragma unroll 1
   for (int p = 0; p < 3; ++p) {
     const uint32_t pa = a + (p == 2 ? kTileBytes : 0), pb = b + (p == 1 ? kTileBytes : 0);
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk) {
       const uint32_t at = kk / 4 * kPart + kk % 4 * 32;
-      mma_bf16(d, sw128_desc(pa + at, 16, 1024), sw128_desc(pb + at, 16, 1024), id, p > 0 || kk > 0);
+      const int n0 = kk * 16 & ~(width - 1);  // the block's first row of B, column of D
+      mma_bf16(d + n0, sw128_desc(pa + at, 16, 1024), sw128_desc(pb + at + n0 * 128, 16, 1024), id, p > 0 || kk * 16 > n0);
     }
   }
 }
@@ -489,171 +492,215 @@ __device__ __forceinline__ void tmem_put_row32(uint32_t base, int col, const flo
 }
 
 // `first`: G is of the update itself, whose norm is taken here.  Otherwise G is of X in the
-// scratch, times kXScale^2.
-__global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid_constant__ MuonTable tab, int steps, bool first) {
+// scratch, times kXScale^2.  Blocks work through tiles one after the other; the sums of the next are on
+// their way while the last product of one runs.  Where all matrices of a tile have s = 64 or less, most of
+// a square tile is 0: only warps whose rows and columns meet a matrix work on it.
+__global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid_constant__ MuonTable tab, int tiles, int steps, bool first) {
+  constexpr int kEach = kTile * kTile / 4 / kPolyThreads;
   extern __shared__ uint8_t muon_smem[];
-  __shared__ uint64_t done;
+  __shared__ uint64_t done[2];
   __shared__ uint32_t slot;
   __shared__ float diag[kTile];
   uint8_t* sm = aligned_smem(muon_smem);
   uint8_t *qt = sm, *gt = sm + kPoly, *pt = sm + 2 * kPoly;
-  const int tile = blockIdx.x;
-  int ti = 0;
-  while (ti + 1 < tab.n && tile >= tab.t[ti + 1].tile0) ++ti;
-  const MuonTensor& t = tab.t[ti];
-  const int rows = (int)min((int64_t)t.per, t.batch - (int64_t)(tile - t.tile0) * t.per) * t.s;
   const int row = my_row(), col = my_part() * 32;
-  // the columns [lo, hi) of this thread's 32 that belong to its row's matrix
-  const int block = row < rows ? row / t.s * t.s : kTile;
-  const int lo = block - col, hi = min(block + t.s, rows) - col;
-  const bool whole = t.s == kTile;
-  const auto scaled = [&](float (&v)[32], float f) {  // times f, and 0 outside the matrix
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float2 x = mul2(make_float2(v[i], v[i + 1]), both(f));
-      v[i] = x.x;
-      v[i + 1] = x.y;
-    }
-    if (!whole)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = i >= lo && i < hi ? v[i] : 0.f;
-  };
   if (threadIdx.x == 0) {
-    mbar_init(&done, 1);
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
     fence_mbar_init();
   }
   launch_next();
   const uint32_t tmem = tmem_open(&slot, kPolyCols);
   const uint32_t g_at = tmem, x_at = tmem + kTile, p_at = tmem + 2 * kTile;  // G, another product, P
   Waits wait{tab.err};
-  wait_for_last();
-  // G: the stretches' sums in order, then with the transpose, through shared memory
-  float v[32];
-  {
-    constexpr int kEach = kTile * kTile / 4 / kPolyThreads;
+  uint32_t phase[2] = {0, 0};
+  const uint32_t qa = smem_u32(qt), ga = smem_u32(gt), pa = smem_u32(pt);
+  const float ka = tab.a * kQScale, kb = tab.b * (kQScale / kGScale), kc = tab.c * (kQScale / (kGScale * kGScale));
+  const auto tensor_of = [&](int tile) {
+    int ti = 0;
+    while (ti + 1 < tab.n && tile >= tab.t[ti + 1].tile0) ++ti;
+    return ti;
+  };
+  // This thread's share of the sums of a tile's stretches, in order.
+  float4 sum[kEach];
+  const auto load_sums = [&](int tile) {
+    const MuonTensor& t = tab.t[tensor_of(tile)];
     const int x = t.chunk0 + (tile - t.tile0) * t.chunks;
     const int64_t s0 = stretch_slot(tab, tile, x);
     const int stretches = (int)(stretch_slot(tab, tile, x + t.chunks - 1) - s0) + 1;
     const float4* in = reinterpret_cast<const float4*>(tab.gram + s0 * kTile * kTile) + threadIdx.x;
-    float4 sum[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kEach; ++i) sum[i] = in[i * kPolyThreads];
 #pragma unroll 2
-    for (int p = 0; p < stretches; ++p)
+    for (int p = 1; p < stretches; ++p)
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const float4 u = in[p * (kTile * kTile / 4) + i * kPolyThreads];
         sum[i] = make_float4(sum[i].x + u.x, sum[i].y + u.y, sum[i].z + u.z, sum[i].w + u.w);
       }
-    float* e = reinterpret_cast<float*>(qt);
+  };
+  wait_for_last();
+  load_sums(blockIdx.x);
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const MuonTensor& t = tab.t[tensor_of(tile)];
+    const int rows = (int)min((int64_t)t.per, t.batch - (int64_t)(tile - t.tile0) * t.per) * t.s;
+    // the columns [lo, hi) of this thread's 32 that belong to its row's matrix
+    const int block = row < rows ? row / t.s * t.s : kTile;
+    const int lo = block - col, hi = min(block + t.s, rows) - col;
+    const bool whole = t.s == kTile;
+    const bool even = (t.s & (t.s - 1)) == 0;  // matrices that fill blocks of 16, 32, 64 or 128
+    const int width = even ? max(t.s, 16) : kTile;
+    // whether any of this warp's rows meets any of its columns
+    const int r0 = row & ~31;
+    const bool busy = width == kTile || (col < (r0 & ~(width - 1)) + max(width, 32) && col + 32 > (r0 & ~(width - 1)));
+    const auto scaled = [&](float (&v)[32], float f) {  // times f, and 0 outside the matrix
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int at = (threadIdx.x + i * kPolyThreads) * 4;
-      float* to = e + at / kTile * (kTile + 1) + at % kTile;
-      to[0] = sum[i].x;
-      to[1] = sum[i].y;
-      to[2] = sum[i].z;
-      to[3] = sum[i].w;
+      for (int i = 0; i < 32; i += 2) {
+        const float2 x = mul2(make_float2(v[i], v[i + 1]), both(f));
+        v[i] = x.x;
+        v[i + 1] = x.y;
+      }
+      if (!whole)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i >= lo && i < hi ? v[i] : 0.f;
+    };
+    // Runs products issued by one thread; operands are in shared memory.  begin and end apart: the second
+    // of two is under way while the first one's result is used.
+    const auto begin = [&] {
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (threadIdx.x == 0) tc_fence_after();
+    };
+    const auto product = [&](int bar, uint32_t d, uint32_t a, uint32_t b) {
+      if (threadIdx.x == 0) {
+        square_product(d, a, b, width);
+        mma_commit(&done[bar]);
+      }
+    };
+    const auto end = [&](int bar) {
+      wait(&done[bar], phase[bar]);
+      phase[bar] ^= 1;
+    };
+    // G: the sums and their transpose meet in shared memory
+    float v[32];
+    {
+      float* e = reinterpret_cast<float*>(qt);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int at = (threadIdx.x + i * kPolyThreads) * 4;
+        float* to = e + at / kTile * (kTile + 1) + at % kTile;
+        to[0] = sum[i].x;
+        to[1] = sum[i].y;
+        to[2] = sum[i].z;
+        to[3] = sum[i].w;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = e[row * (kTile + 1) + col + i] + e[(col + i) * (kTile + 1) + row];
     }
-    __syncthreads();
+    float unit = 1.f / (kXScale * kXScale);  // X in the scratch is scaled
+    bool fine = true;
+    if (first) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = e[row * (kTile + 1) + col + i] + e[(col + i) * (kTile + 1) + row];
-    __syncthreads();
-  }
-  float unit = 1.f / (kXScale * kXScale);  // X in the scratch is scaled
-  bool fine = true;
-  if (first) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i == row) diag[row] = v[i];
-    __syncthreads();
-    float n2 = 0.f;
-    for (int i = max(lo, -col); i < hi; ++i) n2 += diag[col + i];
-    // a norm whose square fp32 does not hold: 0, or not finite, which is passed on as NaN
-    fine = n2 < INFINITY;
-    const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
-    // X = u / (norm + eps) = (u * up) * down, up a power of two that makes the matrix's norm 2^9 to 2^10
-    const float up = norm > 0.f ? ldexpf(1.f, 9 - ilogbf(norm)) : 0.f;
-    unit = norm > 0.f ? inv * inv : 0.f;
-    if (my_part() == 0) {
-      tab.norm[(int64_t)tile * 2 * kTile + row] = up;
-      tab.norm[(int64_t)tile * 2 * kTile + kTile + row] = !fine ? NAN : norm > 0.f ? inv / up : 0.f;
+      for (int i = 0; i < 32; ++i)
+        if (col + i == row) diag[row] = v[i];
+      __syncthreads();
+      float n2 = 0.f;
+      for (int i = lo; i < hi; ++i) n2 += diag[col + i];
+      // a norm whose square fp32 does not hold: 0, or not finite, which is passed on as NaN
+      fine = n2 < INFINITY;
+      const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
+      // X = u / (norm + eps) = (u * up) * down, up a power of two that makes the matrix's norm 2^9 to 2^10
+      const float up = norm > 0.f ? ldexpf(1.f, 9 - ilogbf(norm)) : 0.f;
+      unit = norm > 0.f ? inv * inv : 0.f;
+      if (my_part() == 0) {
+        tab.norm[(int64_t)tile * 2 * kTile + row] = up;
+        tab.norm[(int64_t)tile * 2 * kTile + kTile + row] = !fine ? NAN : norm > 0.f ? inv / up : 0.f;
+      }
     }
-  }
-  if (!fine)
+    if (!fine)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-  // all matrices are held times their scales from here on
-  scaled(v, unit * kGScale);
-  tmem_put_row32(g_at, col, v);
-  uint32_t phase = 0;
-  // Runs products issued by one thread; operands are in shared memory.
-  const auto products = [&](auto issue) {
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    // all matrices are held times their scales from here on
+    scaled(v, unit * kGScale);
+    if (threadIdx.x == 0) bulk_wait_group_read<0>();  // the last tile's P
+    __syncthreads();                                   // and all have read the sums
+    if (busy) tmem_put_row32(g_at, col, v);
+    put_row32(gt, v);
+    if (!busy) {  // what stays 0 is written once
+      put_row32(qt, v);
+      put_row32(pt, v);
+    }
+    if (steps == 0) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = col + i == row ? kQScale : 0.f;
+      scaled(v, 1.f);
+      put_row32(pt, v);
+    }
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+      const bool last = k == steps - 1;
+      begin();
+      product(0, x_at, ga, ga);
+      if (last && tile + gridDim.x < tiles) load_sums(tile + gridDim.x);
+      end(0);
+      if (busy) {
+        float g[32];
+        tmem_row32(g_at, col, g);
+        tmem_row32(x_at, col, v);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 x = fma2(both(kc), make_float2(v[i], v[i + 1]), mul2(both(kb), make_float2(g[i], g[i + 1])));
+          v[i] = x.x + (col + i == row ? ka : 0.f);
+          v[i + 1] = x.y + (col + i + 1 == row ? ka : 0.f);
+        }
+        if (!whole) scaled(v, 1.f);
+        put_row32(qt, v);
+        if (k == 0) put_row32(pt, v);
+      }
+      if (last && k == 0) break;
+      begin();
+      if (!last) product(0, x_at, qa, ga);
+      if (k > 0) product(1, p_at, qa, pa);
+      if (!last) {
+        end(0);
+        if (busy) {
+          tmem_row32(x_at, col, v);
+          scaled(v, 1.f / kQScale);
+          put_row32(gt, v);
+        }
+      }
+      if (k > 0) {
+        end(1);
+        if (busy) {
+          tmem_row32(p_at, col, v);
+          scaled(v, 1.f / kQScale);
+          put_row32(pt, v);
+        }
+      }
+      if (last) break;
+      begin();
+      product(0, x_at, qa, ga);
+      end(0);
+      if (busy) {
+        tmem_row32(x_at, col, v);
+        scaled(v, 1.f / kQScale);
+        tmem_put_row32(g_at, col, v);
+        put_row32(gt, v);
+      }
+    }
+    if (steps == 0 && tile + gridDim.x < tiles) load_sums(tile + gridDim.x);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     if (threadIdx.x == 0) {
-      tc_fence_after();
-      issue();
-      mma_commit(&done);
+      bulk_store(tab.poly + (int64_t)tile * kPoly, pt, kPoly);
+      bulk_commit_group();
     }
-    wait(&done, phase);
-    phase ^= 1;
-  };
-  const uint32_t qa = smem_u32(qt), ga = smem_u32(gt), pa = smem_u32(pt);
-  put_row32(gt, v);
-  if (steps == 0) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = col + i == row ? kQScale : 0.f;
-    scaled(v, 1.f);
-    put_row32(pt, v);
   }
-  const float ka = tab.a * kQScale, kb = tab.b * (kQScale / kGScale), kc = tab.c * (kQScale / (kGScale * kGScale));
-#pragma unroll 1
-  for (int k = 0; k < steps; ++k) {
-    products([&] { square_product(x_at, ga, ga); });
-    {
-      float g[32];
-      tmem_row32(g_at, col, g);
-      tmem_row32(x_at, col, v);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 x = fma2(both(kc), make_float2(v[i], v[i + 1]), mul2(both(kb), make_float2(g[i], g[i + 1])));
-        v[i] = x.x + (col + i == row ? ka : 0.f);
-        v[i + 1] = x.y + (col + i + 1 == row ? ka : 0.f);
-      }
-      if (!whole) scaled(v, 1.f);
-    }
-    put_row32(qt, v);
-    if (k == 0) put_row32(pt, v);
-    const bool last = k == steps - 1;
-    if (last && k == 0) break;
-    products([&] {
-      if (!last) square_product(x_at, qa, ga);
-      if (k > 0) square_product(p_at, qa, pa);
-    });
-    if (k > 0) {
-      tmem_row32(p_at, col, v);
-      scaled(v, 1.f / kQScale);
-      put_row32(pt, v);
-    }
-    if (last) break;
-    tmem_row32(x_at, col, v);
-    scaled(v, 1.f / kQScale);
-    put_row32(gt, v);
-    products([&] { square_product(x_at, qa, ga); });
-    tmem_row32(x_at, col, v);
-    scaled(v, 1.f / kQScale);
-    tmem_put_row32(g_at, col, v);
-    put_row32(gt, v);
-  }
-  fence_proxy_async_smem();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    bulk_store(tab.poly + (int64_t)tile * kPoly, pt, kPoly);
-    bulk_commit_group();
-    bulk_wait_group<0>();
-  }
+  if (threadIdx.x == 0) bulk_wait_group<0>();
   tmem_close(tmem, kPolyCols);
 }
 
@@ -997,7 +1044,7 @@ int launch_muon(int slot, K kernel, int64_t grid, int threads, size_t smem, bool
 }
 
 // The five launches over up to kMaxTensors tensors.
-int run_muon(const moe_lora_muon* o, const moe_lora_muon_tensor* in, int n, uint8_t* ws, cudaStream_t s) {
+int run_muon(const moe_lora_muon* o, const moe_lora_muon_tensor* in, int n, uint8_t* ws, int sms, cudaStream_t s) {
   const Layout l = layout_of(in, n);
   if (l.tiles == 0) return MOE_LORA_OK;
   MuonTable tab;
@@ -1031,9 +1078,9 @@ int run_muon(const moe_lora_muon* o, const moe_lora_muon_tensor* in, int n, uint
   const int first = std::min(kFirstSteps, o->steps > 3 ? 2 : 1);
   int rc;
   if ((rc = launch_muon(K_MUON_GRAM, muon_gram_kernel, l.blocks, kThreads, kGramSmem, false, s, tab)) ||
-      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, l.tiles, kPolyThreads, kPolySmem, true, s, tab, first, true)) ||
+      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, std::min<int64_t>(l.tiles, sms), kPolyThreads, kPolySmem, true, s, tab, (int)l.tiles, first, true)) ||
       (rc = launch_muon(K_MUON_APPLY, muon_apply_kernel, l.blocks, kThreads, kApplySmem, true, s, tab)) ||
-      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, l.tiles, kPolyThreads, kPolySmem, true, s, tab, o->steps - first, false)))
+      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, std::min<int64_t>(l.tiles, sms), kPolyThreads, kPolySmem, true, s, tab, (int)l.tiles, o->steps - first, false)))
     return rc;
   bool overlap = true;  // the first kind's launch with what is before it; the others follow it as any launch does
   const auto update = [&](auto kernel, int dtype, bool master) {
@@ -1088,7 +1135,7 @@ extern "C" int moe_lora_muon_step(const moe_lora_muon* o, const moe_lora_muon_te
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int i = 0; i < n; i += kMaxTensors)
-    if ((rc = run_muon(o, tensors + i, std::min(kMaxTensors, n - i), static_cast<uint8_t*>(scratch), s))) return rc;
+    if ((rc = run_muon(o, tensors + i, std::min(kMaxTensors, n - i), static_cast<uint8_t*>(scratch), sms, s))) return rc;
   return MOE_LORA_OK;
 }
 

@@ -334,14 +334,12 @@ __device__ __forceinline__ void sum_terms_here(const float* terms, int64_t strid
     }
   }
 }
-// Notes that this warp's terms are written; true for all lanes of the warp that came last of `all`.
+// Notes that this warp's terms are written (by its first lane); true for all lanes of the warp that
+// came last of `all`.
 __device__ __forceinline__ bool came_last(unsigned* ticket, unsigned all) {
   unsigned at = 0;
-  if ((threadIdx.x & 31) == 0) {
-    __threadfence();
-    at = atomicInc(ticket, all - 1);  // back to 0 after the last
-    __threadfence();
-  }
+  if ((threadIdx.x & 31) == 0)  // back to 0 after the last
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(at) : "l"(ticket), "r"(all - 1) : "memory");
   return __shfl_sync(0xffffffffu, at, 0) == all - 1;
 }
 __device__ __forceinline__ int live_in(const int32_t* targets, int n, int64_t lo, int64_t hi) {
@@ -748,6 +746,9 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
     off[j] = at;
   }
   if (bad && g.err && threadIdx.x == 0) atomicOr(g.err, MOE_LORA_DEV_BAD_ID);
+  // asked for early, used late
+  const int a = range_of(ad, i);
+  const float ref[2] = {g.ref ? g.ref[2 * i] : 0.f, g.ref ? g.ref[2 * i + 1] : 0.f}, up = g.dloss ? g.dloss[a] : 1.f;
   const int64_t base = off[0] & ~(int64_t)3;
   const int64_t vecs = (off[2] - base + 3) / 4;  // of four tokens, on 16 bytes; the first and last may be partly outside
   const auto load_mask = [&](int64_t v, float (&x)[4]) {  // live tokens of a vector that belong to the pair, and their values
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
       cnt[q] = g.average ? (float)max(k, 1) : 1.f;
       if (g.average) r[q] = r[q].over(cnt[q]);
       if (g.seq_logp && lane == 0) g.seq_logp[2 * i + q] = r[q].value();
-      if (g.ref) r[q].add(-g.ref[2 * i + q]);
+      if (g.ref) r[q].add(-ref[q]);
     }
     Long d = r[0];
     d.add(Long{-r[1].hi, -r[1].lo});
@@ -834,7 +835,6 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
       dh = x < 1.f ? -g.beta : 0.f;
     }
     if (isnan(x)) loss = dh = x;
-    const int a = range_of(ad, i);
     if (lane == 0) {
       float* to = g.terms + i;
       to[0] = loss;
@@ -842,9 +842,9 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
       to[2 * g.pairs] = g.beta * r[0].value();
       to[3 * g.pairs] = g.beta * r[1].value();
       to[4 * g.pairs] = h;
-      const float up = (g.dloss ? g.dloss[a] : 1.f) / (float)(ad.off[a + 1] - ad.off[a]);
-      per_token[0] = up * dh / cnt[0];
-      per_token[1] = -up * dh / cnt[1];
+      const float each = up / (float)(ad.off[a + 1] - ad.off[a]);
+      per_token[0] = each * dh / cnt[0];
+      per_token[1] = -each * dh / cnt[1];
     }
   }
   if (g.dlogp) {
