@@ -496,7 +496,7 @@ __device__ __forceinline__ void tmem_put_row32(uint32_t base, int col, const flo
 // their way while the last product of one runs.  Where all matrices of a tile have s = 64 or less, most of
 // a square tile is 0: only warps whose rows and columns meet a matrix work on it.
 __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid_constant__ MuonTable tab, int tiles, int steps, bool first) {
-  constexpr int kEach = kTile * kTile / 4 / kPolyThreads;
+  constexpr int kEach = kTile * kTile / kPolyThreads;
   extern __shared__ uint8_t muon_smem[];
   __shared__ uint64_t done[2];
   __shared__ uint32_t slot;
@@ -522,22 +522,18 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
     return ti;
   };
   // This thread's share of the sums of a tile's stretches, in order.
-  float4 sum[kEach];
+  float sum[kEach];
   const auto load_sums = [&](int tile) {
     const MuonTensor& t = tab.t[tensor_of(tile)];
     const int x = t.chunk0 + (tile - t.tile0) * t.chunks;
     const int64_t s0 = stretch_slot(tab, tile, x);
     const int stretches = (int)(stretch_slot(tab, tile, x + t.chunks - 1) - s0) + 1;
-    const float4* in = reinterpret_cast<const float4*>(tab.gram + s0 * kTile * kTile) + threadIdx.x;
+    const float* in = tab.gram + s0 * kTile * kTile + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) sum[i] = in[i * kPolyThreads];
-#pragma unroll 2
     for (int p = 1; p < stretches; ++p)
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const float4 u = in[p * (kTile * kTile / 4) + i * kPolyThreads];
-        sum[i] = make_float4(sum[i].x + u.x, sum[i].y + u.y, sum[i].z + u.z, sum[i].w + u.w);
-      }
+      for (int i = 0; i < kEach; ++i) sum[i] += in[p * kTile * kTile + i * kPolyThreads];
   };
   wait_for_last();
   load_sums(blockIdx.x);
@@ -586,15 +582,9 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
     float v[32];
     {
       float* e = reinterpret_cast<float*>(qt);
+      float* to = e + threadIdx.x / kTile * (kTile + 1) + threadIdx.x % kTile;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int at = (threadIdx.x + i * kPolyThreads) * 4;
-        float* to = e + at / kTile * (kTile + 1) + at % kTile;
-        to[0] = sum[i].x;
-        to[1] = sum[i].y;
-        to[2] = sum[i].z;
-        to[3] = sum[i].w;
-      }
+      for (int i = 0; i < kEach; ++i) to[i * (kPolyThreads / kTile) * (kTile + 1)] = sum[i];
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = e[row * (kTile + 1) + col + i] + e[(col + i) * (kTile + 1) + row];
@@ -607,7 +597,14 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
         if (col + i == row) diag[row] = v[i];
       __syncthreads();
       float n2 = 0.f;
-      for (int i = lo; i < hi; ++i) n2 += diag[col + i];
+      if (whole) {
+        for (int i = threadIdx.x & 31; i < kTile; i += 32) n2 += diag[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      } else {
+#pragma unroll 8
+        for (int i = lo; i < hi; ++i) n2 += diag[col + i];
+      }
       // a norm whose square fp32 does not hold: 0, or not finite, which is passed on as NaN
       fine = n2 < INFINITY;
       const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
