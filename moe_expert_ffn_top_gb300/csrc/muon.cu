@@ -118,87 +118,99 @@ __device__ __forceinline__ Place place_of(const MuonTable& tab, int x, int end) 
 // ------------------------------------------------------------------ a thread's share of a chunk
 // A thread's quads of a chunk, four neighbouring elements in memory each.  Of [s, L]: along the
 // long side, 16 to a row.  Of tall matrices [L, s]: along the short side; a warp's 32 are one run of
-// memory where s is a power of two (128 / s long places of one matrix), and otherwise a long place of
-// all matrices of the tile.  With the latter for s = 8 too, whose runs are then 16 or 32 bytes, 38.6 M
-// elements took 488 us instead of XXX.  Steps from quad to quad and from chunk to chunk are the same
-// throughout, divisions are done once.
+// memory where s is a power of two from 8 on (128 / s long places of one matrix), and otherwise a long
+// place of all matrices of the tile.  (That for s = 8 too, in runs of 16 or 32 bytes: 38.6 M elements
+// 488 us instead of 437.)  Divisions are done once: quad i is i % 4 short and i / 4 long steps from quad 0.
 struct Walk {
-  int64_t at, hop, chunk;     // element of quad 0 in chunk 0 of the tile; to the next quad, chunk
-  int row, col;               // of quad 0: short side within the tile, long side within the chunk
-  int hop_row, hop_col;       // one of them is 0
+  int64_t at, hop, hop4, chunk;  // element of quad 0 in chunk 0 of the tile; the steps, and to the next chunk
+  int row, col;                  // of quad 0: short side within the tile, long side within the chunk
+  int hop_row, hop_col, hop_row4, hop_col4;
+  uint32_t place, hop_place;     // bytes in a part of an operand tile, where all steps are the same
+  uint32_t whole;                // quads of a whole chunk that lie inside, a bit each
   int rows, L;
-  bool tall;
-  __device__ __forceinline__ Walk(const MuonTensor& t, int64_t first, int rows_) : rows(rows_), L(t.L), tall(t.tall) {
+  // Operand tiles have rows of 128 bytes whose 16-byte units are exchanged by row (unit ^ row % 8).
+  // A chunk of [s, L]: 128 rows of 64 long places.  Of [L, s]: two halves of 64 short places, a
+  // row per long place.  No step changes row % 8 or the unit.
+  __device__ __forceinline__ Walk(const MuonTensor& t, int64_t first, int rows_) : rows(rows_), L(t.L) {
     constexpr int kWarps = kThreads / 32;
     const int64_t base = first * t.s * t.L;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    hop_row = hop_col = 0;
-    if (!tall) {
+    hop_row = hop_col = hop_row4 = 0;
+    int line, k;
+    if (!t.tall) {
       row = threadIdx.x >> 4;
       col = (threadIdx.x & 15) * 4;
       hop_row = kThreads / 16;
+      hop_row4 = 4 * hop_row;
+      hop_col4 = 0;
+      hop_place = hop_row * 128;
       at = base + (int64_t)row * L + col;
+      line = row, k = col;
     } else {
       int j, r;  // matrix, and place on its short side
-      if (t.s >= 4 && (t.s & (t.s - 1)) == 0) {
-        const int places = kTile / t.s, runs = kChunk / places, mats = kTile / t.s;  // of a run; of a matrix; of the tile
+      if (t.s >= 8 && (t.s & (t.s - 1)) == 0) {
+        const int places = kTile / t.s, mats = min(places, kWarps);  // of a run; matrices that the warps take side by side
         r = lane * 4 % t.s;
-        col = lane * 4 / t.s;
-        if (mats <= kWarps) {
-          j = warp % mats;
-          col += warp / mats * places;
-          hop_col = kWarps / mats * places;
-        } else {
-          j = warp / runs;
-          col += warp % runs * places;
-          hop_row = kWarps / runs * t.s;
-        }
+        j = warp % mats;
+        col = lane * 4 / t.s + warp / mats * places;
+        hop_col = kWarps / mats * places;
       } else {
         j = lane * 4 / t.s;
         r = lane * 4 - j * t.s;
         col = warp;
         hop_col = kWarps;
       }
+      hop_col4 = 4 * hop_col;
+      if (hop_col4 == kChunk) {  // s = 8: four steps go through the chunk, the other four take the other half
+        hop_col4 = 0;
+        hop_row4 = kTile / 2;
+      }
+      hop_place = hop_col * 128;
       row = j * t.s + r;
       at = base + ((int64_t)j * L + col) * t.s + r;
+      line = col, k = row % 64;
     }
-    hop = hop_row ? (int64_t)hop_row * L : (int64_t)hop_col * t.s;
-    chunk = tall ? (int64_t)kChunk * t.s : kChunk;
+    place = line * 128 + ((((k >> 3) ^ (line & 7)) << 4) | ((k & 4) << 1)) + (t.tall ? row / 64 * (kPart / 2) : 0);
+    hop = (int64_t)hop_row * L + (int64_t)hop_col * t.s;
+    hop4 = (int64_t)hop_row4 * L + (int64_t)hop_col4 * t.s;
+    chunk = t.tall ? (int64_t)kChunk * t.s : kChunk;
+    whole = 0;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) whole |= (uint32_t)(row_of(i) < rows) << i;
   }
-  // Bytes of quad i in a part of an operand tile.  These have rows of 128 bytes whose 16-byte units are
-  // exchanged by row (unit ^ row % 8).  A chunk of [s, L]: 128 rows of 64 long places.  Of [L, s]: two
-  // halves of 64 short places, a row per long place.
-  __device__ __forceinline__ uint32_t operand(int i) const {
-    const int r = row + i * hop_row, c = col + i * hop_col;
-    const uint32_t line = tall ? c : r, k = tall ? r % 64 : c, half = tall ? r / 64 * (kPart / 2) : 0;
-    return half + line * 128 + ((((k >> 3) ^ (line & 7)) << 4) | ((k & 4) << 1));
-  }
-  // How many of the quads of chunk c lie inside, where quads lie inside or outside as a whole.
-  __device__ __forceinline__ int inside(int c) const {
-    const int l = L - c * kChunk - col, r = rows - row;
-    if (hop_row) return l <= 0 || r <= 0 ? 0 : min(kQuads, (r + hop_row - 1) / hop_row);
-    return l <= 0 || r <= 0 ? 0 : min(kQuads, (l + hop_col - 1) / hop_col);
+  __device__ __forceinline__ int64_t element(int i) const { return (i & 3) * hop + (i >> 2) * hop4; }  // from quad 0
+  __device__ __forceinline__ int row_of(int i) const { return row + (i & 3) * hop_row + (i >> 2) * hop_row4; }
+  __device__ __forceinline__ int col_of(int i) const { return col + (i & 3) * hop_col + (i >> 2) * hop_col4; }
+  __device__ __forceinline__ uint32_t operand(int i) const { return place + i * hop_place; }
+  // The same of chunk c, where quads lie inside or outside as a whole.
+  __device__ __forceinline__ uint32_t inside(int c) const {
+    const int l = L - c * kChunk;
+    if (l >= kChunk) return whole;
+    uint32_t in = 0;
+#pragma unroll 1
+    for (int i = 0; i < kQuads; ++i) in |= (uint32_t)(col_of(i) < l) << i;
+    return in & whole;
   }
 };
 // Whether quads lie inside one matrix's run of memory, and on 16 bytes (8 of 16-bit types).
 __device__ __forceinline__ bool quads_aligned(const MuonTensor& t) { return t.tall ? t.s % 4 == 0 : t.L % 4 == 0; }
 // Element e of quad i elsewhere: its offset, or -1 outside.
 __device__ __forceinline__ int64_t element_at(const MuonTensor& t, const Walk& w, int64_t first, int c, int i, int e) {
-  const int row = w.row + i * w.hop_row + (t.tall ? e : 0), l = c * kChunk + w.col + i * w.hop_col + (t.tall ? 0 : e);
+  const int row = w.row_of(i) + (t.tall ? e : 0), l = c * kChunk + w.col_of(i) + (t.tall ? 0 : e);
   if (row >= w.rows || l >= t.L) return -1;
   const int j = row / t.s, r = row - j * t.s;
   return (first + j) * t.s * t.L + (t.tall ? (int64_t)l * t.s + r : (int64_t)r * t.L + l);
 }
 
+struct Four {
+  float2 a, b;
+};
 template <int kType>
 __device__ __forceinline__ uint4 ld_quad(const void* p, int64_t i) {
   if (kType == MOE_LORA_F32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
   const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
   return make_uint4(u.x, u.y, 0, 0);
 }
-struct Four {
-  float2 a, b;
-};
 template <int kType>
 __device__ __forceinline__ Four widen(const uint4& u) {
   if constexpr (kType == MOE_LORA_F32) return Four{Two<float>::get(&u.x), Two<float>::get(&u.z)};
@@ -228,39 +240,54 @@ __device__ __forceinline__ void st_one(void* p, int64_t i, float v) {
   static_cast<E*>(p)[i] = from_f32<E>(v);
 }
 
+// A pointer in registers: the table's own lie in the constant bank, and reading one again for every
+// quad held the warps up.
+template <class P>
+__device__ __forceinline__ P* in_register(P* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
 // The gradient and momentum of a thread's quads of a chunk, on their way: the next chunk's take a
 // quad's place as soon as it is used.
-struct Loads {
-  uint4 g[kQuads], m[kQuads];
-};
 template <int kType>
-__device__ __forceinline__ void load_quad(const Place& pl, const Walk& w, int c, int i, int n, bool aligned, bool with_g, Loads& ld) {
-  const MuonTensor& t = *pl.t;
-  ld.g[i] = ld.m[i] = make_uint4(0, 0, 0, 0);
-  if (aligned) {
-    if (i < n) {
-      const int64_t at = w.at + c * w.chunk + i * w.hop;
-      if (with_g) ld.g[i] = ld_quad<kType>(t.g, at);
-      ld.m[i] = ld_quad<MOE_LORA_F32>(t.m, at);
+struct Loads {
+  const void* gp;
+  const float* mp;
+  uint4 g[kQuads], m[kQuads];
+  __device__ __forceinline__ explicit Loads(const MuonTensor& t) : gp(in_register(t.g)), mp(in_register(t.m)) {}
+  __device__ __forceinline__ void quad(int64_t at, int i, bool in, bool with_g) {
+    g[i] = m[i] = make_uint4(0, 0, 0, 0);
+    if (in) {
+      if (with_g) g[i] = ld_quad<kType>(gp, at);
+      m[i] = ld_quad<MOE_LORA_F32>(mp, at);
     }
-    return;
   }
-  uint32_t g[4] = {}, m[4] = {};  // element by element, 16-bit ones packed again
+  __device__ __forceinline__ void chunk(const Walk& w, int c, bool with_g) {
+    const uint32_t in = w.inside(c);
+    const int64_t at = w.at + c * w.chunk;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) quad(at + w.element(i), i, in >> i & 1, with_g);
+  }
+};
+// Four elements of a quad that does not lie on 16 bytes or within one matrix.
+template <int kType>
+__device__ __forceinline__ Four ld_loose(const void* p, const MuonTensor& t, const Walk& w, int64_t first, int c, int i) {
+  float f[4] = {};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int64_t at = element_at(t, w, pl.first, c, i, e);
-    if (at < 0) continue;
-    m[e] = __float_as_uint(t.m[at]);
-    if (with_g) g[e] = kType == MOE_LORA_F32 ? static_cast<const uint32_t*>(t.g)[at] : static_cast<const uint16_t*>(t.g)[at];
+    const int64_t at = element_at(t, w, first, c, i, e);
+    if (at >= 0) f[e] = ld_one<kType>(p, at);
   }
-  ld.m[i] = make_uint4(m[0], m[1], m[2], m[3]);
-  ld.g[i] = kType == MOE_LORA_F32 ? make_uint4(g[0], g[1], g[2], g[3]) : make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, 0, 0);
+  return Four{make_float2(f[0], f[1]), make_float2(f[2], f[3])};
 }
 template <int kType>
-__device__ __forceinline__ void load_chunk(const Place& pl, const Walk& w, int c, bool aligned, bool with_g, Loads& ld) {
-  const int n = w.inside(c);
+__device__ __forceinline__ void st_loose(void* p, const MuonTensor& t, const Walk& w, int64_t first, int c, int i, const Four& v) {
+  const float f[4] = {v.a.x, v.a.y, v.b.x, v.b.y};
 #pragma unroll
-  for (int i = 0; i < kQuads; ++i) load_quad<kType>(pl, w, c, i, n, aligned, with_g, ld);
+  for (int e = 0; e < 4; ++e) {
+    const int64_t at = element_at(t, w, first, c, i, e);
+    if (at >= 0) st_one<kType>(p, at, f[e]);
+  }
 }
 // mu m + nu g
 __device__ __forceinline__ Four mix(float mu, const Four& m, float nu, const Four& g) {
@@ -336,15 +363,22 @@ __device__ __forceinline__ int my_part() { return threadIdx.x >> 7; }  // of the
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// f(integral constant of the tensor's type)
+// f(integral constant of the tensor's type, constant of whether its quads are aligned): a loop of its
+// own for each, small enough for the instruction caches
 template <class F>
-__device__ __forceinline__ void with_type(int dtype, F f) {
+__device__ __forceinline__ void with_kind(int dtype, bool aligned, F f) {
+  const auto typed = [&](auto type) {
+    if (aligned)
+      f(type, std::true_type{});
+    else
+      f(type, std::false_type{});
+  };
   if (dtype == MOE_LORA_F32)
-    f(std::integral_constant<int, MOE_LORA_F32>{});
+    typed(std::integral_constant<int, MOE_LORA_F32>{});
   else if (dtype == MOE_LORA_BF16)
-    f(std::integral_constant<int, MOE_LORA_BF16>{});
+    typed(std::integral_constant<int, MOE_LORA_BF16>{});
   else
-    f(std::integral_constant<int, MOE_LORA_F16>{});
+    typed(std::integral_constant<int, MOE_LORA_F16>{});
 }
 
 // ------------------------------------------------------------------ gram
@@ -369,39 +403,43 @@ __global__ void __launch_bounds__(kThreads, 2) muon_gram_kernel(const __grid_con
   for (int x = first_chunk(tab, blockIdx.x); x < end;) {
     const Place pl = place_of(tab, x, end);
     const MuonTensor& t = *pl.t;
-    const bool aligned = quads_aligned(t), tall = t.tall;
+    const bool tall = t.tall;
     const Walk w(t, pl.first, pl.rows);
-    with_type(t.g_dtype, [&](auto type) {
+    with_kind(t.g_dtype, quads_aligned(t), [&](auto type, auto quads) {
       constexpr int kType = decltype(type)::value;
-      Loads ld;
-      load_chunk<kType>(pl, w, pl.c0, aligned, true, ld);
+      constexpr bool kAligned = decltype(quads)::value;
+      Loads<kType> ld(t);
+      float* const mp = in_register(t.m);
+      if (kAligned) ld.chunk(w, pl.c0, true);
       for (int c = pl.c0; c < pl.c1; ++c, ++used) {
         const int st = used % kGramStages;
         uint8_t* part = sm + st * 3 * kPart;
         if (used >= kGramStages) wait(&done[st], (used / kGramStages - 1) & 1);
-        const int n = w.inside(c), next = c + 1 < pl.c1 ? w.inside(c + 1) : 0;
-        const int64_t at = w.at + c * w.chunk;
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const Four g = widen<kType>(ld.g[i]);
-          const Four m = mix(tab.mu, widen<MOE_LORA_F32>(ld.m[i]), nu, g);
-          if (c + 1 < pl.c1) load_quad<kType>(pl, w, c + 1, i, next, aligned, true, ld);
-          if (aligned) {
-            if (i < n) st_quad<MOE_LORA_F32>(t.m, at + i * w.hop, m);
-          } else {
-            const float y[4] = {m.a.x, m.a.y, m.b.x, m.b.y};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int64_t to = element_at(t, w, pl.first, c, i, e);
-              if (to >= 0) t.m[to] = y[e];
-            }
-          }
+        const auto put = [&](int i, const Four& g, const Four& m) {
           Four u = tab.nesterov ? mix(tab.mu, m, nu, g) : m;
           uint8_t* to = part + w.operand(i);
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
             const uint32_t a = take_bf16(u.a), b = take_bf16(u.b);
             *reinterpret_cast<uint2*>(to + q * kPart) = make_uint2(a, b);
+          }
+        };
+        if constexpr (kAligned) {
+          const uint32_t in = w.inside(c), next = c + 1 < pl.c1 ? w.inside(c + 1) : 0;
+          const int64_t at = w.at + c * w.chunk;
+#pragma unroll
+          for (int i = 0; i < kQuads; ++i) {
+            const Four g = widen<kType>(ld.g[i]), m = mix(tab.mu, widen<MOE_LORA_F32>(ld.m[i]), nu, g);
+            ld.quad(at + w.chunk + w.element(i), i, next >> i & 1, true);
+            if (in >> i & 1) st_quad<MOE_LORA_F32>(mp, at + w.element(i), m);
+            put(i, g, m);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kQuads; ++i) {
+            const Four g = ld_loose<kType>(ld.gp, t, w, pl.first, c, i), m = mix(tab.mu, ld_loose<MOE_LORA_F32>(mp, t, w, pl.first, c, i), nu, g);
+            st_loose<MOE_LORA_F32>(mp, t, w, pl.first, c, i, m);
+            put(i, g, m);
           }
         }
         fence_proxy_async_smem();
@@ -751,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
   for (int x = first_chunk(tab, blockIdx.x); x < end;) {
     const Place pl = place_of(tab, x, end);
     const MuonTensor& t = *pl.t;
-    const bool aligned = quads_aligned(t), tall = t.tall;
+    const bool tall = t.tall;
     const Walk w(t, pl.first, pl.rows);
     copy_async<kPoly>(pt, tab.poly + (int64_t)pl.tile * kPoly);  // no product is under way here
     const float* norm = tab.norm + (int64_t)pl.tile * 2 * kTile;
@@ -759,10 +797,11 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
     if (threadIdx.x < kTile) row_up[threadIdx.x] = norm[threadIdx.x];
     // P's scale, and the factor that makes the products X
     const float factor = norm[kTile + r], down = factor == factor ? factor * (kXScale / kQScale) : 0.f;
-    with_type(t.g_dtype, [&](auto type) {
+    with_kind(t.g_dtype, quads_aligned(t), [&](auto type, auto quads) {
       constexpr int kType = decltype(type)::value;
-      Loads ld;
-      load_chunk<kType>(pl, w, pl.c0, aligned, with_g, ld);
+      constexpr bool kAligned = decltype(quads)::value;
+      Loads<kType> ld(t);
+      if (kAligned) ld.chunk(w, pl.c0, with_g);
       async_wait<0>();
       __syncthreads();
       for (int c = pl.c0; c < pl.c1; ++c, ++used) {
@@ -771,13 +810,9 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
           if (threadIdx.x == 0) bulk_wait_group_read<0>();
           __syncthreads();
         }
-        const int next = c + 1 < pl.c1 ? w.inside(c + 1) : 0;
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          Four u = widen<MOE_LORA_F32>(ld.m[i]);
-          if (with_g) u = mix(tab.mu, u, nu, widen<kType>(ld.g[i]));
-          if (c + 1 < pl.c1) load_quad<kType>(pl, w, c + 1, i, next, aligned, with_g, ld);
-          const float* f = row_up + w.row + i * w.hop_row;
+        const auto put = [&](int i, Four u, const Four& g) {
+          if (with_g) u = mix(tab.mu, u, nu, g);
+          const float* f = row_up + w.row_of(i);
           const float2 fa = tall ? make_float2(f[0], f[1]) : both(f[0]), fb = tall ? make_float2(f[2], f[3]) : both(f[0]);
           u = Four{mul2(u.a, fa), mul2(u.b, fb)};
           // matrices without a norm (0, or not finite) take no part
@@ -789,6 +824,15 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
           uint8_t* to = xt + w.operand(i);
           *reinterpret_cast<uint2*>(to) = hi;
           *reinterpret_cast<uint2*>(to + kPart) = lo;
+        };
+        if constexpr (kAligned) {
+#pragma unroll
+          for (int i = 0; i < kQuads; ++i) put(i, widen<MOE_LORA_F32>(ld.m[i]), widen<kType>(ld.g[i]));
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kQuads; ++i)
+            put(i, ld_loose<MOE_LORA_F32>(ld.mp, t, w, pl.first, c, i),
+                with_g ? ld_loose<kType>(ld.gp, t, w, pl.first, c, i) : Four{both(0.f), both(0.f)});
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -798,6 +842,9 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
           poly_product(acc, smem_u32(pt), smem_u32(xt), tall);
           mma_commit(&done[0]);
         }
+        // not before: the products wait for the operands' stores, which the loads would hold up (573 us
+        // against 5xx for 203 M elements)
+        if (kAligned && c + 1 < pl.c1) ld.chunk(w, c + 1, with_g);
         wait(&done[0], used & 1);
         // rows of 64 long places from here on: half a row each
         {
@@ -889,14 +936,16 @@ __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_c
     // NaN for a matrix whose norm is not finite
     const float f = (factor == factor ? 1.f : factor) * (1.f / (kXScale * kQScale));
     const bool aligned = quads_aligned(t), tall = t.tall;
-    const void* wp = kMaster ? static_cast<const void*>(t.master) : t.p;
+    const void* const wp = in_register(kMaster ? static_cast<void*>(t.master) : t.p);
+    void* const pp = in_register(t.p);
+    const float decay = t.decay, step = t.step;
     const Walk w(t, pl.first, pl.rows);
     float* o = reinterpret_cast<float*>(xt);
     // a thread's quads among the products
     const float* mine = tall ? o + w.col * kTallPitch + w.row : o + w.row * kPitch + w.col;
-    const int hop = tall ? w.hop_col * kTallPitch + w.hop_row : w.hop_row * kPitch;
+    const int hop = tall ? w.hop_col * kTallPitch : w.hop_row * kPitch, hop4 = tall ? w.hop_col4 * kTallPitch + w.hop_row4 : 4 * hop;
     for (int c = pl.c0; c < pl.c1; ++c, ++used) {
-      const int n = w.inside(c);
+      const uint32_t in = w.inside(c);
       const int64_t at = w.at + c * w.chunk;
       async_wait<0>();
       fence_proxy_async_smem();
@@ -908,8 +957,9 @@ __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_c
         mma_commit(&done);
       }
       uint4 old[kQuads];
+      if (aligned)
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) old[i] = aligned && i < n ? ld_quad<kW>(wp, at + i * w.hop) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kQuads; ++i) old[i] = in >> i & 1 ? ld_quad<kW>(wp, at + w.element(i)) : make_uint4(0, 0, 0, 0);
       wait(&done, used & 1);
       {
         float v[32];
@@ -925,15 +975,20 @@ __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_c
         }
       }
       __syncthreads();
-      float4 y[kQuads];  // the products, then the weights
+      const auto stepped = [&](const Four& u, const float4& y) {
+        return Four{fma2(both(-step), make_float2(y.x, y.y), mul2(u.a, both(decay))),
+                    fma2(both(-step), make_float2(y.z, y.w), mul2(u.b, both(decay)))};
+      };
+      Four y[kQuads];  // the weights
+      if (aligned) {
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        y[i] = *reinterpret_cast<const float4*>(mine + i * hop);
-        if (aligned) {
-          const Four u = widen<kW>(old[i]);
-          const float2 a = fma2(both(-t.step), make_float2(y[i].x, y[i].y), mul2(u.a, both(t.decay)));
-          const float2 b = fma2(both(-t.step), make_float2(y[i].z, y[i].w), mul2(u.b, both(t.decay)));
-          y[i] = make_float4(a.x, a.y, b.x, b.y);
+        for (int i = 0; i < kQuads; ++i) y[i] = stepped(widen<kW>(old[i]), *reinterpret_cast<const float4*>(mine + (i & 3) * hop + (i >> 2) * hop4));
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kQuads; ++i) {
+          const Four u = stepped(ld_loose<kW>(wp, t, w, pl.first, c, i), *reinterpret_cast<const float4*>(mine + (i & 3) * hop + (i >> 2) * hop4));
+          if (kMaster) st_loose<MOE_LORA_F32>(const_cast<void*>(wp), t, w, pl.first, c, i, u);
+          st_loose<kP>(pp, t, w, pl.first, c, i, u);
         }
       }
       __syncthreads();
@@ -942,24 +997,11 @@ __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_c
       if (aligned) {
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
-          if (i < n) {
-            const Four u{make_float2(y[i].x, y[i].y), make_float2(y[i].z, y[i].w)};
-            if (kMaster) st_quad<MOE_LORA_F32>(t.master, at + i * w.hop, u);
-            st_quad<kP>(t.p, at + i * w.hop, u);
+          if (in >> i & 1) {
+            const Four& u = y[i];
+            if (kMaster) st_quad<MOE_LORA_F32>(const_cast<void*>(wp), at + w.element(i), u);
+            st_quad<kP>(pp, at + w.element(i), u);
           }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const float z[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int64_t to = element_at(t, w, pl.first, c, i, e);
-            if (to < 0) continue;
-            const float u = fmaf(-t.step, z[e], ld_one<kW>(wp, to) * t.decay);
-            if (kMaster) t.master[to] = u;
-            st_one<kP>(t.p, to, u);
-          }
-        }
       }
     }
   }
