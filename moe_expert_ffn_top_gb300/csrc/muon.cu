@@ -739,6 +739,149 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
   tmem_close(tmem, kPolyCols);
 }
 
+// The same where all short sides are 32 or less: a warp per matrix, in fp32 without tensor cores, whose
+// 24 instructions for a product take as long for 16 columns as for 128 (smallest training configuration:
+// 74 us a step, so XX).  A lane has a column; matrices lie in shared memory, symmetric, so that a row of
+// the left factor, read by all lanes at once, stands for its column.  Only the matrices' own blocks of the
+// sums are read.
+constexpr int kSmall = 32, kSmallThreads = 512;
+constexpr int kSmallBytes = 8 * 3 * kSmall * kSmall * 4;  // three matrices for each of eight warps, or more smaller ones
+constexpr int kSmallSmem = kPoly + kSmallBytes + 1024;
+
+// S: 8, 16 or 32, at least s; the tile has at most 128 / (S / 2 + 1) matrices beyond S = 8, which has two a warp or more.
+template <int S>
+__device__ __forceinline__ void small_polys(const MuonTable& tab, const MuonTensor& t, int tile, int mats, int steps, bool first, uint8_t* pt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, s = t.s;
+  constexpr int kWarps = S == 32 ? 8 : kSmallThreads / 32;
+  static_assert(kWarps * 3 * S * S * 4 <= kSmallBytes, "shared memory");
+  if (warp >= kWarps) return;
+  float* const gm = reinterpret_cast<float*>(pt + kPoly) + warp * 3 * S * S;
+  float *const qm = gm + S * S, *const pm = qm + S * S;
+  const int x = t.chunk0 + (tile - t.tile0) * t.chunks;
+  const int64_t s0 = stretch_slot(tab, tile, x);
+  const int stretches = (int)(stretch_slot(tab, tile, x + t.chunks - 1) - s0) + 1;
+  const float* sums = tab.gram + s0 * kTile * kTile;
+  float* norms = tab.norm + (int64_t)tile * 2 * kTile;
+  const bool in = lane < s;
+  const auto put = [&](float* to, const float (&v)[S]) {
+    __syncwarp();
+    if (lane < S)
+#pragma unroll
+      for (int i = 0; i < S; ++i) to[i * S + lane] = v[i];
+    __syncwarp();
+  };
+  const auto times = [&](const float* left, const float* right, float (&acc)[S]) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) {
+      const float v = right[k * S + lane % S];
+#pragma unroll
+      for (int i = 0; i < S; i += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(left + k * S + i);
+        acc[i] = fmaf(u.x, v, acc[i]);
+        acc[i + 1] = fmaf(u.y, v, acc[i + 1]);
+        acc[i + 2] = fmaf(u.z, v, acc[i + 2]);
+        acc[i + 3] = fmaf(u.w, v, acc[i + 3]);
+      }
+    }
+  };
+#pragma unroll 1
+  for (int mat = warp; mat < mats; mat += kWarps) {
+    const int at = mat * s;  // first row and column
+    float g[S], v[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) g[i] = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < stretches; ++k) {
+      const float* e = sums + (int64_t)k * kTile * kTile;
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        if (in && i < s) g[i] += e[(at + i) * kTile + at + lane] + e[(at + lane) * kTile + at + i];
+    }
+    float unit = 1.f / (kXScale * kXScale);
+    if (first) {  // as in the kernel above
+      float n2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < S; ++i) n2 += i == lane ? g[i] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      const bool fine = n2 < INFINITY;
+      const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
+      const float up = norm > 0.f ? ldexpf(1.f, 9 - ilogbf(norm)) : 0.f;
+      unit = norm > 0.f ? inv * inv : 0.f;
+      if (in) {
+        norms[at + lane] = up;
+        norms[kTile + at + lane] = !fine ? NAN : norm > 0.f ? inv / up : 0.f;
+      }
+      if (!fine)
+#pragma unroll
+        for (int i = 0; i < S; ++i) g[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      g[i] *= unit;
+      v[i] = i == lane ? 1.f : 0.f;
+    }
+    put(gm, g);
+    if (steps == 0) put(pm, v);
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+      times(gm, gm, v);
+#pragma unroll
+      for (int i = 0; i < S; ++i) v[i] = fmaf(tab.c, v[i], fmaf(tab.b, g[i], i == lane && in ? tab.a : 0.f));
+      put(qm, v);
+      if (k > 0) times(qm, pm, v);
+      put(pm, v);
+      if (k < steps - 1) {
+        times(qm, gm, g);
+        put(gm, g);
+        times(qm, gm, g);
+        put(gm, g);
+      }
+    }
+    if (in)
+#pragma unroll 4
+      for (int i = 0; i < s; ++i) {
+        const float f = pm[i * S + lane] * kQScale;
+        const __half hi = __float2half_rn(f), lo = __float2half_rn(f - __half2float(hi));
+        const int r = at + i, c = at + lane;
+        uint8_t* to = pt + (c >> 6) * kPart + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
+        *reinterpret_cast<__half*>(to) = hi;
+        *reinterpret_cast<__half*>(to + kTileBytes) = lo;
+      }
+  }
+}
+__global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __grid_constant__ MuonTable tab, int steps, bool first) {
+  extern __shared__ uint8_t muon_smem[];
+  uint8_t* pt = aligned_smem(muon_smem);
+  const int tile = blockIdx.x;
+  launch_next();
+  int ti = 0;
+  while (ti + 1 < tab.n && tile >= tab.t[ti + 1].tile0) ++ti;
+  const MuonTensor& t = tab.t[ti];
+  const int mats = (int)min((int64_t)t.per, t.batch - (int64_t)(tile - t.tile0) * t.per), row = threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kPoly / 16 / kSmallThreads; ++i) reinterpret_cast<uint4*>(pt)[threadIdx.x + i * kSmallThreads] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  wait_for_last();
+  if (first && row < kTile && row >= mats * t.s)  // rows of no matrix
+    tab.norm[(int64_t)tile * 2 * kTile + row] = tab.norm[(int64_t)tile * 2 * kTile + kTile + row] = 0.f;
+  if (t.s <= 8)
+    small_polys<8>(tab, t, tile, mats, steps, first, pt);
+  else if (t.s <= 16)
+    small_polys<16>(tab, t, tile, mats, steps, first, pt);
+  else
+    small_polys<32>(tab, t, tile, mats, steps, first, pt);
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    bulk_store(tab.poly + (int64_t)tile * kPoly, pt, kPoly);
+    bulk_commit_group();
+    bulk_wait_group<0>();
+  }
+}
+
 // ------------------------------------------------------------------ apply and update
 // D [128 x 64] = P X of a chunk.  X as two fp16 parts: rows of 64 long places (a short side
 // each), or two halves of 64 short places (a row per long place).
@@ -1116,10 +1259,16 @@ int run_muon(const moe_lora_muon* o, const moe_lora_muon_tensor* in, int n, uint
   }
   const int first = std::min(kFirstSteps, o->steps > 3 ? 2 : 1);
   int rc;
-  if ((rc = launch_muon(K_MUON_GRAM, muon_gram_kernel, l.blocks, kThreads, kGramSmem, false, s, tab)) ||
-      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, std::min<int64_t>(l.tiles, sms), kPolyThreads, kPolySmem, true, s, tab, (int)l.tiles, first, true)) ||
+  bool small = true;
+  for (int i = 0; i < tab.n; ++i) small = small && tab.t[i].s <= kSmall;
+  const auto poly = [&](int steps, bool is_first) {
+    return small ? launch_muon(K_MUON_POLY, muon_small_kernel, l.tiles, kSmallThreads, kSmallSmem, true, s, tab, steps, is_first)
+                 : launch_muon(K_MUON_POLY, muon_poly_kernel, std::min<int64_t>(l.tiles, sms), kPolyThreads, kPolySmem, true, s, tab,
+                               (int)l.tiles, steps, is_first);
+  };
+  if ((rc = launch_muon(K_MUON_GRAM, muon_gram_kernel, l.blocks, kThreads, kGramSmem, false, s, tab)) || (rc = poly(first, true)) ||
       (rc = launch_muon(K_MUON_APPLY, muon_apply_kernel, l.blocks, kThreads, kApplySmem, true, s, tab)) ||
-      (rc = launch_muon(K_MUON_POLY, muon_poly_kernel, std::min<int64_t>(l.tiles, sms), kPolyThreads, kPolySmem, true, s, tab, (int)l.tiles, o->steps - first, false)))
+      (rc = poly(o->steps - first, false)))
     return rc;
   bool overlap = true;  // the first kind's launch with what is before it; the others follow it as any launch does
   const auto update = [&](auto kernel, int dtype, bool master) {
