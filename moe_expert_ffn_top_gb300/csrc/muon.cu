@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
 
 // The same where all short sides are 32 or less: a warp per matrix, in fp32 without tensor cores, whose
 // 24 instructions for a product take as long for 16 columns as for 128 (smallest training configuration:
-// 74 us a step, so XX).  A lane has a column; matrices lie in shared memory, symmetric, so that a row of
+// a step 51 us instead of 74, 38.6 M elements of rank 8 312 instead of 396).  A lane has a column; matrices lie in shared memory, symmetric, so that a row of
 // the left factor, read by all lanes at once, stands for its column.  Only the matrices' own blocks of the
 // sums are read.
 constexpr int kSmall = 32, kSmallThreads = 512;
@@ -985,8 +985,8 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
           poly_product(acc, smem_u32(pt), smem_u32(xt), tall);
           mma_commit(&done[0]);
         }
-        // not before: the products wait for the operands' stores, which the loads would hold up (573 us
-        // against 5xx for 203 M elements)
+        // not before: the products wait for the operands' stores, which the loads would hold up (734 us
+        // instead of 606 for 203 M elements, all else equal)
         if (kAligned && c + 1 < pl.c1) ld.chunk(w, c + 1, with_g);
         wait(&done[0], used & 1);
         // rows of 64 long places from here on: half a row each
@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
           }
           mma_commit(&done[1]);
           // the tile as it lies, 32 KB in one copy (16-byte stores by the threads that formed it: 789 us
-          // instead of 5xx for 203 M elements)
+          // instead of 539 for 203 M elements)
           bulk_store(tab.x + (x + c - pl.c0) * (int64_t)kImage, xt, kImage);
           bulk_commit_group();
         }
@@ -1181,8 +1181,10 @@ Shape shape_of(const moe_lora_muon_tensor& t) {
   h.chunks = (h.L + kChunk - 1) / kChunk;
   return h;
 }
-// Two blocks on each of 152 SMs share the chunks of a launch.
-constexpr int kBlocks = 304;
+// Two blocks on each of 152 SMs share the chunks of a launch; where that would be more than 128 chunks a
+// block, twice, three times, ... as many do (a stretch adds up in one accumulator of the tensor cores,
+// whose additions are cut off rather than rounded).
+constexpr int kBlocks = 304, kMaxStretch = 128;
 struct Layout {
   size_t err, norm, poly, gram, x, total;
   int blocks;
@@ -1195,7 +1197,7 @@ Layout layout_of(const moe_lora_muon_tensor* t, int n) {
     l.tiles += h.tiles;
     l.chunks += h.tiles * h.chunks;
   }
-  l.blocks = (int)std::min<int64_t>(kBlocks, l.chunks);
+  l.blocks = (int)std::min<int64_t>(l.chunks, kBlocks * std::max<int64_t>(1, (l.chunks + kBlocks * kMaxStretch - 1) / (kBlocks * kMaxStretch)));
   size_t o = 0;
   const auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   l.err = take(16);

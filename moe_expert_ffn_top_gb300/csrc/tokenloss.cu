@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
 
 // dlogits from a saved lse: no reduction, every element on its own.  A block takes up to
 // kBwdVecs vectors a thread of one row, all their loads under way together.
-constexpr int kBwdThreads = 256, kBwdVecs = 4;
+constexpr int kBwdThreads = 256, kBwdVecs = 4, kBwdWarpVecs = 1024;
 template <class T, int kTeam>
 __global__ void __launch_bounds__(kBwdThreads)
     token_bwd_kernel(const __grid_constant__ RowArgs g, const __grid_constant__ GradArgs dg, const float* dlogp, int slices, int per) {
@@ -929,15 +929,21 @@ int launch_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, cons
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
 
-// Slices of a row and what a block holds of it.  Rows of a few thousand elements belong to
-// a warp.  Longer ones to the fewest blocks that hold 64 KB each (128 KB beyond eight), and
-// to more, up to eight, where there are too few rows to give every SM a block.
+// Slices of a row and what a block holds of it.  Up to 128 vectors (1,024 elements of 16 bits) belong to
+// a warp (20,000 x 1,000 log probabilities 8.2 us, as blocks 11.8; 200 x 1,000 2.1 and 2.3), up to 512
+// where there are enough rows for every SM's warps (20,000 x 4,000 27.8 and 33.1 us, the policy's gradient 64
+// and 117; 2,000 x 4,096 11.7 and 15.4, but 600 x 4,000 8.8 and 6.8).  Longer rows belong to the fewest
+// blocks that hold 64 KB each (128 KB beyond eight): 32 KB took 449 us instead of 406 for 16,384 x 65,536
+// log probabilities and 952 instead of 772 for the policy loss over 8,192 x 151,936, 128 KB 562 and
+// 1,305.  Blocks have 256 threads, for log probabilities alone 128 with twice the vectors each (393 us
+// instead of 417; the policy loss 1,037 instead of 755).  Where there are too few rows to give every SM
+// a block, a row is shared by more, up to eight (one row of 32,000: 2.9 us instead of 4.4).
 template <class T, bool kEntropy, bool kPolicy, bool kGrad>
 int pick_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, const Ranges& ad, int sms, bool overlap, cudaStream_t s) {
   constexpr int VL = 16 / sizeof(T);
   const int vecs = g.n / VL;
   if (vecs <= 32 * kGroup) return launch_rows<T, 32, 1, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
-  if (vecs <= 32 * 4 * kGroup && g.rows >= sms) return launch_rows<T, 32, 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
+  if (vecs <= 32 * 4 * kGroup && g.rows >= 8 * sms) return launch_rows<T, 32, 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
   constexpr int kTeam = kPolicy ? kRowThreads : kReadThreads, one = kTeam * kGroup, kFull = 4 * kRowThreads / kTeam;
   const auto need = [&](int per) { return (vecs + per - 1) / per; };
   int slices = need(kFull * one);
@@ -960,11 +966,13 @@ int run_policy(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, const
                : pick_rows<T, true, true, false>(g, pg, dg, ad, sms, overlap, s);
 }
 template <class T>
-int run_bwd(const RowArgs& g, const GradArgs& dg, const float* dlogp, cudaStream_t s) {
+int run_bwd(const RowArgs& g, const GradArgs& dg, const float* dlogp, int sms, cudaStream_t s) {
   constexpr int VL = 16 / sizeof(T);
   const int vecs = g.n / VL, slices = std::max(1, (vecs + kBwdThreads * kBwdVecs - 1) / (kBwdThreads * kBwdVecs));
   prof_begin(K_TOKEN_BWD, s);
-  if (vecs <= 32 * kBwdVecs)
+  // a warp per row: 20,000 x 1,000 9.9 us, as blocks 32; 20,000 x 4,000 53 and 74; 20,000 x 8,000 102 and
+  // 106; but 1,300 x 8,000 9.3 and 6.2
+  if (vecs <= 32 * kBwdVecs || (vecs <= kBwdWarpVecs && g.rows >= 16 * sms))
     token_bwd_kernel<T, 32><<<(unsigned)((g.rows + kBwdThreads / 32 - 1) / (kBwdThreads / 32)), kBwdThreads, 0, s>>>(g, dg, dlogp, 1, vecs);
   else
     token_bwd_kernel<T, kBwdThreads><<<(unsigned)(g.rows * slices), kBwdThreads, 0, s>>>(g, dg, dlogp, slices, (vecs + slices - 1) / slices);
@@ -998,8 +1006,10 @@ int launch_sums(const SumArgs& g, const Ranges& ad, cudaStream_t s) {
 // Scratch of the losses: a ticket, the items' terms, then the adapters' partial counts.
 constexpr size_t kTicketBytes = 256;
 size_t terms_bytes(int64_t items) { return align_up(sizeof(float) * kTerms * (size_t)std::max<int64_t>(items, 1), 256); }
-// Few items: counted, and their terms added, where the items are worked on, in one launch.
-constexpr int kFew = 256;
+// Few items: counted, and their terms added, where the items are worked on, in one launch.  64 rows of
+// 4,096: 8.5 us in one launch or three on the GPU, 12 and 16 us of the host's time; 128 rows 6.4 and
+// 5.8 us, 200 rows 7.8 and 5.4.  64 pairs 6.0 us either way, 256 pairs 8.2 and 8.6, 1,024 pairs 22 and 12.
+constexpr int kFewRows = 64, kFewPairs = 256;
 
 }  // namespace
 
@@ -1040,9 +1050,9 @@ extern "C" int moe_lora_token_logp_backward(const moe_lora_rows* r, const void* 
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return r->dtype == MOE_LORA_F32    ? run_bwd<float>(g, dg, dlogp, s)
-         : r->dtype == MOE_LORA_BF16 ? run_bwd<__nv_bfloat16>(g, dg, dlogp, s)
-                                     : run_bwd<__half>(g, dg, dlogp, s);
+  return r->dtype == MOE_LORA_F32    ? run_bwd<float>(g, dg, dlogp, sms, s)
+         : r->dtype == MOE_LORA_BF16 ? run_bwd<__nv_bfloat16>(g, dg, dlogp, sms, s)
+                                     : run_bwd<__half>(g, dg, dlogp, sms, s);
 }
 
 extern "C" size_t moe_lora_policy_scratch_bytes(int64_t rows, int32_t adapters) {
@@ -1077,7 +1087,7 @@ extern "C" int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_polic
   char* at = static_cast<char*>(scratch);
   float* terms = reinterpret_cast<float*>(at + kTicketBytes);
   int* count = reinterpret_cast<int*>(at + kTicketBytes + terms_bytes(r->rows));
-  const bool few = r->rows > 0 && r->rows <= kFew;
+  const bool few = r->rows > 0 && r->rows <= kFewRows;
   const PolicyArgs pg{advantages, old_logp, ref_logp, weight, dloss, 1.f - o->clip_low, 1.f + o->clip_high, o->kl_coef, count, terms,
                       few, reinterpret_cast<unsigned*>(at), loss, stats};
   if (!weight && !few) {
@@ -1123,13 +1133,14 @@ extern "C" int moe_lora_preference_loss(const moe_lora_preference* o, const floa
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* terms = reinterpret_cast<float*>(static_cast<char*>(scratch) + kTicketBytes);
   if (o->pairs > 0) {
-    const bool few = o->pairs <= kFew;
+    const bool few = o->pairs <= kFewPairs;
     const double target = 0.5 / (double)o->beta;
     const PrefArgs g{logp, targets, o->tokens, seq_offsets, ref, o->beta, o->margin, o->label_smoothing, o->kind, o->average,
                      dloss, seq_logp, dlogp, terms, o->pairs, err, Long{(float)target, (float)(target - (float)target)},
                      few, static_cast<unsigned*>(scratch), loss, stats};
-    // pairs of more tokens than a small block has under way get a large one
-    const bool wide = o->tokens / o->pairs >= 256 * 4 * kPrefAhead;
+    // few pairs of more tokens than a small block has under way get large blocks: 16 of 40,000 tokens
+    // 21 us instead of 39, 64 of 8,000 8.5 and 9.7; but 512 of 6,000 22 and 15
+    const bool wide = o->pairs <= sms && o->tokens / o->pairs >= 256 * 4 * kPrefAhead;
     prof_begin(K_PREF, s);
     if (wide)
       pref_kernel<1024><<<(unsigned)o->pairs, 1024, 0, s>>>(g, ad);
