@@ -27,6 +27,12 @@
 // whose products with each other are set to 0 wherever a tile of G is read.  A chunk is 64
 // places of the long side.  Blocks share all chunks evenly; what a block has of one tile is a
 // stretch, and leaves one partial G.
+//
+// Measured on one GB300, 203 M elements of rank 128 (bf16 weights, fp32 masters and gradients): 1,711 us,
+// of which gram 449 (12 bytes an element, 5.4 TB/s), apply 531 (12 bytes, 4.6), update 472 (14 bytes,
+// 6.0) and the two polys 242 together.  The three that stream are bound by the chain of a chunk (loads,
+// operand stores, a barrier, products; in apply twice), which two blocks an SM cover in part: registers
+// and tensor memory take no third.  38.6 M elements of rank 8 in bf16: 312 us.
 #include <math.h>
 
 #include <algorithm>
