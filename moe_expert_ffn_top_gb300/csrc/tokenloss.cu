@@ -345,7 +345,9 @@ __device__ __forceinline__ bool came_last(unsigned* ticket, unsigned all) {
   unsigned at = 0;
   if ((threadIdx.x & 31) == 0)  // back to 0 after the last
     asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(at) : "l"(ticket), "r"(all - 1) : "memory");
-  return __shfl_sync(0xffffffffu, at, 0) == all - 1;
+  const bool last = __shfl_sync(0xffffffffu, at, 0) == all - 1;
+  __syncwarp();  // what the first lane has seen, all have
+  return last;
 }
 __device__ __forceinline__ int live_in(const int32_t* targets, int n, int64_t lo, int64_t hi) {
   int c = 0;
@@ -857,8 +859,10 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
     const float p0 = per_token[0], p1 = per_token[1];
     for (int64_t v = threadIdx.x, j = 0; v < vecs; v += kThreads, ++j) {
       const int64_t t = base + 4 * v;
-      uint32_t live = known >> (4 * j) & 15;
-      if (j >= kPrefAhead) {
+      uint32_t live;
+      if (j < kPrefAhead) {
+        live = known >> (4 * (int)j) & 15;
+      } else {
         float unused[4];
         live = load_mask(v, unused);
       }

@@ -71,3 +71,39 @@ def test_preference_step():
     tol = (want.abs() + r["p"] * b32) * (b32 * serr + float(r["tol"]["p"].max())) + 1e-9
     assert ((dx.double() - want).abs() <= tol).all()
     assert (dx[88:] == 0).all() and (dx[30:35] == 0).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, against the same calls one after the other."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+
+    def problem(rows, n, shape):
+        x = torch.randn(rows, n, generator=g, device="cuda").bfloat16()
+        y = torch.randint(0, n, (rows,), generator=g, device="cuda", dtype=torch.int32)
+        adv, old = torch.randn(rows, generator=g, device="cuda"), -torch.rand(rows, generator=g, device="cuda") * 9
+        u = torch.randn(*shape, generator=g, device="cuda")
+        return x, y, adv, old, u
+
+    def outputs(p):
+        x, _, _, _, u = p
+        out = dict(loss=torch.empty(1, device="cuda"), stats=torch.empty(1, 4, device="cuda"), d=torch.empty_like(x), p=torch.zeros_like(u),
+                   m=torch.zeros_like(u))
+        return out, m.policy_scratch(x.shape[0]), m.MuonTensors([dict(p=out["p"], g=u, m=out["m"], lr=0.1)])
+
+    def call(p, out, sc, t):
+        x, y, adv, old, _ = p
+        for _ in range(5):
+            m.moe_lora_policy_loss(x, y, adv, old, None, out["loss"], out["stats"], sc, dlogits=out["d"])
+            m.moe_lora_muon_step(t)
+    ps = [problem(40, 30000, (64, 16, 500)), problem(700, 9000, (9, 700, 128))]
+    want = [outputs(p) for p in ps]
+    for p, o in zip(ps, want):
+        call(p, *o)
+    got, streams = [outputs(p) for p in ps], [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for p, o, s in zip(ps, got, streams):
+        with torch.cuda.stream(s):
+            call(p, *o)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[0][k], b[0][k]) for k in a[0])
