@@ -3,16 +3,16 @@
 //
 // Rows of logits are long (a vocabulary) and pass through memory once: HBM is the bound.
 // A row is cut into slices, one per block of a cluster; a block copies its slice into
-// shared memory, 64 KB at most where that is enough, so that three blocks of an SM are at
+// shared memory, 32 KB at most where that is enough, so that six blocks of an SM are at
 // different points of their rows: some copy while others write.  A thread reads only what
 // it copied itself, so its copies need no barrier.  It keeps a running maximum and sum over
 // its own elements; the threads' pairs meet once, in distributed shared memory, and where a
 // gradient is wanted it is formed from the slice in shared memory: one read and one write.
 //
 // Measured on one GB300: the policy loss with its gradient over 8,192 x 151,936 bf16, 30% of the rows
-// without a target, 756 us (5.6 TB/s, 82% of the measured copy bandwidth; 710 us without arithmetic: blocks
-// taking turns); log probabilities with entropies of 16,384 x 65,536 bf16 393 us (4.9 TB/s; 353 without
-// arithmetic), their backward 641 us (94%); the preference loss of 1,024 pairs of 1,400 tokens 16 us.
+// without a target, 707 us (6.0 TB/s, 88% of the measured copy bandwidth); log probabilities with
+// entropies of 16,384 x 65,536 bf16 348 us (5.6 TB/s, 82%), their backward 641 us (94%); the preference
+// loss of 1,024 pairs of 1,400 tokens 16 us.
 #include <math.h>
 #include <string.h>
 
@@ -30,8 +30,7 @@ namespace moelora {
 namespace {
 
 constexpr int kGroup = 4;            // vectors of a thread that are waited for together
-constexpr int kRowThreads = 256;     // of a block that works on a slice of a row
-constexpr int kReadThreads = 128;    // of one for log probabilities alone
+constexpr int kRowThreads = 128;     // of a block that works on a slice of a row
 constexpr int kShortThreads = 128;   // of a block whose warps have a row each
 constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 1 << 19;
@@ -400,8 +399,8 @@ struct Token {
 
 // Log probabilities (kPolicy false), or the policy loss's terms and, with kGrad, its
 // gradient.  kTeam threads work on a slice: a block's, or a warp whose slice is the row.
-// What happens once per row is left to one warp: with a slice of 64 KB a warp has 16 vectors
-// a lane, and a few hundred instructions around them cost as much as the vectors.
+// What happens once per row is left to one warp: a lane has 16 vectors of a slice of 32 KB, and a
+// few hundred instructions around them cost as much as the vectors.
 template <class T, int kTeam, int kGroups, bool kEntropy, bool kPolicy, bool kGrad>
 __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam)
     token_row_kernel(const __grid_constant__ RowArgs g, const __grid_constant__ PolicyArgs pg,
@@ -942,27 +941,30 @@ int launch_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, cons
 // a warp (20,000 x 1,000 log probabilities 8.2 us, as blocks 11.8; 200 x 1,000 2.1 and 2.3), up to 512
 // where there are enough rows for every SM's warps (20,000 x 4,000 27.8 and 33.1 us, the policy's gradient 64
 // and 117; 2,000 x 4,096 11.7 and 15.4, but 600 x 4,000 8.8 and 6.8).  Longer rows belong to the fewest
-// blocks that hold 64 KB each (128 KB beyond eight): 32 KB took 449 us instead of 406 for 16,384 x 65,536
-// log probabilities and 952 instead of 772 for the policy loss over 8,192 x 151,936, 128 KB 562 and
-// 1,305.  Blocks have 256 threads, for log probabilities alone 128 with twice the vectors each (393 us
-// instead of 417; the policy loss 1,037 instead of 755).  Where there are too few rows to give every SM
-// a block, a row is shared by more, up to eight (one row of 32,000: 2.9 us instead of 4.4).
+// blocks of 128 threads that hold 32 KB each, up to sixteen, which then hold up to 128 KB.  Log
+// probabilities of 16,384 x 65,536 take 348 us so, with 16 KB 418, with 64 KB 393, with 256 threads
+// and 64 KB 417, with 64 threads 414; of 8,192 x 151,936 467 us in clusters of ten, 589 in five of
+// 64 KB.  The policy loss over 8,192 x 151,936 707 us, with 256 threads and 64 KB 757, 32 KB 812;
+// 2,048 x 50,257 73 and 72.  Where there are too few rows to give every SM a block, a row is shared by
+// more, up to eight (one row of 32,000: 2.9 us instead of 4.4).
 template <class T, bool kEntropy, bool kPolicy, bool kGrad>
 int pick_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, const Ranges& ad, int sms, bool overlap, cudaStream_t s) {
   constexpr int VL = 16 / sizeof(T);
   const int vecs = g.n / VL;
   if (vecs <= 32 * kGroup) return launch_rows<T, 32, 1, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
   if (vecs <= 32 * 4 * kGroup && g.rows >= 8 * sms) return launch_rows<T, 32, 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, 1, overlap, s);
-  constexpr int kTeam = kPolicy ? kRowThreads : kReadThreads, one = kTeam * kGroup, kFull = 4 * kRowThreads / kTeam;
-  const auto need = [&](int per) { return (vecs + per - 1) / per; };
-  int slices = need(kFull * one);
-  if (slices > 8) slices = std::max(8, need(2 * kFull * one));
-  while (slices < 8 && g.rows * (slices + 1) <= sms && vecs / (slices + 1) >= kRowThreads) ++slices;
+  constexpr int one = kRowThreads * kGroup;  // vectors of a group of a block
+  int slices = std::min((vecs + 4 * one - 1) / (4 * one), kMaxCluster);
+  while (slices < 8 && g.rows * (slices + 1) <= sms && vecs / (slices + 1) >= 2 * kRowThreads) ++slices;
   const int per = (vecs + slices - 1) / slices;
-  return per <= kFull / 4 * one   ? launch_rows<T, kTeam, kFull / 4, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
-         : per <= kFull / 2 * one ? launch_rows<T, kTeam, kFull / 2, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
-         : per <= kFull * one     ? launch_rows<T, kTeam, kFull, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s)
-                                  : launch_rows<T, kTeam, 2 * kFull, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s);
+  const auto run = [&](auto groups) {
+    return launch_rows<T, kRowThreads, decltype(groups)::value, kEntropy, kPolicy, kGrad>(g, pg, dg, ad, slices, overlap, s);
+  };
+  return per <= one       ? run(std::integral_constant<int, 1>{})
+         : per <= 2 * one ? run(std::integral_constant<int, 2>{})
+         : per <= 4 * one ? run(std::integral_constant<int, 4>{})
+         : per <= 8 * one ? run(std::integral_constant<int, 8>{})
+                          : run(std::integral_constant<int, 16>{});
 }
 template <class T>
 int run_logp(const RowArgs& g, int sms, cudaStream_t s) {
