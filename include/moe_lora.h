@@ -575,7 +575,8 @@ typedef struct moe_lora_muon {
  * moe_lora_muon_scratch_bytes(tensors, n) bytes (from batch, rows and cols alone; 0 for bad sizes),
  * four bytes per element and a little; its first 16 bytes are the device error word, which the caller
  * clears once and calls only add to.  Calls that may run at the same time need one each.  Sums run in
- * a fixed order, so equal calls give equal bits.  Five launches per 128 tensors. */
+ * a fixed order, so equal calls give equal bits.  Five launches per 128 tensors whose weights are of one
+ * type, one more for each other type among them. */
 MOE_LORA_API size_t moe_lora_muon_scratch_bytes(const moe_lora_muon_tensor* tensors, int32_t n);
 MOE_LORA_API int moe_lora_muon_step(const moe_lora_muon* opt, const moe_lora_muon_tensor* tensors, int32_t n,
                                     void* scratch, size_t scratch_bytes, void* stream);
