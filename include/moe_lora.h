@@ -507,8 +507,9 @@ MOE_LORA_API int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_pol
  *     loss_a = mean of l over the pairs of adapter a (0 without pairs),
  *     dlogp_t = dloss_a / pairs_a * dl/dh * (+1 chosen, -1 rejected) (average: / live tokens of j).
  *   logp [tokens] fp32, e.g. moe_lora_token_logp_forward's; targets [tokens] int32
- *   seq_offsets [2 pairs + 1] int64, DEVICE.  An offset below the one before it or above tokens is
- *            taken as the nearest that is not, and sets MOE_LORA_DEV_BAD_ID in *err.
+ *   seq_offsets [2 pairs + 1] int64, DEVICE.  An offset below one before it or above tokens is taken
+ *            as the nearest that is not (offset j as the largest of 0 and offsets 0 .. j, at most
+ *            tokens), so that no token belongs to two sequences, and sets MOE_LORA_DEV_BAD_ID in *err.
  *   ref [2 pairs] fp32, the reference model's s_j (a call without ref writes them), or NULL for 0
  *   pair_offsets [adapters+1] int64, HOST, as adapter_offsets above, in pairs
  *   loss [adapters] fp32;  stats [adapters,4] fp32: means of [x > 0], beta r_chosen, beta r_rejected, h

@@ -618,6 +618,130 @@ __global__ void __launch_bounds__(256) token_count_kernel(const int32_t* targets
   if (threadIdx.x == 0) count[blockIdx.x] = sum;
 }
 
+// ------------------------------------------------------------------ preference loss
+// A sum as an fp32 number and what its rounding left: a loss lives on the difference of two large
+// sums, and fp64 additions are slow here.
+struct Long {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {  // exactly
+    const float t = hi + v, b = t - hi;
+    lo += (hi - (t - b)) + (v - b);
+    hi = t;
+  }
+  __device__ __forceinline__ void add(const Long& v) {
+    add(v.hi);
+    lo += v.lo;
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
+  __device__ __forceinline__ Long over(float n) const {
+    const float q = hi / n;
+    return Long{q, (fmaf(-q, n, hi) + lo) / n};
+  }
+};
+__device__ __forceinline__ Long long_over_warp(Long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.add(Long{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
+struct PrefArgs {
+  const float* logp;
+  const int32_t* targets;
+  int64_t T;
+  const int64_t* seq;
+  const float* ref;
+  float beta, margin, smooth;
+  int kind, average;
+  const float* dloss;
+  float *seq_logp, *dlogp;
+  float* terms;  // [kTerms][pairs]
+  int64_t pairs;
+  int* err;
+  Long target;   // squared: 1 / (2 beta)
+  bool few;      // so few pairs that the last one done adds the terms
+  unsigned* ticket;
+  unsigned* again;  // set where the offsets go back: see pairs_again
+  float *loss, *stats;
+};
+// What a warp makes of a pair's sums and counts: its terms, and the gradient of each sequence's tokens.
+__device__ __forceinline__ float2 pair_terms(const PrefArgs& g, const Ranges& ad, int64_t i, int a, Long (&r)[2], const int (&count)[2],
+                                             const float (&ref)[2], float up) {
+  const bool writes = (threadIdx.x & 31) == 0;
+  float cnt[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    cnt[q] = g.average ? (float)max(count[q], 1) : 1.f;
+    if (g.average) r[q] = r[q].over(cnt[q]);
+    if (g.seq_logp && writes) g.seq_logp[2 * i + q] = r[q].value();
+    if (g.ref) r[q].add(-ref[q]);
+  }
+  Long d = r[0];
+  d.add(Long{-r[1].hi, -r[1].lo});
+  const float h = d.value(), x = g.beta * h - g.margin;
+  float loss, dh;
+  if (g.kind == MOE_LORA_PREF_SIGMOID) {
+    const float e = expf(-fabsf(x)), soft = log1pf(e), near = e / (1.f + e);  // 1 - sigmoid(|x|)
+    loss = (1.f - g.smooth) * (soft + fmaxf(-x, 0.f)) + g.smooth * (soft + fmaxf(x, 0.f));
+    // sigmoid(x) - (1 - smooth) without the difference of two numbers near 1
+    dh = g.beta * (x >= 0.f ? g.smooth - near : near - (1.f - g.smooth));
+  } else if (g.kind == MOE_LORA_PREF_SQUARED) {
+    d.add(-g.target.hi);
+    d.lo -= g.target.lo;
+    const float o = d.value();
+    loss = o * o;
+    dh = 2.f * o;
+  } else {
+    loss = fmaxf(1.f - x, 0.f);
+    dh = x < 1.f ? -g.beta : 0.f;
+  }
+  if (isnan(x)) loss = dh = x;
+  if (writes) {
+    float* to = g.terms + i;
+    to[0] = loss;
+    to[g.pairs] = x > 0.f ? 1.f : 0.f;
+    to[2 * g.pairs] = g.beta * r[0].value();
+    to[3 * g.pairs] = g.beta * r[1].value();
+    to[4 * g.pairs] = h;
+  }
+  const float each = up / (float)(ad.off[a + 1] - ad.off[a]);
+  return make_float2(each * dh / cnt[0], -each * dh / cnt[1]);
+}
+// Pairs [lo, hi) once more, by a warp, where the list of offsets goes back or past the tokens.  Each
+// offset counts as the largest so far, which depends on the whole list, and a pair's block sees its own
+// three: every fault of a list is one of some pair's own three, which share one with the next pair's; its
+// block sets *again, and what adds the terms, which runs after all blocks, comes here first.  Blocks write
+// nothing ahead of the first offset, so all that they have written lies in sequences as they count, and is
+// written anew.  (Looking through the offsets ahead in every block: 1,000 pairs of 100 tokens 9.9 us
+// instead of 8.6.)
+__device__ __noinline__ void pairs_again(const PrefArgs& g, const Ranges& ad, int64_t lo, int64_t hi) {
+  if (lo >= hi) return;
+  const int lane = threadIdx.x & 31;
+  int64_t top = 0;
+  for (int64_t j = lane; j < 2 * lo; j += 32) top = max(top, g.seq[j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max(top, (int64_t)__shfl_xor_sync(0xffffffffu, (long long)top, o));
+  for (int64_t i = lo; i < hi; ++i) {
+    int64_t off[3];
+    for (int j = 0; j < 3; ++j) off[j] = min(top = max(top, g.seq[2 * i + j]), g.T);
+    Long r[2] = {};
+    int n[2] = {0, 0};
+    for (int q = 0; q < 2; ++q) {
+      for (int64_t t = off[q] + lane; t < off[q + 1]; t += 32)
+        if (g.targets[t] >= 0) {
+          r[q].add(g.logp[t]);
+          ++n[q];
+        }
+      r[q] = long_over_warp(r[q]);
+      n[q] = __reduce_add_sync(0xffffffffu, n[q]);
+    }
+    const int a = range_of(ad, i);
+    const float ref[2] = {g.ref ? g.ref[2 * i] : 0.f, g.ref ? g.ref[2 * i + 1] : 0.f};
+    const float2 each = pair_terms(g, ad, i, a, r, n, ref, g.dloss ? g.dloss[a] : 1.f);
+    if (g.dlogp)
+      for (int64_t t = off[0] + lane; t < off[2]; t += 32) g.dlogp[t] = g.targets[t] < 0 ? 0.f : t < off[1] ? each.x : each.y;
+  }
+}
+
 // Sums of an adapter's terms, a cluster per adapter: thread i of the cluster adds its
 // elements i, i + 8192, ... in order, then warps, block and cluster.  Where every adapter
 // has at most 1024 elements the first block alone has any, and runs alone: the same sums.
@@ -628,17 +752,26 @@ struct SumArgs {
   bool by_range;       // divide by the range's length
   float *loss, *stats;
 };
-template <int kC>
-__global__ void __launch_bounds__(kSumThreads) term_sum_kernel(const __grid_constant__ SumArgs g, const __grid_constant__ Ranges ad) {
+template <int kC, bool kPairs>
+__global__ void __launch_bounds__(kSumThreads)
+    term_sum_kernel(const __grid_constant__ SumArgs g, const __grid_constant__ Ranges ad, const __grid_constant__ PrefArgs pref) {
   __shared__ float warp_sum[kSumThreads / 32][kTerms], block_sum[kTerms];
   const int a = blockIdx.x / kC, rank = kC > 1 ? (int)cluster_rank() : 0;
   const int64_t lo = ad.off[a], hi = ad.off[a + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kPairs && __ldcg(pref.again)) {  // the same for all blocks, the last of which clears it
+    const int64_t warps = kC * (kSumThreads / 32), each = (hi - lo + warps - 1) / warps;
+    const int64_t first = min(hi, lo + (rank * (kSumThreads / 32) + (threadIdx.x >> 5)) * each);
+    pairs_again(pref, ad, first, min(hi, first + each));
+    __syncthreads();
+    if (threadIdx.x < 32 && came_last(pref.ticket, gridDim.x) && threadIdx.x == 0) *pref.again = 0;
+    if (kC > 1) cluster_sync_all();
+  }
   float s[kTerms] = {};
 #pragma unroll 2
   for (int64_t i = lo + rank * kSumThreads + threadIdx.x; i < hi; i += kSumCluster * kSumThreads)
 #pragma unroll
-    for (int k = 0; k < kTerms; ++k) s[k] += g.terms[k * g.stride + i];
+    for (int k = 0; k < kTerms; ++k) s[k] += __ldcg(g.terms + k * g.stride + i);
 #pragma unroll
   for (int k = 0; k < kTerms; ++k) {
 #pragma unroll
@@ -685,50 +818,6 @@ __global__ void __launch_bounds__(kSumThreads) term_sum_kernel(const __grid_cons
   if (kC > 1) cluster_sync_all();  // nobody leaves while its sums are read
 }
 
-// ------------------------------------------------------------------ preference loss
-// A sum as an fp32 number and what its rounding left: a loss lives on the difference of two large
-// sums, and fp64 additions are slow here.
-struct Long {
-  float hi, lo;
-  __device__ __forceinline__ void add(float v) {  // exactly
-    const float t = hi + v, b = t - hi;
-    lo += (hi - (t - b)) + (v - b);
-    hi = t;
-  }
-  __device__ __forceinline__ void add(const Long& v) {
-    add(v.hi);
-    lo += v.lo;
-  }
-  __device__ __forceinline__ float value() const { return hi + lo; }
-  __device__ __forceinline__ Long over(float n) const {
-    const float q = hi / n;
-    return Long{q, (fmaf(-q, n, hi) + lo) / n};
-  }
-};
-__device__ __forceinline__ Long long_over_warp(Long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v.add(Long{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
-  return v;
-}
-
-struct PrefArgs {
-  const float* logp;
-  const int32_t* targets;
-  int64_t T;
-  const int64_t* seq;
-  const float* ref;
-  float beta, margin, smooth;
-  int kind, average;
-  const float* dloss;
-  float *seq_logp, *dlogp;
-  float* terms;  // [kTerms][pairs]
-  int64_t pairs;
-  int* err;
-  Long target;   // squared: 1 / (2 beta)
-  bool few;      // so few pairs that the last one done adds the terms
-  unsigned* ticket;
-  float *loss, *stats;
-};
 // A block per pair, whose two sequences lie one behind the other: their sums, the pair's
 // terms, then the gradient.  Latency bounds it: a thread has four vectors of four tokens
 // under way, and what it learnt of the first four (which tokens are live) stays with it.
@@ -745,13 +834,17 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 3; ++j) off[j] = g.seq[2 * i + j];
+  const int64_t start = g.seq[0];
 #pragma unroll
   for (int j = 0; j < 3; ++j) {  // offsets that go back or past the end are noted; what is left of them is inside
-    const int64_t at = max(j ? off[j - 1] : (int64_t)0, min(off[j], g.T));
+    const int64_t at = min(max(j ? off[j - 1] : max(start, (int64_t)0), off[j]), g.T);
     bad |= at != off[j];
     off[j] = at;
   }
-  if (bad && g.err && threadIdx.x == 0) atomicOr(g.err, MOE_LORA_DEV_BAD_ID);
+  if (bad && threadIdx.x == 0) {
+    *g.again = 1;
+    if (g.err) atomicOr(g.err, MOE_LORA_DEV_BAD_ID);
+  }
   // asked for early, used late
   const int a = range_of(ad, i);
   const float ref[2] = {g.ref ? g.ref[2 * i] : 0.f, g.ref ? g.ref[2 * i + 1] : 0.f}, up = g.dloss ? g.dloss[a] : 1.f;
@@ -811,46 +904,16 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
   __syncthreads();
   if (warp == 0) {
     Long r[2];
-    float cnt[2];
+    int count[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       r[q] = long_over_warp(lane < kThreads / 32 ? sums[q][lane] : Long{0.f, 0.f});
-      const int k = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? counts[q][lane] : 0);
-      cnt[q] = g.average ? (float)max(k, 1) : 1.f;
-      if (g.average) r[q] = r[q].over(cnt[q]);
-      if (g.seq_logp && lane == 0) g.seq_logp[2 * i + q] = r[q].value();
-      if (g.ref) r[q].add(-ref[q]);
+      count[q] = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? counts[q][lane] : 0);
     }
-    Long d = r[0];
-    d.add(Long{-r[1].hi, -r[1].lo});
-    const float h = d.value(), x = g.beta * h - g.margin;
-    float loss, dh;
-    if (g.kind == MOE_LORA_PREF_SIGMOID) {
-      const float e = expf(-fabsf(x)), soft = log1pf(e), near = e / (1.f + e);  // 1 - sigmoid(|x|)
-      loss = (1.f - g.smooth) * (soft + fmaxf(-x, 0.f)) + g.smooth * (soft + fmaxf(x, 0.f));
-      // sigmoid(x) - (1 - smooth) without the difference of two numbers near 1
-      dh = g.beta * (x >= 0.f ? g.smooth - near : near - (1.f - g.smooth));
-    } else if (g.kind == MOE_LORA_PREF_SQUARED) {
-      d.add(-g.target.hi);
-      d.lo -= g.target.lo;
-      const float o = d.value();
-      loss = o * o;
-      dh = 2.f * o;
-    } else {
-      loss = fmaxf(1.f - x, 0.f);
-      dh = x < 1.f ? -g.beta : 0.f;
-    }
-    if (isnan(x)) loss = dh = x;
+    const float2 each = pair_terms(g, ad, i, a, r, count, ref, up);
     if (lane == 0) {
-      float* to = g.terms + i;
-      to[0] = loss;
-      to[g.pairs] = x > 0.f ? 1.f : 0.f;
-      to[2 * g.pairs] = g.beta * r[0].value();
-      to[3 * g.pairs] = g.beta * r[1].value();
-      to[4 * g.pairs] = h;
-      const float each = up / (float)(ad.off[a + 1] - ad.off[a]);
-      per_token[0] = each * dh / cnt[0];
-      per_token[1] = -each * dh / cnt[1];
+      per_token[0] = each.x;
+      per_token[1] = each.y;
     }
   }
   if (g.dlogp) {
@@ -877,8 +940,21 @@ __global__ void __launch_bounds__(kThreads) pref_kernel(const __grid_constant__ 
       }
     }
   }
-  if (g.few && warp == 0 && came_last(g.ticket, (unsigned)g.pairs))
-    sum_terms_here(g.terms, g.pairs, ad, [&](int a) { return 1.f / (float)max(ad.off[a + 1] - ad.off[a], (int64_t)1); }, g.loss, g.stats);
+  if (!g.few) return;
+  if (g.dlogp) __syncthreads();  // the block's gradients are written before it counts as done
+  if (warp == 0 && came_last(g.ticket, (unsigned)g.pairs)) {
+    const bool again = __ldcg(g.again);  // on its way while the terms are
+    const auto sum = [&] {
+      sum_terms_here(g.terms, g.pairs, ad, [&](int a) { return 1.f / (float)max(ad.off[a + 1] - ad.off[a], (int64_t)1); }, g.loss, g.stats);
+    };
+    sum();
+    if (again) {
+      pairs_again(g, ad, 0, g.pairs);
+      __syncwarp();
+      sum();
+      if (lane == 0) *g.again = 0;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -1003,13 +1079,15 @@ int make_ranges(int A, const int64_t* off, int64_t n, Ranges* r) {
   return r->off[0] != 0 || r->off[A] != n ? MOE_LORA_ERR_DIMS : MOE_LORA_OK;
 }
 
-int launch_sums(const SumArgs& g, const Ranges& ad, cudaStream_t s) {
+template <bool kPairs>
+int launch_sums(const SumArgs& g, const Ranges& ad, const PrefArgs& pref, cudaStream_t s) {
   int64_t most = 0;
   for (int a = 0; a < ad.n; ++a) most = std::max(most, ad.off[a + 1] - ad.off[a]);
   const bool one = most <= kSumThreads;
   const RowLaunch l((int64_t)ad.n * (one ? 1 : kSumCluster), kSumThreads, 0, one ? 1 : kSumCluster, true, s);
   prof_begin(K_TERM_SUM, s);
-  const cudaError_t e = one ? cudaLaunchKernelEx(&l.cfg, term_sum_kernel<1>, g, ad) : cudaLaunchKernelEx(&l.cfg, term_sum_kernel<kSumCluster>, g, ad);
+  const cudaError_t e = one ? cudaLaunchKernelEx(&l.cfg, term_sum_kernel<1, kPairs>, g, ad, pref)
+                            : cudaLaunchKernelEx(&l.cfg, term_sum_kernel<kSumCluster, kPairs>, g, ad, pref);
   prof_end(K_TERM_SUM, s);
   return e == cudaSuccess ? MOE_LORA_OK : MOE_LORA_ERR_CUDA;
 }
@@ -1113,7 +1191,7 @@ extern "C" int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_polic
                                      : run_policy<__half>(g, pg, dg, ad, sms, !weight && !few, s);
     if (rc || few) return rc;
   }
-  return launch_sums(SumArgs{terms, r->rows, weight ? nullptr : count, false, loss, stats}, ad, s);
+  return launch_sums<false>(SumArgs{terms, r->rows, weight ? nullptr : count, false, loss, stats}, ad, {}, s);
 }
 
 extern "C" size_t moe_lora_preference_scratch_bytes(int64_t pairs) {
@@ -1143,12 +1221,13 @@ extern "C" int moe_lora_preference_loss(const moe_lora_preference* o, const floa
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* terms = reinterpret_cast<float*>(static_cast<char*>(scratch) + kTicketBytes);
+  unsigned* ticket = static_cast<unsigned*>(scratch);
+  const bool few = o->pairs <= kFewPairs;
+  const double target = 0.5 / (double)o->beta;
+  const PrefArgs g{logp, targets, o->tokens, seq_offsets, ref, o->beta, o->margin, o->label_smoothing, o->kind, o->average,
+                   dloss, seq_logp, dlogp, terms, o->pairs, err, Long{(float)target, (float)(target - (float)target)},
+                   few, ticket, ticket + 1, loss, stats};
   if (o->pairs > 0) {
-    const bool few = o->pairs <= kFewPairs;
-    const double target = 0.5 / (double)o->beta;
-    const PrefArgs g{logp, targets, o->tokens, seq_offsets, ref, o->beta, o->margin, o->label_smoothing, o->kind, o->average,
-                     dloss, seq_logp, dlogp, terms, o->pairs, err, Long{(float)target, (float)(target - (float)target)},
-                     few, static_cast<unsigned*>(scratch), loss, stats};
     // few pairs of more tokens than a small block has under way get large blocks: 16 of 40,000 tokens
     // 21 us instead of 39, 64 of 8,000 8.5 and 9.7; but 512 of 6,000 22 and 15
     const bool wide = o->pairs <= sms && o->tokens / o->pairs >= 256 * 4 * kPrefAhead;
@@ -1161,5 +1240,5 @@ extern "C" int moe_lora_preference_loss(const moe_lora_preference* o, const floa
     if (cudaGetLastError() != cudaSuccess) return MOE_LORA_ERR_CUDA;
     if (few) return MOE_LORA_OK;
   }
-  return launch_sums(SumArgs{terms, o->pairs, nullptr, true, loss, stats}, ad, s);
+  return launch_sums<true>(SumArgs{terms, o->pairs, nullptr, true, loss, stats}, ad, g, s);
 }

@@ -1,0 +1,87 @@
+"""Post-training operators at the ends of their arguments' ranges, against 64-bit definitions."""
+import math
+
+import pytest
+import torch
+
+import moe_expert_ffn_top_gb300 as m
+import post_ref as ref
+from post_ref import U32
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+INF = math.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from moe_expert_ffn_top_gb300 import _build
+    _build.build()
+    torch.cuda.set_device(0)
+    yield
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _within(name, got, want, tol):
+    off = (got.double() - want.double()).abs()
+    assert (off <= tol).all(), (name, float((off - tol).max()), float(off.max()))
+
+
+def _corrected(seq, T):
+    out, at = [], 0
+    for v in seq:
+        at = min(max(at, v), T)
+        out.append(at)
+    return out
+
+
+BAD_SEQ = [([0, 10, 5, 20, 30], 20), ([-4, 10, 12, 15, 20], 20), ([0, 1 << 60, 3, 4, 5], 20), ([0, 5, 9, -(1 << 60), 20], 20),
+           ([0, 40, 50, 60, 3, 5, 8, 9, 80], 100), ([7, 30, 2, 9, 4, 60, 50, 55, 70], 90), ([30, 30, 29, 29, 28, 90, 10, 100, 90], 95), ([5, 2, 3], 50), ([0, 9000, 4000, 12000, 15000], 20000)]
+
+
+def _check_offsets(seq, T, average=False, scratch=None):
+    g = _gen(T + len(seq))
+    lp, y = -torch.rand(T, generator=g, device="cuda"), torch.where(torch.rand(T, generator=g, device="cuda") < 0.2, -1, 1).to(torch.int32)
+    P = len(seq) // 2
+    good = _corrected(seq, T)
+    scratch = m.preference_scratch(P) if scratch is None else scratch
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    d = torch.full((T,), 5.0, device="cuda")
+    loss, stats, sl = torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda"), torch.empty(2 * P, device="cuda")
+    beta = torch.tensor(0.1).item()
+    m.moe_lora_preference_loss(lp, y, torch.tensor(seq, device="cuda"), None, loss, stats, scratch, beta=beta, average=average, seq_logp=sl,
+                               dlogp=d, err=err)
+    assert int(err) == (m.MOE_LORA_DEV_BAD_ID if good != list(seq) else 0)
+    wl, ws, wt, wd = ref.preference(lp, y, good, None, [0, P], None, beta, "sigmoid", 0.0, 0.0, average)
+    _within("sums", sl.cpu(), wt, 4 * U32 * wt.abs())
+    assert abs(float(loss) - float(wl)) <= 1e-5 * (1 + abs(float(wl)))
+    inside = ~torch.isnan(wd)
+    assert (d.cpu()[~inside] == 5.0).all()
+    # x is off by beta times the sums' rounding, and the loss's slope by that much
+    size = float(wt.abs().max())
+    _within("dlogp", d.cpu()[inside], wd[inside], beta / P * (32 * U32 + beta * 8 * U32 * size))
+
+
+@pytest.mark.parametrize("seq,T", BAD_SEQ)
+@pytest.mark.parametrize("average", [False, True])
+def test_offsets_that_go_back(seq, T, average):
+    """An offset below one before it, or past the tokens, counts as the nearest that is not; no token belongs to two pairs."""
+    _check_offsets(seq, T, average)
+
+
+@pytest.mark.parametrize("pairs", [200, 300, 2047, 2048, 2049, 5000, 9000])
+def test_offsets_that_go_back_in_long_lists(pairs):
+    """The largest offset so far may lie far before a pair's own."""
+    g = torch.Generator().manual_seed(pairs)
+    base = torch.randint(0, 6, (2 * pairs + 1,), generator=g).cumsum(0)
+    T = int(base[-1])
+    scratch = m.preference_scratch(pairs)  # a call does not see what an earlier list was
+    for at, to in ((None, 0), (3, T // 3), (2 * pairs // 2, T * 3 // 4), (min(4095, 2 * pairs - 1), int(base[min(4095, 2 * pairs - 1)]) + 40), (2 * pairs - 1, 1 << 50),
+                   (min(4096, 2 * pairs), 2), (None, 0)):
+        seq = base.clone()
+        if at is not None:
+            seq[at] = to
+        _check_offsets(seq.tolist(), T, scratch=scratch)
