@@ -550,7 +550,7 @@ MOE_LORA_API int moe_lora_preference_loss(const moe_lora_preference* opt, const 
  * that directions that start small keep their precision: X is within about 1e-5 (its 2-norm) of the
  * definition for usual spectra and 1e-4 for the hardest ones.  It holds for coefficients that keep the
  * singular values below 4 (the usual ones: below 1.3).  A matrix whose |u| is not finite, or whose
- * square passes fp32's range, gives NaN in its own m or weights alone; one whose |u| is below 2^-60
+ * square passes fp32's range, gives NaN in its own m or weights alone; one whose |u| is at most 2^-60
  * counts as 0. */
 typedef struct moe_lora_muon_tensor {
   void* p;       /* [batch, rows, cols] parameter, read (unless master is given) and written */

@@ -56,6 +56,12 @@ constexpr int kPart = kTile * kChunk * 2;              // bytes of a part of a c
 constexpr int kTileBytes = kTile * kTile * 2;          // of a part of a square tile
 constexpr int kImage = 2 * kPart;                      // X of a chunk in the scratch: both parts as they lie in shared memory
 constexpr int kPoly = 2 * kTileBytes;                  // P of a tile, the same
+// A matrix's norm from its square.  One of at most 2^-60 counts as 0: the parts of its squares run out of
+// fp32's range, and so does (1 / norm)^2 kGScale.
+__device__ __forceinline__ float counted_norm(float n2) {
+  const float norm = sqrtf(n2);
+  return norm > 0x1p-60f ? norm : 0.f;
+}
 // Powers of two that bring values into the middle of fp16's range.
 constexpr float kXScale = 1024.f, kGScale = 256.f, kQScale = 64.f;
 
@@ -649,9 +655,9 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
 #pragma unroll 8
         for (int i = lo; i < hi; ++i) n2 += diag[col + i];
       }
-      // a norm whose square fp32 does not hold: 0, or not finite, which is passed on as NaN
+      // a norm whose square fp32 does not hold counts as 0, or is not finite, which is passed on as NaN
       fine = n2 < INFINITY;
-      const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
+      const float norm = fine ? counted_norm(n2) : 0.f, inv = 1.f / (norm + tab.eps);
       // X = u / (norm + eps) = (u * up) * down, up a power of two that makes the matrix's norm 2^9 to 2^10
       const float up = norm > 0.f ? ldexpf(1.f, 9 - ilogbf(norm)) : 0.f;
       unit = norm > 0.f ? inv * inv : 0.f;
@@ -813,7 +819,7 @@ __device__ __forceinline__ void small_polys(const MuonTable& tab, const MuonTens
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
       const bool fine = n2 < INFINITY;
-      const float norm = fine ? sqrtf(n2) : 0.f, inv = 1.f / (norm + tab.eps);
+      const float norm = fine ? counted_norm(n2) : 0.f, inv = 1.f / (norm + tab.eps);
       const float up = norm > 0.f ? ldexpf(1.f, 9 - ilogbf(norm)) : 0.f;
       unit = norm > 0.f ? inv * inv : 0.f;
       if (in) {

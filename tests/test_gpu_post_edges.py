@@ -85,3 +85,34 @@ def test_offsets_that_go_back_in_long_lists(pairs):
         if at is not None:
             seq[at] = to
         _check_offsets(seq.tolist(), T, scratch=scratch)
+
+
+# ------------------------------------------------------------------ Muon
+@pytest.mark.parametrize("shape", [(16, 200), (200, 16), (64, 300), (300, 64), (128, 640), (31, 90), (13, 77)])
+def test_smallest_norms(shape):
+    """A matrix whose |u| is at most 2^-60 counts as 0, one above takes a whole step, whatever eps leaves of it."""
+    sizes = (-57.5, -58.5, -59.5, -59.9, -60.1, -60.5, -61.5, -62.5, -63.5, -64.5, -66.0, -72.0, -80.0)
+    u = torch.randn(len(sizes), *shape, generator=_gen(sum(shape)), device="cuda").double()
+    u = (u / u.flatten(1).norm(dim=1)[:, None, None] * (2.0 ** torch.tensor(sizes, dtype=torch.float64, device="cuda"))[:, None, None]).float()
+    p, mom = torch.zeros_like(u), torch.zeros_like(u)
+    t = m.MuonTensors([dict(p=p, g=u, m=mom, lr=-1.0, scale=1.0)])
+    m.moe_lora_muon_step(t, momentum=0.0, nesterov=False, eps=1e-30)
+    want = ref.newton_schulz(u, 5, (3.4445, -4.7750, 2.0315), 1e-30)
+    assert torch.equal(mom, u)
+    for i, size in enumerate(sizes):
+        if size <= -60:
+            assert (p[i] == 0).all(), size
+        else:
+            # 2e-4 as for the hardest spectra: at 2^-60 the squares' sums keep 2^-29 of |u|^2 in steps of the smallest number
+            assert float((p[i].double() - want[i]).norm() / want[i].norm()) <= 2e-4, size
+
+
+def test_norm_at_the_border():
+    for eps in (1e-30,):
+        u = torch.tensor([2.0 ** -60, 2.0 ** -60 * (1 + 2.0 ** -20), -(2.0 ** -59)], device="cuda").view(3, 1, 1)
+        p = torch.zeros_like(u)
+        t = m.MuonTensors([dict(p=p, g=u, m=torch.zeros_like(u), lr=-1.0, scale=1.0)])
+        m.moe_lora_muon_step(t, momentum=0.0, nesterov=False, eps=eps)
+        want = ref.newton_schulz(u, 5, (3.4445, -4.7750, 2.0315), eps)
+        assert float(p[0]) == 0.0
+        assert ((p[1:].double() - want[1:]).abs() <= 2e-4 * want[1:].abs()).all()
