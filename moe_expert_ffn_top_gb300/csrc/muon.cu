@@ -64,6 +64,15 @@ __device__ __forceinline__ float counted_norm(float n2) {
 }
 // Powers of two that bring values into the middle of fp16's range.
 constexpr float kXScale = 1024.f, kGScale = 256.f, kQScale = 64.f;
+// X's where the norm is far below eps and with it X = u / (norm + eps): 2^k kXScale, k for singular values
+// of at most 1 / 4, so that the first steps (a factor of 64 at most) stay in the range; kXScale from about
+// 1 / 8 on.  `factor` is the matrix's (see MuonTable): 2^9 to 2^10 of it make the norm of X.
+__device__ __forceinline__ int x_shift(float factor) {
+  return factor > 0.f ? max(0, 127 - 13 - (int)(__float_as_uint(factor) >> 23)) : 0;
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ float x_scale(float factor) { return kXScale * two_to(x_shift(factor)); }
+__device__ __forceinline__ float x_unit(float factor) { return 1.f / kXScale * two_to(-x_shift(factor)); }
 
 struct MuonTensor {
   void* p;
@@ -84,7 +93,7 @@ struct MuonTable {
   const float* gs;
   int* err;
   float *gram, *norm;            // [tiles + blocks][128][128], [tiles][2][128]: scale and factor of a row's matrix
-  uint8_t *poly, *x;             // [tiles][kPoly], [chunks][kImage]
+  uint8_t *poly, *x;             // [tiles][kPoly], [chunks][kImage]: X times x_scale
   MuonTensor t[kMaxTensors];
 };
 static_assert(sizeof(MuonTable) <= 32764, "kernel parameter limit");
@@ -542,7 +551,7 @@ __device__ __forceinline__ void tmem_put_row32(uint32_t base, int col, const flo
 }
 
 // `first`: G is of the update itself, whose norm is taken here.  Otherwise G is of X in the
-// scratch, times kXScale^2.  Blocks work through tiles one after the other; the sums of the next are on
+// scratch, times x_scale^2.  Blocks work through tiles one after the other; the sums of the next are on
 // their way while the last product of one runs.  Where all matrices of a tile have s = 64 or less, most of
 // a square tile is 0: only warps whose rows and columns meet a matrix work on it.
 __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid_constant__ MuonTable tab, int tiles, int steps, bool first) {
@@ -571,14 +580,15 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
     while (ti + 1 < tab.n && tile >= tab.t[ti + 1].tile0) ++ti;
     return ti;
   };
-  // This thread's share of the sums of a tile's stretches, in order.
-  float sum[kEach];
+  // This thread's share of the sums of a tile's stretches, in order, and the factor of its row's matrix.
+  float sum[kEach], factor = 0.f;
   const auto load_sums = [&](int tile) {
     const MuonTensor& t = tab.t[tensor_of(tile)];
     const int x = t.chunk0 + (tile - t.tile0) * t.chunks;
     const int64_t s0 = stretch_slot(tab, tile, x);
     const int stretches = (int)(stretch_slot(tab, tile, x + t.chunks - 1) - s0) + 1;
     const float* in = tab.gram + s0 * kTile * kTile + threadIdx.x;
+    if (!first) factor = tab.norm[(int64_t)tile * 2 * kTile + kTile + row];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) sum[i] = in[i * kPolyThreads];
     for (int p = 1; p < stretches; ++p)
@@ -639,9 +649,11 @@ __global__ void __launch_bounds__(kPolyThreads, 1) muon_poly_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = e[row * (kTile + 1) + col + i] + e[(col + i) * (kTile + 1) + row];
     }
-    float unit = 1.f / (kXScale * kXScale);  // X in the scratch is scaled
+    float unit = 1.f;
     bool fine = true;
-    if (first) {
+    if (!first) {  // X in the scratch is scaled
+      unit = x_unit(factor) * x_unit(factor);
+    } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (col + i == row) diag[row] = v[i];
@@ -811,8 +823,11 @@ __device__ __forceinline__ void small_polys(const MuonTable& tab, const MuonTens
       for (int i = 0; i < S; ++i)
         if (in && i < s) g[i] += e[(at + i) * kTile + at + lane] + e[(at + lane) * kTile + at + i];
     }
-    float unit = 1.f / (kXScale * kXScale);
-    if (first) {  // as in the kernel above
+    float unit = 1.f;
+    if (!first) {
+      const float factor = norms[kTile + at];
+      unit = x_unit(factor) * x_unit(factor);
+    } else {  // as in the kernel above
       float n2 = 0.f;
 #pragma unroll
       for (int i = 0; i < S; ++i) n2 += i == lane ? g[i] : 0.f;
@@ -951,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_apply_kernel(const __grid_co
     __syncthreads();  // the last stretch's scales have been read
     if (threadIdx.x < kTile) row_up[threadIdx.x] = norm[threadIdx.x];
     // P's scale, and the factor that makes the products X
-    const float factor = norm[kTile + r], down = factor == factor ? factor * (kXScale / kQScale) : 0.f;
+    const float factor = norm[kTile + r], down = factor == factor ? factor * (x_scale(factor) * (1.f / kQScale)) : 0.f;
     with_kind(t.g_dtype, quads_aligned(t), [&](auto type, auto quads) {
       constexpr int kType = decltype(type)::value;
       constexpr bool kAligned = decltype(quads)::value;
@@ -1089,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_update_kernel(const __grid_c
     copy_async<kImage>(xt, image);
     const float factor = tab.norm[(int64_t)pl.tile * 2 * kTile + kTile + my_row()];
     // NaN for a matrix whose norm is not finite
-    const float f = (factor == factor ? 1.f : factor) * (1.f / (kXScale * kQScale));
+    const float f = (factor == factor ? 1.f : factor) * (x_unit(factor) * (1.f / kQScale));
     const bool aligned = quads_aligned(t), tall = t.tall;
     const void* const wp = in_register(kMaster ? static_cast<void*>(t.master) : t.p);
     void* const pp = in_register(t.p);

@@ -108,7 +108,7 @@ def test_smallest_norms(shape):
 
 
 def test_norm_at_the_border():
-    for eps in (1e-30,):
+    for eps in (1e-30, 1e-7):
         u = torch.tensor([2.0 ** -60, 2.0 ** -60 * (1 + 2.0 ** -20), -(2.0 ** -59)], device="cuda").view(3, 1, 1)
         p = torch.zeros_like(u)
         t = m.MuonTensors([dict(p=p, g=u, m=torch.zeros_like(u), lr=-1.0, scale=1.0)])
@@ -116,3 +116,21 @@ def test_norm_at_the_border():
         want = ref.newton_schulz(u, 5, (3.4445, -4.7750, 2.0315), eps)
         assert float(p[0]) == 0.0
         assert ((p[1:].double() - want[1:]).abs() <= 2e-4 * want[1:].abs()).all()
+
+
+@pytest.mark.parametrize("eps", [1e-7, 1e-3, 1.0])
+@pytest.mark.parametrize("shape", [(16, 200), (200, 16), (64, 300), (300, 64), (128, 640), (31, 90), (1, 7)])
+def test_norms_below_eps(shape, eps):
+    """X keeps its relative precision where |u| is far below eps: neighbours of one tile, each of another size."""
+    sizes = (30.0, 3.0, 1.0, 0.2, 0.03, 1e-3, 1e-5, 1e-7, 1e-10, 0.5)
+    u = torch.randn(len(sizes), *shape, generator=_gen(sum(shape)), device="cuda").double()
+    u = (u / u.flatten(1).norm(dim=1)[:, None, None] * (eps * torch.tensor(sizes, dtype=torch.float64, device="cuda"))[:, None, None]).float()
+    small = u[[i for i, v in enumerate(sizes) if v <= 1e-5]].clone()  # whose singular values stay below 4 with the last coefficients
+    for u, steps, coefs in ((u, 5, (3.4445, -4.7750, 2.0315)), (u, 1, (3.4445, -4.7750, 2.0315)), (small, 5, (8.0, -12.0, 4.9))):
+        p = torch.zeros_like(u)
+        t = m.MuonTensors([dict(p=p, g=u, m=torch.zeros_like(u), lr=-1.0, scale=1.0)])
+        m.moe_lora_muon_step(t, momentum=0.0, nesterov=False, eps=eps, steps=steps, coefs=coefs)
+        want = ref.newton_schulz(u, steps, coefs, eps)
+        off = (p.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+        # factors to 2^-22 and fp32 sums, as for the hardest spectra
+        assert float(off.max()) <= 2e-4, off.tolist()
