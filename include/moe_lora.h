@@ -506,7 +506,8 @@ MOE_LORA_API int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_pol
  *     squared: l = (h - 1 / (2 beta))^2        hinge: l = max(0, 1 - x)
  *     loss_a = mean of l over the pairs of adapter a (0 without pairs),
  *     dlogp_t = dloss_a / pairs_a * dl/dh * (+1 chosen, -1 rejected) (average: / live tokens of j).
- *   logp [tokens] fp32, e.g. moe_lora_token_logp_forward's; targets [tokens] int32
+ *   logp [tokens] fp32, e.g. moe_lora_token_logp_forward's (-inf at a masked target makes s_j -inf, and the
+ *            loss and gradients what the formulas give there); targets [tokens] int32
  *   seq_offsets [2 pairs + 1] int64, DEVICE.  An offset below one before it or above tokens is taken
  *            as the nearest that is not (offset j as the largest of 0 and offsets 0 .. j, at most
  *            tokens), so that no token belongs to two sequences, and sets MOE_LORA_DEV_BAD_ID in *err.

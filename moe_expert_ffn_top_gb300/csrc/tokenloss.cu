@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(256) token_count_kernel(const int32_t* targets
 
 // ------------------------------------------------------------------ preference loss
 // A sum as an fp32 number and what its rounding left: a loss lives on the difference of two large
-// sums, and fp64 additions are slow here.
+// sums, and fp64 additions are slow here.  Once a sum is infinite what is left is NaN and does not count.
 struct Long {
   float hi, lo;
   __device__ __forceinline__ void add(float v) {  // exactly
@@ -632,7 +632,7 @@ struct Long {
     add(v.hi);
     lo += v.lo;
   }
-  __device__ __forceinline__ float value() const { return hi + lo; }
+  __device__ __forceinline__ float value() const { return isinf(hi) ? hi : hi + lo; }
   __device__ __forceinline__ Long over(float n) const {
     const float q = hi / n;
     return Long{q, (fmaf(-q, n, hi) + lo) / n};
@@ -681,7 +681,8 @@ __device__ __forceinline__ float2 pair_terms(const PrefArgs& g, const Ranges& ad
   float loss, dh;
   if (g.kind == MOE_LORA_PREF_SIGMOID) {
     const float e = expf(-fabsf(x)), soft = log1pf(e), near = e / (1.f + e);  // 1 - sigmoid(|x|)
-    loss = (1.f - g.smooth) * (soft + fmaxf(-x, 0.f)) + g.smooth * (soft + fmaxf(x, 0.f));
+    loss = (1.f - g.smooth) * (soft + fmaxf(-x, 0.f));
+    if (g.smooth > 0.f) loss += g.smooth * (soft + fmaxf(x, 0.f));  // (x may be infinite)
     // sigmoid(x) - (1 - smooth) without the difference of two numbers near 1
     dh = g.beta * (x >= 0.f ? g.smooth - near : near - (1.f - g.smooth));
   } else if (g.kind == MOE_LORA_PREF_SQUARED) {

@@ -134,3 +134,63 @@ def test_norms_below_eps(shape, eps):
         off = (p.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
         # factors to 2^-22 and fp32 sums, as for the hardest spectra
         assert float(off.max()) <= 2e-4, off.tolist()
+
+
+# ------------------------------------------------------------------ preference loss
+@pytest.mark.parametrize("kind,smooth", [("sigmoid", 0.0), ("sigmoid", 0.1), ("hinge", 0.0), ("squared", 0.0)])
+@pytest.mark.parametrize("average", [False, True])
+@pytest.mark.parametrize("each,length", [(1, 5), (120, 7), (2, 3000)])
+def test_infinite_log_probabilities(kind, smooth, average, each, length):
+    """A masked token's log probability of -inf makes its sequence's sum -inf: losses and gradients by the definition.
+    Adapters: chosen answers of that kind, rejected ones, and neither."""
+    P, T = 3 * each, 2 * 3 * each * length
+    lp = -torch.rand(T, generator=_gen(each), device="cuda") - 0.1
+    y = torch.ones(T, dtype=torch.int32, device="cuda")
+    seq = torch.arange(0, T + 1, length, device="cuda")
+    rows = lp.view(P, 2, length)
+    rows[:each, 0, length // 2] = -INF
+    rows[each:2 * each, 1, length - 1] = -INF
+    y.view(P, 2, length)[2 * each:, :, 0] = -1
+    rows[2 * each:, :, 0] = -INF  # tokens without a target may hold anything
+    beta = torch.tensor(0.2).item()
+    smooth = torch.tensor(smooth).item()
+    loss, stats = torch.full((3,), 9.0, device="cuda"), torch.full((3, 4), 9.0, device="cuda")
+    sl, dl = torch.full((2 * P,), 9.0, device="cuda"), torch.full((T,), 9.0, device="cuda")
+    m.moe_lora_preference_loss(lp, y, seq, None, loss, stats, m.preference_scratch(P, 3), beta=beta, kind=kind, label_smoothing=smooth, average=average,
+                               pair_offsets=[0, each, 2 * each, P], seq_logp=sl, dlogp=dl)
+    clean = torch.where(y > 0, lp, 0.0).double().view(P, 2, length).sum(2)
+    n = torch.full((P, 1), length if average else 1, device="cuda")
+    if average:
+        n[2 * each:] = length - 1
+    s = clean / n
+    assert (sl.view(P, 2)[:each, 0] == -INF).all() and (sl.view(P, 2)[each:2 * each, 1] == -INF).all()
+    fin = torch.isfinite(s)
+    # a sum of `length` values in pairs of fp32 numbers, a division, one rounding
+    _within("sums", sl.view(P, 2)[fin], s[fin], 4 * U32 * s[fin].abs())
+    h = s[:, 0] - s[:, 1]
+    x = beta * h
+    if kind == "sigmoid":
+        l = (1 - smooth) * torch.where(x < 0, -x, 0.0) + (smooth * torch.where(x > 0, x, 0.0) if smooth else 0.0) + torch.log1p(torch.exp(-x.abs()))
+        d = beta * (smooth - 1 / (1 + torch.exp(x)))
+    elif kind == "hinge":
+        l, d = (1 - x).clamp(min=0), torch.where(x < 1, -beta, 0.0)
+    else:
+        l, d = (h - 0.5 / beta) ** 2, 2 * (h - 0.5 / beta)
+    want = l.view(3, each).mean(1)
+    for a in range(3):
+        if math.isinf(float(want[a])):
+            assert float(loss[a]) == INF, a
+        else:
+            assert abs(float(loss[a]) - float(want[a])) <= 1e-5 * (1 + abs(float(want[a]))), a
+    assert float(stats[0, 0]) == 0 and abs(float(stats[1, 0]) - 1) <= 4 * U32 and float(stats[0, 1]) == -INF and float(stats[1, 2]) == -INF
+    assert float(stats[0, 3]) == -INF and float(stats[1, 3]) == INF
+    assert torch.isfinite(stats[2]).all() and torch.isfinite(stats[0, 2]) and torch.isfinite(stats[1, 1])
+    g = (d / each)[:, None] / n
+    g = torch.stack([g[:, 0], -g[:, 0]], 1)[:, :, None].expand(P, 2, length)
+    g = torch.where(y.view(P, 2, length) > 0, g, 0.0)
+    got = dl.view(P, 2, length).double()
+    # by its formula: sigma, two products, a division; (h - 1 / (2 beta)) for the squared kind
+    assert (torch.isnan(got) == False).all() and torch.equal(torch.isinf(got), torch.isinf(g))  # noqa: E712
+    assert (torch.sign(got) == torch.sign(g)).all()
+    f = torch.isfinite(g)
+    assert ((got[f] - g[f]).abs() <= 2e-5 * g[f].abs() + 1e-6 / each).all()
