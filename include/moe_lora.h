@@ -450,7 +450,7 @@ typedef struct moe_lora_rows {
  * any other target outside [0, n) counts as -1 and sets MOE_LORA_DEV_BAD_ID in *err.  z
  * below about -7e5 (-inf, masks of a type's lowest value) counts as -7e5: next to any other its
  * probability is 0, and a row of nothing else is uniform; a target at -inf has logp -inf.  NaN, +inf and
- * z beyond fp32 give NaN.
+ * z above 1e38 give NaN.
  *   targets [rows] int32; logp, lse, entropy [rows] fp32, each may be NULL (not all three)
  *   err     DEVICE word (4-byte aligned) whose bits are set and never cleared, or NULL */
 MOE_LORA_API int moe_lora_token_logp_forward(const moe_lora_rows* r, const void* logits, const int32_t* targets,

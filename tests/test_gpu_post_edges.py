@@ -7,6 +7,7 @@ import torch
 import moe_expert_ffn_top_gb300 as m
 import post_ref as ref
 from post_ref import U32
+from train_ops_ref import TINY_OF, UNIT
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -194,3 +195,76 @@ def test_infinite_log_probabilities(kind, smooth, average, each, length):
     assert (torch.sign(got) == torch.sign(g)).all()
     f = torch.isfinite(g)
     assert ((got[f] - g[f]).abs() <= 2e-5 * g[f].abs() + 1e-6 / each).all()
+
+
+# ------------------------------------------------------------------ logits far from 0
+# type, common offset, spread around it, inverse temperature
+FAR = [(F32, 1e6, 3.0, 1.0), (F32, 3e7, 30.0, 1.0), (HF, 3e4, 1e3, 1e6), (F32, 3e9, 3e3, 1.0), (F32, 3e9, 3e3, 1.3), (F32, 1e12, 1e6, 1.7),
+       (BF, 1e30, 1e28, 1.0), (F32, 4e10, 1e6, 1e-6), (F32, 5e37, 1e33, 1.0)]
+
+
+def _far_rows(rows, n, dt, offset, spread, seed):
+    """Rows around an offset; in some, two entries share the largest value, and some have masked entries."""
+    g = _gen(seed)
+    x = (offset + spread * torch.randn(rows, n, generator=g, device="cuda").double()).to(dt)
+    y = torch.randint(0, n, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    top = x.argmax(1)
+    y[::3] = top[::3].to(torch.int32)
+    x[1::4, 3 % n] = x.amax(1)[1::4]
+    x[2::4, n // 2:] = torch.finfo(dt).min
+    x[3::4, : n // 2] = -INF
+    y[2::4] %= n // 2
+    y[3::4] = y[3::4] % (n - n // 2) + n // 2
+    y[rows // 2] = -1
+    return g, x, y
+
+
+def _tokens(x, y, it):
+    """ref.tokens, with entries of -inf as such, and one rounding more in every exponent than it allows (from x c of 2^31
+    on a target's distance from the largest logit is formed first, then multiplied)."""
+    z = x.double() * it
+    r = ref.tokens(torch.where(torch.isinf(x), torch.finfo(F32).min, x.double()), y, it)
+    p = r["p"]
+    far = torch.where(p > 0, (z.amax(1, keepdim=True) - z).abs(), 0.0)
+    one = U32 * (p * far).sum(1)
+    r["tol"]["p"] = r["tol"]["p"] + U32 * far + one[:, None]
+    r["tol"]["logp"] = r["tol"]["logp"] + one + U32 * torch.where(torch.isfinite(r["logp"]), r["logp"].abs(), 0.0)
+    r["tol"]["lse"] = r["tol"]["lse"] + one
+    r["tol"]["entropy"] = r["tol"]["entropy"] + one + U32 * (p * far * far).sum(1)
+    return r
+
+
+@pytest.mark.parametrize("rows,n", [(9, 300), (9, 5000), (5, 40000), (130, 5003), (2500, 1501)])
+@pytest.mark.parametrize("dt,offset,spread,it", FAR)
+def test_far_logits(rows, n, dt, offset, spread, it):
+    """Softmax does not depend on a common offset: log probabilities, entropies, policy loss and its gradient."""
+    it = torch.tensor(it).item()
+    g, x, y = _far_rows(rows, n, dt, offset, spread, rows + n)
+    r = _tokens(x, y, it)
+    out = [torch.full((rows,), 9.0, device="cuda") for _ in range(3)]
+    m.moe_lora_token_logp_forward(x, y, *out, inv_temp=it)
+    for name, got in zip(("logp", "lse", "entropy"), out):
+        _within(name, got, torch.where(r["ok"], r[name], 0.0), torch.where(r["ok"], r["tol"][name], 0.0))
+    alone = torch.full((rows,), 9.0, device="cuda")
+    m.moe_lora_token_logp_forward(x, y, alone, inv_temp=it)
+    _within("logp alone", alone, torch.where(r["ok"], r["logp"], 0.0), torch.where(r["ok"], r["tol"]["logp"], 0.0))
+    # the ratio is near 1 for half of the rows, and far below its border for the others
+    lp = r["logp"].clamp(-1e30, 0)
+    old = (lp + 0.1 * torch.randn(rows, generator=g, device="cuda").clamp(-1, 1)).float()
+    old[1::2] = -0.5 * torch.rand(rows, generator=g, device="cuda")[1::2]
+    adv = torch.rand(rows, generator=g, device="cuda") + 0.1
+    r["logp"] = lp
+    # ratios that fp32 holds, of log probabilities that fp32 holds
+    keep = ((out[0].double() - old.double()).abs() < 60) & (r["tol"]["logp"] < 1e-3)
+    w = torch.where(keep, torch.rand(rows, generator=g, device="cuda") + 0.1, 0.0)
+    loss, stats, d = torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda"), torch.full_like(x, 9.0)
+    m.moe_lora_policy_loss(x, y, adv, old, None, loss, stats, m.policy_scratch(rows), weight=w, dlogits=d, inv_temp=it, clip_low=1.0, clip_high=1e30)
+    wl, ws, wd, lt, st, dtol = ref.policy(r, adv, old, None, w, [0, rows], None, it, 1.0, 1e30, 0.0)
+    _within("loss", loss, wl, lt)
+    _within("stats", stats, ws, st)
+    big = torch.finfo(dt).max
+    wd = wd.clamp(-big, big)
+    # an exponential below 2^-126 is 0, and the sum at least 2^-65 (the reference may miss the maximum by 64, half a
+    # unit of fp32 below 2^31, and is rounded up): a probability below 2^-61 may be lost
+    lost = 2.0 ** -61 * (w * adv * it).double() * torch.exp((lp - old.double()).clamp(max=60))
+    _within("dlogits", d.clamp(-big, big), wd, dtol + UNIT[dt] * (wd.abs() + dtol) + torch.where(wd != 0, TINY_OF[dt] + lost[:, None], 0.0))
