@@ -447,10 +447,10 @@ typedef struct moe_lora_rows {
 /* With z = inv_temp * logits, for row t with target y = targets[t] in [0, n):
  *     lse_t = log sum_e exp z_te,   logp_t = z_ty - lse_t,   entropy_t = lse_t - sum_e p_te z_te,
  * p = exp(z - lse).  Rows with target -1 (prompts, padding) give 0 and their logits are not read;
- * any other target outside [0, n) counts as -1 and sets MOE_LORA_DEV_BAD_ID in *err.  z
- * below about -7e5 (-inf, masks of a type's lowest value) counts as -7e5: next to any other its
- * probability is 0, and a row of nothing else is uniform; a target at -inf has logp -inf.  NaN, +inf and
- * z above 1e38 give NaN.
+ * any other target outside [0, n) counts as -1 and sets MOE_LORA_DEV_BAD_ID in *err.  A
+ * common offset of a row's z does not matter.  z below about -3e37 (-inf, masks of a type's lowest
+ * value) counts as one and the same number: next to any other its probability is 0, and a row of
+ * nothing else is uniform; a target at -inf has logp -inf.  NaN, +inf and z above 1e38 give NaN.
  *   targets [rows] int32; logp, lse, entropy [rows] fp32, each may be NULL (not all three)
  *   err     DEVICE word (4-byte aligned) whose bits are set and never cleared, or NULL */
 MOE_LORA_API int moe_lora_token_logp_forward(const moe_lora_rows* r, const void* logits, const int32_t* targets,

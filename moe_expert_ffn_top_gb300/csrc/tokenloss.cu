@@ -14,7 +14,6 @@
 // entropies of 16,384 x 65,536 bf16 348 us (5.6 TB/s, 82%), their backward 641 us (94%); the preference
 // loss of 1,024 pairs of 1,400 tokens 16 us.
 #include <math.h>
-#include <string.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -192,10 +191,9 @@ struct Softmax {
   }
 };
 
-// z in base 2 is x c.  Logits below `floor` count as `floor`: -inf, the types' lowest numbers, and
-// whatever else masks them.  Next to any other logit their probability is 0, and 0 times their
-// distance is 0, not NaN.  floor c is about -2^20, which leaves room for the fraction of x c - M; floor
-// is a bf16 number.
+// z in base 2 is x c.  Logits below `floor`, whose x up is about -2^126, count as `floor`: -inf, and the types'
+// lowest numbers where they pass that.  Next to any other logit their probability is 0, and 0 times their
+// distance is 0, not NaN.  floor is a bf16 number.
 //
 // M misses x c by 64 at most below 2^31, for which exponents have room.  From there on two different logits'
 // x c are more than 128 apart, so that next to the largest all others' probabilities are 0; with `up`, the power
@@ -1013,15 +1011,12 @@ int check_rows(const moe_lora_rows* r) {
   return MOE_LORA_OK;
 }
 RowArgs row_args(const moe_lora_rows* r, const void* x, const int32_t* targets, float* logp, float* lse, float* entropy, int32_t* err) {
-  const float c = r->inv_temp * kLog2e, floor = -1048576.f / c;
+  const float c = r->inv_temp * kLog2e;
   int e;
   const float up = frexpf(c, &e) == 0.5f ? c : ldexpf(1.f, e);
-  uint32_t bits;
-  memcpy(&bits, &floor, 4);
-  bits &= 0xFFFF0000u;  // a bf16 number
-  float cut;
-  memcpy(&cut, &bits, 4);
-  return RowArgs{x, r->ld ? r->ld : r->n, r->rows, r->n, r->inv_temp, c, up, cut, targets, logp, lse, entropy, err};
+  constexpr float kLowest = -0x1.FEp127f;  // of bf16
+  const float floor = up <= 0.25f ? kLowest : -0x1p126f / up;
+  return RowArgs{x, r->ld ? r->ld : r->n, r->rows, r->n, r->inv_temp, c, up, floor, targets, logp, lse, entropy, err};
 }
 
 template <class T, int kTeam, int kGroups, bool kEntropy, bool kPolicy, bool kGrad>

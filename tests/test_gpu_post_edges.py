@@ -199,8 +199,9 @@ def test_infinite_log_probabilities(kind, smooth, average, each, length):
 
 # ------------------------------------------------------------------ logits far from 0
 # type, common offset, spread around it, inverse temperature
-FAR = [(F32, 1e6, 3.0, 1.0), (F32, 3e7, 30.0, 1.0), (HF, 3e4, 1e3, 1e6), (F32, 3e9, 3e3, 1.0), (F32, 3e9, 3e3, 1.3), (F32, 1e12, 1e6, 1.7),
-       (BF, 1e30, 1e28, 1.0), (F32, 4e10, 1e6, 1e-6), (F32, 5e37, 1e33, 1.0)]
+FAR = [(F32, -1e6, 3.0, 1.0), (F32, 1e6, 3.0, 1.0), (F32, 3e7, 30.0, 1.0), (F32, -2e7, 30.0, 0.9), (BF, -12.0, 3.0, 1e5), (BF, 0.0, 3.0, 1e6), (BF, -9.0, 2.0, 1e6),
+       (HF, -5.0, 1.0, 1e6), (HF, 3e4, 1e3, 1e6), (F32, -300.0, 20.0, 1e5), (F32, 3e9, 3e3, 1.0), (F32, -3e9, 3e3, 1.0), (F32, 3e9, 3e3, 1.3),
+       (F32, 1e12, 1e6, 1.7), (BF, 1e30, 1e28, 1.0), (BF, -1e30, 1e28, 1.0), (F32, 4e10, 1e6, 1e-6), (F32, -2e37, 1e31, 1.0), (F32, 5e37, 1e33, 1.0)]
 
 
 def _far_rows(rows, n, dt, offset, spread, seed):
