@@ -458,7 +458,9 @@ MOE_LORA_API int moe_lora_token_logp_forward(const moe_lora_rows* r, const void*
 
 /* dlogits_te = inv_temp * dlogp_t * ([e = y_t] - exp(z_te - lse_t)), one rounding to dlogits' type.
  * Rows without a target, and rows whose dlogp is 0, get zeros and their logits are not read.
- * lse [rows] as the forward wrote it.  dlogits may be logits (ldd = ld). */
+ * lse [rows] as the forward wrote it; where |lse| is 1,024 or more, which fp32 holds coarsely,
+ * the row's sum is formed anew from its logits (three sweeps instead of one), masks as in the forward.
+ * dlogits may be logits (ldd = ld). */
 MOE_LORA_API int moe_lora_token_logp_backward(const moe_lora_rows* r, const void* logits, const int32_t* targets,
                                               const float* lse, const float* dlogp, void* dlogits, int32_t* err,
                                               void* stream);

@@ -269,3 +269,67 @@ def test_far_logits(rows, n, dt, offset, spread, it):
     # unit of fp32 below 2^31, and is rounded up): a probability below 2^-61 may be lost
     lost = 2.0 ** -61 * (w * adv * it).double() * torch.exp((lp - old.double()).clamp(max=60))
     _within("dlogits", d.clamp(-big, big), wd, dtol + UNIT[dt] * (wd.abs() + dtol) + torch.where(wd != 0, TINY_OF[dt] + lost[:, None], 0.0))
+
+
+@pytest.mark.parametrize("rows,n,pad", [(9, 300, 0), (9, 5000, 3), (5, 40000, 0), (130, 5003, 0), (2500, 1501, 0)])
+@pytest.mark.parametrize("dt,offset,spread,it", FAR)
+def test_far_logits_backward(rows, n, pad, dt, offset, spread, it):
+    """The gradient where fp32 holds lse coarsely, against the definition's own lse; into strided rows and in place."""
+    it = torch.tensor(it).item()
+    g, x, y = _far_rows(rows, n, dt, offset, spread, rows + n)
+    buf = torch.full((rows, n + pad), 7.0, dtype=dt, device="cuda")
+    buf[:, :n] = x
+    x = buf[:, :n]
+    r = _tokens(x, y, it)
+    lp, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    m.moe_lora_token_logp_forward(x, y, lp, lse, inv_temp=it)
+    dlogp = torch.randn(rows, generator=g, device="cuda")
+    dlogp[rows // 3] = 0.0
+    d = torch.full((rows, n + pad), 5.0, dtype=dt, device="cuda")
+    m.moe_lora_token_logp_backward(x, y, lse, dlogp, d[:, :n], inv_temp=it)
+    coef = torch.where(r["ok"], dlogp.double() * it, 0.0)[:, None]
+    hot = torch.zeros_like(r["p"]).scatter_(1, r["y"], 1.0)
+    want = torch.where(coef != 0, coef * (hot - r["p"]), 0.0)
+    tol = coef.abs() * (r["p"] * r["tol"]["p"] + 3 * U32 * (hot + r["p"]))
+    tol = tol + 2.0 ** -61 * coef.abs()  # as above
+    # |lse| below 1,024 is used as saved
+    tol = tol + coef.abs() * r["p"] * torch.where(r["lse"].abs() < 1025, r["tol"]["lse"], 0.0)[:, None]
+    big = torch.finfo(dt).max
+    want = want.clamp(-big, big)
+    _within("dlogits", d[:, :n].clamp(-big, big), want, torch.where(coef != 0, tol + UNIT[dt] * (want.abs() + tol) + TINY_OF[dt], 0.0))
+    if pad:
+        assert (d[:, n:] == 5.0).all()
+    m.moe_lora_token_logp_backward(x, y, lse, dlogp, x, inv_temp=it)
+    assert torch.equal(x, d[:, :n])
+    if pad:
+        assert (buf[:, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+@pytest.mark.parametrize("rows,n", [(6, 300), (6, 5000), (5, 40000), (2500, 1501)])
+def test_masked_rows_backward(rows, n, dt):
+    """Rows of nothing but masks are uniform in the backward as in the forward and the policy loss."""
+    for it in (1.0, 0.25, 1e4):
+        x = torch.randn(rows, n, generator=_gen(n), device="cuda").to(dt)
+        x[0::3] = torch.finfo(dt).min
+        x[1::3] = -INF
+        y = torch.randint(0, n, (rows,), generator=_gen(n + 1), device="cuda", dtype=torch.int32)
+        lp, lse, ent = (torch.empty(rows, device="cuda") for _ in range(3))
+        m.moe_lora_token_logp_forward(x, y, lp, lse, ent, inv_temp=it)
+        dlogp = torch.randn(rows, generator=_gen(3), device="cuda")
+        d, dp = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+        m.moe_lora_token_logp_backward(x, y, lse, dlogp, d, inv_temp=it)
+        flat = torch.arange(rows, device="cuda") % 3 < 2
+        hot = torch.zeros(rows, n, dtype=torch.float64, device="cuda").scatter_(1, y.long()[:, None], 1.0)
+        coef = dlogp.double()[:, None] * it
+        want = coef * (hot - 1.0 / n)
+        # n equal terms: their sum, a quotient, two products and the output's rounding
+        tol = coef.abs() * (hot + 1.0 / n) * 300 * U32
+        _within("masked", d[flat], want[flat], (tol + UNIT[dt] * (want.abs() + tol) + TINY_OF[dt])[flat])
+        assert (ent[flat].double() - math.log(n)).abs().max() <= 1e-4
+        assert ((lp[0::3].double() + math.log(n)).abs() <= 1e-5 * math.log(n)).all() and (lp[1::3] == -INF).all()
+        # the policy loss's gradient on the same rows: ratio 1 and advantages that make the same factor
+        m.moe_lora_policy_loss(x, y, -dlogp, lp.nan_to_num(neginf=0.0), None, torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda"),
+                               m.policy_scratch(rows), weight=torch.ones(rows, device="cuda"), dlogits=dp, inv_temp=it)
+        i = slice(0, rows, 3)
+        _within("policy", dp[i], want[i], (tol + UNIT[dt] * (want.abs() + tol) + TINY_OF[dt])[i])
