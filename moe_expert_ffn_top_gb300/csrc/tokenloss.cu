@@ -336,24 +336,67 @@ __device__ __forceinline__ Vec<T, 16 / sizeof(T)> grad_of(Vec<T, 16 / sizeof(T)>
   return grad_vec<T>(e, q, coef, col, y);
 }
 
+// A sum as an fp32 number and what its rounding left: a preference loss lives on the difference of two
+// large sums, a policy loss on terms of either sign, and fp64 additions are slow here.  Once a sum is infinite what is left is NaN and does not count.
+struct Long {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {  // exactly
+    const float t = hi + v, b = t - hi;
+    lo += (hi - (t - b)) + (v - b);
+    hi = t;
+  }
+  __device__ __forceinline__ void add(const Long& v) {
+    add(v.hi);
+    lo += v.lo;
+  }
+  __device__ __forceinline__ float value() const { return isinf(hi) ? hi : hi + lo; }
+  __device__ __forceinline__ Long over(float n) const {
+    const float q = hi / n;
+    return Long{q, (fmaf(-q, n, hi) + lo) / n};
+  }
+};
+__device__ __forceinline__ Long long_over_warp(Long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.add(Long{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
+// A warp's sums of kTerms numbers: lanes halve what they hold of eight (five of them anything) while they halve
+// themselves, nine additions instead of twenty-five.  Lane 4 j ends with the sum of term j (lane 16 of term 4).
+__device__ __forceinline__ Long terms_over_warp(const Long (&v)[kTerms]) {
+  static_assert(kTerms <= 8, "three halvings");
+  const int lane = threadIdx.x & 31;
+  Long h[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) h[k] = k < kTerms ? v[k < kTerms ? k : 0] : Long{0.f, 0.f};
+#pragma unroll
+  for (int n = 4, o = 16; n > 0; n /= 2, o /= 2)
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const bool up = lane & o;
+      const Long keep = up ? h[k + n] : h[k], give = up ? h[k] : h[k + n];
+      h[k] = keep;
+      h[k].add(Long{__shfl_xor_sync(0xffffffffu, give.hi, o), __shfl_xor_sync(0xffffffffu, give.lo, o)});
+    }
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1) h[0].add(Long{__shfl_xor_sync(0xffffffffu, h[0].hi, o), __shfl_xor_sync(0xffffffffu, h[0].lo, o)});
+  return h[0];
+}
 // The sums of few rows (pairs) by the warp that came last, an adapter after the other: lanes add
 // their elements in order, then a butterfly.
 template <class F>
 __device__ __forceinline__ void sum_terms_here(const float* terms, int64_t stride, const Ranges& ad, F by, float* loss, float* stats) {
   const int lane = threadIdx.x & 31;
   for (int a = 0; a < ad.n; ++a) {
-    float v[kTerms] = {};
+    Long v[kTerms] = {};
 #pragma unroll 4
     for (int64_t i = ad.off[a] + lane; i < ad.off[a + 1]; i += 32)
 #pragma unroll
-      for (int k = 0; k < kTerms; ++k) v[k] += __ldcg(terms + k * stride + i);
+      for (int k = 0; k < kTerms; ++k) v[k].add(__ldcg(terms + k * stride + i));
     const float f = by(a);
-#pragma unroll
-    for (int k = 0; k < kTerms; ++k) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-      if (lane == 0) (k ? stats[a * (kTerms - 1) + k - 1] : loss[a]) = v[k] * f;
-    }
+    const float t = terms_over_warp(v).value() * f;
+    const int k = lane / 4;
+    if (lane % 4 == 0 && k < kTerms) (k ? stats[a * (kTerms - 1) + k - 1] : loss[a]) = t;
   }
 }
 // Notes that this warp's terms are written (by its first lane); true for all lanes of the warp that
@@ -576,31 +619,6 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam, 1)
   finish();
 }
 
-// A sum as an fp32 number and what its rounding left: a loss lives on the difference of two large
-// sums, and fp64 additions are slow here.  Once a sum is infinite what is left is NaN and does not count.
-struct Long {
-  float hi, lo;
-  __device__ __forceinline__ void add(float v) {  // exactly
-    const float t = hi + v, b = t - hi;
-    lo += (hi - (t - b)) + (v - b);
-    hi = t;
-  }
-  __device__ __forceinline__ void add(const Long& v) {
-    add(v.hi);
-    lo += v.lo;
-  }
-  __device__ __forceinline__ float value() const { return isinf(hi) ? hi : hi + lo; }
-  __device__ __forceinline__ Long over(float n) const {
-    const float q = hi / n;
-    return Long{q, (fmaf(-q, n, hi) + lo) / n};
-  }
-};
-__device__ __forceinline__ Long long_over_warp(Long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v.add(Long{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
-  return v;
-}
-
 // dlogits where fp32 holds a row's lse coarsely, to 2^-14 and more, which is then a probability's relative
 // error.  The row's sum is formed anew from its logits, by a warp or a block, in three sweeps: 2.5 ms for
 // 16,384 x 65,536 bf16, 0.64 with logits near 0.
@@ -819,7 +837,7 @@ struct SumArgs {
 template <int kC, bool kPairs>
 __global__ void __launch_bounds__(kSumThreads)
     term_sum_kernel(const __grid_constant__ SumArgs g, const __grid_constant__ Ranges ad, const __grid_constant__ PrefArgs pref) {
-  __shared__ float warp_sum[kSumThreads / 32][kTerms], block_sum[kTerms];
+  __shared__ Long warp_sum[kSumThreads / 32][kTerms], block_sum[kTerms];
   const int a = blockIdx.x / kC, rank = kC > 1 ? (int)cluster_rank() : 0;
   const int64_t lo = ad.off[a], hi = ad.off[a + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -831,23 +849,17 @@ __global__ void __launch_bounds__(kSumThreads)
     if (threadIdx.x < 32 && came_last(pref.ticket, gridDim.x) && threadIdx.x == 0) *pref.again = 0;
     if (kC > 1) cluster_sync_all();
   }
-  float s[kTerms] = {};
+  Long s[kTerms] = {};
 #pragma unroll 2
   for (int64_t i = lo + rank * kSumThreads + threadIdx.x; i < hi; i += kSumCluster * kSumThreads)
 #pragma unroll
-    for (int k = 0; k < kTerms; ++k) s[k] += __ldcg(g.terms + k * g.stride + i);
-#pragma unroll
-  for (int k = 0; k < kTerms; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5][k] = s[k];
-  }
-  __syncthreads();
-  const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;  // a warp per term
+    for (int k = 0; k < kTerms; ++k) s[k].add(__ldcg(g.terms + k * g.stride + i));
+  const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Long mine = terms_over_warp(s);
+  if (lane % 4 == 0 && lane / 4 < kTerms) warp_sum[k][lane / 4] = mine;
+  __syncthreads();  // a warp per term from here on
   if (k < kTerms) {
-    float v = warp_sum[lane][k];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const Long v = long_over_warp(warp_sum[lane][k]);
     if (lane == 0) block_sum[k] = v;
   }
   if (kC > 1)
@@ -855,15 +867,20 @@ __global__ void __launch_bounds__(kSumThreads)
   else
     __syncthreads();
   if (rank == 0 && k < kTerms) {
-    float v = 0.f;
+    Long sum{0.f, 0.f};
     if (lane < kC) {
-      if (kC > 1)
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&block_sum[k]), lane)) : "memory");
-      else
-        v = block_sum[k];
+      if (kC > 1) {
+        const uint32_t at = mapa_shared(smem_u32(&block_sum[k]), lane);
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(sum.hi) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(sum.lo) : "r"(at + 4) : "memory");
+      } else {
+        sum = block_sum[k];
+      }
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = kSumCluster / 2; o > 0; o >>= 1)
+      sum.add(Long{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+    const float v = sum.value();
     if (lane == 0) {
       float by = 1.f;
       if (g.count) {

@@ -333,3 +333,48 @@ def test_masked_rows_backward(rows, n, dt):
                                m.policy_scratch(rows), weight=torch.ones(rows, device="cuda"), dlogits=dp, inv_temp=it)
         i = slice(0, rows, 3)
         _within("policy", dp[i], want[i], (tol + UNIT[dt] * (want.abs() + tol) + TINY_OF[dt])[i])
+
+
+# ------------------------------------------------------------------ sums over tokens and pairs
+# Pairs of fp32 numbers: a chain of k <= 24 additions leaves at most k 2^-24 of the terms' size in the lower number, whose
+# own additions are each off by 2^-24 of that: k^2 2^-48 < 2^-38 in all.
+PAIRS_KEEP = 2.0 ** -38
+
+
+@pytest.mark.parametrize("rows,adapters", [(64, 1), (50, 3), (700, 1), (20000, 2), (30000, 1)])
+def test_policy_sums_that_cancel(rows, adapters):
+    """Terms of either sign: with the ratios at 1 they are the advantages, and only their sum's rounding is left."""
+    n = 16
+    g = _gen(rows)
+    x = torch.randn(rows, n, generator=g, device="cuda")
+    y = torch.randint(0, n, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    adv = torch.randn(rows, generator=g, device="cuda") * 2.0 ** torch.randint(-8, 13, (rows,), generator=g, device="cuda")
+    half = rows // 2
+    adv[half:2 * half] = -adv[:half].flip(0) + 1e-3 * torch.rand(half, generator=g, device="cuda")
+    offs = [0] + [rows * a // adapters // 2 * 2 for a in range(1, adapters)] + [rows]
+    loss, stats, lp = torch.empty(adapters, device="cuda"), torch.empty(adapters, 4, device="cuda"), torch.empty(rows, device="cuda")
+    w = torch.full((rows,), 2.0 ** -12, device="cuda")
+    kw = dict(weight=w, adapter_offsets=offs if adapters > 1 else None, logp=lp)
+    m.moe_lora_policy_loss(x, y, adv, torch.zeros(rows, device="cuda"), None, loss, stats, m.policy_scratch(rows, adapters), **kw)
+    old = lp.clone()
+    m.moe_lora_policy_loss(x, y, adv, old, None, loss, stats, m.policy_scratch(rows, adapters), **kw)
+    assert torch.equal(old, lp)
+    for a in range(adapters):
+        v = -adv[offs[a]:offs[a + 1]].double() * 2.0 ** -12
+        assert abs(float(loss[a]) - float(v.sum())) <= 2 * U32 * abs(float(v.sum())) + PAIRS_KEEP * float(v.abs().sum()), a
+        assert abs(float(stats[a, 2]) - (offs[a + 1] - offs[a]) * 2.0 ** -12) <= U32 * rows * 2.0 ** -12
+
+
+@pytest.mark.parametrize("pairs", [16, 256, 512, 16384])
+def test_preference_sums_that_cancel(pairs):
+    g = _gen(pairs)
+    lp = -torch.rand(2 * pairs, generator=g, device="cuda") * 2.0 ** torch.randint(0, 12, (2 * pairs,), generator=g, device="cuda")
+    v = lp.view(pairs, 2)
+    half = pairs // 2
+    v[half:, 0], v[half:, 1] = v[:half, 1].flip(0), v[:half, 0].flip(0) + 1e-4
+    h32 = v[:, 0] - v[:, 1]
+    loss, stats = torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda")
+    m.moe_lora_preference_loss(lp, torch.ones(2 * pairs, dtype=torch.int32, device="cuda"), torch.arange(2 * pairs + 1, device="cuda"), None, loss, stats,
+                               m.preference_scratch(pairs), beta=0.5)
+    for got, want in ((stats[0, 1], 0.5 * v[:, 0].double()), (stats[0, 2], 0.5 * v[:, 1].double()), (stats[0, 3], h32.double())):
+        assert abs(float(got) - float(want.mean())) <= 2 * U32 * abs(float(want.mean())) + PAIRS_KEEP * float(want.abs().mean())
