@@ -439,7 +439,9 @@ struct Token {
   __device__ __forceinline__ float terms(const PolicyArgs& pg, int64_t rows, int64_t t, float logp, float entropy, bool writes) const {
     const float rho = expf(logp - old), clip = fminf(fmaxf(rho, pg.low), pg.high);
     const bool cut = (adv > 0.f && rho > pg.high) || (adv < 0.f && rho < pg.low);
-    float loss = -(cut ? clip : rho) * adv, kl = 0.f, dl = cut ? 0.f : -rho * adv;
+    // a ratio past fp32's range is a number all the same: none of it is left times an advantage of 0
+    const float gain = adv == 0.f && rho == INFINITY ? 0.f : rho * adv;
+    float loss = cut ? -clip * adv : -gain, kl = 0.f, dl = cut ? 0.f : -gain;
     if (pg.ref) {
       const float d = ref - logp, em = expm1f(d);
       kl = em - d;

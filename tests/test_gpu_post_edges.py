@@ -378,3 +378,23 @@ def test_preference_sums_that_cancel(pairs):
                                m.preference_scratch(pairs), beta=0.5)
     for got, want in ((stats[0, 1], 0.5 * v[:, 0].double()), (stats[0, 2], 0.5 * v[:, 1].double()), (stats[0, 3], h32.double())):
         assert abs(float(got) - float(want.mean())) <= 2 * U32 * abs(float(want.mean())) + PAIRS_KEEP * float(want.abs().mean())
+
+
+# ------------------------------------------------------------------ a token's terms
+@pytest.mark.parametrize("rows,n", [(8, 200), (8, 9000), (300, 9000)])
+def test_ratio_past_fp32_without_advantage(rows, n):
+    """exp(logp - old) may pass fp32's range; times an advantage of 0 it has no part in loss and gradient."""
+    x = torch.randn(rows, n, generator=_gen(rows), device="cuda")
+    y = torch.arange(rows, device="cuda", dtype=torch.int32) % n
+    adv = torch.randn(rows, generator=_gen(2), device="cuda")
+    old = torch.full((rows,), -9.0, device="cuda")
+    far = torch.arange(rows, device="cuda") % 4 == 1
+    adv[far], old[far] = 0.0, -200.0
+    near = torch.where(far, -9.0, old)
+    res = []
+    for o in (old, near):
+        loss, stats, d = torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda"), torch.full_like(x, 9.0)
+        m.moe_lora_policy_loss(x, y, adv, o, None, loss, stats, m.policy_scratch(rows), dlogits=d)
+        res.append((loss, stats[0, :2], stats[0, 3], d))
+    assert all(torch.equal(a, b) for a, b in zip(*res)) and torch.isfinite(res[0][0]).all()
+    assert (res[0][3][far] == 0).all()
