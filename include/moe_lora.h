@@ -470,7 +470,8 @@ MOE_LORA_API int moe_lora_token_logp_backward(const moe_lora_rows* r, const void
  *     l = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + kl_coef * kl,   A = advantages[t],
  *     loss_a = sum over the tokens of adapter a of w_t l_t,
  * w = weight[t], or 1 / (live tokens of the adapter) where weight is NULL.  A token of weight 0
- * takes no part either, whatever its values.  Without ref_logp kl is 0.  The gradient passes where
+ * takes no part either, whatever its values.  Without ref_logp kl is 0; with kl_coef 0 it is
+ * reported alone.  The gradient passes where
  * the clip does not take the minimum, its borders included:
  *     dl/dlogp = -rho A [not clipped] + kl_coef (1 - exp d),
  *     dlogits_te = dloss_a * w_t * dl/dlogp * inv_temp * ([e = y_t] - p_te), zeros for tokens without part.

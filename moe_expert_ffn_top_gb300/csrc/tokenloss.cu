@@ -444,9 +444,11 @@ struct Token {
     float loss = cut ? -clip * adv : -gain, kl = 0.f, dl = cut ? 0.f : -gain;
     if (pg.ref) {
       const float d = ref - logp, em = expm1f(d);
-      kl = em - d;
-      loss += pg.kl * kl;
-      dl -= pg.kl * em;
+      kl = d == INFINITY ? d : em - d;
+      if (pg.kl != 0.f) {  // else it is reported alone, and may be infinite
+        loss += pg.kl * kl;
+        dl -= pg.kl * em;
+      }
     }
     if (writes) {  // a token of weight 0 has no part in the loss, whatever its values
       float* to = pg.terms + t;

@@ -398,3 +398,21 @@ def test_ratio_past_fp32_without_advantage(rows, n):
         res.append((loss, stats[0, :2], stats[0, 3], d))
     assert all(torch.equal(a, b) for a, b in zip(*res)) and torch.isfinite(res[0][0]).all()
     assert (res[0][3][far] == 0).all()
+
+
+@pytest.mark.parametrize("rows,n", [(8, 200), (8, 9000), (300, 9000)])
+def test_kl_without_weight(rows, n):
+    """With kl_coef 0 a reference model only reports: loss and gradient are those without it, however far it lies."""
+    x = torch.randn(rows, n, generator=_gen(rows), device="cuda")
+    y = torch.arange(rows, device="cuda", dtype=torch.int32) % n
+    x[1, 1] = -INF  # a masked target: its logp is -inf, its ratio 0
+    adv, old = torch.randn(rows, generator=_gen(2), device="cuda"), torch.full((rows,), -9.0, device="cuda")
+    rlp = torch.full((rows,), -9.0, device="cuda")
+    res = []
+    for r in (rlp + 150.0, rlp, None):
+        loss, stats, d = torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda"), torch.full_like(x, 9.0)
+        m.moe_lora_policy_loss(x, y, adv, old, r, loss, stats, m.policy_scratch(rows), dlogits=d)
+        res.append((loss, stats[0, 1:], d))
+        if r is not None:
+            assert float(stats[0, 0]) == INF
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(*res)) and torch.isfinite(res[0][2]).all() and torch.isfinite(res[0][0]).all()
