@@ -323,6 +323,9 @@ struct Outcome {
     }
     inv_s = 1.0f / sm.s;
     entropy = kLn2 * (ls - sm.w * inv_s);
+    // Both numbers of a difference are up to 1 where the result is near 0: rounding may carry it past that.
+    asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(logp));
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(entropy));
   }
 };
 // The gradient of a vector whose first element is column `col`: q 2^(x f - m), and coef more at the target.
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kShortThreads : kTeam, 1)
     }
     xy = at_target;
   }
-  if (warp == 0) {
+  if (warp == 0 && (kPolicy || rank == 0)) {
     const Outcome o(sm, xy, z);
     if (clerk && lane == 0) {
       if (g.logp) g.logp[t] = o.logp;

@@ -416,3 +416,23 @@ def test_kl_without_weight(rows, n):
         if r is not None:
             assert float(stats[0, 0]) == INF
     assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(*res)) and torch.isfinite(res[0][2]).all() and torch.isfinite(res[0][0]).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+@pytest.mark.parametrize("rows,n", [(300, 200), (40, 5003), (20, 40000)])
+def test_log_probabilities_of_certain_tokens(rows, n, dt):
+    """Never above 0; entropies never below it."""
+    g = _gen(n)
+    x = torch.randn(rows, n, generator=g, device="cuda")
+    y = torch.randint(0, n, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    at = torch.arange(rows, device="cuda")
+    x[at, y.long()] += torch.linspace(5, 60, rows, device="cuda")
+    x = x.to(dt)
+    for it in (1.0, 0.7, 30.0):
+        it = torch.tensor(it).item()
+        lp, ent = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        m.moe_lora_token_logp_forward(x, y, lp, None, ent, inv_temp=it)
+        r = ref.tokens(x, y, it)
+        assert (lp <= 0).all() and (ent >= 0).all(), (float(lp.max()), float(ent.min()))
+        _within("logp", lp, r["logp"], r["tol"]["logp"])
+        _within("entropy", ent, r["entropy"], r["tol"]["entropy"])
