@@ -436,3 +436,109 @@ def test_log_probabilities_of_certain_tokens(rows, n, dt):
         assert (lp <= 0).all() and (ent >= 0).all(), (float(lp.max()), float(ent.min()))
         _within("logp", lp, r["logp"], r["tol"]["logp"])
         _within("entropy", ent, r["entropy"], r["tol"]["entropy"])
+
+
+@pytest.mark.parametrize("rows,n", [(8, 200), (8, 9000), (300, 9000)])
+def test_weight_zero_whatever_its_values(rows, n):
+    """Tokens of weight 0 may hold anything in every input; the others' results are those of a batch without them."""
+    x = torch.randn(rows, n, generator=_gen(rows), device="cuda")
+    y = torch.arange(rows, device="cuda", dtype=torch.int32) % n
+    adv, old = torch.randn(rows, generator=_gen(2), device="cuda"), torch.full((rows,), -9.0, device="cuda")
+    rlp, w = old + 0.3, torch.rand(rows, generator=_gen(3), device="cuda") + 0.1
+    off = torch.arange(rows, device="cuda") % 4 == 2
+    w[off] = 0.0
+    res = []
+    for bad in (False, True):
+        a, o, r, v, t = adv.clone(), old.clone(), rlp.clone(), x.clone(), y.clone()
+        if bad:
+            a[off], o[off], r[off] = math.nan, -INF, INF
+            v[off] = torch.where(torch.rand(n, generator=_gen(5), device="cuda") < 0.5, INF, math.nan)
+        else:
+            t[off] = -1
+        loss, stats, d = torch.empty(2, device="cuda"), torch.empty(2, 4, device="cuda"), torch.full_like(v, 9.0)
+        m.moe_lora_policy_loss(v, t, a, o, r, loss, stats, m.policy_scratch(rows, 2), weight=w, adapter_offsets=[0, rows // 2, rows], kl_coef=0.1, dlogits=d)
+        res.append((loss, stats, d))
+    assert all(torch.equal(a, b) for a, b in zip(*res)) and all(torch.isfinite(v).all() for v in res[1])
+
+
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+@pytest.mark.parametrize("rows,n,adapters", [(300, 5003, 3), (2500, 1501, 2), (70, 40000, 4), (40, 300, 1)])
+def test_masked_vocabulary_in_the_policy_gradient(rows, n, adapters, dt):
+    """Masked entries (-inf and the type's lowest value) and masked targets, with counted means and several adapters; in place too."""
+    g = _gen(rows)
+    x = (2 * torch.randn(rows, n, generator=g, device="cuda")).to(dt)
+    y = torch.randint(0, n, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    hide = torch.rand(rows, n, generator=g, device="cuda") < 0.5
+    hide.scatter_(1, y.long()[:, None], False)
+    x = torch.where(hide, torch.where(torch.arange(rows, device="cuda")[:, None] % 2 == 0, -INF, torch.finfo(dt).min), x.float()).to(dt)
+    y[5::7] = -1
+    gone = torch.arange(rows, device="cuda") % 11 == 3
+    x[gone, y.clamp(min=0)[gone].long()] = -INF  # masked targets: logp -inf, ratio 0
+    r = _tokens(x, y, 1.0)
+    gone = gone & (y >= 0)
+    old = (torch.where(gone, -8.0, r["logp"]) + 0.1 * torch.randn(rows, generator=g, device="cuda")).float()
+    adv = torch.randn(rows, generator=g, device="cuda")
+    offs = [0] + [rows * (a + 1) // adapters - 1 for a in range(adapters - 1)] + [rows]
+    loss, stats, d = torch.empty(adapters, device="cuda"), torch.empty(adapters, 4, device="cuda"), torch.full_like(x, 9.0)
+    lp = torch.empty(rows, device="cuda")
+    kw = dict(adapter_offsets=offs if adapters > 1 else None, logp=lp)
+    m.moe_lora_policy_loss(x, y, adv, old, None, loss, stats, m.policy_scratch(rows, adapters), dlogits=d, **kw)
+    assert (lp[gone] == -INF).all()
+    r["logp"] = torch.where(gone, -1e5, r["logp"])  # a ratio of 0 in 64 bits too
+    r["tol"]["logp"] = torch.where(gone, 0.0, r["tol"]["logp"])
+    low, high = 0.2, 0.2
+    wl, ws, wd, lt, st, dtol = ref.policy(r, adv, old, None, None, offs, None, 1.0, low, high, 0.0)
+    _within("loss", loss, wl, lt)
+    _within("stats", stats, ws, st)
+    _within("dlogits", d, wd, torch.where(wd != 0, dtol + UNIT[dt] * (wd.abs() + dtol) + TINY_OF[dt], dtol))
+    assert (d[hide] == 0).all() and (d[gone] == 0).all()
+    x2 = x.clone()
+    m.moe_lora_policy_loss(x2, y, adv, old, None, loss, stats, m.policy_scratch(rows, adapters), dlogits=x2, **kw)
+    assert torch.equal(x2, d)
+
+
+def test_edges_captured_and_on_another_stream():
+    """Far rows, coarse lse, bad offsets and small norms replayed from a graph: equal bits to eager calls, word and workspace reset."""
+    T, n = 130, 9000
+    x = torch.randn(T, n, generator=_gen(1), device="cuda")
+    x[::3] *= 1e10
+    x[1::3] -= 1e6
+    x[2::6] = -INF
+    y = torch.randint(0, n, (T,), generator=_gen(2), device="cuda", dtype=torch.int32)
+    seq = torch.arange(0, T + 1, 10, device="cuda")[:13].clone()
+    seq[4] = 3
+    u = torch.randn(5, 16, 90, generator=_gen(3), device="cuda") * torch.tensor([1e-25, 1e-12, 1e-8, 1.0, 1e8], device="cuda")[:, None, None]
+    sc, err = m.preference_scratch(6), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def buffers():
+        z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+        b = dict(lp=z(T), lse=z(T), ent=z(T), loss=z(1), stats=z(1, 4), sl=z(12), dl=z(T), d=torch.zeros_like(x), p=torch.zeros_like(u), m=torch.zeros_like(u))
+        return b, m.MuonTensors([dict(p=b["p"], g=u, m=b["m"], lr=0.5)])
+
+    def call(b, t):
+        m.moe_lora_token_logp_forward(x, y, b["lp"], b["lse"], b["ent"])
+        b["lp"].clamp_(min=-50)
+        m.moe_lora_preference_loss(b["lp"], y, seq, None, b["loss"], b["stats"], sc, seq_logp=b["sl"], dlogp=b["dl"], err=err)
+        m.moe_lora_token_logp_backward(x, y, b["lse"], b["dl"], b["d"])
+        m.moe_lora_muon_step(t)
+    want, got = buffers(), buffers()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(*got)
+    torch.cuda.current_stream().wait_stream(side)
+    call(*want)
+    assert all(torch.equal(want[0][k], got[0][k]) for k in want[0]) and int(err) == m.MOE_LORA_DEV_BAD_ID
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(*got)
+    for to in (3, 40, 1 << 50, 40):
+        seq[4] = to
+        err.zero_()
+        x[5:9].normal_(generator=_gen(to % 1000))
+        graph.replay()
+        bits = int(err)
+        err.zero_()
+        call(*want)
+        assert bits == int(err) == (0 if to == 40 else m.MOE_LORA_DEV_BAD_ID)
+        assert all(torch.equal(want[0][k], got[0][k]) for k in want[0]) and torch.isfinite(want[0]["d"]).all()
