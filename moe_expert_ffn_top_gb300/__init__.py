@@ -672,9 +672,16 @@ def moe_lora_adamw_step(tensors: AdamWTensors, step: int, beta1: float = 0.9, be
 
 
 # ------------------------------------------------------------------ post-training
+def _here(t: torch.Tensor, name: str) -> None:
+    """Launches go to the current device, which does not hold another device's tensors."""
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device, cuda:{torch.cuda.current_device()}, got {t.device}")
+
+
 def _logit_rows(logits: torch.Tensor, dlogits: Optional[torch.Tensor], inv_temp: float):
     """The row description of logits [rows, n] and their gradient, and both pointers."""
     px, ld = _rows(logits, "logits")
+    _here(logits, "logits")
     pd, ldd = (None, 0) if dlogits is None else _rows(dlogits, "dlogits", logits)
     rows, n = logits.shape
     return Rows(rows, ld, ldd, n, _dtype(logits, "logits"), inv_temp), px, pd
@@ -785,6 +792,7 @@ def moe_lora_preference_loss(logp: torch.Tensor, targets: torch.Tensor, seq_offs
         raise ValueError("seq_offsets must have 2 * pairs + 1 entries")
     if kind not in PREFERENCE_KINDS:
         raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}, got {kind!r}")
+    _here(logp, "logp")
     P, T, A, f32 = seq_offsets.numel() // 2, logp.numel(), loss.numel(), torch.float32
     offs = _host_offsets(pair_offsets, A, "pair_offsets")
     opt = Preference(T, P, beta, margin, label_smoothing, PREFERENCE_KINDS[kind], int(average), A)
@@ -804,8 +812,8 @@ class MuonTensors:
     is a dict: p (fp32, bf16 or fp16; its last two axes are a matrix, one of them at most 128, all others
     count matrices), g of p's shape, m (fp32 momentum, started at zero), and optionally master (fp32, for
     a 16-bit p), lr (1e-3), weight_decay (0) and scale (sqrt(max(1, rows / cols))), which multiplies the
-    update.  All contiguous; no two overlap.  The entries hold the tensors alive.  Steps that may run at
-    the same time need an object each."""
+    update.  All contiguous, on one device; no two overlap.  The entries hold the tensors alive.  Steps
+    that may run at the same time need an object each."""
 
     def __init__(self, entries: Sequence[Dict]):
         self.entries = [dict(e) for e in entries]
@@ -827,8 +835,10 @@ class MuonTensors:
         b = int(lib().moe_lora_muon_scratch_bytes(self.table, len(self.entries)))
         if b == 0:
             raise MoeLoraError(-5, "moe_lora_muon_scratch_bytes")
-        device = self.entries[0]["p"].device if self.entries else "cuda"
-        self.scratch = _ticket_scratch(b, device)  # starts with the error word
+        devices = {e[k].device for e in self.entries for k in ("p", "g", "m", "master") if e.get(k) is not None}
+        if len(devices) > 1:
+            raise ValueError(f"tensors must be on one device, got {sorted(map(str, devices))}")
+        self.scratch = _ticket_scratch(b, devices.pop() if devices else "cuda")  # starts with the error word
 
     def set_lr(self, lr: float) -> None:
         for d in self.table:
@@ -841,6 +851,7 @@ def moe_lora_muon_step(tensors: MuonTensors, momentum: float = 0.95, nesterov: b
     """One Muon step over all tensors: momentum, `steps` Newton-Schulz steps with the coefficients (a, b, c)
     on every matrix, weights.  grad_scale: a device fp32 scalar that multiplies every gradient."""
     a, b, c = coefs
+    _here(tensors.scratch, "the tensors")
     opt = Muon(momentum, eps, a, b, c, int(nesterov), steps, _vec(grad_scale, 1, "grad_scale", torch.float32))
     rc = lib().moe_lora_muon_step(opt, tensors.table, len(tensors.entries), tensors.scratch.data_ptr(),
                                   tensors.scratch.numel(), _stream(stream))

@@ -542,3 +542,18 @@ def test_edges_captured_and_on_another_stream():
         call(*want)
         assert bits == int(err) == (0 if to == 40 else m.MOE_LORA_DEV_BAD_ID)
         assert all(torch.equal(want[0][k], got[0][k]) for k in want[0]) and torch.isfinite(want[0]["d"]).all()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Before any launch: calls go to the current device."""
+    x, y, v = torch.zeros(4, 8, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+    one, four, seq = torch.zeros(1, device="cuda"), torch.zeros(1, 4, device="cuda"), torch.tensor([0, 2, 4], device="cuda")
+    psc, fsc = m.policy_scratch(4), m.preference_scratch(1)
+    t = m.MuonTensors([dict(p=x.clone(), g=x, m=x.clone())])
+    calls = [lambda: m.moe_lora_token_logp_forward(x, y, v), lambda: m.moe_lora_token_logp_backward(x, y, v, v, x),
+             lambda: m.moe_lora_policy_loss(x, y, v, v, None, one, four, psc), lambda: m.moe_lora_preference_loss(v, y, seq, None, one, four, fsc),
+             lambda: m.moe_lora_muon_step(t)]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
