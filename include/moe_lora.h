@@ -577,11 +577,14 @@ typedef struct moe_lora_muon {
 } moe_lora_muon;
 
 /* tensors [n]: HOST array, read before the call returns.  The tensors do not overlap.  scratch:
- * moe_lora_muon_scratch_bytes(tensors, n) bytes (from batch, rows and cols alone; 0 for bad sizes),
- * four bytes per element and a little; its first 16 bytes are the device error word, which the caller
- * clears once and calls only add to.  Calls that may run at the same time need one each.  Sums run in
- * a fixed order, so equal calls give equal bits.  Five launches per 128 tensors whose weights are of one
- * type, one more for each other type among them. */
+ * moe_lora_muon_scratch_bytes(tensors, n) bytes (from batch, rows and cols alone; 0 for bad sizes).  With
+ * s the short and L the long side, a tile is floor(128 / s) matrices: it takes 32 KB for each started
+ * 64 of L, and 129 KB; up to 304 times 64 KB (more where there are more than 38,912 such pieces) come
+ * on top.  That is 4 bytes an element and a little for s a divisor of 128 and a long L, 12 for 128 x 128, and
+ * for other s as much more as 128 passes the rows that a tile fills.  Its first 16 bytes are the device error
+ * word, which the caller clears once and calls only add to.  Calls that may run at the same time need one each.
+ * Sums run in a fixed order, so equal calls give equal bits.  Five launches per 128 tensors whose weights are
+ * of one type, one more for each other type among them. */
 MOE_LORA_API size_t moe_lora_muon_scratch_bytes(const moe_lora_muon_tensor* tensors, int32_t n);
 MOE_LORA_API int moe_lora_muon_step(const moe_lora_muon* opt, const moe_lora_muon_tensor* tensors, int32_t n,
                                     void* scratch, size_t scratch_bytes, void* stream);

@@ -28,11 +28,11 @@
 // places of the long side.  Blocks share all chunks evenly; what a block has of one tile is a
 // stretch, and leaves one partial G.
 //
-// Measured on one GB300, 203 M elements of rank 128 (bf16 weights, fp32 masters and gradients): 1,711 us,
-// of which gram 449 (12 bytes an element, 5.4 TB/s), apply 531 (12 bytes, 4.6), update 472 (14 bytes,
-// 6.0) and the two polys 242 together.  The three that stream are bound by the chain of a chunk (loads,
+// Measured on one GB300, 203 M elements of rank 128 (bf16 weights, fp32 masters and gradients): 1,722 us,
+// of which gram 455 (12 bytes an element, 5.3 TB/s), apply 540 (12 bytes, 4.5), update 475 (14 bytes,
+// 6.0) and the two polys 248 together.  The three that stream are bound by the chain of a chunk (loads,
 // operand stores, a barrier, products; in apply twice), which two blocks an SM cover in part: registers
-// and tensor memory take no third.  38.6 M elements of rank 8 in bf16: 312 us.
+// and tensor memory take no third.  38.6 M elements of rank 8 in bf16: 308 us.
 #include <math.h>
 
 #include <algorithm>

@@ -9,10 +9,10 @@
 // its own elements; the threads' pairs meet once, in distributed shared memory, and where a
 // gradient is wanted it is formed from the slice in shared memory: one read and one write.
 //
-// Measured on one GB300: the policy loss with its gradient over 8,192 x 151,936 bf16, 30% of the rows
-// without a target, 707 us (6.0 TB/s, 88% of the measured copy bandwidth); log probabilities with
-// entropies of 16,384 x 65,536 bf16 348 us (5.6 TB/s, 82%), their backward 641 us (94%); the preference
-// loss of 1,024 pairs of 1,400 tokens 16 us.
+// Measured on one GB300 (GPU time): the policy loss with its gradient over 8,192 x 151,936 bf16, 30% of the rows
+// without a target, 680 us (6.2 TB/s, 92% of the measured copy bandwidth); log probabilities with
+// entropies of 16,384 x 65,536 bf16 341 us (5.7 TB/s, 83%), their backward 639 us (94%); the preference
+// loss of 1,024 pairs of 1,400 tokens 14 us.
 #include <math.h>
 
 #include <algorithm>
@@ -1105,10 +1105,10 @@ int launch_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, cons
 // where there are enough rows for every SM's warps (20,000 x 4,000 27.8 and 33.1 us, the policy's gradient 64
 // and 117; 2,000 x 4,096 11.7 and 15.4, but 600 x 4,000 8.8 and 6.8).  Longer rows belong to the fewest
 // blocks of 128 threads that hold 32 KB each, up to sixteen, which then hold up to 128 KB.  Log
-// probabilities of 16,384 x 65,536 take 348 us so, with 16 KB 418, with 64 KB 393, with 256 threads
+// probabilities of 16,384 x 65,536 took 348 us so, with 16 KB 418, with 64 KB 393, with 256 threads
 // and 64 KB 417, with 64 threads 414; of 8,192 x 151,936 467 us in clusters of ten, 589 in five of
 // 64 KB.  The policy loss over 8,192 x 151,936 707 us, with 256 threads and 64 KB 757, 32 KB 812;
-// 2,048 x 50,257 73 and 72.  Where there are too few rows to give every SM a block, a row is shared by
+// 2,048 x 50,257 73 and 72 (each with the gradient's loop unrolled by sixteen).  Where there are too few rows to give every SM a block, a row is shared by
 // more, up to eight (one row of 32,000: 2.9 us instead of 4.4).
 template <class T, bool kEntropy, bool kPolicy, bool kGrad>
 int pick_rows(const RowArgs& g, const PolicyArgs& pg, const GradArgs& dg, const Ranges& ad, int sms, bool overlap, cudaStream_t s) {
