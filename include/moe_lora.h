@@ -518,8 +518,8 @@ MOE_LORA_API int moe_lora_policy_loss(const moe_lora_rows* r, const moe_lora_pol
  *   pair_offsets [adapters+1] int64, HOST, as adapter_offsets above, in pairs
  *   loss [adapters] fp32;  stats [adapters,4] fp32: means of [x > 0], beta r_chosen, beta r_rejected, h
  *   seq_logp [2 pairs] fp32 (s_j) or NULL
- *   dlogp [tokens] fp32 or NULL: 0 at the sequences' tokens that are not live; tokens of no sequence
- *            are left as they were
+ *   dlogp [tokens] fp32 or NULL, not logp: 0 at the sequences' tokens that are not live; tokens of no
+ *            sequence are left as they were
  * scratch: moe_lora_preference_scratch_bytes(pairs) bytes, whose first 16 bytes the caller clears
  * once; calls that may run at the same time need one each. */
 #define MOE_LORA_PREF_SIGMOID 0

@@ -815,11 +815,13 @@ __device__ __noinline__ void pairs_again(const PrefArgs& g, const Ranges& ad, in
     Long r[2] = {};
     int n[2] = {0, 0};
     for (int q = 0; q < 2; ++q) {
-      for (int64_t t = off[q] + lane; t < off[q + 1]; t += 32)
-        if (g.targets[t] >= 0) {
-          r[q].add(g.logp[t]);
-          ++n[q];
-        }
+#pragma unroll 8
+      for (int64_t t = off[q] + lane; t < off[q + 1]; t += 32) {  // both loaded, so that many are on their way
+        const bool live = g.targets[t] >= 0;
+        const float f = g.logp[t];
+        r[q].add(live ? f : 0.f);
+        n[q] += live;
+      }
       r[q] = long_over_warp(r[q]);
       n[q] = __reduce_add_sync(0xffffffffu, n[q]);
     }
@@ -827,6 +829,7 @@ __device__ __noinline__ void pairs_again(const PrefArgs& g, const Ranges& ad, in
     const float ref[2] = {g.ref ? g.ref[2 * i] : 0.f, g.ref ? g.ref[2 * i + 1] : 0.f};
     const float2 each = pair_terms(g, ad, i, a, r, n, ref, g.dloss ? g.dloss[a] : 1.f);
     if (g.dlogp)
+#pragma unroll 8
       for (int64_t t = off[0] + lane; t < off[2]; t += 32) g.dlogp[t] = g.targets[t] < 0 ? 0.f : t < off[1] ? each.x : each.y;
   }
 }
