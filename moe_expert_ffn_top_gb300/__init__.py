@@ -672,16 +672,17 @@ def moe_lora_adamw_step(tensors: AdamWTensors, step: int, beta1: float = 0.9, be
 
 
 # ------------------------------------------------------------------ post-training
-def _here(t: torch.Tensor, name: str) -> None:
-    """Launches go to the current device, which does not hold another device's tensors."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device, cuda:{torch.cuda.current_device()}, got {t.device}")
+def _stream_of(t: torch.Tensor, name: str, stream) -> int:
+    """The stream's handle.  Launches go to the current device, which does not hold another device's tensors."""
+    device = torch._C._cuda_getDevice()
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device, cuda:{device}, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _logit_rows(logits: torch.Tensor, dlogits: Optional[torch.Tensor], inv_temp: float):
     """The row description of logits [rows, n] and their gradient, and both pointers."""
     px, ld = _rows(logits, "logits")
-    _here(logits, "logits")
     pd, ldd = (None, 0) if dlogits is None else _rows(dlogits, "dlogits", logits)
     rows, n = logits.shape
     return Rows(rows, ld, ldd, n, _dtype(logits, "logits"), inv_temp), px, pd
@@ -698,7 +699,7 @@ def moe_lora_token_logp_forward(logits: torch.Tensor, targets: torch.Tensor, log
     rc = lib().moe_lora_token_logp_forward(r, px, _vec(targets, T, "targets", torch.int32),
                                            _vec(logp, T, "logp", torch.float32), _vec(lse, T, "lse", torch.float32),
                                            _vec(entropy, T, "entropy", torch.float32), _vec(err, 1, "err", torch.int32),
-                                           _stream(stream))
+                                           _stream_of(logits, "logits", stream))
     _check(rc, "moe_lora_token_logp_forward")
 
 
@@ -711,7 +712,7 @@ def moe_lora_token_logp_backward(logits: torch.Tensor, targets: torch.Tensor, ls
     T = r.rows
     rc = lib().moe_lora_token_logp_backward(r, px, _vec(targets, T, "targets", torch.int32),
                                             _vec(lse, T, "lse", torch.float32), _vec(dlogp, T, "dlogp", torch.float32),
-                                            pd, _vec(err, 1, "err", torch.int32), _stream(stream))
+                                            pd, _vec(err, 1, "err", torch.int32), _stream_of(logits, "logits", stream))
     _check(rc, "moe_lora_token_logp_backward")
 
 
@@ -761,7 +762,7 @@ def moe_lora_policy_loss(logits: torch.Tensor, targets: torch.Tensor, advantages
                                     _vec(dloss, A, "dloss", f32), _vec(loss, A, "loss", f32),
                                     _vec(stats, 4 * A, "stats", f32), _vec(logp, T, "logp", f32), pd,
                                     _vec(err, 1, "err", torch.int32), _ptr(scratch, None, "scratch"),
-                                    scratch.numel() * scratch.element_size(), _stream(stream))
+                                    scratch.numel() * scratch.element_size(), _stream_of(logits, "logits", stream))
     _check(rc, "moe_lora_policy_loss")
 
 
@@ -792,7 +793,6 @@ def moe_lora_preference_loss(logp: torch.Tensor, targets: torch.Tensor, seq_offs
         raise ValueError("seq_offsets must have 2 * pairs + 1 entries")
     if kind not in PREFERENCE_KINDS:
         raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}, got {kind!r}")
-    _here(logp, "logp")
     P, T, A, f32 = seq_offsets.numel() // 2, logp.numel(), loss.numel(), torch.float32
     offs = _host_offsets(pair_offsets, A, "pair_offsets")
     opt = Preference(T, P, beta, margin, label_smoothing, PREFERENCE_KINDS[kind], int(average), A)
@@ -803,7 +803,7 @@ def moe_lora_preference_loss(logp: torch.Tensor, targets: torch.Tensor, seq_offs
                                         _vec(stats, 4 * A, "stats", f32), _vec(seq_logp, 2 * P, "seq_logp", f32),
                                         _vec(dlogp, T, "dlogp", f32), _vec(err, 1, "err", torch.int32),
                                         _ptr(scratch, None, "scratch"), scratch.numel() * scratch.element_size(),
-                                        _stream(stream))
+                                        _stream_of(logp, "logp", stream))
     _check(rc, "moe_lora_preference_loss")
 
 
@@ -851,10 +851,9 @@ def moe_lora_muon_step(tensors: MuonTensors, momentum: float = 0.95, nesterov: b
     """One Muon step over all tensors: momentum, `steps` Newton-Schulz steps with the coefficients (a, b, c)
     on every matrix, weights.  grad_scale: a device fp32 scalar that multiplies every gradient."""
     a, b, c = coefs
-    _here(tensors.scratch, "the tensors")
     opt = Muon(momentum, eps, a, b, c, int(nesterov), steps, _vec(grad_scale, 1, "grad_scale", torch.float32))
     rc = lib().moe_lora_muon_step(opt, tensors.table, len(tensors.entries), tensors.scratch.data_ptr(),
-                                  tensors.scratch.numel(), _stream(stream))
+                                  tensors.scratch.numel(), _stream_of(tensors.scratch, "the tensors", stream))
     _check(rc, "moe_lora_muon_step")
 
 

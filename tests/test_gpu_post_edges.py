@@ -553,7 +553,7 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     calls = [lambda: m.moe_lora_token_logp_forward(x, y, v), lambda: m.moe_lora_token_logp_backward(x, y, v, v, x),
              lambda: m.moe_lora_policy_loss(x, y, v, v, None, one, four, psc), lambda: m.moe_lora_preference_loss(v, y, seq, None, one, four, fsc),
              lambda: m.moe_lora_muon_step(t)]
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call()
